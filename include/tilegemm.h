@@ -1,7 +1,8 @@
 /*
- * tilegemm — tiled dense GEMM, weight-only 4-bit dequant GEMM, MX-format GEMM
- * and 2:4 structured-sparse GEMM for one AMD Instinct MI355X (gfx950), as
- * hand-written HIP kernels behind a C ABI.
+ * tilegemm — tiled dense GEMM, weight-only 4-bit dequant GEMM, MX-format GEMM,
+ * 2:4 structured-sparse GEMM, 8-bit integer GEMM with its quantisation, and
+ * the norms between transformer blocks, for one AMD Instinct MI355X (gfx950),
+ * as hand-written HIP kernels behind a C ABI.
  *
  * The operation follows the pages' problem statement:
  *   - "TileLang ... 一个高效 GEMM 内核" (mhpq.cn), section 3.2: the caller
@@ -55,8 +56,9 @@ typedef enum {
     TG_ERR_ALIAS = 5,        /* C overlaps an input                               */
     TG_ERR_NO_CONFIG = 6,    /* forced config index out of range / wrong op       */
     TG_ERR_HIP = 7,          /* the HIP runtime reported an error at launch       */
-    TG_ERR_BAD_LAYOUT = 8,   /* trans_a / trans_b not 0 or 1                      */
-    TG_ERR_WORKSPACE = 9,    /* split-K workspace NULL, too small or misaligned    */
+    TG_ERR_BAD_LAYOUT = 8,   /* trans_a / trans_b not 0 or 1; block norm: operands */
+                             /* that do not go together                           */
+    TG_ERR_WORKSPACE = 9,    /* workspace NULL, too small or misaligned            */
     TG_ERR_SCRATCH = 10      /* split-K partials exceed TG_SPLITK_SCRATCH_BYTES    */
 } tg_status;
 
@@ -260,6 +262,179 @@ tg_status tg_gemm_mx(int64_t M, int64_t N, int64_t K, tg_mx_format a_fmt, const 
 tg_status tg_gemm_sp24(int64_t M, int64_t N, int64_t K, tg_dtype dtype, const void* Ac,
                        const uint8_t* Ai, const void* B, void* C, tg_epilogue epi,
                        tg_stream_t stream);
+
+/*
+ * Quantisation of activations to 8-bit integers, one scale for each row
+ * (token): for row m with a = max(max_k |X[m][k]|, 127 * 2^-126),
+ *   Q[m][k] = round(127 X[m][k] / a), ties to even;  s[m] = a / 127 (fp32),
+ * so that X[m][k] is Q[m][k] s[m] to half a level.  (The lower bound on a
+ * keeps s normal: a row of zeros gets zero levels and the scale 2^-126.)
+ * A row that holds an infinity or NaN gets zero levels and the scale NaN:
+ * every product taken from it is NaN.
+ *   X: [M][K] of `dtype`, row stride ldx; Q: int8 [M][K], row stride ldq;
+ *   s: fp32 [M].  Strides in elements, at least K.  Any alignment.
+ *   The levels are the exact ones for fp32, fp16 and bf16 inputs.
+ * Errors: TG_ERR_BAD_DTYPE, TG_ERR_BAD_SHAPE (negative or above 2^31 - 1, or a
+ *   stride below K), TG_ERR_NULL_POINTER, TG_ERR_ALIAS (Q or s overlaps X or
+ *   each other), TG_ERR_HIP.
+ */
+tg_status tg_quant_i8(int64_t M, int64_t K, tg_dtype dtype, const void* X, int64_t ldx, int8_t* Q,
+                      int64_t ldq, float* s, tg_stream_t stream);
+
+/*
+ * 8-bit integer GEMM with a scale for each token and channel:
+ *   C[m][n] = epilogue(sa[m] sw[n] sum_k A[m][k] W[n][k] + bias[n]).
+ *   A: int8 [M][K], row stride lda, with fp32 scales sa [M];
+ *   W: int8 [N][K], row stride ldw, with fp32 scales sw [N];
+ *   bias: fp32 [N] or NULL; C: [M][N] of `dtype`, row stride ldc.
+ *   Strides in elements.  All 256 levels are valid.  The sum is exact (32-bit
+ *   integers, hence K <= 131071); it is converted to fp32, scaled by sa, then
+ *   sw with the bias added, the ReLU applied as in tg_gemm, and rounded once to `dtype`.
+ *   Any sizes and alignment; rows of A and W that start at 16-byte boundaries
+ *   with K % 16 == 0 take the fast kernels.  K == 0: C = epilogue(bias); A and
+ *   W may be NULL then.
+ * The pages name low-bit GEMM workloads ("TileLang架构深度剖析", the performance
+ * section) but not this format.
+ * Errors: TG_ERR_BAD_DTYPE, TG_ERR_BAD_EPILOGUE, TG_ERR_BAD_SHAPE (also a
+ *   stride below its row length, K > 131071), TG_ERR_NULL_POINTER,
+ *   TG_ERR_ALIAS (C overlaps an input), TG_ERR_HIP.
+ */
+tg_status tg_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda,
+                     const float* sa, const int8_t* W, int64_t ldw, const float* sw,
+                     const float* bias, tg_dtype dtype, void* C, int64_t ldc, tg_epilogue epi,
+                     tg_stream_t stream);
+
+/*
+ * The two above in one call: C = epilogue(X W^T + bias) with the rows of X
+ * quantised as by tg_quant_i8 and W in 8 bits as in tg_gemm_i8.
+ *   X: [M][K] of `dtype`, row stride ldx; C: [M][N] of `dtype`, row stride ldc.
+ *   workspace: device memory, 16-byte aligned, of at least the size
+ *     tg_linear_i8_workspace_size reports (it holds the levels and scales; 0
+ *     bytes, and NULL, where the call needs none).  Its contents need not be
+ *     kept between calls; calls that share it must not run concurrently.
+ *   The result has the bits of tg_quant_i8 followed by tg_gemm_i8.
+ * Errors: as for those; TG_ERR_WORKSPACE when the workspace is NULL, smaller
+ *   than needed or not 16-byte aligned; TG_ERR_ALIAS also when it overlaps an
+ *   operand.
+ */
+tg_status tg_linear_i8(int64_t M, int64_t N, int64_t K, tg_dtype dtype, const void* X, int64_t ldx,
+                       const int8_t* W, int64_t ldw, const float* sw, const float* bias, void* C,
+                       int64_t ldc, tg_epilogue epi, void* workspace, size_t workspace_bytes,
+                       tg_stream_t stream);
+tg_status tg_linear_i8_workspace_size(int64_t M, int64_t N, int64_t K, tg_dtype dtype,
+                                      size_t* bytes);
+
+/*
+ * The norms, gate and residual between two blocks of a transformer, in one
+ * pass.  For each token t (row of D values), with norm(v) = v r and
+ * r = 1 / sqrt(mean(v^2) + eps):
+ *   x_out[t] = alpha x[t] + gate[t / gate_rows] * norm(y[t]) * w_post
+ *   h[t]     = norm(x_out[t]) * w_pre
+ * y is the output of the block before, x the residual stream beside it, h the
+ * input of the block after.
+ *   x, x_out: [T][D] of `xtype`; y, h: [T][D] of `btype`; gate: [ceil(T /
+ *     gate_rows)][D], w_post, w_pre: [D], of `btype`, dense.  (xtype, btype):
+ *     equal, or TG_F32 with TG_F16 or TG_BF16.  Row strides in elements.
+ *   y NULL: there is no block before; x_out must be NULL, h = norm(x) * w_pre.
+ *   post_norm 0: y[t] stands in place of norm(y[t]) * w_post (w_post NULL).
+ *   gate, w_post, w_pre NULL: ones.
+ *   h, hq: either, both or (x_out not NULL) neither.  hq: int8 [T][D] with
+ *     fp32 scales hs [T]: h quantised as by tg_quant_i8 from its fp32 values,
+ *     which tg_gemm_i8 takes as A and sa.  (A value within an fp32 rounding of
+ *     the border between two levels may get either.)
+ *   r_post, r_pre: fp32 [T] or NULL: the norms' r, for the gradients.
+ *   x_out may be x itself (same address and stride).
+ * Sums and intermediate values are fp32; x_out is rounded to xtype, and h is
+ * computed from the rounded x_out, so that the call equals one that computes
+ * x_out and one that computes h from it, bit for bit.
+ * D <= 32768.  T == 0 or D == 0: nothing is launched.
+ * Errors: TG_ERR_BAD_DTYPE, TG_ERR_BAD_SHAPE (sizes, strides below D,
+ *   gate_rows < 1 with a gate), TG_ERR_NULL_POINTER (x, or nothing to write,
+ *   or hq without hs or the reverse, x_out NULL with y), TG_ERR_BAD_LAYOUT (x_out, gate, w_post
+ *   or r_post without y; w_post or r_post without post_norm; r_pre or w_pre
+ *   without h or hq), TG_ERR_ALIAS (an output overlaps an input, except x_out
+ *   being x, or another output), TG_ERR_HIP.
+ */
+typedef struct {
+    int64_t T, D;
+    tg_dtype xtype, btype;
+    const void* x;
+    int64_t ldx;
+    const void* y;
+    int64_t ldy;
+    const void* gate;
+    int64_t gate_rows;
+    const void* w_post;
+    const void* w_pre;
+    float alpha, eps;
+    int post_norm;
+    void* x_out;
+    int64_t ldx_out;
+    void* h;
+    int64_t ldh;
+    int8_t* hq;
+    int64_t ldhq;
+    float* hs;
+    float* r_post;
+    float* r_pre;
+} tg_block_norm_args;
+
+tg_status tg_block_norm(const tg_block_norm_args* args, tg_stream_t stream);
+
+/*
+ * Gradients of tg_block_norm (h as h; the 8-bit h has none).  In: x_new, the
+ * x_out of the forward call (its x when y is NULL), y, gate, gate_rows,
+ * w_post, w_pre, alpha, post_norm and the saved r_post, r_pre; the gradients
+ * dx_new at x_out and dh at h (either may be NULL: zeros).  Out, each NULL if
+ * not wanted:
+ *   dx [T][D] of xtype, dy [T][D] of btype,
+ *   dgate [ceil(T / gate_rows)][D], dw_post [D], dw_pre [D] in fp32: sums over
+ *     the tokens that share them.
+ *   Sums are fp32 in a fixed order: the same call gives the same bits.
+ *   workspace: device memory, 16-byte aligned, of at least the size
+ *     tg_block_norm_backward_workspace_size reports for the same arguments; it
+ *     holds partial sums.  Its contents need not be kept; calls that share it must not run
+ *     concurrently.
+ * D <= 32768.  T == 0: dgate, dw_post and dw_pre are not written.
+ * Errors: as tg_block_norm; TG_ERR_NULL_POINTER also when an input that an
+ *   output needs is NULL (x_new and r_pre with dh, r_post with post_norm) or
+ *   when nothing is to be written; TG_ERR_BAD_LAYOUT also for dy, dgate, dw_post without
+ *   their y, gate, w_post, and dw_pre without w_pre and dh; TG_ERR_ALIAS (an
+ *   output or the workspace overlaps an input or another output);
+ *   TG_ERR_WORKSPACE.
+ */
+typedef struct {
+    int64_t T, D;
+    tg_dtype xtype, btype;
+    const void* x_new;
+    int64_t ldx_new;
+    const void* y;
+    int64_t ldy;
+    const void* gate;
+    int64_t gate_rows;
+    const void* w_post;
+    const void* w_pre;
+    float alpha;
+    int post_norm;
+    const float* r_post;
+    const float* r_pre;
+    const void* dx_new;
+    int64_t lddx_new;
+    const void* dh;
+    int64_t lddh;
+    void* dx;
+    int64_t lddx;
+    void* dy;
+    int64_t lddy;
+    float* dgate;
+    float* dw_post;
+    float* dw_pre;
+} tg_block_norm_grad_args;
+
+tg_status tg_block_norm_backward(const tg_block_norm_grad_args* args, void* workspace,
+                                 size_t workspace_bytes, tg_stream_t stream);
+tg_status tg_block_norm_backward_workspace_size(const tg_block_norm_grad_args* args,
+                                                size_t* bytes);
 
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* tg_status_str(tg_status s);

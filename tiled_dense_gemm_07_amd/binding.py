@@ -11,6 +11,7 @@ PyTorch is used only for device memory and streams.
 
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -30,10 +31,48 @@ EXPORTS = ("tg_gemm", "tg_gemm_ex", "tg_dequant_gemm_w4", "tg_status_str", "tg_q
            "tg_gemm_ex_config", "tg_dequant_gemm_w4_config", "tg_tile_map", "tg_gemm_mx",
            "tg_gemm_mx_config", "tg_gemm_sp24", "tg_gemm_sp24_config", "tg_gemm_splitk",
            "tg_gemm_splitk_workspace_size", "tg_gemm_splitk_config", "tg_gemm_splitk_noalloc",
-           "tg_set_clock_stamps", "tg_set_swizzle_override", "tg_config_occupancy")
+           "tg_set_clock_stamps", "tg_set_swizzle_override", "tg_config_occupancy",
+           "tg_quant_i8", "tg_gemm_i8", "tg_linear_i8", "tg_linear_i8_workspace_size",
+           "tg_block_norm", "tg_block_norm_backward", "tg_block_norm_backward_workspace_size")
 TG_SPLITK_SCRATCH_BYTES = 16 * 1024 * 1024
 
 _lib = None
+
+
+class BlockNormArgs(ctypes.Structure):
+    """tg_block_norm_args."""
+
+    _fields_ = [("T", ctypes.c_int64), ("D", ctypes.c_int64), ("xtype", ctypes.c_int),
+                ("btype", ctypes.c_int), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("gate", ctypes.c_void_p),
+                ("gate_rows", ctypes.c_int64), ("w_post", ctypes.c_void_p),
+                ("w_pre", ctypes.c_void_p), ("alpha", ctypes.c_float), ("eps", ctypes.c_float),
+                ("post_norm", ctypes.c_int), ("x_out", ctypes.c_void_p),
+                ("ldx_out", ctypes.c_int64), ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+                ("hq", ctypes.c_void_p), ("ldhq", ctypes.c_int64), ("hs", ctypes.c_void_p),
+                ("r_post", ctypes.c_void_p), ("r_pre", ctypes.c_void_p)]
+
+
+class BlockNormGradArgs(ctypes.Structure):
+    """tg_block_norm_grad_args."""
+
+    _fields_ = [("T", ctypes.c_int64), ("D", ctypes.c_int64), ("xtype", ctypes.c_int),
+                ("btype", ctypes.c_int), ("x_new", ctypes.c_void_p), ("ldx_new", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("gate", ctypes.c_void_p),
+                ("gate_rows", ctypes.c_int64), ("w_post", ctypes.c_void_p),
+                ("w_pre", ctypes.c_void_p), ("alpha", ctypes.c_float),
+                ("post_norm", ctypes.c_int), ("r_post", ctypes.c_void_p),
+                ("r_pre", ctypes.c_void_p), ("dx_new", ctypes.c_void_p),
+                ("lddx_new", ctypes.c_int64), ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dy", ctypes.c_void_p),
+                ("lddy", ctypes.c_int64), ("dgate", ctypes.c_void_p),
+                ("dw_post", ctypes.c_void_p), ("dw_pre", ctypes.c_void_p)]
+
+
+# Result of block_norm: the new residual stream, h (block type, or int8 levels
+# with their scales hs), and the norms' reciprocal roots (None unless saved).
+BlockNorm = collections.namedtuple("BlockNorm", "x h hs r_post r_pre")
+BlockNormGrad = collections.namedtuple("BlockNormGrad", "dx dy dgate dw_post dw_pre")
 
 
 class TileGemmError(RuntimeError):
@@ -108,6 +147,21 @@ def load_library():
     lib.tg_set_swizzle_override.restype = None
     lib.tg_config_occupancy.argtypes = [c_int, c_int, c_int, ctypes.POINTER(c_int)]
     lib.tg_config_occupancy.restype = c_int
+    size_p = ctypes.POINTER(ctypes.c_size_t)
+    lib.tg_quant_i8.argtypes = [i64, i64, c_int, p, i64, p, i64, p, p]
+    lib.tg_gemm_i8.argtypes = [i64, i64, i64, p, i64, p, p, i64, p, p, c_int, p, i64, c_int, p]
+    lib.tg_linear_i8.argtypes = [i64, i64, i64, c_int, p, i64, p, i64, p, p, p, i64, c_int, p,
+                                 ctypes.c_size_t, p]
+    lib.tg_linear_i8_workspace_size.argtypes = [i64, i64, i64, c_int, size_p]
+    lib.tg_block_norm.argtypes = [ctypes.POINTER(BlockNormArgs), p]
+    lib.tg_block_norm_backward.argtypes = [ctypes.POINTER(BlockNormGradArgs), p, ctypes.c_size_t,
+                                           p]
+    lib.tg_block_norm_backward_workspace_size.argtypes = [ctypes.POINTER(BlockNormGradArgs),
+                                                          size_p]
+    for name in ("tg_quant_i8", "tg_gemm_i8", "tg_linear_i8", "tg_linear_i8_workspace_size",
+                 "tg_block_norm", "tg_block_norm_backward",
+                 "tg_block_norm_backward_workspace_size"):
+        getattr(lib, name).restype = c_int
     _lib = lib
     return lib
 
@@ -437,6 +491,294 @@ def gemm_sp24(Ac, Ai, B, C=None, epilogue=None, stream=None, config=None):
     lib = load_library()
     _check(lib.tg_gemm_sp24(*args) if config is None else lib.tg_gemm_sp24_config(config, *args))
     return C
+
+
+# --------------------------------------------------------------------------
+# 8-bit integer path and block norms.  These take row-strided 2-D tensors
+# (unit stride along a row), for instance slices of a wider buffer.
+# --------------------------------------------------------------------------
+def _rows(name, t, shape=None, dtype=None):
+    """Row stride of the 2-D GPU tensor t; checks shape and dtype."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError("%s must be %s, got %s"
+                         % (name, "2-D" if shape is None else list(shape), tuple(t.shape)))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if cols > 1 and unit != 1:
+        raise ValueError("%s must have unit stride along its rows" % name)
+    if rows <= 1:
+        return cols
+    if ld < cols:
+        raise ValueError("%s must have rows that do not overlap" % name)
+    return ld
+
+
+def _vector(name, t, n, dtype):
+    """Device pointer of the dense 1-D GPU tensor t (None: NULL)."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.numel() != n or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError("%s must be a dense vector of %d values" % (name, n))
+    return t.data_ptr()
+
+
+def _one_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("operands must be on one device: %s and %s"
+                             % (first.device, t.device))
+
+
+def _empty(shape, dtype, like, stream):
+    """An output or workspace on like's device that belongs to the call's stream."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def quant_i8(X, Q=None, s=None, stream=None):
+    """Rows of X to 8-bit levels and one fp32 scale each (tg_quant_i8): returns
+    (Q int8 [M, K], s fp32 [M]) with X about Q * s[:, None]."""
+    import torch
+
+    ldx = _rows("X", X)
+    M, K = X.shape
+    if Q is None:
+        Q = _empty((M, K), torch.int8, X, stream)
+    if s is None:
+        s = _empty((M,), torch.float32, X, stream)
+    _one_device(X, Q, s)
+    ldq = _rows("Q", Q, (M, K), torch.int8)
+    _check(load_library().tg_quant_i8(M, K, _dtype_code(X), X.data_ptr(), ldx, Q.data_ptr(), ldq,
+                                      _vector("s", s, M, torch.float32),
+                                      _stream_ptr(X.device, stream)))
+    return Q, s
+
+
+def gemm_i8(A, sa, W, sw, bias=None, out_dtype=None, C=None, epilogue=None, stream=None):
+    """C = epilogue((A @ W^T) * sa[:, None] * sw + bias) with A [M, K] and W
+    [N, K] in int8, fp32 scales sa [M] and sw [N], fp32 bias [N] or None; C
+    [M, N] of out_dtype (bfloat16 unless C or out_dtype says otherwise)."""
+    import torch
+
+    lda = _rows("A", A, dtype=torch.int8)
+    ldw = _rows("W", W, dtype=torch.int8)
+    M, K = A.shape
+    N = W.shape[0]
+    if W.shape[1] != K:
+        raise ValueError("inner dimensions differ: A is %s, W is %s"
+                         % (tuple(A.shape), tuple(W.shape)))
+    if C is None:
+        C = _empty((M, N), out_dtype or torch.bfloat16, A, stream)
+    elif out_dtype is not None and C.dtype != out_dtype:
+        raise TypeError("C must be %s, got %s" % (out_dtype, C.dtype))
+    ldc = _rows("C", C, (M, N))
+    _one_device(A, sa, W, sw, bias, C)
+    _check(load_library().tg_gemm_i8(
+        M, N, K, A.data_ptr(), lda, _vector("sa", sa, M, torch.float32), W.data_ptr(), ldw,
+        _vector("sw", sw, N, torch.float32), _vector("bias", bias, N, torch.float32),
+        _dtype_code(C), C.data_ptr(), ldc, _epi_code(epilogue), _stream_ptr(A.device, stream)))
+    return C
+
+
+def linear_i8_workspace_size(M: int, N: int, K: int, dtype: int) -> int:
+    """Workspace bytes :func:`linear_i8` needs (0: none)."""
+    out = ctypes.c_size_t(0)
+    _check(load_library().tg_linear_i8_workspace_size(M, N, K, dtype, ctypes.byref(out)))
+    return out.value
+
+
+def linear_i8(X, W, sw, bias=None, C=None, epilogue=None, workspace=None, stream=None):
+    """C = epilogue(X @ W^T * sw + bias) with the rows of X [M, K] (fp32, fp16
+    or bf16) quantised within the call, as :func:`quant_i8` and
+    :func:`gemm_i8` one after the other; C [M, N] of X's dtype.  workspace: a
+    uint8 device tensor of at least :func:`linear_i8_workspace_size` bytes
+    (allocated here when None and needed)."""
+    import torch
+
+    ldx = _rows("X", X)
+    ldw = _rows("W", W, dtype=torch.int8)
+    M, K = X.shape
+    N = W.shape[0]
+    if W.shape[1] != K:
+        raise ValueError("inner dimensions differ: X is %s, W is %s"
+                         % (tuple(X.shape), tuple(W.shape)))
+    if C is None:
+        C = _empty((M, N), X.dtype, X, stream)
+    ldc = _rows("C", C, (M, N), X.dtype)
+    dt = _dtype_code(X)
+    if workspace is None:
+        need = linear_i8_workspace_size(M, N, K, dt)
+        workspace = _empty((need,), torch.uint8, X, stream) if need else None
+    else:
+        _require_gpu_tensor("workspace", workspace)
+    _one_device(X, W, sw, bias, C, workspace)
+    _check(load_library().tg_linear_i8(
+        M, N, K, dt, X.data_ptr(), ldx, W.data_ptr(), ldw, _vector("sw", sw, N, torch.float32),
+        _vector("bias", bias, N, torch.float32), C.data_ptr(), ldc, _epi_code(epilogue),
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream_ptr(X.device, stream)))
+    return C
+
+
+def _gate_arg(gate, gate_rows, T, D, dtype):
+    """(pointer, gate_rows) of a gate [G, D] or [D]; gate_rows may be left out
+    for one row (shared by every token) or one row for each token."""
+    if gate is None:
+        return None, 0
+    G = 1 if gate.dim() == 1 else gate.shape[0]
+    if not gate_rows:
+        if G != 1 and G != T:
+            raise ValueError("gate_rows is needed: gate has %d rows for %d tokens" % (G, T))
+        gate_rows = T if G == 1 else 1
+    if not gate.is_cuda or not gate.is_contiguous():
+        raise ValueError("gate must be a dense GPU tensor")
+    if gate.dtype != dtype:
+        raise TypeError("gate must be %s, got %s" % (dtype, gate.dtype))
+    if gate_rows < 1 or gate.shape[-1] != D or gate.dim() > 2 or (T > 0 and G != -(-T // gate_rows)):
+        raise ValueError("gate must be [ceil(T / gate_rows), D] = [%d, %d], got %s"
+                         % (-(-T // max(1, gate_rows)), D, tuple(gate.shape)))
+    return gate.data_ptr(), gate_rows
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def block_norm(x, y=None, gate=None, gate_rows=None, w_post=None, w_pre=None, alpha=1.0, eps=1e-6,
+               post_norm=True, out="h", x_out=None, h=None, hs=None, save=False, stream=None):
+    """The norms, gate and residual between two blocks (tg_block_norm):
+
+        x' = alpha x + gate * norm(y) * w_post,   h = norm(x') * w_pre
+
+    x [T, D]: residual stream; y [T, D]: output of the block before (None: x'
+    is x); gate [G, D], one row for gate_rows tokens.  out: "h" (h in y's
+    type, x's without y), "i8" (h as int8 levels with scales hs) or None (x'
+    only).  x_out may be x.  save: also return the norms' reciprocal roots
+    for :func:`block_norm_backward`.  Returns a BlockNorm(x, h, hs, r_post,
+    r_pre)."""
+    import torch
+
+    if out not in ("h", "i8", None):
+        raise ValueError("out must be 'h', 'i8' or None")
+    ldx = _rows("x", x)
+    T, D = x.shape
+    shape = (T, D)
+    block = y if y is not None else (h if h is not None and out == "h" else w_pre)
+    bt = x.dtype if block is None else block.dtype
+    a = BlockNormArgs()
+    a.T, a.D, a.xtype, a.btype = T, D, _dtype_code(x), _dtype_code(x if block is None else block)
+    a.x, a.ldx = x.data_ptr(), ldx
+    a.alpha, a.eps, a.post_norm = alpha, eps, bool(post_norm)
+    if y is not None:
+        a.y, a.ldy = y.data_ptr(), _rows("y", y, shape)
+        if x_out is None:
+            x_out = _empty(shape, x.dtype, x, stream)
+    if x_out is not None:
+        a.x_out, a.ldx_out = x_out.data_ptr(), _rows("x_out", x_out, shape, x.dtype)
+    a.gate, a.gate_rows = _gate_arg(gate, gate_rows, T, D, bt)
+    a.w_post = _vector("w_post", w_post, D, bt)
+    a.w_pre = _vector("w_pre", w_pre, D, bt)
+    if out == "h":
+        if h is None:
+            h = _empty(shape, bt, x, stream)
+        a.h, a.ldh = h.data_ptr(), _rows("h", h, shape, bt)
+    elif out == "i8":
+        if h is None:
+            h = _empty(shape, torch.int8, x, stream)
+        if hs is None:
+            hs = _empty((T,), torch.float32, x, stream)
+        a.hq, a.ldhq = h.data_ptr(), _rows("h", h, shape, torch.int8)
+        a.hs = _vector("hs", hs, T, torch.float32)
+    r_post = r_pre = None
+    if save:
+        if y is not None and post_norm:
+            r_post = _empty((T,), torch.float32, x, stream)
+            a.r_post = r_post.data_ptr()
+        if out is not None:
+            r_pre = _empty((T,), torch.float32, x, stream)
+            a.r_pre = r_pre.data_ptr()
+    _one_device(x, y, gate, w_post, w_pre, x_out, h, hs)
+    _check(load_library().tg_block_norm(ctypes.byref(a), _stream_ptr(x.device, stream)))
+    return BlockNorm(x if x_out is None else x_out, h, hs, r_post, r_pre)
+
+
+def block_norm_backward(x_new, dx_new=None, dh=None, y=None, gate=None, gate_rows=None,
+                        w_post=None, w_pre=None, r_post=None, r_pre=None, alpha=1.0,
+                        post_norm=True, workspace=None, stream=None):
+    """Gradients of :func:`block_norm` (tg_block_norm_backward) from those at
+    x' (dx_new) and at h (dh), either of which may be None.  x_new, r_post and
+    r_pre are the forward call's x, r_post and r_pre.  Returns a
+    BlockNormGrad(dx, dy, dgate, dw_post, dw_pre), dx and dy in their inputs'
+    types, the rest (None where there is no such input) in fp32."""
+    import torch
+
+    T, D = x_new.shape
+    shape = (T, D)
+    block = y if y is not None else (dh if dh is not None else w_pre)
+    bt = x_new.dtype if block is None else block.dtype
+    f32 = torch.float32
+    a = BlockNormGradArgs()
+    a.T, a.D, a.xtype = T, D, _dtype_code(x_new)
+    a.btype = a.xtype if block is None else _dtype_code(block)
+    a.x_new, a.ldx_new = x_new.data_ptr(), _rows("x_new", x_new)
+    a.alpha, a.post_norm = alpha, bool(post_norm)
+    dx = _empty(shape, x_new.dtype, x_new, stream)
+    a.dx, a.lddx = dx.data_ptr(), D
+    dy = dgate = dw_post = dw_pre = None
+    if y is not None:
+        a.y, a.ldy = y.data_ptr(), _rows("y", y, shape)
+        dy = _empty(shape, bt, x_new, stream)
+        a.dy, a.lddy = dy.data_ptr(), D
+    a.gate, a.gate_rows = _gate_arg(gate, gate_rows, T, D, bt)
+    if gate is not None:
+        dgate = _empty(gate.shape, f32, x_new, stream)
+        a.dgate = dgate.data_ptr()
+    a.w_post = _vector("w_post", w_post, D, bt)
+    if w_post is not None:
+        dw_post = _empty((D,), f32, x_new, stream)
+        a.dw_post = dw_post.data_ptr()
+    a.w_pre = _vector("w_pre", w_pre, D, bt)
+    if dh is not None:
+        a.dh, a.lddh = dh.data_ptr(), _rows("dh", dh, shape, bt)
+        a.r_pre = _vector("r_pre", r_pre, T, f32)
+        if w_pre is not None:
+            dw_pre = _empty((D,), f32, x_new, stream)
+            a.dw_pre = dw_pre.data_ptr()
+    if dx_new is not None:
+        a.dx_new, a.lddx_new = dx_new.data_ptr(), _rows("dx_new", dx_new, shape, x_new.dtype)
+    if post_norm and y is not None:
+        a.r_post = _vector("r_post", r_post, T, f32)
+    if T == 0:  # sums over no tokens; nothing is launched
+        with torch.cuda.stream(stream):
+            for g in (dw_post, dw_pre):
+                if g is not None:
+                    g.zero_()
+    lib = load_library()
+    if workspace is None:
+        need = ctypes.c_size_t(0)
+        _check(lib.tg_block_norm_backward_workspace_size(ctypes.byref(a), ctypes.byref(need)))
+        workspace = _empty((need.value,), torch.uint8, x_new, stream) if need.value else None
+    else:
+        _require_gpu_tensor("workspace", workspace)
+    _one_device(x_new, dx_new, dh, y, gate, w_post, w_pre, r_post, r_pre, workspace)
+    _check(lib.tg_block_norm_backward(
+        ctypes.byref(a), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream_ptr(x_new.device, stream)))
+    return BlockNormGrad(dx, dy, dgate, dw_post, dw_pre)
 
 
 def query_config(op: int, M: int, N: int, K: int, dtype: int = TG_BF16, trans_a: bool = False,

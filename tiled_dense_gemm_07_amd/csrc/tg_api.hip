@@ -21,6 +21,7 @@
 
 #include "../../include/tilegemm.h"
 #include "tg_configs.h"
+#include "tg_host.h"
 #include "tg_kernel.h"
 
 // Scratch of tg_gemm_splitk_noalloc: the split-K arrival counters and fp32
@@ -427,7 +428,7 @@ bool overlaps(const void* a, size_t an, const void* b, size_t bn)
     return a0 < b0 + bn && b0 < a0 + an;
 }
 
-constexpr int64_t kMaxDim = 0x7FFFFFFF;
+using tg::kMaxDim;
 
 // Shape limits that keep every per-tile byte offset inside 31 bits.
 tg_status check_shape(int64_t M, int64_t N, int64_t K, int esize)
@@ -784,6 +785,30 @@ tg_status sp24_impl(const Config* forced, int forced_index, int64_t M, int64_t N
 
 }  // namespace
 
+namespace tg {
+
+unsigned long long* clock_stamps() { return g_stamps.load(std::memory_order_relaxed); }
+int swizzle_override() { return g_group_override.load(std::memory_order_relaxed); }
+
+tg_status launch_kernel(const void* kernel, int64_t grid_x, int64_t grid_y, int threads,
+                        void* params, hipStream_t stream, const char* what)
+{
+    if (grid_x > kMaxDim || grid_y > 65535)
+        return TG_ERR_BAD_SHAPE;
+    const char* fault = getenv("TG_FAULT");
+    if (fault && strcmp(fault, "launch") == 0)
+        return TG_ERR_HIP;
+    if (getenv("TG_LOG"))
+        fprintf(stderr, "[tilegemm] %s grid=%lldx%lld threads=%d\n", what, (long long)grid_x,
+                (long long)grid_y, threads);
+    void* args[] = {params};
+    const hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)grid_x, (unsigned)grid_y),
+                                         dim3((unsigned)threads), args, 0, stream);
+    return e == hipSuccess ? TG_OK : TG_ERR_HIP;
+}
+
+}  // namespace tg
+
 extern "C" {
 
 tg_status tg_gemm(int64_t M, int64_t N, int64_t K, tg_dtype dtype, const void* A, const void* B,
@@ -882,24 +907,25 @@ const char* tg_status_str(tg_status s)
     case TG_ERR_NULL_POINTER:
         return "TG_ERR_NULL_POINTER: a required pointer is NULL";
     case TG_ERR_BAD_SHAPE:
-        return "TG_ERR_BAD_SHAPE: negative or too large size, or K not a multiple of 32 (dequant) "
-               "or 128 (MX)";
+        return "TG_ERR_BAD_SHAPE: negative or too large size, a row stride below the row length, "
+               "or K not a multiple of 32 (dequant) or 128 (MX)";
     case TG_ERR_BAD_DTYPE:
         return "TG_ERR_BAD_DTYPE: dtype must be TG_F32, TG_F16 or TG_BF16 (MX: TG_MX_E2M1 or "
-               "TG_MX_E4M3)";
+               "TG_MX_E4M3; block norms: xtype equal to btype, or TG_F32)";
     case TG_ERR_BAD_EPILOGUE:
         return "TG_ERR_BAD_EPILOGUE: epilogue must be TG_EPI_NONE or TG_EPI_RELU";
     case TG_ERR_ALIAS:
-        return "TG_ERR_ALIAS: the output overlaps an input";
+        return "TG_ERR_ALIAS: an output overlaps an input or another output";
     case TG_ERR_NO_CONFIG:
         return "TG_ERR_NO_CONFIG: no such kernel configuration for this call";
     case TG_ERR_HIP:
         return "TG_ERR_HIP: the HIP runtime reported an error at launch";
     case TG_ERR_BAD_LAYOUT:
-        return "TG_ERR_BAD_LAYOUT: trans_a and trans_b must be 0 or 1";
+        return "TG_ERR_BAD_LAYOUT: trans_a and trans_b must be 0 or 1; block norms: an operand "
+               "without the one it belongs to";
     case TG_ERR_WORKSPACE:
-        return "TG_ERR_WORKSPACE: split-K workspace NULL, smaller than "
-               "tg_gemm_splitk_workspace_size, or not 16-byte aligned";
+        return "TG_ERR_WORKSPACE: workspace NULL, smaller than the call's workspace-size query "
+               "reports, or not 16-byte aligned";
     case TG_ERR_SCRATCH:
         return "TG_ERR_SCRATCH: the split needs more than the fixed scratch array "
                "(TG_SPLITK_SCRATCH_BYTES); use tg_gemm_splitk with a workspace, or fewer splits";

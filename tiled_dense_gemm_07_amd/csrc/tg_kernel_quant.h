@@ -1,0 +1,95 @@
+// Quantisation of activations to 8 bits, one scale for each row (tg_quant_i8).
+// One pass over memory: a team of TPR threads holds a row of up to 8 NC TPR
+// elements in registers between the search for its largest magnitude and the
+// conversion.  Longer rows (NC = 0) are read twice.
+#pragma once
+
+#include "tg_rows.h"
+
+namespace tg {
+
+struct QuantParams {
+    const void* X;
+    int8_t* Q;
+    float* s;
+    int64_t M;
+    int K;
+    int64_t ldx, ldq;
+    int kq;  // columns of Q to write: past K, zeros
+};
+
+template <int DT>
+__device__ __forceinline__ void quant_chunk(const Raw8<DT>& r, const RowLevels& L, int8_t* row,
+                                            int at, int left)
+{
+    int q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (DT == DT_F32)
+            q[i] = L.level64(get8<DT>(r, i));
+        else
+            q[i] = L.level(get8<DT>(r, i));
+    }
+    store_levels(row, at, left, q);
+}
+
+template <int DT>
+__device__ __forceinline__ u32 chunk_amax(const Raw8<DT>& r, u32 m)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const u32 b = __builtin_bit_cast(u32, get8<DT>(r, i)) & 0x7FFFFFFFu;
+        m = b > m ? b : m;
+    }
+    return m;
+}
+
+// NT threads, NT / TPR rows per workgroup.
+template <int DT, int NT, int TPR, int NC>
+__global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void quant_i8_kernel(QuantParams p)
+{
+    __shared__ u32 slot[16];
+    const int t = threadIdx.x % TPR;
+    const int64_t row = (int64_t)blockIdx.x * (NT / TPR) + threadIdx.x / TPR;
+    if (row >= p.M)
+        return;  // whole waves; rows share a workgroup only when TPR is one wave
+    const char* x = elem_ptr<DT>(p.X, row * p.ldx);
+    int8_t* q = p.Q + row * p.ldq;
+    u32 m[1] = {0};
+    RowLevels L;
+    if constexpr (NC > 0) {
+        Raw8<DT> r[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int at = 8 * (t + c * TPR);
+            load8<DT>(r[c], x, at, p.K - at);
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            m[0] = chunk_amax<DT>(r[c], m[0]);
+        row_all<MaxOp, TPR, 1>(m, slot);
+        L.of_amax(m[0]);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int at = 8 * (t + c * TPR);
+            quant_chunk<DT>(r[c], L, q, at, p.kq - at);
+        }
+    } else {
+        for (int at = 8 * t; at < p.K; at += 8 * TPR) {
+            Raw8<DT> r;
+            load8<DT>(r, x, at, p.K - at);
+            m[0] = chunk_amax<DT>(r, m[0]);
+        }
+        row_all<MaxOp, TPR, 1>(m, slot);
+        L.of_amax(m[0]);
+        for (int at = 8 * t; at < p.kq; at += 8 * TPR) {
+            Raw8<DT> r;
+            load8<DT>(r, x, at, p.K - at);
+            quant_chunk<DT>(r, L, q, at, p.kq - at);
+        }
+    }
+    if (t == 0)
+        p.s[row] = L.scale;
+}
+
+}  // namespace tg

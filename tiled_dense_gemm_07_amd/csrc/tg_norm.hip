@@ -1,0 +1,310 @@
+// Entry points of the norms between blocks and their gradients.  Arguments are
+// checked before any HIP call; the kernel is chosen by the row length.
+#include <hip/hip_runtime.h>
+
+#include "tg_host.h"
+#include "tg_kernel_norm.h"
+
+namespace {
+
+using tg::ceil_div;
+using tg::kMaxDim;
+using tg::overlap;
+using tg::Span;
+using tg::span;
+using tg::span1;
+
+constexpr int64_t kMaxD = 32768;
+
+bool types_ok(int xt, int bt)
+{
+    return tg::dtype_ok(xt) && tg::dtype_ok(bt) && (xt == bt || xt == TG_F32);
+}
+
+// Calls f with the two types as compile-time constants.
+template <class F>
+auto by_types(int xt, int bt, const F& f)
+{
+    using std::integral_constant;
+    if (xt == TG_BF16)
+        return f(integral_constant<int, tg::DT_BF16>{}, integral_constant<int, tg::DT_BF16>{});
+    if (xt == TG_F16)
+        return f(integral_constant<int, tg::DT_F16>{}, integral_constant<int, tg::DT_F16>{});
+    if (bt == TG_BF16)
+        return f(integral_constant<int, tg::DT_F32>{}, integral_constant<int, tg::DT_BF16>{});
+    if (bt == TG_F16)
+        return f(integral_constant<int, tg::DT_F32>{}, integral_constant<int, tg::DT_F16>{});
+    return f(integral_constant<int, tg::DT_F32>{}, integral_constant<int, tg::DT_F32>{});
+}
+
+struct Pick {
+    const void* kernel;
+    int threads;  // of a workgroup
+    int rows;     // of a workgroup
+};
+
+Pick pick_forward(int64_t D, int xt, int bt)
+{
+    return by_types(xt, bt, [&](auto X, auto B) -> Pick {
+        constexpr int XT = decltype(X)::value, BT = decltype(B)::value;
+        if (D <= 512)
+            return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 64, 1>, 256, 4};
+        if (D <= 2048)
+            return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 256, 1>, 256, 1};
+        if (D <= 4096)
+            return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 256, 2>, 256, 1};
+        if (D <= 8192)
+            return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 1>, 1024, 1};
+        if (D <= 16384)
+            return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 2>, 1024, 1};
+        return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 4>, 1024, 1};
+    });
+}
+
+Pick pick_backward(int64_t D, int xt, int bt)
+{
+    return by_types(xt, bt, [&](auto X, auto B) -> Pick {
+        constexpr int XT = decltype(X)::value, BT = decltype(B)::value;
+        if (D <= 512)
+            return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 64, 1>, 64, 1};
+        if (D <= 2048)
+            return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 256, 1>, 256, 1};
+        if (D <= 4096)
+            return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 256, 2>, 256, 1};
+        if (D <= 8192)
+            return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 512, 2>, 512, 1};
+        if (D <= 16384)
+            return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 1024, 2>, 1024, 1};
+        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 1024, 4>, 1024, 1};
+    });
+}
+
+bool bad_size(int64_t T, int64_t D) { return T < 0 || D < 0 || T > kMaxDim || D > kMaxD; }
+bool bad_stride(const void* p, int64_t ld, int64_t D) { return p && ld < D; }
+
+// How the gradient kernel's workgroups share the rows, and the workspace.
+struct GradPlan {
+    int64_t groups;  // rows of gate (1 without a gate)
+    int64_t gate_rows;
+    int64_t rows;    // rows of a workgroup
+    int parts;       // workgroups of a group (1: whole groups to a workgroup)
+    int64_t P;       // workgroups
+    int64_t Dp;
+    bool pre, post, gate;  // partial sums kept
+    size_t bytes;
+};
+
+GradPlan grad_plan(const tg_block_norm_grad_args& a)
+{
+    GradPlan g{};
+    // About two workgroups to a compute unit, and at least 8 rows to each:
+    // fewer would write more partial sums than they save in time.
+    int64_t want = ceil_div(a.T, 512);
+    want = want < 8 ? 8 : want;
+    g.gate_rows = a.gate ? (a.gate_rows < a.T ? a.gate_rows : a.T) : a.T;
+    g.groups = ceil_div(a.T, g.gate_rows);
+    if (g.gate_rows <= want) {
+        g.parts = 1;
+        g.rows = ceil_div(want, g.gate_rows) * g.gate_rows;
+        g.P = ceil_div(a.T, g.rows);
+    } else {
+        g.parts = (int)ceil_div(g.gate_rows, want);
+        g.rows = ceil_div(g.gate_rows, g.parts);
+        g.P = g.groups * g.parts;
+    }
+    g.Dp = ceil_div(a.D, 8) * 8;
+    g.pre = a.dw_pre != nullptr;
+    g.post = a.dw_post != nullptr;
+    g.gate = a.dgate != nullptr && g.parts > 1;
+    g.bytes = (size_t)(g.P * g.Dp * 4) * ((g.pre ? 1 : 0) + (g.post ? 1 : 0) + (g.gate ? 1 : 0));
+    return g;
+}
+
+// Sizes, types and the operands that go together.
+tg_status check_grad(const tg_block_norm_grad_args* a)
+{
+    if (!a)
+        return TG_ERR_NULL_POINTER;
+    if (!types_ok(a->xtype, a->btype))
+        return TG_ERR_BAD_DTYPE;
+    if (bad_size(a->T, a->D) || (a->gate && a->gate_rows < 1))
+        return TG_ERR_BAD_SHAPE;
+    if (bad_stride(a->x_new, a->ldx_new, a->D) || bad_stride(a->y, a->ldy, a->D) ||
+        bad_stride(a->dx_new, a->lddx_new, a->D) || bad_stride(a->dh, a->lddh, a->D) ||
+        bad_stride(a->dx, a->lddx, a->D) || bad_stride(a->dy, a->lddy, a->D))
+        return TG_ERR_BAD_SHAPE;
+    return TG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+tg_status tg_block_norm(const tg_block_norm_args* a, tg_stream_t stream)
+{
+    if (!a)
+        return TG_ERR_NULL_POINTER;
+    if (!types_ok(a->xtype, a->btype))
+        return TG_ERR_BAD_DTYPE;
+    const int64_t T = a->T, D = a->D;
+    if (bad_size(T, D) || (a->gate && a->gate_rows < 1))
+        return TG_ERR_BAD_SHAPE;
+    if (bad_stride(a->x, a->ldx, D) || bad_stride(a->y, a->ldy, D) ||
+        bad_stride(a->x_out, a->ldx_out, D) || bad_stride(a->h, a->ldh, D) ||
+        bad_stride(a->hq, a->ldhq, D))
+        return TG_ERR_BAD_SHAPE;
+    if (T == 0 || D == 0)
+        return TG_OK;
+    if (!a->x || (a->y && !a->x_out) || (!a->x_out && !a->h && !a->hq) || (!a->hq != !a->hs))
+        return TG_ERR_NULL_POINTER;
+    if ((!a->y && (a->x_out || a->gate || a->w_post || a->r_post)) ||
+        (!a->post_norm && (a->w_post || a->r_post)) || (!a->h && !a->hq && (a->r_pre || a->w_pre)))
+        return TG_ERR_BAD_LAYOUT;
+    const int xs = tg::dtype_size(a->xtype), bs = tg::dtype_size(a->btype);
+    const int64_t gr = a->gate ? (a->gate_rows < T ? a->gate_rows : T) : T;
+    const Span in[] = {span(a->x, T, D, a->ldx, xs), span(a->y, T, D, a->ldy, bs),
+                       span1(a->gate, ceil_div(T, gr) * D, bs), span1(a->w_post, D, bs),
+                       span1(a->w_pre, D, bs)};
+    const Span out[] = {span(a->x_out, T, D, a->ldx_out, xs), span(a->h, T, D, a->ldh, bs),
+                        span(a->hq, T, D, a->ldhq, 1),        span1(a->hs, T, 4),
+                        span1(a->r_post, T, 4),               span1(a->r_pre, T, 4)};
+    const bool in_place = a->x_out == a->x && a->ldx_out == a->ldx;
+    for (int o = 0; o < 6; ++o) {
+        for (int i = 0; i < 5; ++i)
+            if (overlap(out[o], in[i]) && !(o == 0 && i == 0 && in_place))
+                return TG_ERR_ALIAS;
+        for (int q = 0; q < o; ++q)
+            if (overlap(out[o], out[q]))
+                return TG_ERR_ALIAS;
+    }
+    tg::NormParams p{};
+    p.x = a->x;
+    p.y = a->y;
+    p.gate = a->gate;
+    p.w_post = a->w_post;
+    p.w_pre = a->w_pre;
+    p.x_out = a->x_out;
+    p.h = a->h;
+    p.hq = a->hq;
+    p.hs = a->hs;
+    p.r_post = a->r_post;
+    p.r_pre = a->r_pre;
+    p.T = T;
+    p.ldx = a->ldx;
+    p.ldy = a->ldy;
+    p.ldxo = a->ldx_out;
+    p.ldh = a->ldh;
+    p.ldhq = a->ldhq;
+    p.gate_rows = gr;
+    p.D = (int)D;
+    p.post = a->post_norm != 0;
+    p.alpha = a->alpha;
+    p.eps = a->eps;
+    const Pick k = pick_forward(D, a->xtype, a->btype);
+    return tg::launch_kernel(k.kernel, ceil_div(T, k.rows), 1, k.threads, &p, (hipStream_t)stream,
+                             "block_norm");
+}
+
+tg_status tg_block_norm_backward_workspace_size(const tg_block_norm_grad_args* a, size_t* bytes)
+{
+    if (!bytes)
+        return TG_ERR_NULL_POINTER;
+    if (tg_status s = check_grad(a))
+        return s;
+    *bytes = a->T == 0 || a->D == 0 ? 0 : grad_plan(*a).bytes;
+    return TG_OK;
+}
+
+tg_status tg_block_norm_backward(const tg_block_norm_grad_args* a, void* workspace,
+                                 size_t workspace_bytes, tg_stream_t stream)
+{
+    if (tg_status s = check_grad(a))
+        return s;
+    const int64_t T = a->T, D = a->D;
+    if (T == 0 || D == 0)
+        return TG_OK;
+    if ((!a->dx_new && !a->dh) || (a->dh && (!a->x_new || !a->r_pre)) ||
+        (a->y && a->post_norm && !a->r_post) ||
+        (!a->dx && !a->dy && !a->dgate && !a->dw_post && !a->dw_pre))
+        return TG_ERR_NULL_POINTER;
+    if ((!a->y && (a->gate || a->w_post || a->dy || a->dgate || a->dw_post)) ||
+        (!a->post_norm && a->w_post) || (a->dgate && !a->gate) || (a->dw_post && !a->w_post) ||
+        (a->dw_pre && (!a->w_pre || !a->dh)))
+        return TG_ERR_BAD_LAYOUT;
+    const GradPlan g = grad_plan(*a);
+    if (g.bytes > 0 &&
+        (!workspace || workspace_bytes < g.bytes || ((uintptr_t)workspace & 15)))
+        return TG_ERR_WORKSPACE;
+    const int xs = tg::dtype_size(a->xtype), bs = tg::dtype_size(a->btype);
+    const Span in[] = {span(a->x_new, T, D, a->ldx_new, xs), span(a->y, T, D, a->ldy, bs),
+                       span1(a->gate, g.groups * D, bs),     span1(a->w_post, D, bs),
+                       span1(a->w_pre, D, bs),               span1(a->r_post, T, 4),
+                       span1(a->r_pre, T, 4),                span(a->dx_new, T, D, a->lddx_new, xs),
+                       span(a->dh, T, D, a->lddh, bs)};
+    const Span out[] = {span(a->dx, T, D, a->lddx, xs), span(a->dy, T, D, a->lddy, bs),
+                        span1(a->dgate, g.groups * D, 4), span1(a->dw_post, D, 4),
+                        span1(a->dw_pre, D, 4), span1(workspace, (int64_t)g.bytes, 1)};
+    for (int o = 0; o < 6; ++o) {
+        for (const Span& i : in)
+            if (overlap(out[o], i))
+                return TG_ERR_ALIAS;
+        for (int q = 0; q < o; ++q)
+            if (overlap(out[o], out[q]))
+                return TG_ERR_ALIAS;
+    }
+    tg::NormGradParams p{};
+    p.x_new = a->x_new;
+    p.y = a->y;
+    p.gate = a->gate;
+    p.w_post = a->w_post;
+    p.w_pre = a->w_pre;
+    p.dx_new = a->dx_new;
+    p.dh = a->dh;
+    p.r_post = a->r_post;
+    p.r_pre = a->r_pre;
+    p.dx = a->dx;
+    p.dy = a->dy;
+    p.dgate = a->dgate;
+    p.dw_post = a->dw_post;
+    p.dw_pre = a->dw_pre;
+    float* at = (float*)workspace;
+    if (g.pre) {
+        p.part_pre = at;
+        at += g.P * g.Dp;
+    }
+    if (g.post) {
+        p.part_post = at;
+        at += g.P * g.Dp;
+    }
+    if (g.gate)
+        p.part_gate = at;
+    p.T = T;
+    p.ldx = a->ldx_new;
+    p.ldy = a->ldy;
+    p.lddxn = a->lddx_new;
+    p.lddh = a->lddh;
+    p.lddx = a->lddx;
+    p.lddy = a->lddy;
+    p.gate_rows = g.gate_rows;
+    p.rows = g.rows;
+    p.parts = g.parts;
+    p.D = (int)D;
+    p.Dp = (int)g.Dp;
+    p.post = a->y && a->post_norm;
+    p.alpha = a->alpha;
+    const Pick k = pick_backward(D, a->xtype, a->btype);
+    if (tg_status s = tg::launch_kernel(k.kernel, g.P, 1, k.threads, &p, (hipStream_t)stream,
+                                        "block_norm_grad"))
+        return s;
+    if (g.bytes == 0)
+        return TG_OK;
+    tg::ColumnParams c{p.part_pre, p.part_post, p.part_gate, a->dw_pre, a->dw_post, a->dgate,
+                       a->w_post,  g.P,         g.parts,     (int)D,    (int)g.Dp};
+    const void* kc = by_types(TG_F32, a->btype, [](auto, auto B) {
+        return (const void*)&tg::block_norm_columns_kernel<decltype(B)::value>;
+    });
+    return tg::launch_kernel(kc, ceil_div(g.Dp, 64), 2 + (g.gate ? g.groups : 0), 256, &c,
+                             (hipStream_t)stream, "block_norm_columns");
+}
+
+}  // extern "C"

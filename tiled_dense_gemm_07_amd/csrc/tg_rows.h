@@ -1,0 +1,268 @@
+// Row operators (quantisation, norms): a team of threads holds one row in
+// registers, eight consecutive elements to a chunk, chunk c of thread t being
+// elements 8 (t + c * TPR) ...  Rows start at any element: chunks are moved
+// with 16-byte accesses of element alignment, which the hardware takes, and a
+// row's last chunk element by element.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "tg_kernel.h"
+
+namespace tg {
+
+// Eight elements as stored.
+template <int DT>
+struct Raw8 {
+    u32x4 v[DT == DT_F32 ? 2 : 1];
+};
+
+template <int DT>
+__device__ __forceinline__ const char* elem_ptr(const void* p, int64_t at)
+{
+    return (const char*)p + at * (DT == DT_F32 ? 4 : 2);
+}
+
+template <int DT>
+__device__ __forceinline__ void load8(Raw8<DT>& r, const void* row, int at, int left)
+{
+    if constexpr (DT == DT_F32) {
+        struct __attribute__((packed, aligned(4))) V {
+            u32x4 v;
+        };
+        const float* p = (const float*)row + at;
+        if (left >= 8) {
+            r.v[0] = ((const V*)p)[0].v;
+            r.v[1] = ((const V*)p)[1].v;
+        } else {
+            r.v[0] = r.v[1] = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left)
+                    r.v[i >> 2][i & 3] = __builtin_bit_cast(u32, p[i]);
+        }
+    } else {
+        struct __attribute__((packed, aligned(2))) V {
+            u32x4 v;
+        };
+        const uint16_t* p = (const uint16_t*)row + at;
+        if (left >= 8) {
+            r.v[0] = ((const V*)p)->v;
+        } else {
+            r.v[0] = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left)
+                    r.v[0][i >> 1] |= (u32)p[i] << (16 * (i & 1));
+        }
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ float get8(const Raw8<DT>& r, int i)
+{
+    if constexpr (DT == DT_F32) {
+        const u32 w = r.v[i >> 2][i & 3];  // by value: a bit cast of the vector
+        return __builtin_bit_cast(float, w);  // element itself reads element 0
+    }
+    const u32 w = r.v[0][i >> 1];
+    if constexpr (DT == DT_BF16)
+        return __builtin_bit_cast(float, (i & 1) ? (w & 0xFFFF0000u) : (w << 16));
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)((i & 1) ? (w >> 16) : w));
+}
+
+// Rounds once to the type (nearest even).
+template <int DT>
+__device__ __forceinline__ void put8(Raw8<DT>& r, const float (&v)[8])
+{
+    if constexpr (DT == DT_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            r.v[i >> 2][i & 3] = __builtin_bit_cast(u32, v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r.v[0][i] = pack2(v[2 * i], v[2 * i + 1], DT);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(void* row, int at, int left, const Raw8<DT>& r)
+{
+    if constexpr (DT == DT_F32) {
+        struct __attribute__((packed, aligned(4))) V {
+            u32x4 v;
+        };
+        float* p = (float*)row + at;
+        if (left >= 8) {
+            ((V*)p)[0].v = r.v[0];
+            ((V*)p)[1].v = r.v[1];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left)
+                    p[i] = get8<DT_F32>(r, i);
+        }
+    } else {
+        struct __attribute__((packed, aligned(2))) V {
+            u32x4 v;
+        };
+        uint16_t* p = (uint16_t*)row + at;
+        if (left >= 8) {
+            ((V*)p)->v = r.v[0];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left)
+                    p[i] = (uint16_t)(r.v[0][i >> 1] >> (16 * (i & 1)));
+        }
+    }
+}
+
+// --------------------------------------------------------------------------
+// Reductions over the TPR threads that hold a row.  Every thread gets the
+// result; the order of the additions is fixed.
+// --------------------------------------------------------------------------
+template <int CTRL>
+__device__ __forceinline__ u32 dpp(u32 v)
+{
+    return (u32)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+
+struct SumOp {
+    static __device__ __forceinline__ u32 of(u32 a, u32 b)
+    {
+        return __builtin_bit_cast(u32, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
+    }
+};
+struct MaxOp {  // of bit patterns: for magnitudes, NaN > Inf > finite
+    static __device__ __forceinline__ u32 of(u32 a, u32 b) { return a > b ? a : b; }
+};
+
+template <class Op>
+__device__ __forceinline__ u32 wave_all(u32 v)
+{
+    v = Op::of(v, dpp<0xB1>(v));   // quad_perm 1 0 3 2
+    v = Op::of(v, dpp<0x4E>(v));   // quad_perm 2 3 0 1
+    v = Op::of(v, dpp<0x141>(v));  // row_half_mirror
+    v = Op::of(v, dpp<0x140>(v));  // row_mirror
+    const auto s16 = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = Op::of(s16[0], s16[1]);
+    const auto s32 = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return Op::of(s32[0], s32[1]);
+}
+
+// N values reduced together over TPR threads (whole waves).  `slot`: LDS of
+// N * 16 words that no reduction in flight uses; reductions that alternate
+// between two slots need no barrier between them.
+template <class Op, int TPR, int N>
+__device__ __forceinline__ void row_all(u32 (&v)[N], u32* slot)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = wave_all<Op>(v[i]);
+    if constexpr (TPR > 64) {
+        constexpr int NW = TPR / 64;
+        const int w = (threadIdx.x % TPR) >> 6;
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                slot[i * 16 + w] = v[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            u32 s = slot[i * 16];
+#pragma unroll
+            for (int j = 1; j < NW; ++j)
+                s = Op::of(s, slot[i * 16 + j]);
+            v[i] = s;
+        }
+    }
+}
+
+template <int TPR, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], u32* slot)
+{
+    u32 b[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        b[i] = __builtin_bit_cast(u32, v[i]);
+    row_all<SumOp, TPR, N>(b, slot);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = __builtin_bit_cast(float, b[i]);
+}
+
+// --------------------------------------------------------------------------
+// Quantisation of a row to 8-bit levels: q = 127 v / a with ties to even, a =
+// the row's largest magnitude (at least 127 * 2^-126, so that the scale
+// a / 127 is never subnormal).  A row with an infinity or NaN gets the scale
+// NaN and zero levels: whatever is computed from it is NaN.
+// --------------------------------------------------------------------------
+struct RowLevels {
+    float scale;  // a / 127, rounded
+    float c;      // 127, or 127 * 2^-32 where 127 a would overflow
+    float a, ra;  // a (times the same power of two), and its reciprocal
+    bool ok;
+
+    __device__ __forceinline__ void of_amax(u32 bits)
+    {
+        ok = bits < 0x7F800000u;
+        float m = __builtin_bit_cast(float, bits);
+        m = ok ? fmaxf(m, 127.0f * 0x1p-126f) : 1.0f;
+        scale = ok ? m / 127.0f : __builtin_nanf("");
+        const bool big = m > 0x1p100f;
+        c = big ? 127.0f * 0x1p-32f : 127.0f;
+        a = big ? m * 0x1p-32f : m;
+        ra = 1.0f / a;
+    }
+
+    // One Newton step corrects the quotient to its rounded value.  For 16-bit
+    // v, 127 v is exact and a quotient that is no tie lies more than 2^-13
+    // (relative) from one: the level is the exact one.  For v computed in
+    // fp32 a quotient within an fp32 rounding of a tie may go either way.
+    __device__ __forceinline__ int level(float v) const
+    {
+        const float x = v * c;
+        const float q0 = x * ra;
+        const float q = __builtin_fmaf(__builtin_fmaf(-q0, a, x), ra, q0);
+        return ok ? (int)__builtin_rintf(q) : 0;
+    }
+
+    // The same for fp32 inputs in 64 bits, where 127 v is exact and a
+    // quotient that is no tie lies more than 2^-32 from one.
+    __device__ __forceinline__ int level64(float v) const
+    {
+        const double x = 127.0 * (double)v, d = (double)(a * (c == 127.0f ? 1.0f : 0x1p32f));
+        const double r = (double)ra * (c == 127.0f ? 1.0 : 0x1p-32);
+        double q = x * r;                                   // to about 2^-23
+        q = __builtin_fma(__builtin_fma(-q, d, x), r, q);   // to about 2^-46
+        q = __builtin_fma(__builtin_fma(-q, d, x), r, q);   // rounded
+        return ok ? (int)__builtin_rint(q) : 0;
+    }
+};
+
+// Eight levels to bytes.
+__device__ __forceinline__ void store_levels(int8_t* row, int at, int left, const int (&q)[8])
+{
+    struct __attribute__((packed, aligned(1))) V {
+        u32x2 v;
+    };
+    if (left >= 8) {
+        u32x2 b;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            b[i] = (u32)(q[4 * i] & 255) | (u32)(q[4 * i + 1] & 255) << 8 |
+                   (u32)(q[4 * i + 2] & 255) << 16 | (u32)q[4 * i + 3] << 24;
+        ((V*)(row + at))->v = b;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left)
+                row[at + i] = (int8_t)q[i];
+    }
+}
+
+}  // namespace tg
