@@ -66,7 +66,13 @@ typedef enum { TG_F32 = 0, TG_F16 = 1, TG_BF16 = 2 } tg_dtype;
 
 typedef enum { TG_EPI_NONE = 0, TG_EPI_RELU = 1 } tg_epilogue;
 
-typedef enum { TG_OP_GEMM = 0, TG_OP_DEQUANT_W4 = 1, TG_OP_MX = 2, TG_OP_SP24 = 3 } tg_op;
+typedef enum {
+    TG_OP_GEMM = 0,
+    TG_OP_DEQUANT_W4 = 1,
+    TG_OP_MX = 2,
+    TG_OP_SP24 = 3,
+    TG_OP_I8 = 4 /* tg_query_config only: its kernels are chosen by rule, not listed */
+} tg_op;
 
 /* Element format of the activations of tg_gemm_mx. */
 typedef enum { TG_MX_E2M1 = 0, TG_MX_E4M3 = 1 } tg_mx_format;
@@ -444,7 +450,8 @@ const char* tg_status_str(tg_status s);
  * Writes a NUL-terminated description (tile sizes, waves, stages, swizzle
  * group, launch grid) into buf[0 .. len-1], truncating if needed.
  * op: TG_OP_GEMM, TG_OP_DEQUANT_W4 (dtype ignored), TG_OP_MX (dtype
- * carries the tg_mx_format of the activations) or TG_OP_SP24.
+ * carries the tg_mx_format of the activations), TG_OP_SP24 or TG_OP_I8 (dtype
+ * is C's; rows at 16-byte boundaries assumed).
  * Errors: TG_ERR_NULL_POINTER (buf NULL or len 0), TG_ERR_BAD_SHAPE,
  *   TG_ERR_BAD_DTYPE, TG_ERR_NO_CONFIG (op unknown).
  */

@@ -22,7 +22,7 @@ _DEFAULT_LIB = os.path.join(HERE, "libtilegemm.so")
 
 TG_F32, TG_F16, TG_BF16 = 0, 1, 2
 TG_EPI_NONE, TG_EPI_RELU = 0, 1
-TG_OP_GEMM, TG_OP_DEQUANT_W4, TG_OP_MX, TG_OP_SP24 = 0, 1, 2, 3
+TG_OP_GEMM, TG_OP_DEQUANT_W4, TG_OP_MX, TG_OP_SP24, TG_OP_I8 = 0, 1, 2, 3, 4
 TG_MX_E2M1, TG_MX_E4M3 = 0, 1
 
 # exported symbols, as declared in include/tilegemm.h

@@ -791,7 +791,7 @@ unsigned long long* clock_stamps() { return g_stamps.load(std::memory_order_rela
 int swizzle_override() { return g_group_override.load(std::memory_order_relaxed); }
 
 tg_status launch_kernel(const void* kernel, int64_t grid_x, int64_t grid_y, int threads,
-                        void* params, hipStream_t stream, const char* what)
+                        void* params, hipStream_t stream, const char* what, unsigned lds)
 {
     if (grid_x > kMaxDim || grid_y > 65535)
         return TG_ERR_BAD_SHAPE;
@@ -803,7 +803,7 @@ tg_status launch_kernel(const void* kernel, int64_t grid_x, int64_t grid_y, int 
                 (long long)grid_y, threads);
     void* args[] = {params};
     const hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)grid_x, (unsigned)grid_y),
-                                         dim3((unsigned)threads), args, 0, stream);
+                                         dim3((unsigned)threads), args, lds, stream);
     return e == hipSuccess ? TG_OK : TG_ERR_HIP;
 }
 
@@ -938,8 +938,19 @@ tg_status tg_query_config_ex(int op, int64_t M, int64_t N, int64_t K, tg_dtype d
 {
     if (!buf || len == 0)
         return TG_ERR_NULL_POINTER;
-    if (op != TG_OP_GEMM && op != TG_OP_DEQUANT_W4 && op != TG_OP_MX && op != TG_OP_SP24)
+    if (op != TG_OP_GEMM && op != TG_OP_DEQUANT_W4 && op != TG_OP_MX && op != TG_OP_SP24 &&
+        op != TG_OP_I8)
         return TG_ERR_NO_CONFIG;
+    if (op == TG_OP_I8) {
+        if (!tg::dtype_ok(dtype))
+            return TG_ERR_BAD_DTYPE;
+        if (trans_a || trans_b)
+            return TG_ERR_BAD_LAYOUT;
+        if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > tg::kMaxI8K)
+            return TG_ERR_BAD_SHAPE;
+        tg::describe_i8(M, N, K, buf, len);
+        return TG_OK;
+    }
     if (op == TG_OP_SP24 && dtype != TG_F16 && dtype != TG_BF16)
         return TG_ERR_BAD_DTYPE;
     if (op == TG_OP_GEMM && dtype != TG_F32 && dtype != TG_F16 && dtype != TG_BF16)

@@ -9,6 +9,7 @@
 namespace tg {
 
 constexpr int64_t kMaxDim = 0x7FFFFFFF;
+constexpr int64_t kMaxI8K = 131071;  // 128 * 128 * K stays below 2^31
 
 // Settings of tg_set_clock_stamps and tg_set_swizzle_override.
 unsigned long long* clock_stamps();
@@ -19,7 +20,11 @@ int swizzle_override();
 // runtime's own launch errors give TG_ERR_HIP.  `what` names the launch in
 // the log (environment TG_LOG).
 tg_status launch_kernel(const void* kernel, int64_t grid_x, int64_t grid_y, int threads,
-                        void* params, hipStream_t stream, const char* what);
+                        void* params, hipStream_t stream, const char* what, unsigned lds = 0);
+
+// Name and grid of the kernel a tg_gemm_i8 call with 16-byte aligned rows
+// would launch (for tg_query_config).
+void describe_i8(int64_t M, int64_t N, int64_t K, char* buf, size_t len);
 
 // A strided matrix of `rows` rows of `cols` elements: its byte range, row
 // length and row stride.  Two matrices of one stride may interleave (column

@@ -3,8 +3,11 @@
 // by sizes and alignment.
 #include <hip/hip_runtime.h>
 
+#include <stdio.h>
+
 #include "tg_host.h"
 #include "tg_kernel_i8.h"
+#include "tg_kernel_i8_gemv.h"
 #include "tg_kernel_quant.h"
 
 namespace {
@@ -46,26 +49,159 @@ tg_status launch_quant(const tg::QuantParams& p, int dtype, hipStream_t stream)
     return tg::launch_kernel(k, ceil_div(p.M, rows), 1, threads, &q, stream, "quant_i8");
 }
 
-constexpr int64_t kMaxK = 131071;  // 128 * 128 * K stays below 2^31
-
 tg_status check_dims(int64_t M, int64_t N, int64_t K)
 {
-    if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxK)
+    if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > tg::kMaxI8K)
         return TG_ERR_BAD_SHAPE;
     return TG_OK;
+}
+
+constexpr int64_t kFusedTokens = 4;
+
+// The LDS-DMA kernels, and what one costs on this card in microseconds with
+// its weights from HBM: t0 + strips of 128 k times `one` when every workgroup
+// has a compute unit to itself, else times `full` for each round of 256 per_cu
+// workgroups.  Fitted to 150 shapes (M 17 to 8192, N and K 1000 to 8192, odd
+// ones among them): within 10 to 15% on average, and the choice by it 4% on
+// average above the fastest kernel of the set (33% at most, on 5 us calls).
+struct I8Tile {
+    const char* name;
+    const void* kernel[3];  // by C's type
+    int bm, bn, threads, per_cu;
+    float t0, one, full;
+};
+
+#define TG_I8_TILE(BM, BN, BK, WGM, WGN, NS, OCC, PER_CU, T0, ONE, FULL)                   \
+    {                                                                                      \
+        "i8_" #BM "x" #BN "x" #BK "_w" #WGM "x" #WGN "_s" #NS "_dma",                      \
+            {(const void*)&tg::i8_dma_kernel<tg::DT_F32, BM, BN, BK, WGM, WGN, NS, OCC>,   \
+             (const void*)&tg::i8_dma_kernel<tg::DT_F16, BM, BN, BK, WGM, WGN, NS, OCC>,   \
+             (const void*)&tg::i8_dma_kernel<tg::DT_BF16, BM, BN, BK, WGM, WGN, NS, OCC>}, \
+            BM, BN, WGM* WGN * 64, PER_CU, T0, ONE, FULL                                   \
+    }
+const I8Tile kTiles[] = {
+    TG_I8_TILE(32, 64, 256, 1, 2, 4, 1, 1, 3.68f, 0.182f, 0.261f),
+    TG_I8_TILE(64, 64, 128, 2, 2, 5, 2, 2, 3.26f, 0.230f, 0.498f),
+    TG_I8_TILE(128, 64, 128, 4, 2, 6, 2, 1, 4.27f, 0.273f, 0.893f),
+    TG_I8_TILE(128, 128, 128, 2, 4, 4, 2, 1, 3.86f, 0.427f, 0.694f),
+    TG_I8_TILE(128, 128, 128, 2, 2, 2, 2, 2, 3.53f, 0.738f, 1.144f),
+    TG_I8_TILE(256, 256, 128, 2, 4, 2, 2, 1, 6.00f, 1.250f, 1.820f),
+};
+
+// The streaming kernel's cost, likewise: HBM for W once, or all the loads of
+// its workgroups (32 or 48 rows of operands for each) through L2.
+float gemv_cost(int64_t M, int64_t N, int64_t K, int rows, float t0, float per)
+{
+    const float hbm = (float)N * (float)K / 5e6f;
+    const float l2 = (float)(ceil_div(M, 16) * ceil_div(N, rows)) * (16 + rows) * (float)K / 1.3e7f;
+    return t0 + per * (hbm > l2 ? hbm : l2);
+}
+
+struct I8Pick {
+    const I8Tile* tile;  // NULL: gemv (rows > 0) or the kernel for any layout
+    int rows;            // W rows of a gemv workgroup
+};
+
+// Up to 16 tokens: the streaming kernel, with 16 rows of W to a workgroup
+// (M = 1, 8192 x 8192: 14.6 us, and 18.4 for the best tile kernel; M = 16: 17.3
+// and 19.0).  Up to 128: whichever costs less, with 32 rows to a workgroup
+// (M = 32, 4096 x 4096: 8.2 us and 11.2; M = 32, 8192 x 8192: 26 and 19.8).
+// Above: the cheapest tile.  Rows that do not start at 16-byte boundaries, or
+// K % 16 != 0, leave the streaming kernel up to 64 tokens (it takes any
+// address) and i8_any_kernel.
+I8Pick pick_i8(int64_t M, int64_t N, int64_t K, bool aligned)
+{
+    if (M <= 16)
+        return {nullptr, 16};
+    if (!aligned)
+        return {nullptr, M <= 64 ? 32 : 0};
+    float best = M <= 128 ? gemv_cost(M, N, K, 32, 3.23f, 1.335f) : 1e30f;
+    I8Pick p{nullptr, 32};
+    for (const I8Tile& t : kTiles) {
+        const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
+        const float strips = (float)ceil_div(K, 128);
+        const float c = t.t0 + strips * (tiles <= 256 ? t.one
+                                                      : t.full * (float)ceil_div(tiles, 256 * t.per_cu));
+        if (c < best) {
+            best = c;
+            p = {&t, 0};
+        }
+    }
+    return p;
+}
+
+// Rows that the LDS-DMA copies can take: whole 16-byte chunks, and a tile's
+// 256 rows within 31 bits of offset.
+bool dma_rows(const void* p, int64_t ld)
+{
+    return ((uintptr_t)p & 15) == 0 && ld % 16 == 0 && 256 * ld <= kMaxDim;
 }
 
 tg_status launch_i8(tg::I8Params p, hipStream_t stream)
 {
     p.stamps = tg::clock_stamps();
-    p.group_m = tg::swizzle_override() > 0 ? tg::swizzle_override() : 8;
-    p.tiles_m = (int)ceil_div(p.M, tg::I8Any::BM);
-    p.tiles_n = (int)ceil_div(p.N, tg::I8Any::BN);
-    return tg::launch_kernel((const void*)&tg::i8_any_kernel, (int64_t)p.tiles_m * p.tiles_n, 1,
-                             256, &p, stream, "i8_any");
+    const int es = tg::dtype_size(p.dt_out);
+    const bool aligned = p.K > 0 && p.K % 16 == 0 && dma_rows(p.A, p.lda) && dma_rows(p.W, p.ldw);
+    const I8Pick k = pick_i8(p.M, p.N, p.K, aligned);
+    if (k.rows > 0 && ceil_div(p.M, 16) <= 65535) {
+        const int ng = k.rows / 16;
+        return tg::launch_kernel(ng == 1 ? (const void*)&tg::i8_gemv_kernel<1, 1, 8>
+                                         : (const void*)&tg::i8_gemv_kernel<2, 1, 8>,
+                                 ceil_div(p.N, k.rows), ceil_div(p.M, 16), 512, &p, stream,
+                                 "i8_gemv", 8 * ng * 1024);
+    }
+    const int bm = k.tile ? k.tile->bm : tg::I8Any::BM, bn = k.tile ? k.tile->bn : tg::I8Any::BN;
+    // Tile order: patches of 4 tile rows, as the 16-bit kernels' largest tiles.
+    p.group_m = tg::swizzle_override() > 0 ? tg::swizzle_override() : 4;
+    p.tiles_m = (int)ceil_div(p.M, bm);
+    p.tiles_n = (int)ceil_div(p.N, bn);
+    p.c_vec = ((uintptr_t)p.C & 15) == 0 && p.ldc * es % 16 == 0 && p.N * es % 16 == 0 &&
+              32 * p.ldc * es <= kMaxDim;
+    return tg::launch_kernel(k.tile ? k.tile->kernel[p.dt_out] : (const void*)&tg::i8_any_kernel,
+                             (int64_t)p.tiles_m * p.tiles_n, 1, k.tile ? k.tile->threads : 256, &p,
+                             stream, k.tile ? k.tile->name : "i8_any");
+}
+
+// tg_linear_i8 in one launch: few tokens, and their levels fit the LDS kept
+// for them.
+bool fused_linear(int64_t M, int64_t K)
+{
+    return M <= kFusedTokens && K > 0 &&
+           M * tg::I8Gemv<tg::DT_BF16, 1, 1, 8, true>::level_row((int)K) <= tg::kGemvLevels;
+}
+
+tg_status launch_fused(const tg::I8Params& p, int dtype, const void* X, int64_t ldx,
+                       hipStream_t stream)
+{
+    tg::I8LinearParams l{p, {X, ldx}};
+    l.p.stamps = tg::clock_stamps();
+    const void* k = dtype == TG_F32   ? (const void*)&tg::i8_linear_gemv_kernel<tg::DT_F32, 1, 8>
+                    : dtype == TG_F16 ? (const void*)&tg::i8_linear_gemv_kernel<tg::DT_F16, 1, 8>
+                                      : (const void*)&tg::i8_linear_gemv_kernel<tg::DT_BF16, 1, 8>;
+    const unsigned levels =
+        (unsigned)(p.M * tg::I8Gemv<tg::DT_BF16, 1, 1, 8, true>::level_row(p.K));
+    return tg::launch_kernel(k, ceil_div(p.N, 16), 1, 512, &l, stream, "i8_linear_gemv",
+                             levels > 8192 ? levels : 8192);
 }
 
 }  // namespace
+
+namespace tg {
+
+void describe_i8(int64_t M, int64_t N, int64_t K, char* buf, size_t len)
+{
+    const I8Pick k = pick_i8(M, N, K, K > 0 && K % 16 == 0);
+    if (k.rows > 0)
+        snprintf(buf, len, "i8_gemv_%d grid=%lldx%lld threads=512", k.rows,
+                 (long long)ceil_div(N, k.rows), (long long)ceil_div(M, 16));
+    else
+        snprintf(buf, len, "%s grid=%lld threads=%d", k.tile ? k.tile->name : "i8_any",
+                 (long long)(ceil_div(M, k.tile ? k.tile->bm : I8Any::BM) *
+                             ceil_div(N, k.tile ? k.tile->bn : I8Any::BN)),
+                 k.tile ? k.tile->threads : 256);
+}
+
+}  // namespace tg
 
 extern "C" {
 
@@ -138,8 +274,9 @@ tg_status tg_linear_i8_workspace_size(int64_t M, int64_t N, int64_t K, tg_dtype 
     if (tg_status st = check_dims(M, N, K))
         return st;
     // scales, then rows of levels padded to whole 16-byte chunks
-    *bytes = M == 0 || N == 0 ? 0
-                              : (size_t)(ceil_div(4 * M, 256) * 256 + M * ceil_div(K, 16) * 16);
+    *bytes = M == 0 || N == 0 || fused_linear(M, K)
+                 ? 0
+                 : (size_t)(ceil_div(4 * M, 256) * 256 + M * ceil_div(K, 16) * 16);
     return TG_OK;
 }
 
@@ -170,16 +307,8 @@ tg_status tg_linear_i8(int64_t M, int64_t N, int64_t K, tg_dtype dtype, const vo
     if (overlap(c, x) || overlap(c, w) || overlap(c, s) || overlap(c, bs) || overlap(ws, c) ||
         overlap(ws, x) || overlap(ws, w) || overlap(ws, s) || overlap(ws, bs))
         return TG_ERR_ALIAS;
-    const int64_t ldq = ceil_div(K, 16) * 16;
-    float* sa = (float*)workspace;
-    int8_t* A = (int8_t*)workspace + ceil_div(4 * M, 256) * 256;
-    tg::QuantParams q{X, A, sa, M, (int)K, ldx, ldq, (int)ldq};
-    if (tg_status st = launch_quant(q, dtype, (hipStream_t)stream))
-        return st;
     tg::I8Params p{};
-    p.A = A;
     p.W = W;
-    p.sa = sa;
     p.sw = sw;
     p.bias = bias;
     p.C = C;
@@ -187,10 +316,20 @@ tg_status tg_linear_i8(int64_t M, int64_t N, int64_t K, tg_dtype dtype, const vo
     p.M = (int)M;
     p.N = (int)N;
     p.K = (int)K;
-    p.lda = ldq;
     p.ldw = ldw;
     p.ldc = ldc;
     p.relu = epi == TG_EPI_RELU;
+    if (fused_linear(M, K))
+        return launch_fused(p, dtype, X, ldx, (hipStream_t)stream);
+    const int64_t ldq = ceil_div(K, 16) * 16;
+    float* sa = (float*)workspace;
+    int8_t* A = (int8_t*)workspace + ceil_div(4 * M, 256) * 256;
+    tg::QuantParams q{X, A, sa, M, (int)K, ldx, ldq, (int)ldq};
+    if (tg_status st = launch_quant(q, dtype, (hipStream_t)stream))
+        return st;
+    p.A = A;
+    p.sa = sa;
+    p.lda = ldq;
     return launch_i8(p, (hipStream_t)stream);
 }
 
