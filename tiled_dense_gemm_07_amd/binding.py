@@ -198,12 +198,21 @@ def _epi_code(epilogue) -> int:
     raise ValueError("epilogue must be None/'none' or 'relu'")
 
 
+_raw_stream = None
+
+
 def _stream_ptr(device, stream=None):
-    if stream is None:
+    """Handle of `stream`, or of the device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
         import torch
 
-        stream = torch.cuda.current_stream(device)
-    return stream.cuda_stream
+        # the handle without a Stream object: 0.1 us instead of 1.9 on every call
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(device.index)
 
 
 def _require_gpu_tensor(name, t):
@@ -497,18 +506,21 @@ def gemm_sp24(Ac, Ai, B, C=None, epilogue=None, stream=None, config=None):
 # 8-bit integer path and block norms.  These take row-strided 2-D tensors
 # (unit stride along a row), for instance slices of a wider buffer.
 # --------------------------------------------------------------------------
+# Argument checks here cost a good part of a small call's time, so they take
+# the cheapest properties of a tensor, each once.
 def _rows(name, t, shape=None, dtype=None):
     """Row stride of the 2-D GPU tensor t; checks shape and dtype."""
     if not t.is_cuda:
         raise ValueError("%s must be a GPU tensor" % name)
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+    size = t.shape
+    if len(size) != 2 or (shape is not None and size != shape):
         raise ValueError("%s must be %s, got %s"
-                         % (name, "2-D" if shape is None else list(shape), tuple(t.shape)))
+                         % (name, "2-D" if shape is None else list(shape), tuple(size)))
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    rows, cols = t.shape
+    rows, cols = size
     ld, unit = t.stride()
-    if cols > 1 and unit != 1:
+    if unit != 1 and cols > 1:
         raise ValueError("%s must have unit stride along its rows" % name)
     if rows <= 1:
         return cols
@@ -525,26 +537,36 @@ def _vector(name, t, n, dtype):
         raise ValueError("%s must be a GPU tensor" % name)
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.numel() != n or t.dim() != 1 or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError("%s must be a dense vector of %d values" % (name, n))
     return t.data_ptr()
 
 
 def _one_device(first, *others):
+    index = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise ValueError("operands must be on one device: %s and %s"
                              % (first.device, t.device))
 
 
 def _empty(shape, dtype, like, stream):
     """An output or workspace on like's device that belongs to the call's stream."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
     import torch
 
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _empty_as(t, stream):
+    """An output of t's shape and type, dense."""
+    if stream is not None or not t.is_contiguous():
+        return _empty(t.shape, t.dtype, t, stream)
+    import torch
+
+    return torch.empty_like(t)
 
 
 def quant_i8(X, Q=None, s=None, stream=None):
@@ -558,11 +580,11 @@ def quant_i8(X, Q=None, s=None, stream=None):
         Q = _empty((M, K), torch.int8, X, stream)
     if s is None:
         s = _empty((M,), torch.float32, X, stream)
-    _one_device(X, Q, s)
     ldq = _rows("Q", Q, (M, K), torch.int8)
+    ps = _vector("s", s, M, torch.float32)
+    _one_device(X, Q, s)
     _check(load_library().tg_quant_i8(M, K, _dtype_code(X), X.data_ptr(), ldx, Q.data_ptr(), ldq,
-                                      _vector("s", s, M, torch.float32),
-                                      _stream_ptr(X.device, stream)))
+                                      ps, _stream_ptr(X.device, stream)))
     return Q, s
 
 
@@ -572,11 +594,12 @@ def gemm_i8(A, sa, W, sw, bias=None, out_dtype=None, C=None, epilogue=None, stre
     [M, N] of out_dtype (bfloat16 unless C or out_dtype says otherwise)."""
     import torch
 
-    lda = _rows("A", A, dtype=torch.int8)
-    ldw = _rows("W", W, dtype=torch.int8)
+    i8, f32 = torch.int8, torch.float32
+    lda = _rows("A", A, None, i8)
+    ldw = _rows("W", W, None, i8)
     M, K = A.shape
-    N = W.shape[0]
-    if W.shape[1] != K:
+    N, K2 = W.shape
+    if K2 != K:
         raise ValueError("inner dimensions differ: A is %s, W is %s"
                          % (tuple(A.shape), tuple(W.shape)))
     if C is None:
@@ -584,11 +607,11 @@ def gemm_i8(A, sa, W, sw, bias=None, out_dtype=None, C=None, epilogue=None, stre
     elif out_dtype is not None and C.dtype != out_dtype:
         raise TypeError("C must be %s, got %s" % (out_dtype, C.dtype))
     ldc = _rows("C", C, (M, N))
+    ps, pw, pb = _vector("sa", sa, M, f32), _vector("sw", sw, N, f32), _vector("bias", bias, N, f32)
     _one_device(A, sa, W, sw, bias, C)
     _check(load_library().tg_gemm_i8(
-        M, N, K, A.data_ptr(), lda, _vector("sa", sa, M, torch.float32), W.data_ptr(), ldw,
-        _vector("sw", sw, N, torch.float32), _vector("bias", bias, N, torch.float32),
-        _dtype_code(C), C.data_ptr(), ldc, _epi_code(epilogue), _stream_ptr(A.device, stream)))
+        M, N, K, A.data_ptr(), lda, ps, W.data_ptr(), ldw, pw, pb, _dtype_code(C), C.data_ptr(),
+        ldc, _epi_code(epilogue), _stream_ptr(A.device, stream)))
     return C
 
 
@@ -607,29 +630,32 @@ def linear_i8(X, W, sw, bias=None, C=None, epilogue=None, workspace=None, stream
     (allocated here when None and needed)."""
     import torch
 
+    f32 = torch.float32
     ldx = _rows("X", X)
-    ldw = _rows("W", W, dtype=torch.int8)
+    ldw = _rows("W", W, None, torch.int8)
     M, K = X.shape
-    N = W.shape[0]
-    if W.shape[1] != K:
+    N, K2 = W.shape
+    if K2 != K:
         raise ValueError("inner dimensions differ: X is %s, W is %s"
                          % (tuple(X.shape), tuple(W.shape)))
     if C is None:
         C = _empty((M, N), X.dtype, X, stream)
     ldc = _rows("C", C, (M, N), X.dtype)
     dt = _dtype_code(X)
+    wp, wn = None, 0
     if workspace is None:
-        need = linear_i8_workspace_size(M, N, K, dt)
-        workspace = _empty((need,), torch.uint8, X, stream) if need else None
+        wn = linear_i8_workspace_size(M, N, K, dt)
+        if wn:
+            workspace = _empty((wn,), torch.uint8, X, stream)
+            wp = workspace.data_ptr()
     else:
         _require_gpu_tensor("workspace", workspace)
+        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    pw, pb = _vector("sw", sw, N, f32), _vector("bias", bias, N, f32)
     _one_device(X, W, sw, bias, C, workspace)
     _check(load_library().tg_linear_i8(
-        M, N, K, dt, X.data_ptr(), ldx, W.data_ptr(), ldw, _vector("sw", sw, N, torch.float32),
-        _vector("bias", bias, N, torch.float32), C.data_ptr(), ldc, _epi_code(epilogue),
-        None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _stream_ptr(X.device, stream)))
+        M, N, K, dt, X.data_ptr(), ldx, W.data_ptr(), ldw, pw, pb, C.data_ptr(), ldc,
+        _epi_code(epilogue), wp, wn, _stream_ptr(X.device, stream)))
     return C
 
 
@@ -638,7 +664,8 @@ def _gate_arg(gate, gate_rows, T, D, dtype):
     for one row (shared by every token) or one row for each token."""
     if gate is None:
         return None, 0
-    G = 1 if gate.dim() == 1 else gate.shape[0]
+    size = gate.shape
+    G = 1 if len(size) == 1 else size[0]
     if not gate_rows:
         if G != 1 and G != T:
             raise ValueError("gate_rows is needed: gate has %d rows for %d tokens" % (G, T))
@@ -647,14 +674,10 @@ def _gate_arg(gate, gate_rows, T, D, dtype):
         raise ValueError("gate must be a dense GPU tensor")
     if gate.dtype != dtype:
         raise TypeError("gate must be %s, got %s" % (dtype, gate.dtype))
-    if gate_rows < 1 or gate.shape[-1] != D or gate.dim() > 2 or (T > 0 and G != -(-T // gate_rows)):
+    if gate_rows < 1 or size[-1] != D or len(size) > 2 or (T > 0 and G != -(-T // gate_rows)):
         raise ValueError("gate must be [ceil(T / gate_rows), D] = [%d, %d], got %s"
-                         % (-(-T // max(1, gate_rows)), D, tuple(gate.shape)))
+                         % (-(-T // max(1, gate_rows)), D, tuple(size)))
     return gate.data_ptr(), gate_rows
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
 
 
 def block_norm(x, y=None, gate=None, gate_rows=None, w_post=None, w_pre=None, alpha=1.0, eps=1e-6,
@@ -674,27 +697,32 @@ def block_norm(x, y=None, gate=None, gate_rows=None, w_post=None, w_pre=None, al
     if out not in ("h", "i8", None):
         raise ValueError("out must be 'h', 'i8' or None")
     ldx = _rows("x", x)
-    T, D = x.shape
-    shape = (T, D)
+    shape = x.shape
+    T, D = shape
     block = y if y is not None else (h if h is not None and out == "h" else w_pre)
-    bt = x.dtype if block is None else block.dtype
+    if block is None:
+        block = x
+    xt, bt = x.dtype, block.dtype
     a = BlockNormArgs()
-    a.T, a.D, a.xtype, a.btype = T, D, _dtype_code(x), _dtype_code(x if block is None else block)
+    a.T, a.D, a.xtype, a.btype = T, D, _dtype_code(x), _dtype_code(block)
     a.x, a.ldx = x.data_ptr(), ldx
     a.alpha, a.eps, a.post_norm = alpha, eps, bool(post_norm)
     if y is not None:
         a.y, a.ldy = y.data_ptr(), _rows("y", y, shape)
         if x_out is None:
-            x_out = _empty(shape, x.dtype, x, stream)
-    if x_out is not None:
-        a.x_out, a.ldx_out = x_out.data_ptr(), _rows("x_out", x_out, shape, x.dtype)
+            x_out = _empty_as(x, stream)
+            a.x_out, a.ldx_out = x_out.data_ptr(), D
+    if x_out is not None and not a.x_out:
+        a.x_out, a.ldx_out = x_out.data_ptr(), _rows("x_out", x_out, shape, xt)
     a.gate, a.gate_rows = _gate_arg(gate, gate_rows, T, D, bt)
     a.w_post = _vector("w_post", w_post, D, bt)
     a.w_pre = _vector("w_pre", w_pre, D, bt)
     if out == "h":
         if h is None:
-            h = _empty(shape, bt, x, stream)
-        a.h, a.ldh = h.data_ptr(), _rows("h", h, shape, bt)
+            h = _empty_as(y, stream) if y is not None else _empty(shape, bt, x, stream)
+            a.h, a.ldh = h.data_ptr(), D
+        else:
+            a.h, a.ldh = h.data_ptr(), _rows("h", h, shape, bt)
     elif out == "i8":
         if h is None:
             h = _empty(shape, torch.int8, x, stream)
@@ -725,59 +753,68 @@ def block_norm_backward(x_new, dx_new=None, dh=None, y=None, gate=None, gate_row
     types, the rest (None where there is no such input) in fp32."""
     import torch
 
-    T, D = x_new.shape
-    shape = (T, D)
+    shape = x_new.shape
+    ldx = _rows("x_new", x_new)
+    T, D = shape
     block = y if y is not None else (dh if dh is not None else w_pre)
-    bt = x_new.dtype if block is None else block.dtype
-    f32 = torch.float32
+    if block is None:
+        block = x_new
+    xt, bt, f32 = x_new.dtype, block.dtype, torch.float32
     a = BlockNormGradArgs()
-    a.T, a.D, a.xtype = T, D, _dtype_code(x_new)
-    a.btype = a.xtype if block is None else _dtype_code(block)
-    a.x_new, a.ldx_new = x_new.data_ptr(), _rows("x_new", x_new)
+    a.T, a.D, a.xtype, a.btype = T, D, _dtype_code(x_new), _dtype_code(block)
+    a.x_new, a.ldx_new = x_new.data_ptr(), ldx
     a.alpha, a.post_norm = alpha, bool(post_norm)
-    dx = _empty(shape, x_new.dtype, x_new, stream)
+    dx = _empty_as(x_new, stream)
     a.dx, a.lddx = dx.data_ptr(), D
     dy = dgate = dw_post = dw_pre = None
     if y is not None:
         a.y, a.ldy = y.data_ptr(), _rows("y", y, shape)
-        dy = _empty(shape, bt, x_new, stream)
+        dy = _empty_as(y, stream)
         a.dy, a.lddy = dy.data_ptr(), D
+        if post_norm:
+            a.r_post = _vector("r_post", r_post, T, f32)
     a.gate, a.gate_rows = _gate_arg(gate, gate_rows, T, D, bt)
     if gate is not None:
         dgate = _empty(gate.shape, f32, x_new, stream)
         a.dgate = dgate.data_ptr()
     a.w_post = _vector("w_post", w_post, D, bt)
-    if w_post is not None:
-        dw_post = _empty((D,), f32, x_new, stream)
-        a.dw_post = dw_post.data_ptr()
     a.w_pre = _vector("w_pre", w_pre, D, bt)
+    want_pre = dh is not None and w_pre is not None
+    if w_post is not None and want_pre:  # one allocation for both
+        dw_post, dw_pre = _empty((2, D), f32, x_new, stream).unbind(0)
+    elif w_post is not None:
+        dw_post = _empty((D,), f32, x_new, stream)
+    elif want_pre:
+        dw_pre = _empty((D,), f32, x_new, stream)
+    if dw_post is not None:
+        a.dw_post = dw_post.data_ptr()
+    if dw_pre is not None:
+        a.dw_pre = dw_pre.data_ptr()
     if dh is not None:
         a.dh, a.lddh = dh.data_ptr(), _rows("dh", dh, shape, bt)
         a.r_pre = _vector("r_pre", r_pre, T, f32)
-        if w_pre is not None:
-            dw_pre = _empty((D,), f32, x_new, stream)
-            a.dw_pre = dw_pre.data_ptr()
     if dx_new is not None:
-        a.dx_new, a.lddx_new = dx_new.data_ptr(), _rows("dx_new", dx_new, shape, x_new.dtype)
-    if post_norm and y is not None:
-        a.r_post = _vector("r_post", r_post, T, f32)
+        a.dx_new, a.lddx_new = dx_new.data_ptr(), _rows("dx_new", dx_new, shape, xt)
     if T == 0:  # sums over no tokens; nothing is launched
         with torch.cuda.stream(stream):
             for g in (dw_post, dw_pre):
                 if g is not None:
                     g.zero_()
     lib = load_library()
+    ref = ctypes.byref(a)
+    wp, wn = None, 0
     if workspace is None:
         need = ctypes.c_size_t(0)
-        _check(lib.tg_block_norm_backward_workspace_size(ctypes.byref(a), ctypes.byref(need)))
-        workspace = _empty((need.value,), torch.uint8, x_new, stream) if need.value else None
+        _check(lib.tg_block_norm_backward_workspace_size(ref, ctypes.byref(need)))
+        wn = need.value
+        if wn:
+            workspace = _empty((wn,), torch.uint8, x_new, stream)
+            wp = workspace.data_ptr()
     else:
         _require_gpu_tensor("workspace", workspace)
+        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _one_device(x_new, dx_new, dh, y, gate, w_post, w_pre, r_post, r_pre, workspace)
-    _check(lib.tg_block_norm_backward(
-        ctypes.byref(a), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _stream_ptr(x_new.device, stream)))
+    _check(lib.tg_block_norm_backward(ref, wp, wn, _stream_ptr(x_new.device, stream)))
     return BlockNormGrad(dx, dy, dgate, dw_post, dw_pre)
 
 
