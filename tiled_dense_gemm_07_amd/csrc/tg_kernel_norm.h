@@ -18,35 +18,42 @@ struct NormParams {
     void *x_out, *h;
     int8_t* hq;
     float *hs, *r_post, *r_pre;
-    int64_t T, ldx, ldy, ldxo, ldh, ldhq, gate_rows;
-    int D;
+    int64_t ldx, ldy, ldxo, ldh, ldhq;
+    int T, gate_rows, D;
     int post;
     float alpha, eps;
 };
 
-template <int XT, int BT, int NT, int TPR, int NC>
+template <int XT, int BT, int NT, int TPR, int NC, bool VEC>
 __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void block_norm_kernel(NormParams p)
 {
     __shared__ u32 slots[3][16];
     const int t = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * (NT / TPR) + threadIdx.x / TPR;
+    const int row = (int)blockIdx.x * (NT / TPR) +
+                    __builtin_amdgcn_readfirstlane((int)(threadIdx.x / TPR));
     if (row >= p.T)
         return;  // whole waves; rows share a workgroup only when TPR is one wave
-    const char* x = elem_ptr<XT>(p.x, row * p.ldx);
     const float inv_d = 1.0f / (float)p.D;
+    const auto at = [&](int c) { return 8 * (t + c * TPR); };
+    const Row<BT, VEC> w1(p.w_post, 0, 0, p.D), w2(p.w_pre, 0, 0, p.D);
+    const Row<XT, VEC> x(p.x, row, p.ldx, p.D);
     Raw8<XT> rx[NC];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const int at = 8 * (t + c * TPR);
-        load8<XT>(rx[c], x, at, p.D - at);
-    }
+    for (int c = 0; c < NC; ++c)
+        x.load(rx[c], at(c));
     if (p.y) {
-        const char* y = elem_ptr<BT>(p.y, row * p.ldy);
-        Raw8<BT> ry[NC];
+        const Row<BT, VEC> y(p.y, row, p.ldy, p.D);
+        const Row<BT, VEC> gate(
+            p.gate, __builtin_amdgcn_readfirstlane(p.gate ? row / p.gate_rows : 0), p.D, p.D);
+        const Row<XT, VEC> xo(p.x_out, row, p.ldxo, p.D);
+        Raw8<BT> ry[NC], rw[NC], rg[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            y.load(ry[c], at(c));
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int at = 8 * (t + c * TPR);
-            load8<BT>(ry[c], y, at, p.D - at);
+            w1.load(rw[c], at(c));
+            gate.load(rg[c], at(c));
         }
         float r1 = 1.0f;
         if (p.post) {
@@ -63,40 +70,35 @@ __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void block_norm_
             if (p.r_post && t == 0)
                 p.r_post[row] = r1;
         }
-        const char* gate =
-            p.gate ? elem_ptr<BT>(p.gate, row / p.gate_rows * (int64_t)p.D) : nullptr;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int at = 8 * (t + c * TPR);
-            const int left = p.D - at;
             float z[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 z[i] = get8<BT>(ry[c], i) * r1;
             if (p.w_post) {
-                Raw8<BT> w;
-                load8<BT>(w, p.w_post, at, left);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    z[i] *= get8<BT>(w, i);
+                    z[i] *= get8<BT>(rw[c], i);
             }
-            if (gate) {
-                Raw8<BT> g;
-                load8<BT>(g, gate, at, left);
+            if (p.gate) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    z[i] *= get8<BT>(g, i);
+                    z[i] *= get8<BT>(rg[c], i);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 z[i] = __builtin_fmaf(p.alpha, get8<XT>(rx[c], i), z[i]);
             put8<XT>(rx[c], z);
-            if (p.x_out)
-                store8<XT>(const_cast<char*>(elem_ptr<XT>(p.x_out, row * p.ldxo)), at, left, rx[c]);
+            xo.store(rx[c], at(c));
         }
     }
     if (!p.h && !p.hq)
         return;
+    Raw8<BT> rw[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+        w2.load(rw[c], at(c));
     float s[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < NC; ++c)
@@ -112,25 +114,22 @@ __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void block_norm_
     float h[NC][8];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const int at = 8 * (t + c * TPR);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             h[c][i] = get8<XT>(rx[c], i) * r2;
         if (p.w_pre) {
-            Raw8<BT> w;
-            load8<BT>(w, p.w_pre, at, p.D - at);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                h[c][i] *= get8<BT>(w, i);
+                h[c][i] *= get8<BT>(rw[c], i);
         }
     }
     if (p.h) {
+        const Row<BT, VEC> out(p.h, row, p.ldh, p.D);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int at = 8 * (t + c * TPR);
             Raw8<BT> r;
             put8<BT>(r, h[c]);
-            store8<BT>(const_cast<char*>(elem_ptr<BT>(p.h, row * p.ldh)), at, p.D - at, r);
+            out.store(r, at(c));
         }
     }
     if (p.hq) {
@@ -140,7 +139,7 @@ __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void block_norm_
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const u32 b = __builtin_bit_cast(u32, h[c][i]) & 0x7FFFFFFFu;
-                if (8 * (t + c * TPR) + i < p.D)
+                if (at(c) + i < p.D)
                     m[0] = b > m[0] ? b : m[0];
             }
         row_all<MaxOp, TPR, 1>(m, slots[2]);
@@ -152,8 +151,7 @@ __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void block_norm_
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 q[i] = L.level(h[c][i]);
-            const int at = 8 * (t + c * TPR);
-            store_levels(p.hq + row * p.ldhq, at, p.D - at, q);
+            store_levels(p.hq + row * p.ldhq, at(c), p.D - at(c), q);
         }
         if (t == 0)
             p.hs[row] = L.scale;
@@ -167,43 +165,93 @@ __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void block_norm_
 //   dy = r1 (d g w_post - n c1),   c1 = mean(d q) = mean(e q) - r2 c2 mean(u q)
 //   dw_pre = sum dh u,  dgate = w_post sum_group d n,  dw_post = sum d g n
 // The three means of a row are taken together, so a row needs one reduction.
-// A workgroup takes consecutive rows: whole groups of rows that share a gate
-// row, or a part of one group; it keeps the column sums in registers and
-// leaves one partial row of each in the workspace, which
+// A workgroup of NT threads holds NT / TPR teams, each with a row in flight
+// and the next one's loads issued before this one's arithmetic.  It takes
+// consecutive rows: whole groups of rows that share a gate row (parts == 1; a
+// group to a team), or a part of one group (its rows to the teams in turn).
+// Column sums stay in registers over those rows, are added over the teams in
+// LDS, and leave one partial row of each in the workspace, which
 // block_norm_columns_kernel adds in a fixed order.
 // --------------------------------------------------------------------------
 struct NormGradParams {
     const void *x_new, *y, *gate, *w_post, *w_pre, *dx_new, *dh;
     const float *r_post, *r_pre;
     void *dx, *dy;
-    float *dgate, *dw_post, *dw_pre;
-    float *part_pre, *part_post, *part_gate;  // [P][Dp], or NULL
-    int64_t T, ldx, ldy, lddxn, lddh, lddx, lddy, gate_rows;
-    int64_t rows;  // rows for each workgroup (parts == 1), or of each part of a group
-    int parts;     // parts of each group (1: whole groups)
+    float* dgate;
+    // [P][Dp] or NULL: sums of dh u; and of d n for each part of a group, or
+    // of d g n where a workgroup takes whole groups (and writes dgate itself)
+    float *part_pre, *part_y;
+    int64_t ldx, ldy, lddxn, lddh, lddx, lddy;
+    int T, gate_rows;
+    int rows;   // rows of a workgroup
+    int parts;  // workgroups of a group (1: whole groups to a workgroup)
     int D, Dp;
     int post;
     float alpha;
 };
 
-template <int XT, int BT, int TPR, int NC>
-__global__ __attribute__((amdgpu_flat_work_group_size(TPR, TPR))) void
+template <int XT, int BT, int NC>
+struct GradRow {
+    Raw8<XT> x[NC], d[NC];
+    Raw8<BT> y[NC], h[NC];
+    float r1, r2;
+};
+
+template <int XT, int BT, int TPR, int NC, bool VEC>
+__device__ __forceinline__ void load_grad_row(GradRow<XT, BT, NC>& R, const NormGradParams& p,
+                                              int row, int t)
+{
+    // x' is read with dh only; a matrix that is not there reads as zeros
+    const Row<XT, VEC> x(p.dh ? p.x_new : nullptr, row, p.ldx, p.D), d(p.dx_new, row, p.lddxn, p.D);
+    const Row<BT, VEC> y(p.y, row, p.ldy, p.D), h(p.dh, row, p.lddh, p.D);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int at = 8 * (t + c * TPR);
+        x.load(R.x[c], at);
+        h.load(R.h[c], at);
+        d.load(R.d[c], at);
+        y.load(R.y[c], at);
+    }
+    R.r1 = p.post ? p.r_post[row] : 1.0f;
+    R.r2 = p.dh ? p.r_pre[row] : 0.0f;
+}
+
+template <int XT, int BT, int NT, int TPR, int NC, int WPE, bool VEC>
+__global__ __attribute__((amdgpu_flat_work_group_size(NT, NT), amdgpu_waves_per_eu(WPE, WPE))) void
 block_norm_grad_kernel(NormGradParams p)
 {
-    __shared__ u32 slots[2][48];
-    const int t = threadIdx.x;
+    constexpr int TEAMS = NT / TPR;
+    __shared__ u32 slots[2][TEAMS][48];
+    __shared__ float sums[TEAMS > 1 ? NT * 8 : 1];
+    const int t = threadIdx.x % TPR;
+    const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
     const float inv_d = 1.0f / (float)p.D;
-    const int64_t b = blockIdx.x;
-    int64_t r0, r1;
-    if (p.parts == 1) {
+    const bool whole = p.parts == 1;
+    // Row numbers fit 32 bits.  The divisions are done on the vector ALU:
+    // their results are read back as scalars, so that row addresses are.
+    const int b = (int)blockIdx.x;
+    const int per = whole ? p.gate_rows : 1;  // rows a team takes together
+    int group = __builtin_amdgcn_readfirstlane(whole ? 0 : b / p.parts);
+    int r0, r1;
+    if (whole) {
         r0 = b * p.rows;
         r1 = r0 + p.rows;
+        group = __builtin_amdgcn_readfirstlane(r0 / per) + team;
     } else {
-        const int64_t base = b / p.parts * p.gate_rows;
-        r0 = base + b % p.parts * p.rows;
+        const int base = group * p.gate_rows;
+        r0 = base + (b - group * p.parts) * p.rows;
         r1 = r0 + p.rows < base + p.gate_rows ? r0 + p.rows : base + p.gate_rows;
     }
     r1 = r1 < p.T ? r1 : p.T;
+
+    // The team's rows: of a part, every TEAMS-th; of whole groups, the rows of
+    // every TEAMS-th group in turn.  All teams take `count` steps, so that
+    // they meet at the barriers; a step past r1 has no row.
+    const int n = r1 > r0 ? r1 - r0 : 0;
+    const int count =
+        __builtin_amdgcn_readfirstlane(((n + per - 1) / per + TEAMS - 1) / TEAMS) * per;
+    int row = r0 + team * per;
+    int in_group = 0;  // row's place in its group (whole)
 
     float a_pre[NC][8], a_post[NC][8], a_g[NC][8];
 #pragma unroll
@@ -222,142 +270,161 @@ block_norm_grad_kernel(NormGradParams p)
         put8<BT>(w2[c], one);
         put8<BT>(g[c], one);
         if (p.w_post)
-            load8<BT>(w1[c], p.w_post, at, p.D - at);
+            Row<BT, VEC>(p.w_post, 0, 0, p.D).load(w1[c], at);
         if (p.w_pre)
-            load8<BT>(w2[c], p.w_pre, at, p.D - at);
+            Row<BT, VEC>(p.w_pre, 0, 0, p.D).load(w2[c], at);
     }
-
-    int64_t group = -1, group_end = r0;
-    const auto flush = [&]() {  // end of the rows of one gate row in this workgroup
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int at = 8 * (t + c * TPR);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float s = a_g[c][i];
-                a_post[c][i] = __builtin_fmaf(get8<BT>(g[c], i), s, a_post[c][i]);
-                if (p.dgate && p.parts == 1 && at + i < p.D)
-                    p.dgate[group * p.D + at + i] = get8<BT>(w1[c], i) * s;
-                if (p.parts == 1)
-                    a_g[c][i] = 0.0f;
-            }
-        }
-    };
-
-    for (int64_t row = r0; row < r1; ++row) {
-        if (row >= group_end) {
-            if (group >= 0)
-                flush();
-            group = p.gate ? row / p.gate_rows : 0;
-            group_end = p.gate ? (group + 1) * p.gate_rows : p.T;
-            if (p.gate) {
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const int at = 8 * (t + c * TPR);
-                    load8<BT>(g[c], elem_ptr<BT>(p.gate, group * (int64_t)p.D), at, p.D - at);
-                }
-            }
-        }
-        Raw8<XT> rx[NC], rd[NC];
-        Raw8<BT> ry[NC], rh[NC];
-        const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int at = 8 * (t + c * TPR);
-            const int left = p.D - at;
-            if (p.dx_new)
-                load8<XT>(rd[c], elem_ptr<XT>(p.dx_new, row * p.lddxn), at, left);
-            else
-                put8<XT>(rd[c], zero);
-            if (p.dh) {
-                load8<XT>(rx[c], elem_ptr<XT>(p.x_new, row * p.ldx), at, left);
-                load8<BT>(rh[c], elem_ptr<BT>(p.dh, row * p.lddh), at, left);
-            } else {
-                put8<XT>(rx[c], zero);
-                put8<BT>(rh[c], zero);
-            }
-            if (p.y)
-                load8<BT>(ry[c], elem_ptr<BT>(p.y, row * p.ldy), at, left);
-            else
-                put8<BT>(ry[c], zero);
-        }
-        const float rr1 = p.post ? p.r_post[row] : 1.0f;
-        const float rr2 = p.dh ? p.r_pre[row] : 0.0f;
-        float s[3] = {0.0f, 0.0f, 0.0f};
+    const auto load_gate = [&]() {
+        const Row<BT, VEC> gate(p.gate, group, p.D, p.D);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
+            gate.load(g[c], 8 * (t + c * TPR));
+    };
+    if (!whole && p.gate && n > 0)
+        load_gate();
+
+    GradRow<XT, BT, NC> R;
+    // the next row's loads in flight during this one's arithmetic, where the
+    // registers hold two rows
+    constexpr bool AHEAD = NC == 1;
+    if (AHEAD && row < r1)
+        load_grad_row<XT, BT, TPR, NC, VEC>(R, p, row, t);
+    for (int i = 0; i < count; ++i) {
+        const bool valid = row < r1;
+        if (whole && p.gate && valid && in_group == 0)
+            load_gate();
+        if (!AHEAD && valid)
+            load_grad_row<XT, BT, TPR, NC, VEC>(R, p, row, t);
+        GradRow<XT, BT, NC> Q = R;
+        const bool last = in_group + 1 == per;  // of its group, where that is whole
+        const int next = last ? row + 1 + (TEAMS - 1) * per : row + 1;
+        if (AHEAD && i + 1 < count && next < r1)
+            load_grad_row<XT, BT, TPR, NC, VEC>(R, p, next, t);
+        float s[3] = {0.0f, 0.0f, 0.0f};
+        if (valid) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float pp = get8<BT>(rh[c], i) * get8<BT>(w2[c], i);
-                const float u = get8<XT>(rx[c], i) * rr2;
-                const float e = __builtin_fmaf(rr2, pp, get8<XT>(rd[c], i));
-                const float q =
-                    get8<BT>(g[c], i) * get8<BT>(w1[c], i) * (get8<BT>(ry[c], i) * rr1);
-                s[0] = __builtin_fmaf(pp, u, s[0]);
-                s[1] = __builtin_fmaf(e, q, s[1]);
-                s[2] = __builtin_fmaf(u, q, s[2]);
-            }
-        row_sum<TPR, 3>(s, slots[row & 1]);
-        const float k2 = rr2 * s[0] * inv_d;
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float pp = get8<BT>(Q.h[c], k) * get8<BT>(w2[c], k);
+                    const float u = get8<XT>(Q.x[c], k) * Q.r2;
+                    const float e = __builtin_fmaf(Q.r2, pp, get8<XT>(Q.d[c], k));
+                    const float q =
+                        get8<BT>(g[c], k) * get8<BT>(w1[c], k) * (get8<BT>(Q.y[c], k) * Q.r1);
+                    s[0] = __builtin_fmaf(pp, u, s[0]);
+                    s[1] = __builtin_fmaf(e, q, s[1]);
+                    s[2] = __builtin_fmaf(u, q, s[2]);
+                }
+        }
+        row_sum<TPR, 3>(s, slots[i & 1][team]);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            repack<XT>(Q.x[c]);
+            repack<XT>(Q.d[c]);
+            repack<BT>(Q.y[c]);
+            repack<BT>(Q.h[c]);
+            repack<BT>(w1[c]);
+            repack<BT>(w2[c]);
+            repack<BT>(g[c]);
+        }
+        const int at_row = row, at_group = group;
+        row = next;
+        in_group = last ? 0 : in_group + 1;
+        group = whole && last ? group + TEAMS : group;
+        if (!valid)
+            continue;
+        const float k2 = Q.r2 * s[0] * inv_d;
         const float c1 = p.post ? (s[1] - k2 * s[2]) * inv_d : 0.0f;
+        const Row<XT, VEC> rdx(p.dx, at_row, p.lddx, p.D);
+        const Row<BT, VEC> rdy(p.dy, at_row, p.lddy, p.D);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int at = 8 * (t + c * TPR);
             float dx[8], dy[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float dh = get8<BT>(rh[c], i);
-                const float u = get8<XT>(rx[c], i) * rr2;
+            for (int k = 0; k < 8; ++k) {
+                const float dh = get8<BT>(Q.h[c], k);
+                const float u = get8<XT>(Q.x[c], k) * Q.r2;
                 const float e =
-                    __builtin_fmaf(rr2, dh * get8<BT>(w2[c], i), get8<XT>(rd[c], i));
+                    __builtin_fmaf(Q.r2, dh * get8<BT>(w2[c], k), get8<XT>(Q.d[c], k));
                 const float d = __builtin_fmaf(-k2, u, e);
-                const float n = get8<BT>(ry[c], i) * rr1;
-                a_pre[c][i] = __builtin_fmaf(dh, u, a_pre[c][i]);
-                a_g[c][i] = __builtin_fmaf(d, n, a_g[c][i]);
-                dx[i] = p.alpha * d;
-                dy[i] = rr1 * __builtin_fmaf(d, get8<BT>(g[c], i) * get8<BT>(w1[c], i), -n * c1);
+                const float nn = get8<BT>(Q.y[c], k) * Q.r1;
+                a_pre[c][k] = __builtin_fmaf(dh, u, a_pre[c][k]);
+                a_g[c][k] = __builtin_fmaf(d, nn, a_g[c][k]);
+                dx[k] = p.alpha * d;
+                dy[k] = Q.r1 * __builtin_fmaf(d, get8<BT>(g[c], k) * get8<BT>(w1[c], k), -nn * c1);
             }
-            if (p.dx) {
-                Raw8<XT> r;
-                put8<XT>(r, dx);
-                store8<XT>(const_cast<char*>(elem_ptr<XT>(p.dx, row * p.lddx)), at, p.D - at, r);
-            }
-            if (p.dy) {
-                Raw8<BT> r;
-                put8<BT>(r, dy);
-                store8<BT>(const_cast<char*>(elem_ptr<BT>(p.dy, row * p.lddy)), at, p.D - at, r);
+            Raw8<XT> ox;
+            put8<XT>(ox, dx);
+            rdx.store(ox, at);
+            Raw8<BT> oy;
+            put8<BT>(oy, dy);
+            rdy.store(oy, at);
+        }
+        // the end of a group that this team holds whole
+        if (whole && (last || at_row + 1 == r1)) {
+            const Row<DT_F32, VEC> out(p.dgate, at_group, p.D, p.D);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    a_post[c][k] = __builtin_fmaf(get8<BT>(g[c], k), a_g[c][k], a_post[c][k]);
+                    v[k] = get8<BT>(w1[c], k) * a_g[c][k];
+                    a_g[c][k] = 0.0f;
+                }
+                Raw8<DT_F32> r;
+                put8<DT_F32>(r, v);
+                out.store(r, 8 * (t + c * TPR));
             }
         }
     }
-    if (group >= 0)
-        flush();
-    // partial column sums (Dp is D rounded up to whole chunks)
+
+    // partial column sums (Dp is D rounded up to whole chunks), over the
+    // teams in order
+    const auto leave = [&](float* to, float (&v)[NC][8]) {
+        if (!to)
+            return;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const int at = 8 * (t + c * TPR);
-        if (at >= p.Dp)
-            continue;
-        const int64_t o = b * p.Dp + at;
+        for (int c = 0; c < NC; ++c) {
+            const int at = 8 * (t + c * TPR);
+            if constexpr (TEAMS > 1) {
+                __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const auto put = [&](float* to, const float (&v)[8]) {
-                if (to)
-                    *(f32x4*)(to + o + 4 * i) =
-                        f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-            };
-            put(p.part_pre, a_pre[c]);
-            put(p.part_post, a_post[c]);
-            put(p.part_gate, a_g[c]);
+                for (int k = 0; k < 8; ++k)
+                    sums[k * NT + threadIdx.x] = v[c][k];
+                __syncthreads();
+                if (team == 0) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        for (int j = 1; j < TEAMS; ++j)
+                            v[c][k] += sums[k * NT + j * TPR + t];
+                }
+            }
+            if (team == 0 && at < p.Dp) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    *(f32x4*)(to + (int64_t)b * p.Dp + at + 4 * k) =
+                        f32x4{v[c][4 * k], v[c][4 * k + 1], v[c][4 * k + 2], v[c][4 * k + 3]};
+            }
         }
-    }
+    };
+    leave(p.part_pre, a_pre);
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            a_g[c][k] = whole ? a_post[c][k] : a_g[c][k];
+    leave(p.part_y, a_g);
 }
 
-// Sums of the partial rows: blockIdx.y 0 and 1 take dw_pre and dw_post (P
-// rows each), 2 + j the gate row j (its `parts` rows, times w_post).
+// Sums of the partial rows: blockIdx.y 0 takes dw_pre, 1 takes dw_post (the
+// sums of d n of a part times its group's gate), 2 + j the gate row j (its
+// `parts` rows, times w_post).
 struct ColumnParams {
-    const float *part_pre, *part_post, *part_gate;
+    const float *part_pre, *part_y;
     float *dw_pre, *dw_post, *dgate;
-    const void* w_post;
+    const void *w_post, *gate;
     int64_t P;
     int parts, D, Dp;
 };
@@ -366,22 +433,36 @@ template <int BT>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void
 block_norm_columns_kernel(ColumnParams p)
 {
-    constexpr int CL = 16, RL = 16;  // threads along columns (4 each) and rows
+    constexpr int CL = 8, RL = 32;  // threads along columns (4 each) and rows
     __shared__ f32x4 red[RL][CL];
     const int which = blockIdx.y;
-    const float* from = which == 0 ? p.part_pre : (which == 1 ? p.part_post : p.part_gate);
+    const float* from = which == 0 ? p.part_pre : p.part_y;
     float* to = which == 0 ? p.dw_pre : (which == 1 ? p.dw_post : p.dgate);
     if (!from || !to)
         return;
     const int64_t group = which < 2 ? 0 : which - 2;
     const int64_t first = which < 2 ? 0 : group * p.parts;
     const int64_t rows = which < 2 ? p.P : p.parts;
+    const bool weigh = which == 1 && p.parts > 1 && p.gate;
     const int cl = threadIdx.x % CL, rl = threadIdx.x / CL;
     const int at = 4 * (blockIdx.x * CL + cl);
     f32x4 s = {0, 0, 0, 0};
-    if (at < p.Dp)
-        for (int64_t r = rl; r < rows; r += RL)
-            s += *(const f32x4*)(from + (first + r) * p.Dp + at);
+    if (at < p.Dp) {
+#pragma unroll 4
+        for (int64_t r = rl; r < rows; r += RL) {
+            const f32x4 v = *(const f32x4*)(from + (first + r) * p.Dp + at);
+            if (weigh) {
+                Raw8<BT> g;
+                load8<BT>(g, elem_ptr<BT>(p.gate, r / p.parts * (int64_t)p.D), at,
+                          p.D - at < 4 ? p.D - at : 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[i] = __builtin_fmaf(get8<BT>(g, i), v[i], s[i]);
+            } else {
+                s += v;
+            }
+        }
+    }
     red[rl][cl] = s;
     __syncthreads();
     if (rl == 0 && at < p.Dp) {

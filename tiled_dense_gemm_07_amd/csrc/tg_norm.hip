@@ -43,44 +43,68 @@ struct Pick {
     int rows;     // of a workgroup
 };
 
-Pick pick_forward(int64_t D, int xt, int bt)
+// VEC: rows of whole 16-byte chunks at 16-byte boundaries.
+template <int XT, int BT, bool VEC>
+Pick pick_forward_of(int64_t D)
+{
+    if (D <= 512)
+        return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 64, 1, VEC>, 256, 4};
+    if (D <= 2048)
+        return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 256, 1, VEC>, 256, 1};
+    if (D <= 4096)
+        return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 256, 2, VEC>, 256, 1};
+    if (D <= 8192)
+        return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 1, VEC>, 1024, 1};
+    if (D <= 16384)
+        return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 2, VEC>, 1024, 1};
+    return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 4, VEC>, 1024, 1};
+}
+
+Pick pick_forward(int64_t D, int xt, int bt, bool vec)
 {
     return by_types(xt, bt, [&](auto X, auto B) -> Pick {
         constexpr int XT = decltype(X)::value, BT = decltype(B)::value;
-        if (D <= 512)
-            return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 64, 1>, 256, 4};
-        if (D <= 2048)
-            return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 256, 1>, 256, 1};
-        if (D <= 4096)
-            return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 256, 2>, 256, 1};
-        if (D <= 8192)
-            return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 1>, 1024, 1};
-        if (D <= 16384)
-            return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 2>, 1024, 1};
-        return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 4>, 1024, 1};
+        return vec ? pick_forward_of<XT, BT, true>(D) : pick_forward_of<XT, BT, false>(D);
     });
 }
 
-Pick pick_backward(int64_t D, int xt, int bt)
+// 512 threads in teams for rows up to 4096, two workgroups to a compute unit
+// (128 registers a thread; 256 where both types are fp32).
+template <int XT, int BT, bool VEC>
+Pick pick_backward_of(int64_t D)
+{
+    constexpr int W = XT == tg::DT_F32 && BT == tg::DT_F32 ? 2 : 4;
+    if (D <= 512)
+        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 512, 64, 1, W, VEC>, 512, 1};
+    if (D <= 1024)
+        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 512, 128, 1, W, VEC>, 512, 1};
+    if (D <= 2048)
+        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 512, 256, 1, W, VEC>, 512, 1};
+    if (D <= 4096)
+        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 512, 512, 1, W, VEC>, 512, 1};
+    if (D <= 8192)
+        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 1024, 1024, 1, 4, VEC>, 1024, 1};
+    if (D <= 16384)
+        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 1024, 1024, 2, 4, VEC>, 1024, 1};
+    return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 1024, 1024, 4, 4, VEC>, 1024, 1};
+}
+
+Pick pick_backward(int64_t D, int xt, int bt, bool vec)
 {
     return by_types(xt, bt, [&](auto X, auto B) -> Pick {
         constexpr int XT = decltype(X)::value, BT = decltype(B)::value;
-        if (D <= 512)
-            return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 64, 1>, 64, 1};
-        if (D <= 2048)
-            return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 256, 1>, 256, 1};
-        if (D <= 4096)
-            return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 256, 2>, 256, 1};
-        if (D <= 8192)
-            return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 512, 2>, 512, 1};
-        if (D <= 16384)
-            return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 1024, 2>, 1024, 1};
-        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 1024, 4>, 1024, 1};
+        return vec ? pick_backward_of<XT, BT, true>(D) : pick_backward_of<XT, BT, false>(D);
     });
 }
 
 bool bad_size(int64_t T, int64_t D) { return T < 0 || D < 0 || T > kMaxDim || D > kMaxD; }
 bool bad_stride(const void* p, int64_t ld, int64_t D) { return p && ld < D; }
+
+// Rows of the matrix start at 16-byte boundaries (or it is not there).
+bool at16(const void* p, int64_t ld, int esize)
+{
+    return !p || (((uintptr_t)p & 15) == 0 && ld * esize % 16 == 0);
+}
 
 // How the gradient kernel's workgroups share the rows, and the workspace.
 struct GradPlan {
@@ -90,17 +114,17 @@ struct GradPlan {
     int parts;       // workgroups of a group (1: whole groups to a workgroup)
     int64_t P;       // workgroups
     int64_t Dp;
-    bool pre, post, gate;  // partial sums kept
+    bool pre, y;     // partial sums kept: of dw_pre; of dw_post and shared gates
     size_t bytes;
 };
 
 GradPlan grad_plan(const tg_block_norm_grad_args& a)
 {
     GradPlan g{};
-    // About two workgroups to a compute unit, and at least 8 rows to each:
+    // About two workgroups to a compute unit, and at least 4 rows to each:
     // fewer would write more partial sums than they save in time.
     int64_t want = ceil_div(a.T, 512);
-    want = want < 8 ? 8 : want;
+    want = want < 4 ? 4 : want;
     g.gate_rows = a.gate ? (a.gate_rows < a.T ? a.gate_rows : a.T) : a.T;
     g.groups = ceil_div(a.T, g.gate_rows);
     if (g.gate_rows <= want) {
@@ -114,9 +138,8 @@ GradPlan grad_plan(const tg_block_norm_grad_args& a)
     }
     g.Dp = ceil_div(a.D, 8) * 8;
     g.pre = a.dw_pre != nullptr;
-    g.post = a.dw_post != nullptr;
-    g.gate = a.dgate != nullptr && g.parts > 1;
-    g.bytes = (size_t)(g.P * g.Dp * 4) * ((g.pre ? 1 : 0) + (g.post ? 1 : 0) + (g.gate ? 1 : 0));
+    g.y = a.dw_post != nullptr || (a.dgate != nullptr && g.parts > 1);
+    g.bytes = (size_t)(g.P * g.Dp * 4) * ((g.pre ? 1 : 0) + (g.y ? 1 : 0));
     return g;
 }
 
@@ -189,18 +212,21 @@ tg_status tg_block_norm(const tg_block_norm_args* a, tg_stream_t stream)
     p.hs = a->hs;
     p.r_post = a->r_post;
     p.r_pre = a->r_pre;
-    p.T = T;
+    p.T = (int)T;
     p.ldx = a->ldx;
     p.ldy = a->ldy;
     p.ldxo = a->ldx_out;
     p.ldh = a->ldh;
     p.ldhq = a->ldhq;
-    p.gate_rows = gr;
+    p.gate_rows = (int)gr;
     p.D = (int)D;
     p.post = a->post_norm != 0;
     p.alpha = a->alpha;
     p.eps = a->eps;
-    const Pick k = pick_forward(D, a->xtype, a->btype);
+    const bool vec = D % 8 == 0 && at16(a->x, a->ldx, xs) && at16(a->y, a->ldy, bs) &&
+                     at16(a->gate, D, bs) && at16(a->w_post, D, bs) && at16(a->w_pre, D, bs) &&
+                     at16(a->x_out, a->ldx_out, xs) && at16(a->h, a->ldh, bs);
+    const Pick k = pick_forward(D, a->xtype, a->btype, vec);
     return tg::launch_kernel(k.kernel, ceil_div(T, k.rows), 1, k.threads, &p, (hipStream_t)stream,
                              "block_norm");
 }
@@ -265,45 +291,44 @@ tg_status tg_block_norm_backward(const tg_block_norm_grad_args* a, void* workspa
     p.dx = a->dx;
     p.dy = a->dy;
     p.dgate = a->dgate;
-    p.dw_post = a->dw_post;
-    p.dw_pre = a->dw_pre;
     float* at = (float*)workspace;
     if (g.pre) {
         p.part_pre = at;
         at += g.P * g.Dp;
     }
-    if (g.post) {
-        p.part_post = at;
-        at += g.P * g.Dp;
-    }
-    if (g.gate)
-        p.part_gate = at;
-    p.T = T;
+    if (g.y)
+        p.part_y = at;
+    p.T = (int)T;
     p.ldx = a->ldx_new;
     p.ldy = a->ldy;
     p.lddxn = a->lddx_new;
     p.lddh = a->lddh;
     p.lddx = a->lddx;
     p.lddy = a->lddy;
-    p.gate_rows = g.gate_rows;
-    p.rows = g.rows;
+    p.gate_rows = (int)g.gate_rows;
+    p.rows = (int)g.rows;
     p.parts = g.parts;
     p.D = (int)D;
     p.Dp = (int)g.Dp;
     p.post = a->y && a->post_norm;
     p.alpha = a->alpha;
-    const Pick k = pick_backward(D, a->xtype, a->btype);
+    const bool vec = D % 8 == 0 && at16(a->x_new, a->ldx_new, xs) && at16(a->y, a->ldy, bs) &&
+                     at16(a->gate, D, bs) && at16(a->w_post, D, bs) && at16(a->w_pre, D, bs) &&
+                     at16(a->dx_new, a->lddx_new, xs) && at16(a->dh, a->lddh, bs) &&
+                     at16(a->dx, a->lddx, xs) && at16(a->dy, a->lddy, bs) && at16(a->dgate, D, 4);
+    const Pick k = pick_backward(D, a->xtype, a->btype, vec);
     if (tg_status s = tg::launch_kernel(k.kernel, g.P, 1, k.threads, &p, (hipStream_t)stream,
                                         "block_norm_grad"))
         return s;
     if (g.bytes == 0)
         return TG_OK;
-    tg::ColumnParams c{p.part_pre, p.part_post, p.part_gate, a->dw_pre, a->dw_post, a->dgate,
-                       a->w_post,  g.P,         g.parts,     (int)D,    (int)g.Dp};
+    const bool shared = a->dgate && g.parts > 1;  // gate rows of several workgroups
+    tg::ColumnParams c{p.part_pre, p.part_y, a->dw_pre, a->dw_post, a->dgate, a->w_post,
+                       a->gate,    g.P,      g.parts,   (int)D,     (int)g.Dp};
     const void* kc = by_types(TG_F32, a->btype, [](auto, auto B) {
         return (const void*)&tg::block_norm_columns_kernel<decltype(B)::value>;
     });
-    return tg::launch_kernel(kc, ceil_div(g.Dp, 64), 2 + (g.gate ? g.groups : 0), 256, &c,
+    return tg::launch_kernel(kc, ceil_div(g.Dp, 32), 2 + (shared ? g.groups : 0), 256, &c,
                              (hipStream_t)stream, "block_norm_columns");
 }
 

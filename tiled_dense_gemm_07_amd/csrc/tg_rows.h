@@ -72,6 +72,17 @@ __device__ __forceinline__ float get8(const Raw8<DT>& r, int i)
     return (float)__builtin_bit_cast(_Float16, (uint16_t)((i & 1) ? (w >> 16) : w));
 }
 
+// Keeps the compiler from holding the unpacked values of r across this point:
+// they are unpacked again after it, which takes an instruction each and no
+// registers.
+template <int DT>
+__device__ __forceinline__ void repack(Raw8<DT>& r)
+{
+    asm volatile("" : "+v"(r.v[0]));
+    if constexpr (DT == DT_F32)
+        asm volatile("" : "+v"(r.v[1]));
+}
+
 // Rounds once to the type (nearest even).
 template <int DT>
 __device__ __forceinline__ void put8(Raw8<DT>& r, const float (&v)[8])
@@ -119,6 +130,68 @@ __device__ __forceinline__ void store8(void* row, int at, int left, const Raw8<D
         }
     }
 }
+
+// One row of a matrix, through a buffer resource of the row: the lane's place is
+// one register for all rows and all matrices, and the hardware's range check
+// gives zeros past the end of the row, or from a matrix that is not there
+// (NULL), and drops stores there.  VEC: rows of whole chunks at 16-byte
+// boundaries; else the chunk across the end is moved element by element, and
+// chunks may start at any element.  The row number has to be uniform over the
+// wave.
+template <int DT, bool VEC>
+struct Row {
+    static constexpr int ES = DT == DT_F32 ? 4 : 2;
+    int n;
+    __amdgpu_buffer_rsrc_t rs;
+
+    __device__ __forceinline__ Row(const void* base, int64_t row, int64_t ld, int cols)
+    {
+        n = base ? cols : 0;
+        rs = make_rsrc((const char*)base + row * ld * ES, (u32)(n * ES));
+    }
+    __device__ __forceinline__ bool across(int at) const
+    {
+        return !VEC && at < n && at + 8 > n;
+    }
+    __device__ __forceinline__ void load(Raw8<DT>& r, int at) const
+    {
+        const u32 off = (u32)at * (u32)ES;
+        if (!across(at)) {
+            r.v[0] = buf_load16(rs, off);
+            if constexpr (DT == DT_F32)
+                r.v[1] = buf_load16(rs, off + 16u);
+        } else if constexpr (DT == DT_F32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                r.v[i >> 2][i & 3] = buf_load4(rs, off + 4u * i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                r.v[0][i] = buf_load2(rs, off + 4u * i) | buf_load2(rs, off + 4u * i + 2u) << 16;
+        }
+    }
+    __device__ __forceinline__ void store(const Raw8<DT>& r, int at) const
+    {
+        const int off = at * ES;
+        if (!across(at)) {
+            __builtin_amdgcn_raw_buffer_store_b128(r.v[0], rs, off, 0, 0);
+            if constexpr (DT == DT_F32)
+                __builtin_amdgcn_raw_buffer_store_b128(r.v[1], rs, off + 16, 0, 0);
+        } else if constexpr (DT == DT_F32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const u32 w = r.v[i >> 2][i & 3];
+                __builtin_amdgcn_raw_buffer_store_b32(w, rs, off + 4 * i, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint16_t w = (uint16_t)(r.v[0][i >> 1] >> (16 * (i & 1)));
+                __builtin_amdgcn_raw_buffer_store_b16(w, rs, off + 2 * i, 0, 0);
+            }
+        }
+    }
+};
 
 // --------------------------------------------------------------------------
 // Reductions over the TPR threads that hold a row.  Every thread gets the
