@@ -20,31 +20,39 @@ using tg::span1;
 
 // Kernel for rows of K elements: one wave for a row, four waves, or sixteen,
 // with 1, 2 or 4 chunks of 8 elements for each thread.
-template <int DT>
+// ODD: 16-bit rows of an odd length.
+template <int DT, bool ODD>
 const void* quant_kernel(int64_t K, int* threads, int* rows)
 {
     *threads = 256;
     *rows = K <= 2048 ? 4 : 1;
     if (K <= 512)
-        return (const void*)&tg::quant_i8_kernel<DT, 256, 64, 1>;
+        return (const void*)&tg::quant_i8_kernel<DT, 256, 64, 1, ODD>;
     if (K <= 2048)
-        return (const void*)&tg::quant_i8_kernel<DT, 256, 64, 4>;
+        return (const void*)&tg::quant_i8_kernel<DT, 256, 64, 4, ODD>;
     if (K <= 4096)
-        return (const void*)&tg::quant_i8_kernel<DT, 256, 256, 2>;
+        return (const void*)&tg::quant_i8_kernel<DT, 256, 256, 2, ODD>;
     if (K <= 8192)
-        return (const void*)&tg::quant_i8_kernel<DT, 256, 256, 4>;
+        return (const void*)&tg::quant_i8_kernel<DT, 256, 256, 4, ODD>;
     *threads = 1024;
     if (K <= 32768)
-        return (const void*)&tg::quant_i8_kernel<DT, 1024, 1024, 4>;
-    return (const void*)&tg::quant_i8_kernel<DT, 1024, 1024, 0>;
+        return (const void*)&tg::quant_i8_kernel<DT, 1024, 1024, 4, ODD>;
+    return (const void*)&tg::quant_i8_kernel<DT, 1024, 1024, 0, ODD>;
 }
 
 tg_status launch_quant(const tg::QuantParams& p, int dtype, hipStream_t stream)
 {
     int threads, rows;
-    const void* k = dtype == TG_F32   ? quant_kernel<tg::DT_F32>(p.K, &threads, &rows)
-                    : dtype == TG_F16 ? quant_kernel<tg::DT_F16>(p.K, &threads, &rows)
-                                      : quant_kernel<tg::DT_BF16>(p.K, &threads, &rows);
+    const bool odd = p.K % 2 != 0;
+    const void* k;
+    if (dtype == TG_F32)
+        k = quant_kernel<tg::DT_F32, false>(p.K, &threads, &rows);
+    else if (dtype == TG_F16)
+        k = odd ? quant_kernel<tg::DT_F16, true>(p.K, &threads, &rows)
+                : quant_kernel<tg::DT_F16, false>(p.K, &threads, &rows);
+    else
+        k = odd ? quant_kernel<tg::DT_BF16, true>(p.K, &threads, &rows)
+                : quant_kernel<tg::DT_BF16, false>(p.K, &threads, &rows);
     tg::QuantParams q = p;
     return tg::launch_kernel(k, ceil_div(p.M, rows), 1, threads, &q, stream, "quant_i8");
 }
@@ -210,7 +218,7 @@ tg_status tg_quant_i8(int64_t M, int64_t K, tg_dtype dtype, const void* X, int64
 {
     if (!tg::dtype_ok(dtype))
         return TG_ERR_BAD_DTYPE;
-    if (M < 0 || K < 0 || M > kMaxDim || K > kMaxDim / 2 || ldx < K || ldq < K)
+    if (M < 0 || K < 0 || M > kMaxDim || K > kMaxDim / 4 || ldx < K || ldq < K)
         return TG_ERR_BAD_SHAPE;
     if (M == 0)
         return TG_OK;
@@ -220,7 +228,7 @@ tg_status tg_quant_i8(int64_t M, int64_t K, tg_dtype dtype, const void* X, int64
                ss = span1(s, M, 4);
     if (overlap(x, q) || overlap(x, ss) || overlap(q, ss))
         return TG_ERR_ALIAS;
-    tg::QuantParams p{X, Q, s, M, (int)K, ldx, ldq, (int)K};
+    tg::QuantParams p{X, Q, s, (int)M, (int)K, ldx, ldq, (int)K};
     return launch_quant(p, dtype, (hipStream_t)stream);
 }
 
@@ -324,7 +332,7 @@ tg_status tg_linear_i8(int64_t M, int64_t N, int64_t K, tg_dtype dtype, const vo
     const int64_t ldq = ceil_div(K, 16) * 16;
     float* sa = (float*)workspace;
     int8_t* A = (int8_t*)workspace + ceil_div(4 * M, 256) * 256;
-    tg::QuantParams q{X, A, sa, M, (int)K, ldx, ldq, (int)ldq};
+    tg::QuantParams q{X, A, sa, (int)M, (int)K, ldx, ldq, (int)ldq};
     if (tg_status st = launch_quant(q, dtype, (hipStream_t)stream))
         return st;
     p.A = A;

@@ -24,7 +24,7 @@ struct NormParams {
     float alpha, eps;
 };
 
-template <int XT, int BT, int NT, int TPR, int NC, bool VEC>
+template <int XT, int BT, int NT, int TPR, int NC, bool ODD>
 __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void block_norm_kernel(NormParams p)
 {
     __shared__ u32 slots[3][16];
@@ -35,17 +35,17 @@ __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void block_norm_
         return;  // whole waves; rows share a workgroup only when TPR is one wave
     const float inv_d = 1.0f / (float)p.D;
     const auto at = [&](int c) { return 8 * (t + c * TPR); };
-    const Row<BT, VEC> w1(p.w_post, 0, 0, p.D), w2(p.w_pre, 0, 0, p.D);
-    const Row<XT, VEC> x(p.x, row, p.ldx, p.D);
+    const Row<BT, ODD> w1(p.w_post, 0, 0, p.D), w2(p.w_pre, 0, 0, p.D);
+    const Row<XT, ODD> x(p.x, row, p.ldx, p.D);
     Raw8<XT> rx[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c)
         x.load(rx[c], at(c));
     if (p.y) {
-        const Row<BT, VEC> y(p.y, row, p.ldy, p.D);
-        const Row<BT, VEC> gate(
+        const Row<BT, ODD> y(p.y, row, p.ldy, p.D);
+        const Row<BT, ODD> gate(
             p.gate, __builtin_amdgcn_readfirstlane(p.gate ? row / p.gate_rows : 0), p.D, p.D);
-        const Row<XT, VEC> xo(p.x_out, row, p.ldxo, p.D);
+        const Row<XT, ODD> xo(p.x_out, row, p.ldxo, p.D);
         Raw8<BT> ry[NC], rw[NC], rg[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -124,7 +124,7 @@ __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void block_norm_
         }
     }
     if (p.h) {
-        const Row<BT, VEC> out(p.h, row, p.ldh, p.D);
+        const Row<BT, ODD> out(p.h, row, p.ldh, p.D);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             Raw8<BT> r;
@@ -194,16 +194,17 @@ template <int XT, int BT, int NC>
 struct GradRow {
     Raw8<XT> x[NC], d[NC];
     Raw8<BT> y[NC], h[NC];
+    Raw8<BT> g[NC];  // the row's gate, if it opens a group
     float r1, r2;
 };
 
-template <int XT, int BT, int TPR, int NC, bool VEC>
+template <int XT, int BT, int TPR, int NC, bool ODD>
 __device__ __forceinline__ void load_grad_row(GradRow<XT, BT, NC>& R, const NormGradParams& p,
-                                              int row, int t)
+                                              int row, int t, int gate_row)
 {
     // x' is read with dh only; a matrix that is not there reads as zeros
-    const Row<XT, VEC> x(p.dh ? p.x_new : nullptr, row, p.ldx, p.D), d(p.dx_new, row, p.lddxn, p.D);
-    const Row<BT, VEC> y(p.y, row, p.ldy, p.D), h(p.dh, row, p.lddh, p.D);
+    const Row<XT, ODD> x(p.dh ? p.x_new : nullptr, row, p.ldx, p.D), d(p.dx_new, row, p.lddxn, p.D);
+    const Row<BT, ODD> y(p.y, row, p.ldy, p.D), h(p.dh, row, p.lddh, p.D);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int at = 8 * (t + c * TPR);
@@ -212,11 +213,17 @@ __device__ __forceinline__ void load_grad_row(GradRow<XT, BT, NC>& R, const Norm
         d.load(R.d[c], at);
         y.load(R.y[c], at);
     }
+    if (gate_row >= 0) {
+        const Row<BT, ODD> gate(p.gate, gate_row, p.D, p.D);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            gate.load(R.g[c], 8 * (t + c * TPR));
+    }
     R.r1 = p.post ? p.r_post[row] : 1.0f;
     R.r2 = p.dh ? p.r_pre[row] : 0.0f;
 }
 
-template <int XT, int BT, int NT, int TPR, int NC, int WPE, bool VEC>
+template <int XT, int BT, int NT, int TPR, int NC, int WPE, bool ODD>
 __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT), amdgpu_waves_per_eu(WPE, WPE))) void
 block_norm_grad_kernel(NormGradParams p)
 {
@@ -270,36 +277,39 @@ block_norm_grad_kernel(NormGradParams p)
         put8<BT>(w2[c], one);
         put8<BT>(g[c], one);
         if (p.w_post)
-            Row<BT, VEC>(p.w_post, 0, 0, p.D).load(w1[c], at);
+            Row<BT, ODD>(p.w_post, 0, 0, p.D).load(w1[c], at);
         if (p.w_pre)
-            Row<BT, VEC>(p.w_pre, 0, 0, p.D).load(w2[c], at);
+            Row<BT, ODD>(p.w_pre, 0, 0, p.D).load(w2[c], at);
     }
-    const auto load_gate = [&]() {
-        const Row<BT, VEC> gate(p.gate, group, p.D, p.D);
+    if (!whole && p.gate && n > 0) {
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-            gate.load(g[c], 8 * (t + c * TPR));
-    };
-    if (!whole && p.gate && n > 0)
-        load_gate();
+            Row<BT, ODD>(p.gate, group, p.D, p.D).load(g[c], 8 * (t + c * TPR));
+    }
 
     GradRow<XT, BT, NC> R;
     // the next row's loads in flight during this one's arithmetic, where the
     // registers hold two rows
     constexpr bool AHEAD = NC == 1;
+    const bool own_gate = whole && p.gate;  // each group's gate with its first row
     if (AHEAD && row < r1)
-        load_grad_row<XT, BT, TPR, NC, VEC>(R, p, row, t);
+        load_grad_row<XT, BT, TPR, NC, ODD>(R, p, row, t, own_gate ? group : -1);
     for (int i = 0; i < count; ++i) {
         const bool valid = row < r1;
-        if (whole && p.gate && valid && in_group == 0)
-            load_gate();
         if (!AHEAD && valid)
-            load_grad_row<XT, BT, TPR, NC, VEC>(R, p, row, t);
+            load_grad_row<XT, BT, TPR, NC, ODD>(R, p, row, t,
+                                                own_gate && in_group == 0 ? group : -1);
         GradRow<XT, BT, NC> Q = R;
+        if (own_gate && in_group == 0) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                g[c] = Q.g[c];
+        }
         const bool last = in_group + 1 == per;  // of its group, where that is whole
         const int next = last ? row + 1 + (TEAMS - 1) * per : row + 1;
         if (AHEAD && i + 1 < count && next < r1)
-            load_grad_row<XT, BT, TPR, NC, VEC>(R, p, next, t);
+            load_grad_row<XT, BT, TPR, NC, ODD>(R, p, next, t,
+                                                own_gate && last ? group + TEAMS : -1);
         float s[3] = {0.0f, 0.0f, 0.0f};
         if (valid) {
 #pragma unroll
@@ -335,8 +345,8 @@ block_norm_grad_kernel(NormGradParams p)
             continue;
         const float k2 = Q.r2 * s[0] * inv_d;
         const float c1 = p.post ? (s[1] - k2 * s[2]) * inv_d : 0.0f;
-        const Row<XT, VEC> rdx(p.dx, at_row, p.lddx, p.D);
-        const Row<BT, VEC> rdy(p.dy, at_row, p.lddy, p.D);
+        const Row<XT, ODD> rdx(p.dx, at_row, p.lddx, p.D);
+        const Row<BT, ODD> rdy(p.dy, at_row, p.lddy, p.D);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int at = 8 * (t + c * TPR);
@@ -363,7 +373,7 @@ block_norm_grad_kernel(NormGradParams p)
         }
         // the end of a group that this team holds whole
         if (whole && (last || at_row + 1 == r1)) {
-            const Row<DT_F32, VEC> out(p.dgate, at_group, p.D, p.D);
+            const Row<DT_F32, ODD> out(p.dgate, at_group, p.D, p.D);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 float v[8];
@@ -447,21 +457,30 @@ block_norm_columns_kernel(ColumnParams p)
     const int cl = threadIdx.x % CL, rl = threadIdx.x / CL;
     const int at = 4 * (blockIdx.x * CL + cl);
     f32x4 s = {0, 0, 0, 0};
-    if (at < p.Dp) {
+    if (at < p.Dp && weigh) {
+        // elements past the end of a gate row are not used, and past the end
+        // of the matrix read as zeros (shared gates: a few hundred rows, so
+        // offsets stay far below 32 bits)
+        constexpr int ES = BT == DT_F32 ? 4 : 2;
+        const auto gate = make_rsrc(p.gate, clamp_bytes(rows / p.parts * (int64_t)p.D * ES));
 #pragma unroll 4
-        for (int64_t r = rl; r < rows; r += RL) {
-            const f32x4 v = *(const f32x4*)(from + (first + r) * p.Dp + at);
-            if (weigh) {
-                Raw8<BT> g;
-                load8<BT>(g, elem_ptr<BT>(p.gate, r / p.parts * (int64_t)p.D), at,
-                          p.D - at < 4 ? p.D - at : 4);
+        for (int r = rl; r < (int)rows; r += RL) {
+            const f32x4 v = *(const f32x4*)(from + (int64_t)r * p.Dp + at);
+            const u32 o = (u32)(r / p.parts * (int64_t)p.D + at) * (u32)ES;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s[i] = __builtin_fmaf(get8<BT>(g, i), v[i], s[i]);
-            } else {
-                s += v;
+            for (int i = 0; i < 4; ++i) {
+                Raw8<BT> g;
+                if constexpr (BT == DT_F32)
+                    g.v[0][0] = buf_load4(gate, o + 4u * i);
+                else
+                    g.v[0][0] = buf_load2(gate, o + 2u * i);
+                s[i] = __builtin_fmaf(get8<BT>(g, 0), v[i], s[i]);
             }
         }
+    } else if (at < p.Dp) {
+#pragma unroll 4
+        for (int64_t r = rl; r < rows; r += RL)
+            s += *(const f32x4*)(from + (first + r) * p.Dp + at);
     }
     red[rl][cl] = s;
     __syncthreads();

@@ -12,8 +12,7 @@ struct QuantParams {
     const void* X;
     int8_t* Q;
     float* s;
-    int64_t M;
-    int K;
+    int M, K;
     int64_t ldx, ldq;
     int kq;  // columns of Q to write: past K, zeros
 };
@@ -45,15 +44,16 @@ __device__ __forceinline__ u32 chunk_amax(const Raw8<DT>& r, u32 m)
 }
 
 // NT threads, NT / TPR rows per workgroup.
-template <int DT, int NT, int TPR, int NC>
+template <int DT, int NT, int TPR, int NC, bool ODD>
 __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void quant_i8_kernel(QuantParams p)
 {
     __shared__ u32 slot[16];
     const int t = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * (NT / TPR) + threadIdx.x / TPR;
+    const int row = (int)blockIdx.x * (NT / TPR) +
+                    __builtin_amdgcn_readfirstlane((int)(threadIdx.x / TPR));
     if (row >= p.M)
         return;  // whole waves; rows share a workgroup only when TPR is one wave
-    const char* x = elem_ptr<DT>(p.X, row * p.ldx);
+    const Row<DT, ODD> x(p.X, row, p.ldx, p.K);
     int8_t* q = p.Q + row * p.ldq;
     u32 m[1] = {0};
     RowLevels L;
@@ -62,7 +62,7 @@ __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void quant_i8_ke
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int at = 8 * (t + c * TPR);
-            load8<DT>(r[c], x, at, p.K - at);
+            x.load(r[c], at);
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -77,14 +77,14 @@ __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void quant_i8_ke
     } else {
         for (int at = 8 * t; at < p.K; at += 8 * TPR) {
             Raw8<DT> r;
-            load8<DT>(r, x, at, p.K - at);
+            x.load(r, at);
             m[0] = chunk_amax<DT>(r, m[0]);
         }
         row_all<MaxOp, TPR, 1>(m, slot);
         L.of_amax(m[0]);
         for (int at = 8 * t; at < p.kq; at += 8 * TPR) {
             Raw8<DT> r;
-            load8<DT>(r, x, at, p.K - at);
+            x.load(r, at);
             quant_chunk<DT>(r, L, q, at, p.kq - at);
         }
     }

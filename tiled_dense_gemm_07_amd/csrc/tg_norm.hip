@@ -43,68 +43,69 @@ struct Pick {
     int rows;     // of a workgroup
 };
 
-// VEC: rows of whole 16-byte chunks at 16-byte boundaries.
-template <int XT, int BT, bool VEC>
+// ODD: rows with an odd number of elements, some of them of 16 bits.
+template <int XT, int BT, bool ODD>
 Pick pick_forward_of(int64_t D)
 {
     if (D <= 512)
-        return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 64, 1, VEC>, 256, 4};
+        return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 64, 1, ODD>, 256, 4};
     if (D <= 2048)
-        return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 256, 1, VEC>, 256, 1};
+        return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 256, 1, ODD>, 256, 1};
     if (D <= 4096)
-        return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 256, 2, VEC>, 256, 1};
+        return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 256, 2, ODD>, 256, 1};
     if (D <= 8192)
-        return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 1, VEC>, 1024, 1};
+        return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 1, ODD>, 1024, 1};
     if (D <= 16384)
-        return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 2, VEC>, 1024, 1};
-    return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 4, VEC>, 1024, 1};
+        return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 2, ODD>, 1024, 1};
+    return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 4, ODD>, 1024, 1};
 }
 
-Pick pick_forward(int64_t D, int xt, int bt, bool vec)
+Pick pick_forward(int64_t D, int xt, int bt)
 {
     return by_types(xt, bt, [&](auto X, auto B) -> Pick {
         constexpr int XT = decltype(X)::value, BT = decltype(B)::value;
-        return vec ? pick_forward_of<XT, BT, true>(D) : pick_forward_of<XT, BT, false>(D);
+        if constexpr (BT == tg::DT_F32)
+            return pick_forward_of<XT, BT, false>(D);
+        else
+            return D % 2 ? pick_forward_of<XT, BT, true>(D) : pick_forward_of<XT, BT, false>(D);
     });
 }
 
-// 512 threads in teams for rows up to 4096, two workgroups to a compute unit
-// (128 registers a thread; 256 where both types are fp32).
-template <int XT, int BT, bool VEC>
+// One workgroup to a compute unit: 1024 threads (128 registers each) in teams,
+// or 512 where both types are fp32, whose rows take twice the registers.
+template <int XT, int BT, bool ODD>
 Pick pick_backward_of(int64_t D)
 {
-    constexpr int W = XT == tg::DT_F32 && BT == tg::DT_F32 ? 2 : 4;
+    constexpr int NT = XT == tg::DT_F32 && BT == tg::DT_F32 ? 512 : 1024;
+    constexpr int W = NT / 256;  // waves to a SIMD
     if (D <= 512)
-        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 512, 64, 1, W, VEC>, 512, 1};
+        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, NT, 64, 1, W, ODD>, NT, 1};
     if (D <= 1024)
-        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 512, 128, 1, W, VEC>, 512, 1};
+        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, NT, 128, 1, W, ODD>, NT, 1};
     if (D <= 2048)
-        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 512, 256, 1, W, VEC>, 512, 1};
+        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, NT, 256, 1, W, ODD>, NT, 1};
     if (D <= 4096)
-        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 512, 512, 1, W, VEC>, 512, 1};
+        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, NT, 512, 1, W, ODD>, NT, 1};
     if (D <= 8192)
-        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 1024, 1024, 1, 4, VEC>, 1024, 1};
+        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 1024, 1024, 1, 4, ODD>, 1024, 1};
     if (D <= 16384)
-        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 1024, 1024, 2, 4, VEC>, 1024, 1};
-    return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 1024, 1024, 4, 4, VEC>, 1024, 1};
+        return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 1024, 1024, 2, 4, ODD>, 1024, 1};
+    return {(const void*)&tg::block_norm_grad_kernel<XT, BT, 1024, 1024, 4, 4, ODD>, 1024, 1};
 }
 
-Pick pick_backward(int64_t D, int xt, int bt, bool vec)
+Pick pick_backward(int64_t D, int xt, int bt)
 {
     return by_types(xt, bt, [&](auto X, auto B) -> Pick {
         constexpr int XT = decltype(X)::value, BT = decltype(B)::value;
-        return vec ? pick_backward_of<XT, BT, true>(D) : pick_backward_of<XT, BT, false>(D);
+        if constexpr (BT == tg::DT_F32)
+            return pick_backward_of<XT, BT, false>(D);
+        else
+            return D % 2 ? pick_backward_of<XT, BT, true>(D) : pick_backward_of<XT, BT, false>(D);
     });
 }
 
 bool bad_size(int64_t T, int64_t D) { return T < 0 || D < 0 || T > kMaxDim || D > kMaxD; }
 bool bad_stride(const void* p, int64_t ld, int64_t D) { return p && ld < D; }
-
-// Rows of the matrix start at 16-byte boundaries (or it is not there).
-bool at16(const void* p, int64_t ld, int esize)
-{
-    return !p || (((uintptr_t)p & 15) == 0 && ld * esize % 16 == 0);
-}
 
 // How the gradient kernel's workgroups share the rows, and the workspace.
 struct GradPlan {
@@ -121,10 +122,12 @@ struct GradPlan {
 GradPlan grad_plan(const tg_block_norm_grad_args& a)
 {
     GradPlan g{};
-    // About two workgroups to a compute unit, and at least 4 rows to each:
-    // fewer would write more partial sums than they save in time.
-    int64_t want = ceil_div(a.T, 512);
-    want = want < 4 ? 4 : want;
+    // One workgroup to a compute unit, and at least a row for each of its
+    // teams and two in all: with fewer, the partial sums would cost more than
+    // the rows.
+    const int64_t teams = a.D <= 512 ? 16 : (a.D <= 1024 ? 8 : (a.D <= 2048 ? 4 : 2));
+    int64_t want = ceil_div(a.T, 256);
+    want = want < teams ? teams : want;
     g.gate_rows = a.gate ? (a.gate_rows < a.T ? a.gate_rows : a.T) : a.T;
     g.groups = ceil_div(a.T, g.gate_rows);
     if (g.gate_rows <= want) {
@@ -223,10 +226,7 @@ tg_status tg_block_norm(const tg_block_norm_args* a, tg_stream_t stream)
     p.post = a->post_norm != 0;
     p.alpha = a->alpha;
     p.eps = a->eps;
-    const bool vec = D % 8 == 0 && at16(a->x, a->ldx, xs) && at16(a->y, a->ldy, bs) &&
-                     at16(a->gate, D, bs) && at16(a->w_post, D, bs) && at16(a->w_pre, D, bs) &&
-                     at16(a->x_out, a->ldx_out, xs) && at16(a->h, a->ldh, bs);
-    const Pick k = pick_forward(D, a->xtype, a->btype, vec);
+    const Pick k = pick_forward(D, a->xtype, a->btype);
     return tg::launch_kernel(k.kernel, ceil_div(T, k.rows), 1, k.threads, &p, (hipStream_t)stream,
                              "block_norm");
 }
@@ -312,11 +312,7 @@ tg_status tg_block_norm_backward(const tg_block_norm_grad_args* a, void* workspa
     p.Dp = (int)g.Dp;
     p.post = a->y && a->post_norm;
     p.alpha = a->alpha;
-    const bool vec = D % 8 == 0 && at16(a->x_new, a->ldx_new, xs) && at16(a->y, a->ldy, bs) &&
-                     at16(a->gate, D, bs) && at16(a->w_post, D, bs) && at16(a->w_pre, D, bs) &&
-                     at16(a->dx_new, a->lddx_new, xs) && at16(a->dh, a->lddh, bs) &&
-                     at16(a->dx, a->lddx, xs) && at16(a->dy, a->lddy, bs) && at16(a->dgate, D, 4);
-    const Pick k = pick_backward(D, a->xtype, a->btype, vec);
+    const Pick k = pick_backward(D, a->xtype, a->btype);
     if (tg_status s = tg::launch_kernel(k.kernel, g.P, 1, k.threads, &p, (hipStream_t)stream,
                                         "block_norm_grad"))
         return s;

@@ -1,8 +1,7 @@
 // Row operators (quantisation, norms): a team of threads holds one row in
 // registers, eight consecutive elements to a chunk, chunk c of thread t being
-// elements 8 (t + c * TPR) ...  Rows start at any element: chunks are moved
-// with 16-byte accesses of element alignment, which the hardware takes, and a
-// row's last chunk element by element.
+// elements 8 (t + c * TPR) ...  Rows start at any element: the hardware takes
+// 16-byte accesses at any address.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -132,15 +131,18 @@ __device__ __forceinline__ void store8(void* row, int at, int left, const Raw8<D
 }
 
 // One row of a matrix, through a buffer resource of the row: the lane's place is
-// one register for all rows and all matrices, and the hardware's range check
-// gives zeros past the end of the row, or from a matrix that is not there
-// (NULL), and drops stores there.  VEC: rows of whole chunks at 16-byte
-// boundaries; else the chunk across the end is moved element by element, and
-// chunks may start at any element.  The row number has to be uniform over the
-// wave.
-template <int DT, bool VEC>
+// one register for all rows and all matrices, chunks may start at any address,
+// and the hardware's range check, which looks at each dword of an access by
+// itself, gives zeros past the end of the row, or from a matrix that is not
+// there (NULL), and drops stores there.  ODD: rows with an odd number of
+// elements, whose last 16-bit element ends inside a dword and fails that check:
+// it is moved by an access of its own, in the lane that holds it.  No access
+// stands in a branch, so that all of a row's loads are in flight together.
+// The row number has to be uniform over the wave.
+template <int DT, bool ODD>
 struct Row {
     static constexpr int ES = DT == DT_F32 ? 4 : 2;
+    static constexpr bool LAST = ODD && DT != DT_F32;
     int n;
     __amdgpu_buffer_rsrc_t rs;
 
@@ -149,46 +151,39 @@ struct Row {
         n = base ? cols : 0;
         rs = make_rsrc((const char*)base + row * ld * ES, (u32)(n * ES));
     }
-    __device__ __forceinline__ bool across(int at) const
+    // Offset of the last element in the lane whose chunk (at `at`) holds it,
+    // out of range in the others; it is the low half of dword last_dword().
+    __device__ __forceinline__ u32 last_offset(int at) const
     {
-        return !VEC && at < n && at + 8 > n;
+        return (u32)(n - 1 - at) < 8u ? (u32)(n - 1) * 2u : kOob;
     }
+    __device__ __forceinline__ int last_dword() const { return ((n - 1) & 7) >> 1; }
+
     __device__ __forceinline__ void load(Raw8<DT>& r, int at) const
     {
         const u32 off = (u32)at * (u32)ES;
-        if (!across(at)) {
-            r.v[0] = buf_load16(rs, off);
-            if constexpr (DT == DT_F32)
-                r.v[1] = buf_load16(rs, off + 16u);
-        } else if constexpr (DT == DT_F32) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                r.v[i >> 2][i & 3] = buf_load4(rs, off + 4u * i);
-        } else {
+        r.v[0] = buf_load16(rs, off);
+        if constexpr (DT == DT_F32)
+            r.v[1] = buf_load16(rs, off + 16u);
+        if constexpr (LAST) {
+            const u32 e = buf_load2(rs, last_offset(at));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                r.v[0][i] = buf_load2(rs, off + 4u * i) | buf_load2(rs, off + 4u * i + 2u) << 16;
+                r.v[0][i] |= i == last_dword() ? e : 0u;
         }
     }
     __device__ __forceinline__ void store(const Raw8<DT>& r, int at) const
     {
         const int off = at * ES;
-        if (!across(at)) {
-            __builtin_amdgcn_raw_buffer_store_b128(r.v[0], rs, off, 0, 0);
-            if constexpr (DT == DT_F32)
-                __builtin_amdgcn_raw_buffer_store_b128(r.v[1], rs, off + 16, 0, 0);
-        } else if constexpr (DT == DT_F32) {
+        __builtin_amdgcn_raw_buffer_store_b128(r.v[0], rs, off, 0, 0);
+        if constexpr (DT == DT_F32)
+            __builtin_amdgcn_raw_buffer_store_b128(r.v[1], rs, off + 16, 0, 0);
+        if constexpr (LAST) {
+            u32 w = r.v[0][0];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const u32 w = r.v[i >> 2][i & 3];
-                __builtin_amdgcn_raw_buffer_store_b32(w, rs, off + 4 * i, 0, 0);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint16_t w = (uint16_t)(r.v[0][i >> 1] >> (16 * (i & 1)));
-                __builtin_amdgcn_raw_buffer_store_b16(w, rs, off + 2 * i, 0, 0);
-            }
+            for (int i = 1; i < 4; ++i)
+                w = i == last_dword() ? r.v[0][i] : w;
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)w, rs, (int)last_offset(at), 0, 0);
         }
     }
 };
