@@ -302,7 +302,8 @@ tg_status tg_quant_i8(int64_t M, int64_t K, tg_dtype dtype, const void* X, int64
  * The pages name low-bit GEMM workloads ("TileLang架构深度剖析", the performance
  * section) but not this format.
  * Errors: TG_ERR_BAD_DTYPE, TG_ERR_BAD_EPILOGUE, TG_ERR_BAD_SHAPE (also a
- *   stride below its row length, K > 131071), TG_ERR_NULL_POINTER,
+ *   stride below its row length, K > 131071, lda or ldw > 8388607),
+ *   TG_ERR_NULL_POINTER,
  *   TG_ERR_ALIAS (C overlaps an input), TG_ERR_HIP.
  */
 tg_status tg_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda,

@@ -51,6 +51,8 @@ def test_gemm_argument_errors(lib):
         assert gemm(lib, **{k: -1}) == SHAPE
         assert gemm(lib, **{k: 1 << 31}) == SHAPE
     assert gemm(lib, K=131072) == SHAPE  # 128 * 128 * K would leave 32 bits
+    assert gemm(lib, lda=1 << 23) == SHAPE  # 256 rows of a tile within 31 bits
+    assert gemm(lib, ldw=1 << 23) == SHAPE
     assert gemm(lib, lda=31) == SHAPE
     assert gemm(lib, ldw=31) == SHAPE
     assert gemm(lib, ldc=3) == SHAPE
@@ -64,6 +66,18 @@ def test_gemm_argument_errors(lib):
     assert gemm(lib, M=0, A=None, sa=None, C=None) == OK
     assert gemm(lib, N=0, W=None, sw=None, C=None) == OK
     assert gemm(lib, K=0, A=None, W=None, C=None) == NULLP
+
+
+def test_query_names_the_kernel():
+    q = lambda *a: binding.query_config(binding.TG_OP_I8, *a)
+    assert q(1, 8192, 8192).startswith("i8_gemv_16 grid=512x1 ")
+    assert q(4096, 4096, 4096).startswith("i8_256x256x128")
+    assert q(1000, 1001, 1003).startswith("i8_any_64x64")
+    assert q(0, 64, 64).startswith("i8_")
+    for bad, status in (((-1, 4, 4), SHAPE), ((4, 4, 131072), SHAPE), ((4, 4, 4, 9), DTYPE)):
+        with pytest.raises(binding.TileGemmError) as e:
+            q(*bad)
+        assert e.value.status == status
 
 
 def linear(lib, M=4, N=4, K=32, dt=BF16, X=P[0], ldx=None, W=P[1], ldw=None, sw=P[2], bias=None,

@@ -29,19 +29,36 @@ struct I8Params {
     unsigned long long* stamps;  // optional clock record, as in GemmParams
 };
 
-// 16 bytes of a row from any byte address, or the `left` (< 16, or <= 0)
-// bytes that the row still has and zeros after them.  The hardware takes
-// 16-byte global loads from any byte address.
-__device__ __forceinline__ u32x4 load16_any(const int8_t* p, int left)
+// v shifted down by s bytes (0 .. 16), zeros from above.
+__device__ __forceinline__ u32x4 shift_bytes(u32x4 v, int s)
+{
+    uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+    lo = s & 8 ? hi : lo;
+    hi = s & 8 ? 0 : hi;
+    const int b = (s & 7) * 8;
+    lo = b ? lo >> b | hi << (64 - b) : lo;
+    hi = hi >> b;
+    const bool none = s >= 16;
+    return u32x4{none ? 0u : (u32)lo, none ? 0u : (u32)(lo >> 32), none ? 0u : (u32)hi,
+                 none ? 0u : (u32)(hi >> 32)};
+}
+
+// 16 bytes of a row of K at k, from any address (the hardware takes 16-byte
+// loads at any byte), zeros past K.  A chunk across the end is the row's last
+// 16 bytes shifted down, so that it, too, is one load and no branch.
+__device__ __forceinline__ u32x4 load16_row(const int8_t* row, int k, int K)
 {
     struct __attribute__((packed, aligned(1))) Any {
         u32x4 v;
     };
-    if (left >= 16)
-        return ((const Any*)p)->v;
+    if (K >= 16) {
+        const int over = k - (K - 16);
+        const int s = over < 0 ? 0 : (over < 16 ? over : 16);
+        return shift_bytes(((const Any*)(row + (over < 0 ? k : K - 16)))->v, s);
+    }
     u32x4 v = {0, 0, 0, 0};
-    for (int i = 0; i < left; ++i)
-        v[i >> 2] |= (u32)(uint8_t)p[i] << (8 * (i & 3));
+    for (int i = 0; k + i < K; ++i)
+        v[i >> 2] |= (u32)(uint8_t)row[k + i] << (8 * (i & 3));
     return v;
 }
 

@@ -57,6 +57,8 @@ tg_status launch_quant(const tg::QuantParams& p, int dtype, hipStream_t stream)
     return tg::launch_kernel(k, ceil_div(p.M, rows), 1, threads, &q, stream, "quant_i8");
 }
 
+constexpr int64_t kMaxStride = kMaxDim / 256;  // of A and W: a tile's offsets fit 31 bits
+
 tg_status check_dims(int64_t M, int64_t N, int64_t K)
 {
     if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > tg::kMaxI8K)
@@ -87,6 +89,17 @@ struct I8Tile {
              (const void*)&tg::i8_dma_kernel<tg::DT_BF16, BM, BN, BK, WGM, WGN, NS, OCC>}, \
             BM, BN, WGM* WGN * 64, PER_CU, T0, ONE, FULL                                   \
     }
+// Kernels for any layout, smaller tiles first.
+#define TG_I8_ANY(BM, BN, PD)                                                  \
+    {                                                                          \
+        "i8_any_" #BM "x" #BN,                                                 \
+            {(const void*)&tg::i8_any_kernel<tg::DT_F32, BM, BN, PD>,          \
+             (const void*)&tg::i8_any_kernel<tg::DT_F16, BM, BN, PD>,          \
+             (const void*)&tg::i8_any_kernel<tg::DT_BF16, BM, BN, PD>},        \
+            BM, BN, 256, 0, 0.0f, 0.0f, 0.0f                                   \
+    }
+const I8Tile kAny[] = {TG_I8_ANY(64, 64, 4), TG_I8_ANY(128, 128, 1)};
+
 const I8Tile kTiles[] = {
     TG_I8_TILE(32, 64, 256, 1, 2, 4, 1, 1, 3.68f, 0.182f, 0.261f),
     TG_I8_TILE(64, 64, 128, 2, 2, 5, 2, 2, 3.26f, 0.230f, 0.498f),
@@ -106,8 +119,8 @@ float gemv_cost(int64_t M, int64_t N, int64_t K, int rows, float t0, float per)
 }
 
 struct I8Pick {
-    const I8Tile* tile;  // NULL: gemv (rows > 0) or the kernel for any layout
-    int rows;            // W rows of a gemv workgroup
+    const I8Tile* tile;  // NULL: the streaming kernel
+    int rows;            // W rows of its workgroup
 };
 
 // Up to 16 tokens: the streaming kernel, with 16 rows of W to a workgroup
@@ -115,14 +128,18 @@ struct I8Pick {
 // and 19.0).  Up to 128: whichever costs less, with 32 rows to a workgroup
 // (M = 32, 4096 x 4096: 8.2 us and 11.2; M = 32, 8192 x 8192: 26 and 19.8).
 // Above: the cheapest tile.  Rows that do not start at 16-byte boundaries, or
-// K % 16 != 0, leave the streaming kernel up to 64 tokens (it takes any
-// address) and i8_any_kernel.
+// K % 16 != 0, leave the streaming kernel, which takes any address, up to 32
+// tokens, and above them the kernels for any layout: 128 x 128 tiles where they
+// fill most of the card (1024 x 4096 x 4095: 39.7 us, more than 50 with 64 x
+// 64), else 64 x 64 (256 x 4096 x 4095: 24.3 us, more than 36 with 128 x 128).
 I8Pick pick_i8(int64_t M, int64_t N, int64_t K, bool aligned)
 {
     if (M <= 16)
         return {nullptr, 16};
+    if (!aligned && M <= 32)
+        return {nullptr, 32};
     if (!aligned)
-        return {nullptr, M <= 64 ? 32 : 0};
+        return {ceil_div(M, 128) * ceil_div(N, 128) > 160 ? &kAny[1] : &kAny[0], 0};
     float best = M <= 128 ? gemv_cost(M, N, K, 32, 3.23f, 1.335f) : 1e30f;
     I8Pick p{nullptr, 32};
     for (const I8Tile& t : kTiles) {
@@ -138,12 +155,9 @@ I8Pick pick_i8(int64_t M, int64_t N, int64_t K, bool aligned)
     return p;
 }
 
-// Rows that the LDS-DMA copies can take: whole 16-byte chunks, and a tile's
-// 256 rows within 31 bits of offset.
-bool dma_rows(const void* p, int64_t ld)
-{
-    return ((uintptr_t)p & 15) == 0 && ld % 16 == 0 && 256 * ld <= kMaxDim;
-}
+// Rows that the LDS-DMA copies can take: whole 16-byte chunks at 16-byte
+// boundaries.
+bool dma_rows(const void* p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && ld % 16 == 0; }
 
 tg_status launch_i8(tg::I8Params p, hipStream_t stream)
 {
@@ -151,23 +165,21 @@ tg_status launch_i8(tg::I8Params p, hipStream_t stream)
     const int es = tg::dtype_size(p.dt_out);
     const bool aligned = p.K > 0 && p.K % 16 == 0 && dma_rows(p.A, p.lda) && dma_rows(p.W, p.ldw);
     const I8Pick k = pick_i8(p.M, p.N, p.K, aligned);
-    if (k.rows > 0 && ceil_div(p.M, 16) <= 65535) {
+    if (!k.tile) {
         const int ng = k.rows / 16;
         return tg::launch_kernel(ng == 1 ? (const void*)&tg::i8_gemv_kernel<1, 1, 8>
                                          : (const void*)&tg::i8_gemv_kernel<2, 1, 8>,
                                  ceil_div(p.N, k.rows), ceil_div(p.M, 16), 512, &p, stream,
                                  "i8_gemv", 8 * ng * 1024);
     }
-    const int bm = k.tile ? k.tile->bm : tg::I8Any::BM, bn = k.tile ? k.tile->bn : tg::I8Any::BN;
     // Tile order: patches of 4 tile rows, as the 16-bit kernels' largest tiles.
     p.group_m = tg::swizzle_override() > 0 ? tg::swizzle_override() : 4;
-    p.tiles_m = (int)ceil_div(p.M, bm);
-    p.tiles_n = (int)ceil_div(p.N, bn);
+    p.tiles_m = (int)ceil_div(p.M, k.tile->bm);
+    p.tiles_n = (int)ceil_div(p.N, k.tile->bn);
     p.c_vec = ((uintptr_t)p.C & 15) == 0 && p.ldc * es % 16 == 0 && p.N * es % 16 == 0 &&
               32 * p.ldc * es <= kMaxDim;
-    return tg::launch_kernel(k.tile ? k.tile->kernel[p.dt_out] : (const void*)&tg::i8_any_kernel,
-                             (int64_t)p.tiles_m * p.tiles_n, 1, k.tile ? k.tile->threads : 256, &p,
-                             stream, k.tile ? k.tile->name : "i8_any");
+    return tg::launch_kernel(k.tile->kernel[p.dt_out], (int64_t)p.tiles_m * p.tiles_n, 1,
+                             k.tile->threads, &p, stream, k.tile->name);
 }
 
 // tg_linear_i8 in one launch: few tokens, and their levels fit the LDS kept
@@ -199,14 +211,12 @@ namespace tg {
 void describe_i8(int64_t M, int64_t N, int64_t K, char* buf, size_t len)
 {
     const I8Pick k = pick_i8(M, N, K, K > 0 && K % 16 == 0);
-    if (k.rows > 0)
+    if (!k.tile)
         snprintf(buf, len, "i8_gemv_%d grid=%lldx%lld threads=512", k.rows,
                  (long long)ceil_div(N, k.rows), (long long)ceil_div(M, 16));
     else
-        snprintf(buf, len, "%s grid=%lld threads=%d", k.tile ? k.tile->name : "i8_any",
-                 (long long)(ceil_div(M, k.tile ? k.tile->bm : I8Any::BM) *
-                             ceil_div(N, k.tile ? k.tile->bn : I8Any::BN)),
-                 k.tile ? k.tile->threads : 256);
+        snprintf(buf, len, "%s grid=%lld threads=%d", k.tile->name,
+                 (long long)(ceil_div(M, k.tile->bm) * ceil_div(N, k.tile->bn)), k.tile->threads);
 }
 
 }  // namespace tg
@@ -243,7 +253,7 @@ tg_status tg_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t l
         return TG_ERR_BAD_EPILOGUE;
     if (tg_status st = check_dims(M, N, K))
         return st;
-    if (lda < K || ldw < K || ldc < N)
+    if (lda < K || ldw < K || ldc < N || lda > kMaxStride || ldw > kMaxStride)
         return TG_ERR_BAD_SHAPE;
     if (M == 0 || N == 0)
         return TG_OK;
@@ -300,7 +310,7 @@ tg_status tg_linear_i8(int64_t M, int64_t N, int64_t K, tg_dtype dtype, const vo
     size_t need = 0;
     if (tg_status st = tg_linear_i8_workspace_size(M, N, K, dtype, &need))
         return st;
-    if (ldx < K || ldw < K || ldc < N)
+    if (ldx < K || ldw < K || ldc < N || ldw > kMaxStride)
         return TG_ERR_BAD_SHAPE;
     if (M == 0 || N == 0)
         return TG_OK;

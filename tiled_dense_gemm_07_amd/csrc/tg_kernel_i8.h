@@ -12,47 +12,15 @@
 // a fragment (16 bytes of one row for each lane) is the operand of
 // v_mfma_i32_32x32x32_i8, which does twice the 16-bit instruction's work.
 //
-// i8_any_kernel: any sizes, strides and addresses.  128 x 128 x 64 tiles, four
-// waves of 64 x 64; strips go through registers with 16-byte loads from any
-// byte address (row tails byte by byte) into a two-stage LDS ring.
+// i8_any_kernel: any sizes, strides and addresses (LDS-DMA copies want aligned
+// ones).  Strips of 128 bytes of k go through registers: 16-byte loads at any
+// byte, PD strips ahead, into a two-stage LDS ring.
 #pragma once
 
 #include "tg_i8.h"
 #include "tg_kernel_dma.h"
 
 namespace tg {
-
-// Results of one wave's FM x FN blocks of 32 x 32 straight from the
-// accumulators: lane l holds row l % 32 and, for element 4 q + e, column
-// 8 q + 4 (l / 32) + e of its block.
-template <int FM, int FN>
-__device__ __forceinline__ void i8_store_direct(const i32x16 (&acc)[FM][FN], const I8Params& p,
-                                                int mw0, int nw0, int lane)
-{
-    const int lr = lane & 31;
-    const int g = lane >> 5;
-#pragma unroll
-    for (int fm = 0; fm < FM; ++fm) {
-        const int m = mw0 + fm * 32 + lr;
-        if (m >= p.M)
-            continue;
-        const float sa = p.sa[m];
-#pragma unroll
-        for (int fn = 0; fn < FN; ++fn) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int n = nw0 + fn * 32 + 8 * q + 4 * g;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (n + e < p.N)
-                        store_out(p.C, p.dt_out, (int64_t)m * p.ldc + n + e,
-                                  i8_result(acc[fm][fn][4 * q + e], sa, p.sw[n + e],
-                                            p.bias ? p.bias[n + e] : 0.0f, p.relu));
-                }
-            }
-        }
-    }
-}
 
 // Results of one wave's FM x FN blocks through its own LDS region `st` (32
 // rows of FN * 32 results), 32 rows at a time: scaled, rounded, written as
@@ -148,105 +116,139 @@ __device__ __forceinline__ void i8_store_staged(const i32x16 (&acc)[FM][FN], con
     }
 }
 
+// BM x BN tiles, four waves in a 2 x 2 grid.  PD: strips whose loads are in
+// flight or in registers.  One barrier for each strip: a strip is written to
+// the stage that the strip two before it used, which every wave has read by the
+// barrier of the strip between them.
+template <int DT, int BM, int BN, int PD>
 struct I8Any {
-    static constexpr int BM = 128, BN = 128, BK = 64;
+    static constexpr int BK = 128;
+    static constexpr int WTM = BM / 2, WTN = BN / 2;
+    static constexpr int FM = WTM / 32, FN = WTN / 32;
+    static constexpr int JA = BM / 32, JB = BN / 32;  // chunks of a thread and strip
     static constexpr int STAGE = (BM + BN) * BK;
+
+    struct Strip {
+        u32x4 a[JA], b[JB];
+    };
 
     static __device__ __forceinline__ void run(const I8Params& p)
     {
-        __shared__ __attribute__((aligned(16))) char smem[2 * STAGE];
+        __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
         lds_char* sm = (lds_char*)smem;
         const int tid = threadIdx.x;
         const int lane = tid & 63;
-        const int w = tid >> 6;
+        const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
         const TileCoord tc = tile_of(blockIdx.x, p.tiles_m, p.tiles_n, p.group_m);
         const int m0 = tc.m * BM, n0 = tc.n * BN;
-        const int wm0 = (w >> 1) * 64, wn0 = (w & 1) * 64;
+        const int wm0 = (w >> 1) * WTM, wn0 = (w & 1) * WTN;
 
-        // thread t moves chunk t % 4 of rows t / 4 and t / 4 + 64 of each
-        // operand; rows past the end read the last row (their results are
-        // not stored)
-        const int c = tid & 3;
-        const int8_t* a[2];
-        const int8_t* b[2];
-        u32 st[2];
+        // thread t moves chunk t % 8 of rows t / 8 + 32 j; rows past the end
+        // read the last row again (their results are not stored)
+        const int c = tid & 7;
+        const int8_t *a[JA], *b[JB];
+        u32 st[JA > JB ? JA : JB];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = (tid >> 2) + 64 * j;
-            const int am = m0 + r < p.M ? m0 + r : p.M - 1;
-            const int bn = n0 + r < p.N ? n0 + r : p.N - 1;
-            a[j] = p.A + (int64_t)am * p.lda;
-            b[j] = p.W + (int64_t)bn * p.ldw;
-            st[j] = r * BK + ((c ^ swz_a(r)) << 4);
+        for (int j = 0; j < (JA > JB ? JA : JB); ++j) {
+            const int r = (tid >> 3) + 32 * j;
+            st[j] = r * BK + ((c ^ swz8(r)) << 4);
+            if (j < JA)
+                a[j] = p.A + (int64_t)(m0 + r < p.M ? m0 + r : p.M - 1) * p.lda;
+            if (j < JB)
+                b[j] = p.W + (int64_t)(n0 + r < p.N ? n0 + r : p.N - 1) * p.ldw;
         }
-        u32x4 ra[2], rb[2];
-        const auto load = [&](int k0) {
-            const int k = k0 + 16 * c;
+        const auto load = [&](Strip& s, int t) {
+            struct __attribute__((packed, aligned(1))) Any {
+                u32x4 v;
+            };
+            const int k = t * BK + 16 * c;
+            if ((t + 1) * BK <= p.K) {  // uniform
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                ra[j] = load16_any(a[j] + k, p.K - k);
-                rb[j] = load16_any(b[j] + k, p.K - k);
+                for (int j = 0; j < JA; ++j)
+                    s.a[j] = ((const Any*)(a[j] + k))->v;
+#pragma unroll
+                for (int j = 0; j < JB; ++j)
+                    s.b[j] = ((const Any*)(b[j] + k))->v;
+            } else if (t * BK < p.K) {
+#pragma unroll
+                for (int j = 0; j < JA; ++j)
+                    s.a[j] = load16_row(a[j], k, p.K);
+#pragma unroll
+                for (int j = 0; j < JB; ++j)
+                    s.b[j] = load16_row(b[j], k, p.K);
             }
         };
-        const auto store = [&](int s) {
+        i32x16 acc[FM][FN];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                *(lds_u32x4*)(sm + s * STAGE + st[j]) = ra[j];
-                *(lds_u32x4*)(sm + s * STAGE + BM * BK + st[j]) = rb[j];
-            }
-        };
-        i32x16 acc[2][2];
+        for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < FN; ++j)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
                     acc[i][j][r] = 0;
 
         const int KT = (p.K + BK - 1) / BK;
-        if (KT > 0) {
-            load(0);
-            store(0);
-        }
-        for (int t = 0; t < KT; ++t) {
-            if (t + 1 < KT)
-                load((t + 1) * BK);
-            // strip t is in stage t & 1, and every wave is done with strip
-            // t - 1, whose stage strip t + 1 takes below
-            __syncthreads();
-            const lds_char* s0 = sm + (t & 1) * STAGE;
+        Strip S[PD];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                i32x4 fa[2], fb[2];
+        for (int j = 0; j < PD; ++j)
+            load(S[j], j);
+        for (int t0 = 0; t0 < KT; t0 += PD) {
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const int rm = wm0 + 32 * f + (lane & 31);
-                    const int rn = wn0 + 32 * f + (lane & 31);
+            for (int j = 0; j < PD; ++j) {
+                const int t = t0 + j;
+                if (t >= KT)
+                    break;  // uniform
+                lds_char* stage = sm + (t & 1) * STAGE;
+#pragma unroll
+                for (int i = 0; i < JA; ++i)
+                    *(lds_u32x4*)(stage + st[i]) = S[j].a[i];
+#pragma unroll
+                for (int i = 0; i < JB; ++i)
+                    *(lds_u32x4*)(stage + BM * BK + st[i]) = S[j].b[i];
+                load(S[j], t + PD);
+                // the LDS writes of all waves, but not the loads in flight
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+                for (int s = 0; s < BK / 32; ++s) {
+                    i32x4 fa[FM], fb[FN];
                     const int ch = 2 * s + (lane >> 5);
-                    fa[f] = __builtin_bit_cast(
-                        i32x4, *(const lds_u32x4*)(s0 + rm * BK + ((ch ^ swz_a(rm)) << 4)));
-                    fb[f] = __builtin_bit_cast(
-                        i32x4,
-                        *(const lds_u32x4*)(s0 + BM * BK + rn * BK + ((ch ^ swz_a(rn)) << 4)));
+#pragma unroll
+                    for (int f = 0; f < FM; ++f) {
+                        const int r = wm0 + 32 * f + (lane & 31);
+                        fa[f] = __builtin_bit_cast(
+                            i32x4, *(const lds_u32x4*)(stage + r * BK + ((ch ^ swz8(r)) << 4)));
+                    }
+#pragma unroll
+                    for (int f = 0; f < FN; ++f) {
+                        const int r = wn0 + 32 * f + (lane & 31);
+                        fb[f] = __builtin_bit_cast(
+                            i32x4, *(const lds_u32x4*)(stage + BM * BK + r * BK +
+                                                       ((ch ^ swz8(r)) << 4)));
+                    }
+#pragma unroll
+                    for (int i = 0; i < FM; ++i)
+#pragma unroll
+                        for (int k = 0; k < FN; ++k)
+                            acc[i][k] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[k], fa[i],
+                                                                             acc[i][k], 0, 0, 0);
                 }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j], fa[i], acc[i][j],
-                                                                         0, 0, 0);
             }
-            if (t + 1 < KT)
-                store((t + 1) & 1);
         }
-        i8_store_direct<2, 2>(acc, p, m0 + wm0, n0 + wn0, lane);
+        __syncthreads();  // the last strips' reads, before the results take their place
+        constexpr int ES = DT == DT_F32 ? 4 : 2;
+        static_assert(4 * 32 * WTN * ES <= 2 * STAGE, "a 32-row stripe for each wave");
+        i8_store_staged<DT, FM, FN>(acc, p, m0 + wm0, n0 + wn0, lane, sm + w * (32 * WTN * ES));
     }
 };
 
+template <int DT, int BM, int BN, int PD>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void i8_any_kernel(I8Params p)
 {
-    I8Any::run(p);
+    GemmParams rec{};
+    rec.stamps = p.stamps;
+    const ClockStamp clk = stamp_begin(rec);
+    I8Any<DT, BM, BN, PD>::run(p);
+    stamp_end(rec, clk);
 }
 
 // BM x BN tiles, strips of BK bytes of k, NS LDS stages, WGM x WGN waves.

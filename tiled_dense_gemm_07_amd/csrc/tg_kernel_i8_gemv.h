@@ -10,8 +10,8 @@
 //  * The loads of a wave's next run are issued before the MFMAs of this one.
 //  * The waves' integer sums are added in LDS.
 //  * Rows past M or N read the last row again; their results are not stored.
-//    Any addresses and strides: 16-byte loads at any byte, and the last,
-//    partial run of a row is loaded with its tail bytes masked to zero.
+//    Any addresses and strides: 16-byte loads at any byte, zeros past the end
+//    of a row in its last, partial run.
 //  * FUSED (tg_linear_i8): A is given in 16 or 32 bits.  Every workgroup
 //    quantises the M rows itself, into LDS, while the loads of its first run
 //    of W are in flight: one launch instead of two, for as few rows as that
@@ -53,7 +53,7 @@ struct I8Gemv {
         struct __attribute__((packed, aligned(1))) Any {
             u32x4 v;
         };
-        return whole ? ((const Any*)(row + k))->v : load16_any(row + k, K - k);
+        return whole ? ((const Any*)(row + k))->v : load16_row(row, k, K);
     }
 
     static __device__ __forceinline__ void load(Run& R, const int8_t* const (&w)[NG],
