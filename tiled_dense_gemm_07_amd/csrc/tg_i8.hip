@@ -66,8 +66,6 @@ tg_status check_dims(int64_t M, int64_t N, int64_t K)
     return TG_OK;
 }
 
-constexpr int64_t kFusedTokens = 4;
-
 // The LDS-DMA kernels, and what one costs on this card in microseconds with
 // its weights from HBM: t0 + strips of 128 k times `one` when every workgroup
 // has a compute unit to itself, else times `full` for each round of 256 per_cu
@@ -182,12 +180,16 @@ tg_status launch_i8(tg::I8Params p, hipStream_t stream)
                              k.tile->threads, &p, stream, k.tile->name);
 }
 
-// tg_linear_i8 in one launch: few tokens, and their levels fit the LDS kept
-// for them.
+// tg_linear_i8 in one launch: up to 8 tokens (a wave or more to a row), whose
+// quantisation in every workgroup takes less than a launch of its own would.
+// Measured with both launches and with one, N = 1024 to 8192: 8 x 1024 5.7 us
+// and 3.9, 8 x 2048 6.2 and 5.4, 4 x 4096 7.6 and 7.3, 8 x 4096 7.8 and 9.7, 2
+// x 8192 16.5 and 16.5, 4 x 8192 16.7 and 19.9; rows count as their power of
+// two.
 bool fused_linear(int64_t M, int64_t K)
 {
-    return M <= kFusedTokens && K > 0 &&
-           M * tg::I8Gemv<tg::DT_BF16, 1, 1, 8, true>::level_row((int)K) <= tg::kGemvLevels;
+    const int64_t rows = M <= 1 ? 1 : (M <= 2 ? 2 : (M <= 4 ? 4 : 8));
+    return M <= 8 && K > 0 && rows * K <= 16384;
 }
 
 tg_status launch_fused(const tg::I8Params& p, int dtype, const void* X, int64_t ldx,

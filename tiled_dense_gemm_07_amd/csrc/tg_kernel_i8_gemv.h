@@ -29,8 +29,6 @@ struct I8Source {
     int64_t ldx;
 };
 
-constexpr int kGemvLevels = 64 * 1024;  // LDS for the levels of the fused form
-
 template <int DTX, int NG, int MT, int NW, bool FUSED>
 struct I8Gemv {
     static constexpr int RUN = 256;
@@ -96,8 +94,8 @@ struct I8Gemv {
         }
     }
 
-    // Quantises the M rows of X into `levels` (rows of `ld` bytes, zeros past
-    // K), their scales into sc.  NW / R waves to a row, R the power of two
+    // Quantises the M <= NW rows of X into `levels` (rows of `ld` bytes, zeros
+    // past K), their scales into sc.  NW / R waves to a row, R the power of two
     // that is at least M.
     static __device__ __forceinline__ void quantise(const I8Params& p, const I8Source& x,
                                                     char* levels, float* sc, u32* amax, int ld)
