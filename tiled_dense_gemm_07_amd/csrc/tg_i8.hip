@@ -18,9 +18,12 @@ using tg::overlap;
 using tg::span;
 using tg::span1;
 
-// Kernel for rows of K elements: one wave for a row, four waves, or sixteen,
-// with 1, 2 or 4 chunks of 8 elements for each thread.
-// ODD: 16-bit rows of an odd length.
+// Kernel for rows of K elements: a row to one wave, or to a workgroup of four,
+// eight or sixteen, the fewest threads whose registers hold it (bf16, 8192
+// rows: K = 1024 5.3 us with two chunks a lane of one wave, 8.6 with one chunk a
+// thread of four; K = 4096 16.8 with two of four waves, 17.7 with one of eight;
+// K = 8192 30.7 with two of eight, 34.2 with one of sixteen).  ODD: 16-bit rows
+// of an odd length.
 template <int DT, bool ODD>
 const void* quant_kernel(int64_t K, int* threads, int* rows)
 {
@@ -28,12 +31,15 @@ const void* quant_kernel(int64_t K, int* threads, int* rows)
     *rows = K <= 2048 ? 4 : 1;
     if (K <= 512)
         return (const void*)&tg::quant_i8_kernel<DT, 256, 64, 1, ODD>;
+    if (K <= 1024)
+        return (const void*)&tg::quant_i8_kernel<DT, 256, 64, 2, ODD>;
     if (K <= 2048)
         return (const void*)&tg::quant_i8_kernel<DT, 256, 64, 4, ODD>;
     if (K <= 4096)
         return (const void*)&tg::quant_i8_kernel<DT, 256, 256, 2, ODD>;
+    *threads = 512;
     if (K <= 8192)
-        return (const void*)&tg::quant_i8_kernel<DT, 256, 256, 4, ODD>;
+        return (const void*)&tg::quant_i8_kernel<DT, 512, 512, 2, ODD>;
     *threads = 1024;
     if (K <= 32768)
         return (const void*)&tg::quant_i8_kernel<DT, 1024, 1024, 4, ODD>;

@@ -43,18 +43,27 @@ struct Pick {
     int rows;     // of a workgroup
 };
 
+// A row to one wave, or to a workgroup of four, eight or sixteen.  Measured
+// (bf16, h and 8-bit h, 8192 rows; 4096 of D = 8192): D = 1024 11.4 and 12.2 us
+// with two chunks a lane of one wave, 14.8 and 18.1 with one chunk a thread of
+// four; D = 2048 20.9 and 21.2 with four of one wave, 21.0 and 22.0 with one of
+// four (2.9 and 2.6 us for one row); D = 4096 39.5 and 37.0 with two of four,
+// 39.2 and 40.0 with one of eight; D = 8192 39.7 and 38.1 with two of eight, 40.6
+// and 43.2 with one of sixteen.
 // ODD: rows with an odd number of elements, some of them of 16 bits.
 template <int XT, int BT, bool ODD>
 Pick pick_forward_of(int64_t D)
 {
     if (D <= 512)
         return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 64, 1, ODD>, 256, 4};
+    if (D <= 1024)
+        return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 64, 2, ODD>, 256, 4};
     if (D <= 2048)
         return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 256, 1, ODD>, 256, 1};
     if (D <= 4096)
         return {(const void*)&tg::block_norm_kernel<XT, BT, 256, 256, 2, ODD>, 256, 1};
     if (D <= 8192)
-        return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 1, ODD>, 1024, 1};
+        return {(const void*)&tg::block_norm_kernel<XT, BT, 512, 512, 2, ODD>, 512, 1};
     if (D <= 16384)
         return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 2, ODD>, 1024, 1};
     return {(const void*)&tg::block_norm_kernel<XT, BT, 1024, 1024, 4, ODD>, 1024, 1};
