@@ -354,7 +354,8 @@ tg_status tg_linear_i8_workspace_size(int64_t M, int64_t N, int64_t K, tg_dtype 
  * Sums and intermediate values are fp32; x_out is rounded to xtype, and h is
  * computed from the rounded x_out, so that the call equals one that computes
  * x_out and one that computes h from it, bit for bit.
- * D <= 32768.  T == 0 or D == 0: nothing is launched.
+ * D <= 32768, T <= 2^30.  T == 0 or D == 0: nothing is launched.  A row of
+ * zeros with eps 0 has no norm (NaN).
  * Errors: TG_ERR_BAD_DTYPE, TG_ERR_BAD_SHAPE (sizes, strides below D,
  *   gate_rows < 1 with a gate), TG_ERR_NULL_POINTER (x, or nothing to write,
  *   or hq without hs or the reverse, x_out NULL with y), TG_ERR_BAD_LAYOUT (x_out, gate, w_post
@@ -402,7 +403,7 @@ tg_status tg_block_norm(const tg_block_norm_args* args, tg_stream_t stream);
  *     tg_block_norm_backward_workspace_size reports for the same arguments; it
  *     holds partial sums.  Its contents need not be kept; calls that share it must not run
  *     concurrently.
- * D <= 32768.  T == 0: dgate, dw_post and dw_pre are not written.
+ * D <= 32768, T <= 2^30.  T == 0: dgate, dw_post and dw_pre are not written.
  * Errors: as tg_block_norm; TG_ERR_NULL_POINTER also when an input that an
  *   output needs is NULL (x_new and r_pre with dh, r_post with post_norm) or
  *   when nothing is to be written; TG_ERR_BAD_LAYOUT also for dy, dgate, dw_post without
@@ -520,8 +521,8 @@ tg_status tg_tile_map(int64_t tiles_m, int64_t tiles_n, int group_m, int32_t* ou
  * GEMM's speed against the theoretical ceiling first; on a power-limited card
  * that ceiling moves with the shader clock, so a benchmark needs the clock the
  * kernel actually ran at.  With `stamps` set (a DEVICE pointer to 32 uint64,
- * caller-owned, NULL to switch off), every kernel launched afterwards by any
- * entry point has wave 0 of its workgroups 0..7 (one per XCD) write
+ * caller-owned, NULL to switch off), every matrix-product kernel launched
+ * afterwards by any entry point has wave 0 of its workgroups 0..7 (one per XCD) write
  * stamps[4 b + 0..3] = shader-clock counter and 100 MHz reference counter at
  * its start, then the same at its end (workgroups b < 8 only; a grid of fewer
  * workgroups leaves the rest untouched).  Each launch overwrites the previous

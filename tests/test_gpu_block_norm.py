@@ -4,6 +4,8 @@ shared and per-token gates, left-out operands, special rows, streams, graphs."""
 
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -336,6 +338,34 @@ def test_backward_strides():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("gate_rows", [1, 30, 100])
+def test_backward_workspace_contents_do_not_matter(gate_rows):
+    T, D = 100, 200
+    s = operands(T, D, BF16, BF16, gate_rows, True, 5)
+    f = binding.block_norm(s["x"], y=s["y"], gate=s["gate"], gate_rows=gate_rows,
+                           w_post=s["w_post"], w_pre=s["w_pre"], eps=EPS, save=True)
+    want = run_backward(s, f, BF16, BF16, gate_rows, 1.0, True)
+    a = binding.BlockNormGradArgs()
+    one = 0x1000  # sizes depend on which operands are there, not on where
+    a.T, a.D, a.xtype, a.btype, a.gate_rows, a.post_norm = T, D, BF16, BF16, gate_rows, 1
+    for k in ("y", "gate", "dgate", "dw_post", "dw_pre"):
+        setattr(a, k, one)
+    a.ldy = D
+    n = ctypes.c_size_t()
+    assert binding.load_library().tg_block_norm_backward_workspace_size(ctypes.byref(a),
+                                                                        ctypes.byref(n)) == 0
+    ws = torch.full((n.value + 512,), 0xFF, dtype=torch.uint8, device=DEV)  # NaN
+    say("block_norm_backward workspace gate_rows=%d" % gate_rows)
+    got = binding.block_norm_backward(
+        f.x, s["dx_new"], s["dh"], y=s["y"], gate=s["gate"], gate_rows=gate_rows,
+        w_post=s["w_post"], w_pre=s["w_pre"], r_post=f.r_post, r_pre=f.r_pre,
+        workspace=ws[:n.value])
+    torch.cuda.synchronize()
+    for u, v in zip(want, got):
+        assert torch.equal(u, v)
+    assert bool((ws[n.value:] == 0xFF).all())
+
+
 def test_refusals():
     x = torch.zeros((6, 32), dtype=torch.bfloat16, device=DEV)
     for y in (x.float(), x.half()):  # pairs of types that are not offered
@@ -396,3 +426,36 @@ def test_stream_and_graph():
         again = both(sets[2 - i])
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(again, want[2 - i]))
+
+
+def test_offsets_past_31_bits():
+    """Rows beyond 2^31 bytes of every matrix: the last rows have the bits of
+    a call on them alone, and sums over all rows those of a plain sum."""
+    T, D = 300000, 4096  # 2.4 GB a matrix
+    g = torch.Generator(device=DEV)
+    g.manual_seed(2)
+    x = torch.randn((T, D), dtype=torch.bfloat16, device=DEV, generator=g)
+    y = torch.randn((T, D), dtype=torch.bfloat16, device=DEV, generator=g)
+    gate = torch.randn((3, D), dtype=torch.bfloat16, device=DEV, generator=g)
+    w = torch.ones(D, dtype=torch.bfloat16, device=DEV)
+    say("block_norm %dx%d" % (T, D))
+    f = binding.block_norm(x, y=y, gate=gate, gate_rows=100000, w_post=w, w_pre=w, save=True)
+    e = binding.block_norm(x[-64:], y=y[-64:], gate=gate[2:], w_post=w, w_pre=w)
+    torch.cuda.synchronize()
+    assert torch.equal(f.x[-64:], e.x) and torch.equal(f.h[-64:], e.h)
+    say("block_norm_backward %dx%d" % (T, D))
+    b = binding.block_norm_backward(f.x, x, y, y=y, gate=gate, gate_rows=100000, w_post=w, w_pre=w,
+                                    r_post=f.r_post, r_pre=f.r_pre)
+    c = binding.block_norm_backward(f.x[-64:], x[-64:], y[-64:], y=y[-64:], gate=gate[2:],
+                                    w_post=w, w_pre=w, r_post=f.r_post[-64:], r_pre=f.r_pre[-64:])
+    torch.cuda.synchronize()
+    assert torch.equal(b.dx[-64:], c.dx) and torch.equal(b.dy[-64:], c.dy)
+    u = torch.zeros(D, dtype=torch.float64, device=DEV)
+    mag = torch.zeros_like(u)
+    for at in range(0, T, 20000):
+        t = y[at:at + 20000].double() * f.x[at:at + 20000].double() * f.r_pre[at:at + 20000, None]
+        u += t.sum(0)
+        mag += t.abs().sum(0)
+    # the longest chain: a workgroup's rows, the partial rows of a lane, and the last sums
+    chain = T // 256 + 256 // 32 + 48
+    assert bool(((b.dw_pre - u).abs() <= chain * ref.U32 * mag).all())

@@ -318,6 +318,23 @@ def test_linear_equals_its_parts(M, N, K, dtype):
                       sw.cpu().numpy(), b.cpu().numpy(), dtype, True)
 
 
+def test_linear_workspace_contents_do_not_matter():
+    """A workspace of the reported size, full of other bytes; the bytes after it
+    stay."""
+    M, N, K = 40, 96, 1000
+    x = torch.randn((M, K), device=DEV, dtype=torch.bfloat16)
+    _, _, W, sw, b = make_product(1, N, K, 3)
+    W, sw, b = dev(W), dev(sw), dev(b)
+    want = binding.linear_i8(x, W, sw, bias=b)
+    need = binding.linear_i8_workspace_size(M, N, K, BF16)
+    for fill in (0xFF, 0x7F):
+        ws = torch.full((need + 512,), fill, dtype=torch.uint8, device=DEV)
+        say("linear_i8 workspace of %02x" % fill)
+        got = binding.linear_i8(x, W, sw, bias=b, workspace=ws[:need])
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and bool((ws[need:] == fill).all())
+
+
 def test_linear_rows_that_are_not_finite():
     for M in (1, 5, 40, 300):
         x = torch.randn((M, 512), device=DEV, dtype=torch.bfloat16)
@@ -361,3 +378,32 @@ def test_stream_and_graph(M, N, K):
         torch.cuda.synchronize()
         assert torch.equal(C, want[i])
         assert torch.equal(binding.linear_i8(xs[2 - i], W, sw, bias=b), want[2 - i])
+
+
+@pytest.mark.parametrize("K", [4096, 4095])
+def test_offsets_past_31_bits(K):
+    """Operands and results beyond 2^31 bytes: the last rows have the bits of a
+    call on them alone."""
+    M, N = 540000, 2056  # A 2.2 GB, C 2.2 GB
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    A = torch.randint(-127, 128, (M, K), dtype=torch.int8, device=DEV, generator=g)
+    W = torch.randint(-127, 128, (N, K), dtype=torch.int8, device=DEV, generator=g)
+    sa = torch.rand(M, device=DEV, generator=g)
+    sw = torch.rand(N, device=DEV, generator=g)
+    say("gemm_i8 %dx%dx%d" % (M, N, K))
+    C = binding.gemm_i8(A, sa, W, sw)
+    torch.cuda.synchronize()
+    assert M * K > 1 << 31 and C.numel() * 2 > 1 << 31
+    for at in (M - 300, (1 << 31) // K - 150):
+        part = binding.gemm_i8(A[at:at + 300], sa[at:at + 300], W, sw)
+        torch.cuda.synchronize()
+        assert torch.equal(part, C[at:at + 300])
+    del C
+    x = A[:300000].to(torch.bfloat16)
+    say("quant_i8 %dx%d" % tuple(x.shape))
+    Q, S = binding.quant_i8(x)
+    torch.cuda.synchronize()
+    q, s = binding.quant_i8(x[-100:])
+    torch.cuda.synchronize()
+    assert torch.equal(Q[-100:], q) and torch.equal(S[-100:], s)

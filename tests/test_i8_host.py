@@ -137,6 +137,7 @@ def test_norm_argument_errors(lib):
     assert f(xtype=BF16, btype=F16) == DTYPE
     assert f(xtype=BF16, btype=F32) == DTYPE
     assert f(T=-1) == SHAPE
+    assert f(T=(1 << 30) + 1) == SHAPE
     assert f(D=-1) == SHAPE
     assert f(D=32769) == SHAPE
     assert f(gate_rows=0) == SHAPE

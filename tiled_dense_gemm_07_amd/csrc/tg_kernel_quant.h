@@ -49,9 +49,9 @@ __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void quant_i8_ke
 {
     __shared__ u32 slot[16];
     const int t = threadIdx.x % TPR;
-    const int row = (int)blockIdx.x * (NT / TPR) +
-                    __builtin_amdgcn_readfirstlane((int)(threadIdx.x / TPR));
-    if (row >= p.M)
+    const u32 row =
+        blockIdx.x * (NT / TPR) + (u32)__builtin_amdgcn_readfirstlane((int)(threadIdx.x / TPR));
+    if (row >= (u32)p.M)
         return;  // whole waves; rows share a workgroup only when TPR is one wave
     const Row<DT, ODD> x(p.X, row, p.ldx, p.K);
     int8_t* q = p.Q + row * p.ldq;

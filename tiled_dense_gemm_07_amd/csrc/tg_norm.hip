@@ -8,13 +8,13 @@
 namespace {
 
 using tg::ceil_div;
-using tg::kMaxDim;
 using tg::overlap;
 using tg::Span;
 using tg::span;
 using tg::span1;
 
-constexpr int64_t kMaxD = 32768;
+constexpr int64_t kMaxD = 32768;    // a row's registers: 1024 threads of 32 elements
+constexpr int64_t kMaxT = 1 << 30;  // sums of two row numbers fit 31 bits
 
 bool types_ok(int xt, int bt)
 {
@@ -113,7 +113,7 @@ Pick pick_backward(int64_t D, int xt, int bt)
     });
 }
 
-bool bad_size(int64_t T, int64_t D) { return T < 0 || D < 0 || T > kMaxDim || D > kMaxD; }
+bool bad_size(int64_t T, int64_t D) { return T < 0 || D < 0 || T > kMaxT || D > kMaxD; }
 bool bad_stride(const void* p, int64_t ld, int64_t D) { return p && ld < D; }
 
 // How the gradient kernel's workgroups share the rows, and the workspace.
