@@ -199,6 +199,17 @@ def _epi_code(epilogue) -> int:
 
 
 _raw_stream = None
+_torch_module = None
+
+
+def _torch():
+    """The torch module (a third of an import statement's time in a hot call)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_ptr(device, stream=None):
@@ -554,8 +565,7 @@ def _empty(shape, dtype, like, stream):
     """An output or workspace on like's device that belongs to the call's stream."""
     if stream is None:
         return like.new_empty(shape, dtype=dtype)
-    import torch
-
+    torch = _torch()
     with torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
 
@@ -564,16 +574,14 @@ def _empty_as(t, stream):
     """An output of t's shape and type, dense."""
     if stream is not None or not t.is_contiguous():
         return _empty(t.shape, t.dtype, t, stream)
-    import torch
-
+    torch = _torch()
     return torch.empty_like(t)
 
 
 def quant_i8(X, Q=None, s=None, stream=None):
     """Rows of X to 8-bit levels and one fp32 scale each (tg_quant_i8): returns
     (Q int8 [M, K], s fp32 [M]) with X about Q * s[:, None]."""
-    import torch
-
+    torch = _torch()
     ldx = _rows("X", X)
     M, K = X.shape
     if Q is None:
@@ -592,8 +600,7 @@ def gemm_i8(A, sa, W, sw, bias=None, out_dtype=None, C=None, epilogue=None, stre
     """C = epilogue((A @ W^T) * sa[:, None] * sw + bias) with A [M, K] and W
     [N, K] in int8, fp32 scales sa [M] and sw [N], fp32 bias [N] or None; C
     [M, N] of out_dtype (bfloat16 unless C or out_dtype says otherwise)."""
-    import torch
-
+    torch = _torch()
     i8, f32 = torch.int8, torch.float32
     lda = _rows("A", A, None, i8)
     ldw = _rows("W", W, None, i8)
@@ -628,8 +635,7 @@ def linear_i8(X, W, sw, bias=None, C=None, epilogue=None, workspace=None, stream
     :func:`gemm_i8` one after the other; C [M, N] of X's dtype.  workspace: a
     uint8 device tensor of at least :func:`linear_i8_workspace_size` bytes
     (allocated here when None and needed)."""
-    import torch
-
+    torch = _torch()
     f32 = torch.float32
     ldx = _rows("X", X)
     ldw = _rows("W", W, None, torch.int8)
@@ -692,8 +698,7 @@ def block_norm(x, y=None, gate=None, gate_rows=None, w_post=None, w_pre=None, al
     only).  x_out may be x.  save: also return the norms' reciprocal roots
     for :func:`block_norm_backward`.  Returns a BlockNorm(x, h, hs, r_post,
     r_pre)."""
-    import torch
-
+    torch = _torch()
     if out not in ("h", "i8", None):
         raise ValueError("out must be 'h', 'i8' or None")
     ldx = _rows("x", x)
@@ -751,8 +756,7 @@ def block_norm_backward(x_new, dx_new=None, dh=None, y=None, gate=None, gate_row
     r_pre are the forward call's x, r_post and r_pre.  Returns a
     BlockNormGrad(dx, dy, dgate, dw_post, dw_pre), dx and dy in their inputs'
     types, the rest (None where there is no such input) in fp32."""
-    import torch
-
+    torch = _torch()
     shape = x_new.shape
     ldx = _rows("x_new", x_new)
     T, D = shape
