@@ -20,17 +20,20 @@
  *   - All matrix pointers are DEVICE pointers owned by the caller.  The library
  *     never allocates, frees or synchronises, and keeps no per-call state.
  *   - Dense row-major storage with implied leading dimensions
- *     (lda = K, ldb = N, ldc = N; packed weights: K/2 bytes per row).
+ *     (lda = K, ldb = N, ldc = N; packed weights: K/2 bytes per row), unless
+ *     the entry takes row strides.
  *   - Calls are asynchronous on `stream` (NULL = the null stream): they return
  *     once the kernel is enqueued.  Thread-safe.
  *   - Arguments are validated before any HIP call; on a non-OK status nothing
- *     has been launched and C is untouched.
+ *     has been launched and C is untouched (TG_ERR_HIP from an entry of two
+ *     launches: the first may have run).
  *   - M == 0 or N == 0: TG_OK, nothing launched (all pointers may be NULL).
  *     K == 0: C = epilogue(0) = 0; the operand pointers may be NULL then.
  *   - Accumulation is always fp32; the output is rounded to its type once,
  *     round-to-nearest-even (fp32 -> fp16 overflow gives +-inf).
- *   - Each operand must fit a 31-bit byte offset per tile row band (up to 256
- *     rows of a k-contiguous operand, up to 128 k-rows of an n-contiguous one):
+ *   - Each operand of the products without row strides must fit a 31-bit byte
+ *     offset per tile row band (up to 256 rows of a k-contiguous operand, up to
+ *     128 k-rows of an n-contiguous one):
  *     the library returns TG_ERR_BAD_SHAPE when 256 * K * element_size or
  *     128 * N * element_size exceeds 2^31 - 1 (and for M, N, K above 2^31 - 1).
  */

@@ -11,10 +11,22 @@
 // swizzles and fragment addresses are those of its k-contiguous operands, and
 // a fragment (16 bytes of one row for each lane) is the operand of
 // v_mfma_i32_32x32x32_i8, which does twice the 16-bit instruction's work.
+// Measured: 8192^3 bf16 out 410-445 us (2.5-2.7 POP/s; power-limited, 1.57 GHz
+// and 81% of the matrix rate at that clock with real data, 308 us and 2.28 GHz
+// with zeros), 4096^3 57-60 us.  256 x 8192 x 8192: 24.5 us; its copies alone
+// take 18.5 us from L2 and the last-level cache and 28 us from HBM, through LDS
+// or registers alike, so what bounds grids of small tiles is the unit's path to
+// L2 (62 GB/s of 85).  Not kept: the sums of k split over wave groups (same
+// time: LDS reads are not the bound), and a dword of each row touched ahead to
+// bring its line into L2 (a third slower: the lines touched count, not the
+// bytes).
 //
 // i8_any_kernel: any sizes, strides and addresses (LDS-DMA copies want aligned
 // ones).  Strips of 128 bytes of k go through registers: 16-byte loads at any
-// byte, PD strips ahead, into a two-stage LDS ring.
+// byte, PD strips ahead, into a two-stage LDS ring.  Measured: 1000 x 1001 x
+// 1003 8.6 us with 64 x 64 tiles and four strips ahead (8.9 with two); 4096 x
+// 4096 x 4095 124 us with 128 x 128 tiles and one strip ahead (180 with two: the
+// registers halve the waves).  Bound by the latency of its loads.
 #pragma once
 
 #include "tg_i8.h"
@@ -28,7 +40,8 @@ namespace tg {
 // stored 16 bytes to a lane, so that a store instruction writes runs of whole
 // rows.  The reads of one 32-row stripe are issued before the writes of the
 // next, and a wave's LDS accesses complete in order.  The stores write through
-// (kStoreThrough) as the other kernels' do (c_vec: whole aligned chunks, and 32
+// (kStoreThrough) as the other kernels' do (8192^3 415 us, 556 with each lane
+// storing its own 4 x 4 results) (c_vec: whole aligned chunks, and 32
 // rows within 31 bits of offset); other C rows take unaligned stores, and the
 // chunk across column N single ones.
 template <int DT, int FM, int FN>

@@ -16,6 +16,11 @@
 //    quantises the M rows itself, into LDS, while the loads of its first run
 //    of W are in flight: one launch instead of two, for as few rows as that
 //    takes no longer than those loads.
+// Measured with W from HBM: one token 8192 x 8192 14.6 us (4.6 TB/s of the 5.2
+// that a large copy reaches), 4096 x 4096 6.4 us; 16 tokens 8192 x 8192 17.3-17.8
+// us: every workgroup reads all of A, as many bytes as its own rows of W.  Eight
+// waves and 16 rows to a workgroup; 4 or 16 waves and 32 rows measured within 6%
+// or slower.
 #pragma once
 
 #include "tg_i8.h"

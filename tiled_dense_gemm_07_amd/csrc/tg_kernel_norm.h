@@ -7,6 +7,9 @@
 // Sums, norms and every intermediate value are fp32; x' is rounded to its
 // stored type before h is computed from it, so that h, and the gradients
 // taken from the stored x', belong to the x' the caller holds.
+// Bound by memory: bf16 8192 x 4096 with h 44.6 us in a trace (268 MB, 6.0 TB/s,
+// part of it from the last-level cache; a large copy reaches 5.2); one row of
+// 4096 2.7 us, which is launch, two reductions and latency.
 #pragma once
 
 #include "tg_rows.h"
@@ -167,11 +170,17 @@ __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void block_norm_
 // The three means of a row are taken together, so a row needs one reduction.
 // A workgroup of NT threads holds NT / TPR teams, each with a row in flight
 // and the next one's loads issued before this one's arithmetic.  It takes
-// consecutive rows: whole groups of rows that share a gate row (parts == 1; a
-// group to a team), or a part of one group (its rows to the teams in turn).
+// consecutive rows: whole groups of rows that share a gate row (parts == 0; a
+// group to a team), or one of the `parts` of a group (its rows to the teams in
+// turn).
 // Column sums stay in registers over those rows, are added over the teams in
 // LDS, and leave one partial row of each in the workspace, which
 // block_norm_columns_kernel adds in a fixed order.
+// Bound by memory: bf16 8192 x 4096 with 2048-token gates 83 us (403 MB and 8 MB
+// of partial sums, 5.0 TB/s) and 5.5 us for the columns.  512 workgroups of half
+// the threads took as long and left twice the partial sums (12.7 us for the
+// columns).  The unpacked values of a row are not kept over its reduction but
+// unpacked again (repack): kept, they spill.
 // --------------------------------------------------------------------------
 struct NormGradParams {
     const void *x_new, *y, *gate, *w_post, *w_pre, *dx_new, *dh;
@@ -184,7 +193,7 @@ struct NormGradParams {
     int64_t ldx, ldy, lddxn, lddh, lddx, lddy;
     int T, gate_rows;
     int rows;   // rows of a workgroup
-    int parts;  // workgroups of a group (1: whole groups to a workgroup)
+    int parts;  // workgroups of a group; 0: whole groups to a workgroup
     int D, Dp;
     int post;
     float alpha;
@@ -233,7 +242,7 @@ block_norm_grad_kernel(NormGradParams p)
     const int t = threadIdx.x % TPR;
     const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
     const float inv_d = 1.0f / (float)p.D;
-    const bool whole = p.parts == 1;
+    const bool whole = p.parts == 0;
     // Row numbers fit 32 bits.  The divisions are done on the vector ALU:
     // their results are read back as scalars, so that row addresses are.
     const int b = (int)blockIdx.x;
@@ -453,27 +462,25 @@ block_norm_columns_kernel(ColumnParams p)
     const int64_t group = which < 2 ? 0 : which - 2;
     const int64_t first = which < 2 ? 0 : group * p.parts;
     const int64_t rows = which < 2 ? p.P : p.parts;
-    const bool weigh = which == 1 && p.parts > 1 && p.gate;
+    const bool weigh = which == 1 && p.parts > 0 && p.gate;
     const int cl = threadIdx.x % CL, rl = threadIdx.x / CL;
     const int at = 4 * (blockIdx.x * CL + cl);
     f32x4 s = {0, 0, 0, 0};
     if (at < p.Dp && weigh) {
-        // elements past the end of a gate row are not used, and past the end
-        // of the matrix read as zeros (shared gates: a few hundred rows, so
-        // offsets stay far below 32 bits)
-        constexpr int ES = BT == DT_F32 ? 4 : 2;
-        const auto gate = make_rsrc(p.gate, clamp_bytes(rows / p.parts * (int64_t)p.D * ES));
+        // past the end of a gate row its last element again: no branch, and
+        // those sums are not stored
 #pragma unroll 4
         for (int r = rl; r < (int)rows; r += RL) {
             const f32x4 v = *(const f32x4*)(from + (int64_t)r * p.Dp + at);
-            const u32 o = (u32)(r / p.parts * (int64_t)p.D + at) * (u32)ES;
+            const char* gate = elem_ptr<BT>(p.gate, (int64_t)(r / p.parts) * p.D);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                const int col = at + i < p.D ? at + i : p.D - 1;
                 Raw8<BT> g;
                 if constexpr (BT == DT_F32)
-                    g.v[0][0] = buf_load4(gate, o + 4u * i);
+                    g.v[0][0] = ((const u32*)gate)[col];
                 else
-                    g.v[0][0] = buf_load2(gate, o + 2u * i);
+                    g.v[0][0] = ((const uint16_t*)gate)[col];
                 s[i] = __builtin_fmaf(get8<BT>(g, 0), v[i], s[i]);
             }
         }

@@ -1,7 +1,10 @@
 // Quantisation of activations to 8 bits, one scale for each row (tg_quant_i8).
 // One pass over memory: a team of TPR threads holds a row of up to 8 NC TPR
 // elements in registers between the search for its largest magnitude and the
-// conversion.  Longer rows (NC = 0) are read twice.
+// conversion.  Longer rows (NC = 0) are read twice.  Bound by memory: bf16 8192
+// x 8192 30.7 us (201 MB, 6.5 TB/s, part of it from the last-level cache), 16 x
+// 8192 2.7 us, which is launch and latency.  The correction of the quotient
+// (three operations an element) hides under the loads.
 #pragma once
 
 #include "tg_rows.h"

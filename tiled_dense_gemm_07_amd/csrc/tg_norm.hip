@@ -120,11 +120,11 @@ bool bad_stride(const void* p, int64_t ld, int64_t D) { return p && ld < D; }
 struct GradPlan {
     int64_t groups;  // rows of gate (1 without a gate)
     int64_t gate_rows;
-    int64_t rows;    // rows of a workgroup
-    int parts;       // workgroups of a group (1: whole groups to a workgroup)
-    int64_t P;       // workgroups
+    int64_t rows;   // rows of a workgroup
+    int64_t parts;  // workgroups of a group; 0: whole groups, each to a team
+    int64_t P;      // workgroups
     int64_t Dp;
-    bool pre, y;     // partial sums kept: of dw_pre; of dw_post and shared gates
+    bool pre, y;    // partial sums kept: of dw_pre; of dw_post and shared gates
     size_t bytes;
 };
 
@@ -134,23 +134,41 @@ GradPlan grad_plan(const tg_block_norm_grad_args& a)
     // One workgroup to a compute unit, and at least a row for each of its
     // teams and two in all: with fewer, the partial sums would cost more than
     // the rows.
-    const int64_t teams = a.D <= 512 ? 16 : (a.D <= 1024 ? 8 : (a.D <= 2048 ? 4 : 2));
+    const int64_t teams =
+        a.D <= 512 ? 16 : (a.D <= 1024 ? 8 : (a.D <= 2048 ? 4 : (a.D <= 4096 ? 2 : 1)));
     int64_t want = ceil_div(a.T, 256);
     want = want < teams ? teams : want;
+    want = want < 2 ? 2 : want;
     g.gate_rows = a.gate ? (a.gate_rows < a.T ? a.gate_rows : a.T) : a.T;
     g.groups = ceil_div(a.T, g.gate_rows);
-    if (g.gate_rows <= want) {
-        g.parts = 1;
-        g.rows = ceil_div(want, g.gate_rows) * g.gate_rows;
-        g.P = ceil_div(a.T, g.rows);
+    // Parts of groups, rows to the teams in turn; or whole groups, at least
+    // one for each team.  The rows that a team takes one after the other, for
+    // each round of 256 workgroups, decide; where a workgroup has one group, its
+    // partial sums count as two rows more, and the sums of each 128 groups as
+    // one.  (Whole groups also where the sums of a group each would be more than
+    // a grid's y dimension.)  Backward of 8192 x 512 with gates of 16 tokens: 16
+    // us and 8 for the column sums by parts; whole groups left one team of 16 at
+    // work.
+    const int64_t parts = ceil_div(g.gate_rows, want);
+    const int64_t part_rows = ceil_div(g.gate_rows, parts);
+    const int64_t inter =
+        ceil_div(g.groups * parts, 256) * (ceil_div(part_rows, teams) + 2) + g.groups / 128;
+    const int64_t least = want > teams * g.gate_rows ? want : teams * g.gate_rows;
+    const int64_t in_wg = ceil_div(least, g.gate_rows);  // groups
+    const int64_t whole =
+        ceil_div(g.groups, 256 * in_wg) * (g.gate_rows * ceil_div(in_wg, teams));
+    if (a.gate && (whole < inter || g.groups > 32768)) {
+        g.parts = 0;
+        g.rows = in_wg * g.gate_rows;
+        g.P = ceil_div(g.groups, in_wg);
     } else {
-        g.parts = (int)ceil_div(g.gate_rows, want);
-        g.rows = ceil_div(g.gate_rows, g.parts);
-        g.P = g.groups * g.parts;
+        g.parts = parts;
+        g.rows = part_rows;
+        g.P = g.groups * parts;
     }
     g.Dp = ceil_div(a.D, 8) * 8;
     g.pre = a.dw_pre != nullptr;
-    g.y = a.dw_post != nullptr || (a.dgate != nullptr && g.parts > 1);
+    g.y = a.dw_post != nullptr || (a.dgate != nullptr && g.parts > 0);
     g.bytes = (size_t)(g.P * g.Dp * 4) * ((g.pre ? 1 : 0) + (g.y ? 1 : 0));
     return g;
 }
@@ -316,7 +334,7 @@ tg_status tg_block_norm_backward(const tg_block_norm_grad_args* a, void* workspa
     p.lddy = a->lddy;
     p.gate_rows = (int)g.gate_rows;
     p.rows = (int)g.rows;
-    p.parts = g.parts;
+    p.parts = (int)g.parts;
     p.D = (int)D;
     p.Dp = (int)g.Dp;
     p.post = a->y && a->post_norm;
@@ -327,13 +345,13 @@ tg_status tg_block_norm_backward(const tg_block_norm_grad_args* a, void* workspa
         return s;
     if (g.bytes == 0)
         return TG_OK;
-    const bool shared = a->dgate && g.parts > 1;  // gate rows of several workgroups
+    const bool by_group = a->dgate && g.parts > 0;
     tg::ColumnParams c{p.part_pre, p.part_y, a->dw_pre, a->dw_post, a->dgate, a->w_post,
-                       a->gate,    g.P,      g.parts,   (int)D,     (int)g.Dp};
+                       a->gate,    g.P,      (int)g.parts, (int)D,  (int)g.Dp};
     const void* kc = by_types(TG_F32, a->btype, [](auto, auto B) {
         return (const void*)&tg::block_norm_columns_kernel<decltype(B)::value>;
     });
-    return tg::launch_kernel(kc, ceil_div(g.Dp, 32), 2 + (shared ? g.groups : 0), 256, &c,
+    return tg::launch_kernel(kc, ceil_div(g.Dp, 32), 2 + (by_group ? g.groups : 0), 256, &c,
                              (hipStream_t)stream, "block_norm_columns");
 }
 
