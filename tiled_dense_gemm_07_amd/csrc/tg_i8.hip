@@ -113,39 +113,46 @@ const I8Tile kTiles[] = {
     TG_I8_TILE(256, 256, 128, 2, 4, 2, 2, 1, 6.00f, 1.250f, 1.820f),
 };
 
-// The streaming kernel's cost, likewise: HBM for W once, or all the loads of
-// its workgroups (32 or 48 rows of operands for each) through L2.
-float gemv_cost(int64_t M, int64_t N, int64_t K, int rows, float t0, float per)
+// The streaming kernel: 16 tokens to a workgroup while every workgroup has a CU
+// to itself, else 32, and its cost, likewise: a CU's workgroups share its path to
+// L2 and HBM, so rounds of 256 workgroups add up.  Fitted over 84 shapes of 17
+// to 128 tokens, N and K from 1000 to 14336.
+struct I8Stream {
+    int tokens;
+    float cost;
+};
+
+I8Stream stream_i8(int64_t M, int64_t N, int64_t K)
 {
-    const float hbm = (float)N * (float)K / 5e6f;
-    const float l2 = (float)(ceil_div(M, 16) * ceil_div(N, rows)) * (16 + rows) * (float)K / 1.3e7f;
-    return t0 + per * (hbm > l2 ? hbm : l2);
+    const int64_t rows = ceil_div(N, 16);
+    if (M <= 16 || ceil_div(M, 16) * rows <= 256)
+        return {16, 3.0f + 7.3e-4f * (float)K};
+    return {32, 2.8f + 1.16e-3f * (float)K * (float)ceil_div(ceil_div(M, 32) * rows, 256)};
 }
 
 struct I8Pick {
     const I8Tile* tile;  // NULL: the streaming kernel
-    int rows;            // W rows of its workgroup
+    int tokens;          // its workgroup's
 };
 
-// Up to 16 tokens: the streaming kernel, with 16 rows of W to a workgroup
-// (M = 1, 8192 x 8192: 14.6 us, and 18.4 for the best tile kernel; M = 16: 17.3
-// and 19.0).  Up to 128: whichever costs less, with 32 rows to a workgroup
-// (M = 32, 4096 x 4096: 8.2 us and 11.2; M = 32, 8192 x 8192: 26 and 19.8).
-// Above: the cheapest tile.  Rows that do not start at 16-byte boundaries, or
+// Up to 16 tokens: the streaming kernel (M = 1, 8192 x 8192: 14.6 us, and 18.4
+// for the best tile kernel; M = 16: 17.3 and 19.0).  Up to 128: whichever costs
+// less (M = 32, 4096 x 4096: 8.5 us and 11.2; M = 32, 8192 x 8192: 24.6 and
+// 19.9; over the 84 shapes the choice is 0.8% slower than the best of all, 13%
+// at most).  Above: the cheapest tile.  Rows that do not start at 16-byte boundaries, or
 // K % 16 != 0, leave the streaming kernel, which takes any address, up to 32
 // tokens, and above them the kernels for any layout: 128 x 128 tiles where they
 // fill most of the card (1024 x 4096 x 4095: 39.7 us, more than 50 with 64 x
 // 64), else 64 x 64 (256 x 4096 x 4095: 24.3 us, more than 36 with 128 x 128).
 I8Pick pick_i8(int64_t M, int64_t N, int64_t K, bool aligned)
 {
-    if (M <= 16)
-        return {nullptr, 16};
-    if (!aligned && M <= 32)
-        return {nullptr, 32};
+    const I8Stream s = stream_i8(M, N, K);
+    if (M <= (aligned ? 16 : 32))
+        return {nullptr, s.tokens};
     if (!aligned)
         return {ceil_div(M, 128) * ceil_div(N, 128) > 160 ? &kAny[1] : &kAny[0], 0};
-    float best = M <= 128 ? gemv_cost(M, N, K, 32, 3.23f, 1.335f) : 1e30f;
-    I8Pick p{nullptr, 32};
+    float best = M <= 128 ? s.cost : 1e30f;
+    I8Pick p{nullptr, s.tokens};
     for (const I8Tile& t : kTiles) {
         const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
         const float strips = (float)ceil_div(K, 128);
@@ -169,13 +176,11 @@ tg_status launch_i8(tg::I8Params p, hipStream_t stream)
     const int es = tg::dtype_size(p.dt_out);
     const bool aligned = p.K > 0 && p.K % 16 == 0 && dma_rows(p.A, p.lda) && dma_rows(p.W, p.ldw);
     const I8Pick k = pick_i8(p.M, p.N, p.K, aligned);
-    if (!k.tile) {
-        const int ng = k.rows / 16;
-        return tg::launch_kernel(ng == 1 ? (const void*)&tg::i8_gemv_kernel<1, 1, 8>
-                                         : (const void*)&tg::i8_gemv_kernel<2, 1, 8>,
-                                 ceil_div(p.N, k.rows), ceil_div(p.M, 16), 512, &p, stream,
-                                 "i8_gemv", 8 * ng * 1024);
-    }
+    if (!k.tile)
+        return tg::launch_kernel(k.tokens == 16 ? (const void*)&tg::i8_gemv_kernel<1, 8>
+                                                : (const void*)&tg::i8_gemv_kernel<2, 8>,
+                                 ceil_div(p.N, 16), ceil_div(p.M, k.tokens), 512, &p, stream,
+                                 "i8_gemv", 8 * (k.tokens / 16) * 1024);
     // Tile order: patches of 4 tile rows, as the 16-bit kernels' largest tiles.
     p.group_m = tg::swizzle_override() > 0 ? tg::swizzle_override() : 4;
     p.tiles_m = (int)ceil_div(p.M, k.tile->bm);
@@ -203,11 +208,11 @@ tg_status launch_fused(const tg::I8Params& p, int dtype, const void* X, int64_t 
 {
     tg::I8LinearParams l{p, {X, ldx}};
     l.p.stamps = tg::clock_stamps();
-    const void* k = dtype == TG_F32   ? (const void*)&tg::i8_linear_gemv_kernel<tg::DT_F32, 1, 8>
-                    : dtype == TG_F16 ? (const void*)&tg::i8_linear_gemv_kernel<tg::DT_F16, 1, 8>
-                                      : (const void*)&tg::i8_linear_gemv_kernel<tg::DT_BF16, 1, 8>;
+    const void* k = dtype == TG_F32   ? (const void*)&tg::i8_linear_gemv_kernel<tg::DT_F32, 8>
+                    : dtype == TG_F16 ? (const void*)&tg::i8_linear_gemv_kernel<tg::DT_F16, 8>
+                                      : (const void*)&tg::i8_linear_gemv_kernel<tg::DT_BF16, 8>;
     const unsigned levels =
-        (unsigned)(p.M * tg::I8Gemv<tg::DT_BF16, 1, 1, 8, true>::level_row(p.K));
+        (unsigned)(p.M * tg::I8Gemv<tg::DT_BF16, 1, 8, true>::level_row(p.K));
     return tg::launch_kernel(k, ceil_div(p.N, 16), 1, 512, &l, stream, "i8_linear_gemv",
                              levels > 8192 ? levels : 8192);
 }
@@ -220,8 +225,8 @@ void describe_i8(int64_t M, int64_t N, int64_t K, char* buf, size_t len)
 {
     const I8Pick k = pick_i8(M, N, K, K > 0 && K % 16 == 0);
     if (!k.tile)
-        snprintf(buf, len, "i8_gemv_%d grid=%lldx%lld threads=512", k.rows,
-                 (long long)ceil_div(N, k.rows), (long long)ceil_div(M, 16));
+        snprintf(buf, len, "i8_gemv_%d grid=%lldx%lld threads=512", k.tokens,
+                 (long long)ceil_div(N, 16), (long long)ceil_div(M, k.tokens));
     else
         snprintf(buf, len, "%s grid=%lld threads=%d", k.tile->name,
                  (long long)(ceil_div(M, k.tile->bm) * ceil_div(N, k.tile->bn)), k.tile->threads);

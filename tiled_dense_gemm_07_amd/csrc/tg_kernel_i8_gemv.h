@@ -1,8 +1,8 @@
 // 8-bit integer product for few tokens (decoding): the time is that of
 // streaming W once, so W goes from memory straight into the operand registers
 // of v_mfma_i32_16x16x64_i8, with no LDS on its way.
-//  * A workgroup owns 16 NG rows of W and 16 MT rows of A, and all of k; its
-//    NW waves take runs of 256 k in turn.  In a run, lane (r = l % 16,
+//  * A workgroup owns 16 rows of W and 16 MT rows of A, and all of k; its NW
+//    waves take runs of 256 k in turn.  In a run, lane (r = l % 16,
 //    g = l / 16) loads 16 bytes of row r at k = 64 c + 16 g, c = 0 .. 3: an
 //    instruction takes 64 contiguous bytes of 16 rows, and the run whole cache
 //    lines.  A and W take the same k in the same lanes, so the order inside a
@@ -18,9 +18,11 @@
 //    takes no longer than those loads.
 // Measured with W from HBM: one token 8192 x 8192 14.6 us (4.6 TB/s of the 5.2
 // that a large copy reaches), 4096 x 4096 6.4 us; 16 tokens 8192 x 8192 17.3-17.8
-// us: every workgroup reads all of A, as many bytes as its own rows of W.  Eight
-// waves and 16 rows to a workgroup; 4 or 16 waves and 32 rows measured within 6%
-// or slower.
+// us: every workgroup reads all of A, as many bytes as its own rows of W.  More
+// tokens: 16 to a workgroup while every workgroup has a CU of its own (32 tokens,
+// 2048 x 8192: 9.7 us, 13.2 with 32), else 32 (17 tokens, 4096 x 4096: 7.3 us,
+// 9.3 with 16).  Eight waves; 4 or 16 waves and 32 rows to a workgroup measured
+// within 6% or slower.
 #pragma once
 
 #include "tg_i8.h"
@@ -34,11 +36,10 @@ struct I8Source {
     int64_t ldx;
 };
 
-template <int DTX, int NG, int MT, int NW, bool FUSED>
+template <int DTX, int MT, int NW, bool FUSED>
 struct I8Gemv {
     static constexpr int RUN = 256;
-    static constexpr int ROWS = 16 * NG, TOKENS = 16 * MT;
-    static constexpr int RED = NW * NG * MT * 256 * 4;  // bytes of the waves' sums
+    static constexpr int TOKENS = 16 * MT;
     // levels: rows of K rounded up to a run, 16 bytes apart from a multiple
     // of the bank line so that the 16 rows of a fragment read spread
     static __host__ __device__ __forceinline__ int level_row(int K)
@@ -47,7 +48,7 @@ struct I8Gemv {
     }
 
     struct Run {
-        u32x4 w[NG][4];
+        u32x4 w[4];
         u32x4 a[FUSED ? 1 : MT][4];
     };
 
@@ -59,16 +60,14 @@ struct I8Gemv {
         return whole ? ((const Any*)(row + k))->v : load16_row(row, k, K);
     }
 
-    static __device__ __forceinline__ void load(Run& R, const int8_t* const (&w)[NG],
+    static __device__ __forceinline__ void load(Run& R, const int8_t* w,
                                                 const int8_t* const (&a)[MT], int k0, int K, int g,
                                                 bool whole)
     {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int k = k0 + 64 * c + 16 * g;
-#pragma unroll
-            for (int q = 0; q < NG; ++q)
-                R.w[q][c] = chunk(w[q], k, K, whole);
+            R.w[c] = chunk(w, k, K, whole);
             if constexpr (!FUSED) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
@@ -77,25 +76,21 @@ struct I8Gemv {
         }
     }
 
-    static __device__ __forceinline__ void multiply(i32x4 (&acc)[NG][MT], const Run& R,
+    static __device__ __forceinline__ void multiply(i32x4 (&acc)[MT], const Run& R,
                                                     const char* levels, int k0, int g)
     {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            i32x4 a[MT];
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
+                i32x4 a;
                 if constexpr (FUSED)
-                    a[m] = *(const i32x4*)(levels + k0 + 64 * c + 16 * g);
+                    a = *(const i32x4*)(levels + k0 + 64 * c + 16 * g);
                 else
-                    a[m] = __builtin_bit_cast(i32x4, R.a[m][c]);
+                    a = __builtin_bit_cast(i32x4, R.a[m][c]);
+                acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, R.w[c]),
+                                                               a, acc[m], 0, 0, 0);
             }
-#pragma unroll
-            for (int q = 0; q < NG; ++q)
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    acc[q][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-                        __builtin_bit_cast(i32x4, R.w[q][c]), a[m], acc[q][m], 0, 0, 0);
         }
     }
 
@@ -168,14 +163,10 @@ struct I8Gemv {
         const int tid = threadIdx.x;
         const int lane = tid & 63;
         const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-        const int m0 = (int)blockIdx.y * TOKENS, n0 = (int)blockIdx.x * ROWS;
+        const int m0 = (int)blockIdx.y * TOKENS, n0 = (int)blockIdx.x * 16;
         const int ln = lane & 15, g = lane >> 4;
-        const int8_t *wr[NG], *ar[MT];
-#pragma unroll
-        for (int q = 0; q < NG; ++q) {
-            const int n = n0 + 16 * q + ln;
-            wr[q] = p.W + (int64_t)(n < p.N ? n : p.N - 1) * p.ldw;
-        }
+        const int8_t *wr, *ar[MT];
+        wr = p.W + (int64_t)(n0 + ln < p.N ? n0 + ln : p.N - 1) * p.ldw;
         const char* levels = nullptr;
         if constexpr (FUSED) {
             levels = gemv_lds + (ln < p.M ? ln : p.M - 1) * level_row(p.K);
@@ -186,12 +177,10 @@ struct I8Gemv {
                 ar[m] = p.A + (int64_t)(t < p.M ? t : p.M - 1) * p.lda;
             }
         }
-        i32x4 acc[NG][MT];
+        i32x4 acc[MT];
 #pragma unroll
-        for (int q = 0; q < NG; ++q)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                acc[q][m] = i32x4{0, 0, 0, 0};
+        for (int m = 0; m < MT; ++m)
+            acc[m] = i32x4{0, 0, 0, 0};
 
         // whole runs w, w + NW, ...; the partial one, if any, is run `whole`
         const int whole = p.K / RUN;
@@ -224,20 +213,18 @@ struct I8Gemv {
         if constexpr (FUSED)
             __syncthreads();  // the levels' last reads
 #pragma unroll
-        for (int q = 0; q < NG; ++q)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                *(i32x4*)&red[((w * NG + q) * MT + m) * 256 + lane * 4] = acc[q][m];
+        for (int m = 0; m < MT; ++m)
+            *(i32x4*)&red[(w * MT + m) * 256 + lane * 4] = acc[m];
         __syncthreads();
         // lane l of a block holds token l % 16, rows 4 (l / 16) + 0 .. 3 of W
-        for (int o = tid; o < NG * MT * 256; o += NW * 64) {
+        for (int o = tid; o < MT * 256; o += NW * 64) {
             int s = 0;
 #pragma unroll
             for (int v = 0; v < NW; ++v)
-                s += red[v * NG * MT * 256 + o];
-            const int l = (o >> 2) & 63, b = o >> 8;
-            const int m = m0 + 16 * (b % MT) + (l & 15);
-            const int n = n0 + 16 * (b / MT) + 4 * (l >> 4) + (o & 3);
+                s += red[v * MT * 256 + o];
+            const int l = (o >> 2) & 63;
+            const int m = m0 + 16 * (o >> 8) + (l & 15);
+            const int n = n0 + 4 * (l >> 4) + (o & 3);
             if (m < p.M && n < p.N)
                 store_out(p.C, p.dt_out, (int64_t)m * p.ldc + n,
                           i8_result(s, FUSED ? sc[m & 15] : p.sa[m], p.sw[n],
@@ -246,14 +233,14 @@ struct I8Gemv {
     }
 };
 
-template <int NG, int MT, int NW>
+template <int MT, int NW>
 __global__ __attribute__((amdgpu_flat_work_group_size(NW * 64, NW * 64))) void
 i8_gemv_kernel(I8Params p)
 {
     GemmParams rec{};
     rec.stamps = p.stamps;
     const ClockStamp clk = stamp_begin(rec);
-    I8Gemv<DT_F32, NG, MT, NW, false>::run(p, I8Source{});
+    I8Gemv<DT_F32, MT, NW, false>::run(p, I8Source{});
     stamp_end(rec, clk);
 }
 
@@ -262,14 +249,14 @@ struct I8LinearParams {
     I8Source x;
 };
 
-template <int DTX, int NG, int NW>
+template <int DTX, int NW>
 __global__ __attribute__((amdgpu_flat_work_group_size(NW * 64, NW * 64))) void
 i8_linear_gemv_kernel(I8LinearParams l)
 {
     GemmParams rec{};
     rec.stamps = l.p.stamps;
     const ClockStamp clk = stamp_begin(rec);
-    I8Gemv<DTX, NG, 1, NW, true>::run(l.p, l.x);
+    I8Gemv<DTX, 1, NW, true>::run(l.p, l.x);
     stamp_end(rec, clk);
 }
 
