@@ -138,6 +138,21 @@ def test_product_strides_and_addresses(M, N, K, pad, shift):
             assert bool((wide == 7.0).all())
 
 
+@pytest.mark.parametrize("M,N,K", [(17, 4112, 512), (20, 4100, 1003), (33, 4097, 272),
+                                   (32, 4200, 2050), (100, 1100, 700)])
+@pytest.mark.parametrize("pad", [(0, 0), (16, 0), (0, 1), (1, 0), (2, 3), (4, 4)], ids=str)
+def test_product_few_tokens(M, N, K, pad):
+    """17 to 128 tokens, more workgroups than compute units: rows of A and of W
+    at 16-byte, 4-byte and single-byte steps."""
+    A, sa, W, sw, b = make_product(M, N, K, M + N + K)
+    say("gemm_i8 %dx%dx%d pads %s" % (M, N, K, pad))
+    dA, dW = strided(dev(A), pad[0], pad[0] // 2), strided(dev(W), pad[1], pad[1] // 2)
+    C = torch.full((M, N), float("nan"), dtype=torch.float32, device=DEV)
+    binding.gemm_i8(dA, dev(sa), dW, dev(sw), bias=dev(b), C=C)
+    torch.cuda.synchronize()
+    check_product(values(C, F32), A, sa, W, sw, b, F32, False)
+
+
 def test_product_largest_sums():
     """The largest magnitudes the sum can take: 128 * 128 * K near 2^31."""
     for M, K in ((3, 131071), (70, 131056)):
@@ -316,6 +331,27 @@ def test_linear_equals_its_parts(M, N, K, dtype):
         q, s = ref.levels(v)
         check_product(values(C, dtype), q, s.astype(np.float32), W.cpu().numpy(),
                       sw.cpu().numpy(), b.cpu().numpy(), dtype, True)
+
+
+@TYPES
+@pytest.mark.parametrize("M,N,K", [(1, 33, 257), (1, 100, 2049), (3, 48, 1003), (8, 17, 1538),
+                                   (5, 30, 15), (16, 50, 770), (40, 4100, 515), (150, 200, 333)])
+def test_linear_rows_at_any_byte(M, N, K, dtype):
+    """W's rows at 4-byte and at single-byte steps: the bits of quant_i8 followed
+    by gemm_i8 on rows at 16-byte boundaries."""
+    r = np.random.Generator(np.random.PCG64(M + N + K))
+    x = activations(r, M, K, dtype)
+    _, _, W, sw, b = make_product(1, N, K, 3)
+    W, sw, b = dev(W), dev(sw), dev(b)
+    q, s = binding.quant_i8(x)
+    wide = (K + 15) // 16 * 16
+    want = binding.gemm_i8(strided(q, wide - K), s, strided(W, wide - K), sw, bias=b,
+                           out_dtype=torch_dtype(dtype))
+    for pad, shift in ((0, 0), (1, 0), (2, 1), ((-K) % 4, 0), ((-K) % 4, 3), ((-K) % 16, 2)):
+        say("linear_i8 %dx%dx%d %s pad=%d shift=%d" % (M, N, K, DNAME[dtype], pad, shift))
+        got = binding.linear_i8(x, strided(W, pad, shift), sw, bias=b)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
 
 
 def test_linear_workspace_contents_do_not_matter():

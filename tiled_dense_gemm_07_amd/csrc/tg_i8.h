@@ -62,6 +62,55 @@ __device__ __forceinline__ u32x4 load16_row(const int8_t* row, int k, int K)
     return v;
 }
 
+// A row, and 16-byte chunks of it from whole dwords: the hardware takes 16-byte
+// loads at any byte, but those that are not at a dword take four times as long.
+// SHIFT: the chunk at k is in the 5 dwords from the one that holds byte k on;
+// 4 where the row starts at a dword, and the fifth is the fourth again.  Every
+// dword read holds a byte of the chunk, so it lies in the row's memory pages.
+template <bool SHIFT>
+struct Row16 {
+    const int8_t* p;  // SHIFT: down to the dword that holds the first byte
+    u32 s;            // bytes from there to the row
+    int x;            // offset of the fifth dword
+
+    struct Chunk {
+        u32x4 v;
+        u32 x;
+    };
+
+    __device__ __forceinline__ void at(const int8_t* row)
+    {
+        s = SHIFT ? (u32)(uintptr_t)row & 3 : 0;
+        x = s ? 16 : 12;
+        p = row - s;
+    }
+    // of a whole chunk (k + 16 <= K), as it was loaded
+    __device__ __forceinline__ Chunk load(int k) const
+    {
+        struct __attribute__((packed, aligned(SHIFT ? 4 : 1))) Any {
+            u32x4 v;
+        };
+        Chunk c;
+        c.v = ((const Any*)(p + k))->v;
+        c.x = SHIFT ? *(const u32*)(p + k + x) : 0;
+        return c;
+    }
+    // across or past the row's end: zeros past K, nothing to shift
+    __device__ __forceinline__ Chunk load_end(int k, int K) const
+    {
+        return Chunk{load16_row(p + s, k, K), 0};
+    }
+    static __device__ __forceinline__ u32x4 bytes(const Chunk& c, u32 s)
+    {
+        if constexpr (!SHIFT)
+            return c.v;
+        return u32x4{__builtin_amdgcn_alignbyte(c.v[1], c.v[0], s),
+                     __builtin_amdgcn_alignbyte(c.v[2], c.v[1], s),
+                     __builtin_amdgcn_alignbyte(c.v[3], c.v[2], s),
+                     __builtin_amdgcn_alignbyte(c.x, c.v[3], s)};
+    }
+};
+
 // One result of the product: the exact integer sum, scaled in fp32.
 __device__ __forceinline__ float i8_result(int acc, float sa, float sw, float bias, int relu)
 {

@@ -113,21 +113,32 @@ const I8Tile kTiles[] = {
     TG_I8_TILE(256, 256, 128, 2, 4, 2, 2, 1, 6.00f, 1.250f, 1.820f),
 };
 
+// Rows of W (1), or of A or both (2), that do not start at dwords.
+int shift_i8(const void* A, int64_t lda, const void* W, int64_t ldw)
+{
+    const auto off = [](const void* p, int64_t ld) { return (((uintptr_t)p | (uint64_t)ld) & 3) != 0; };
+    return off(A, lda) ? 2 : (off(W, ldw) ? 1 : 0);
+}
+
 // The streaming kernel: 16 tokens to a workgroup while every workgroup has a CU
 // to itself, else 32, and its cost, likewise: a CU's workgroups share its path to
-// L2 and HBM, so rounds of 256 workgroups add up.  Fitted over 84 shapes of 17
-// to 128 tokens, N and K from 1000 to 14336.
+// L2 and HBM, so rounds of 256 workgroups add up.  Fitted to 84 shapes of 17 to
+// 128 tokens, N and K from 1000 to 14336, and 99 with odd K.  Shifting A as well
+// leaves registers for one workgroup of 32 tokens on a CU, which gains nothing
+// (32 x 4096 x 4095: 14.0 us and 15.5 with 16; 32 x 5120 x 5119: 31.0 and 26.3).
 struct I8Stream {
     int tokens;
     float cost;
 };
 
-I8Stream stream_i8(int64_t M, int64_t N, int64_t K)
+I8Stream stream_i8(int64_t M, int64_t N, int64_t K, int shift)
 {
+    static const float kPerK[3][2] = {{7.3e-4f, 1.16e-3f}, {1.2e-3f, 1.75e-3f}, {1.5e-3f, 0.0f}};
     const int64_t rows = ceil_div(N, 16);
-    if (M <= 16 || ceil_div(M, 16) * rows <= 256)
-        return {16, 3.0f + 7.3e-4f * (float)K};
-    return {32, 2.8f + 1.16e-3f * (float)K * (float)ceil_div(ceil_div(M, 32) * rows, 256)};
+    const int64_t r16 = ceil_div(ceil_div(M, 16) * rows, 256);
+    if (M <= 16 || r16 <= 1 || shift == 2)
+        return {16, 3.0f + kPerK[shift][0] * (float)(K * r16)};
+    return {32, 2.8f + kPerK[shift][1] * (float)(K * ceil_div(ceil_div(M, 32) * rows, 256))};
 }
 
 struct I8Pick {
@@ -139,20 +150,26 @@ struct I8Pick {
 // for the best tile kernel; M = 16: 17.3 and 19.0).  Up to 128: whichever costs
 // less (M = 32, 4096 x 4096: 8.5 us and 11.2; M = 32, 8192 x 8192: 24.6 and
 // 19.9; over the 84 shapes the choice is 0.8% slower than the best of all, 13%
-// at most).  Above: the cheapest tile.  Rows that do not start at 16-byte boundaries, or
-// K % 16 != 0, leave the streaming kernel, which takes any address, up to 32
-// tokens, and above them the kernels for any layout: 128 x 128 tiles where they
-// fill most of the card (1024 x 4096 x 4095: 39.7 us, more than 50 with 64 x
-// 64), else 64 x 64 (256 x 4096 x 4095: 24.3 us, more than 36 with 128 x 128).
-I8Pick pick_i8(int64_t M, int64_t N, int64_t K, bool aligned)
+// at most).  Above: the cheapest tile.
+// Rows that do not start at 16-byte boundaries, or K % 16 != 0, leave the
+// streaming kernel, which takes any address (M = 32, 4096 x 4095, levels of
+// linear_i8: 11.4 us, and 26.3 with tiles; 64 x 8192 x 8191: 57.5 and 48.4), and
+// the tiles for any layout: 128 x 128 where they fill most of the card (1024 x
+// 4096 x 4095: 39.7 us, more than 50 with 64 x 64), else 64 x 64 (256 x 4096 x
+// 4095: 24.3 us, more than 36 with 128 x 128).
+I8Pick pick_i8(int64_t M, int64_t N, int64_t K, bool aligned, int shift)
 {
-    const I8Stream s = stream_i8(M, N, K);
-    if (M <= (aligned ? 16 : 32))
+    const I8Stream s = stream_i8(M, N, K, shift);
+    if (M <= 16)
         return {nullptr, s.tokens};
-    if (!aligned)
-        return {ceil_div(M, 128) * ceil_div(N, 128) > 160 ? &kAny[1] : &kAny[0], 0};
     float best = M <= 128 ? s.cost : 1e30f;
     I8Pick p{nullptr, s.tokens};
+    if (!aligned) {
+        const int64_t tiles = ceil_div(M, 64) * ceil_div(N, 64);
+        if (best < 3.0f + 4.9e-3f * (float)(K * ceil_div(tiles, 256)))
+            return p;
+        return {ceil_div(M, 128) * ceil_div(N, 128) > 160 ? &kAny[1] : &kAny[0], 0};
+    }
     for (const I8Tile& t : kTiles) {
         const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
         const float strips = (float)ceil_div(K, 128);
@@ -175,12 +192,17 @@ tg_status launch_i8(tg::I8Params p, hipStream_t stream)
     p.stamps = tg::clock_stamps();
     const int es = tg::dtype_size(p.dt_out);
     const bool aligned = p.K > 0 && p.K % 16 == 0 && dma_rows(p.A, p.lda) && dma_rows(p.W, p.ldw);
-    const I8Pick k = pick_i8(p.M, p.N, p.K, aligned);
-    if (!k.tile)
-        return tg::launch_kernel(k.tokens == 16 ? (const void*)&tg::i8_gemv_kernel<1, 8>
-                                                : (const void*)&tg::i8_gemv_kernel<2, 8>,
-                                 ceil_div(p.N, 16), ceil_div(p.M, k.tokens), 512, &p, stream,
-                                 "i8_gemv", 8 * (k.tokens / 16) * 1024);
+    const int shift = shift_i8(p.A, p.lda, p.W, p.ldw);
+    const I8Pick k = pick_i8(p.M, p.N, p.K, aligned, shift);
+    if (!k.tile) {
+        static const void* const kernels[3][2] = {
+            {(const void*)&tg::i8_gemv_kernel<1, 8, 0>, (const void*)&tg::i8_gemv_kernel<2, 8, 0>},
+            {(const void*)&tg::i8_gemv_kernel<1, 8, 1>, (const void*)&tg::i8_gemv_kernel<2, 8, 1>},
+            {(const void*)&tg::i8_gemv_kernel<1, 8, 2>, nullptr}};
+        const int mt = k.tokens / 16;
+        return tg::launch_kernel(kernels[shift][mt - 1], ceil_div(p.N, 16), ceil_div(p.M, k.tokens),
+                                 512, &p, stream, "i8_gemv", 8 * mt * 1024);
+    }
     // Tile order: patches of 4 tile rows, as the 16-bit kernels' largest tiles.
     p.group_m = tg::swizzle_override() > 0 ? tg::swizzle_override() : 4;
     p.tiles_m = (int)ceil_div(p.M, k.tile->bm);
@@ -208,11 +230,16 @@ tg_status launch_fused(const tg::I8Params& p, int dtype, const void* X, int64_t 
 {
     tg::I8LinearParams l{p, {X, ldx}};
     l.p.stamps = tg::clock_stamps();
-    const void* k = dtype == TG_F32   ? (const void*)&tg::i8_linear_gemv_kernel<tg::DT_F32, 8>
-                    : dtype == TG_F16 ? (const void*)&tg::i8_linear_gemv_kernel<tg::DT_F16, 8>
-                                      : (const void*)&tg::i8_linear_gemv_kernel<tg::DT_BF16, 8>;
+    static const void* const kernels[2][3] = {
+        {(const void*)&tg::i8_linear_gemv_kernel<tg::DT_F32, 8, 0>,
+         (const void*)&tg::i8_linear_gemv_kernel<tg::DT_F16, 8, 0>,
+         (const void*)&tg::i8_linear_gemv_kernel<tg::DT_BF16, 8, 0>},
+        {(const void*)&tg::i8_linear_gemv_kernel<tg::DT_F32, 8, 1>,
+         (const void*)&tg::i8_linear_gemv_kernel<tg::DT_F16, 8, 1>,
+         (const void*)&tg::i8_linear_gemv_kernel<tg::DT_BF16, 8, 1>}};
+    const void* k = kernels[shift_i8(nullptr, 0, p.W, p.ldw)][dtype];
     const unsigned levels =
-        (unsigned)(p.M * tg::I8Gemv<tg::DT_BF16, 1, 8, true>::level_row(p.K));
+        (unsigned)(p.M * tg::I8Gemv<tg::DT_BF16, 1, 8, 0, true>::level_row(p.K));
     return tg::launch_kernel(k, ceil_div(p.N, 16), 1, 512, &l, stream, "i8_linear_gemv",
                              levels > 8192 ? levels : 8192);
 }
@@ -223,7 +250,7 @@ namespace tg {
 
 void describe_i8(int64_t M, int64_t N, int64_t K, char* buf, size_t len)
 {
-    const I8Pick k = pick_i8(M, N, K, K > 0 && K % 16 == 0);
+    const I8Pick k = pick_i8(M, N, K, K > 0 && K % 16 == 0, shift_i8(nullptr, K, nullptr, K));
     if (!k.tile)
         snprintf(buf, len, "i8_gemv_%d grid=%lldx%lld threads=512", k.tokens,
                  (long long)ceil_div(N, 16), (long long)ceil_div(M, k.tokens));

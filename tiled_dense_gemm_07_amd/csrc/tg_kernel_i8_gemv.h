@@ -10,8 +10,11 @@
 //  * The loads of a wave's next run are issued before the MFMAs of this one.
 //  * The waves' integer sums are added in LDS.
 //  * Rows past M or N read the last row again; their results are not stored.
-//    Any addresses and strides: 16-byte loads at any byte, zeros past the end
-//    of a row in its last, partial run.
+//    Zeros past the end of a row in its last, partial run.  Any addresses and
+//    strides: rows that do not start at dwords are read in whole dwords and
+//    shifted (SHIFT; W from HBM, 8192 x 8191, one token: 18.7 us, 33.9 with
+//    16-byte loads at any byte; 16 tokens: 27.9 and 59.4; where the rows do
+//    start at dwords it costs up to a quarter more).
 //  * FUSED (tg_linear_i8): A is given in 16 or 32 bits.  Every workgroup
 //    quantises the M rows itself, into LDS, while the loads of its first run
 //    of W are in flight: one launch instead of two, for as few rows as that
@@ -36,7 +39,7 @@ struct I8Source {
     int64_t ldx;
 };
 
-template <int DTX, int MT, int NW, bool FUSED>
+template <int DTX, int MT, int NW, int SHIFT, bool FUSED>
 struct I8Gemv {
     static constexpr int RUN = 256;
     static constexpr int TOKENS = 16 * MT;
@@ -47,49 +50,46 @@ struct I8Gemv {
         return (K + RUN - 1) / RUN * RUN + 16;
     }
 
+    // SHIFT: rows that do not start at dwords, of W (1), of W or A (2)
+    using RowW = Row16<(SHIFT >= 1)>;
+    using RowA = Row16<(SHIFT >= 2)>;
+
     struct Run {
-        u32x4 w[4];
-        u32x4 a[FUSED ? 1 : MT][4];
+        typename RowW::Chunk w[4];
+        typename RowA::Chunk a[FUSED ? 1 : MT][4];
     };
 
-    static __device__ __forceinline__ u32x4 chunk(const int8_t* row, int k, int K, bool whole)
-    {
-        struct __attribute__((packed, aligned(1))) Any {
-            u32x4 v;
-        };
-        return whole ? ((const Any*)(row + k))->v : load16_row(row, k, K);
-    }
-
-    static __device__ __forceinline__ void load(Run& R, const int8_t* w,
-                                                const int8_t* const (&a)[MT], int k0, int K, int g,
-                                                bool whole)
+    static __device__ __forceinline__ void load(Run& R, const RowW& w, const RowA (&a)[MT],
+                                                int k0, int K, int g, bool whole)
     {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int k = k0 + 64 * c + 16 * g;
-            R.w[c] = chunk(w, k, K, whole);
+            R.w[c] = whole ? w.load(k) : w.load_end(k, K);
             if constexpr (!FUSED) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
-                    R.a[m][c] = chunk(a[m], k, K, whole);
+                    R.a[m][c] = whole ? a[m].load(k) : a[m].load_end(k, K);
             }
         }
     }
 
-    static __device__ __forceinline__ void multiply(i32x4 (&acc)[MT], const Run& R,
-                                                    const char* levels, int k0, int g)
+    static __device__ __forceinline__ void multiply(i32x4 (&acc)[MT], const Run& R, const RowW& w,
+                                                    const RowA (&a)[MT], const char* levels, int k0,
+                                                    int g, bool whole)
     {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+            const u32x4 vw = RowW::bytes(R.w[c], whole ? w.s : 0);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                i32x4 a;
+                u32x4 va;
                 if constexpr (FUSED)
-                    a = *(const i32x4*)(levels + k0 + 64 * c + 16 * g);
+                    va = *(const u32x4*)(levels + k0 + 64 * c + 16 * g);
                 else
-                    a = __builtin_bit_cast(i32x4, R.a[m][c]);
-                acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, R.w[c]),
-                                                               a, acc[m], 0, 0, 0);
+                    va = RowA::bytes(R.a[m][c], whole ? a[m].s : 0);
+                acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                    __builtin_bit_cast(i32x4, vw), __builtin_bit_cast(i32x4, va), acc[m], 0, 0, 0);
             }
         }
     }
@@ -165,8 +165,9 @@ struct I8Gemv {
         const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int m0 = (int)blockIdx.y * TOKENS, n0 = (int)blockIdx.x * 16;
         const int ln = lane & 15, g = lane >> 4;
-        const int8_t *wr, *ar[MT];
-        wr = p.W + (int64_t)(n0 + ln < p.N ? n0 + ln : p.N - 1) * p.ldw;
+        RowW wr;
+        RowA ar[MT];
+        wr.at(p.W + (int64_t)(n0 + ln < p.N ? n0 + ln : p.N - 1) * p.ldw);
         const char* levels = nullptr;
         if constexpr (FUSED) {
             levels = gemv_lds + (ln < p.M ? ln : p.M - 1) * level_row(p.K);
@@ -174,7 +175,7 @@ struct I8Gemv {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const int t = m0 + 16 * m + ln;
-                ar[m] = p.A + (int64_t)(t < p.M ? t : p.M - 1) * p.lda;
+                ar[m].at(p.A + (int64_t)(t < p.M ? t : p.M - 1) * p.lda);
             }
         }
         i32x4 acc[MT];
@@ -201,12 +202,12 @@ struct I8Gemv {
             if (next < whole)
                 load(R, wr, ar, next * RUN, p.K, g, true);
             __builtin_amdgcn_sched_barrier(0);
-            multiply(acc, S, levels, r * RUN, g);
+            multiply(acc, S, wr, ar, levels, r * RUN, g, true);
             r = next;
         }
         if (p.K % RUN != 0 && w == whole % NW) {
             load(R, wr, ar, whole * RUN, p.K, g, false);
-            multiply(acc, R, levels, whole * RUN, g);
+            multiply(acc, R, wr, ar, levels, whole * RUN, g, false);
         }
 
         int* red = (int*)gemv_lds;
@@ -233,14 +234,14 @@ struct I8Gemv {
     }
 };
 
-template <int MT, int NW>
+template <int MT, int NW, int SHIFT>
 __global__ __attribute__((amdgpu_flat_work_group_size(NW * 64, NW * 64))) void
 i8_gemv_kernel(I8Params p)
 {
     GemmParams rec{};
     rec.stamps = p.stamps;
     const ClockStamp clk = stamp_begin(rec);
-    I8Gemv<DT_F32, MT, NW, false>::run(p, I8Source{});
+    I8Gemv<DT_F32, MT, NW, SHIFT, false>::run(p, I8Source{});
     stamp_end(rec, clk);
 }
 
@@ -249,14 +250,14 @@ struct I8LinearParams {
     I8Source x;
 };
 
-template <int DTX, int NW>
+template <int DTX, int NW, int SHIFT>
 __global__ __attribute__((amdgpu_flat_work_group_size(NW * 64, NW * 64))) void
 i8_linear_gemv_kernel(I8LinearParams l)
 {
     GemmParams rec{};
     rec.stamps = l.p.stamps;
     const ClockStamp clk = stamp_begin(rec);
-    I8Gemv<DTX, 1, NW, true>::run(l.p, l.x);
+    I8Gemv<DTX, 1, NW, SHIFT, true>::run(l.p, l.x);
     stamp_end(rec, clk);
 }
 
