@@ -153,6 +153,22 @@ def test_product_few_tokens(M, N, K, pad):
     check_product(values(C, F32), A, sa, W, sw, b, F32, False)
 
 
+@pytest.mark.parametrize("M,N,K,pad", [(1500, 2100, 385, 0), (1500, 2100, 384, 1),
+                                       (2100, 2300, 515, 0), (2100, 2300, 512, 1),
+                                       (2100, 2300, 130, 2), (600, 3000, 100, 0),
+                                       (2000, 2050, 770, 0), (2000, 2050, 768, 3),
+                                       (700, 900, 9, 0)])
+def test_product_any_layout_tiles(M, N, K, pad):
+    """Every tile of the kernels for any layout: rows with and without an end of
+    less than a strip, rows shorter than a strip."""
+    A, sa, W, sw, b = make_product(M, N, K, M + N + K)
+    say("gemm_i8 %dx%dx%d pad %d" % (M, N, K, pad))
+    C = binding.gemm_i8(strided(dev(A), pad, 1), dev(sa), strided(dev(W), pad, 1), dev(sw),
+                        bias=dev(b), out_dtype=torch.bfloat16, epilogue="relu")
+    torch.cuda.synchronize()
+    check_product(values(C, BF16), A, sa, W, sw, b, BF16, True)
+
+
 def test_product_largest_sums():
     """The largest magnitudes the sum can take: 128 * 128 * K near 2^31."""
     for M, K in ((3, 131071), (70, 131056)):

@@ -46,20 +46,34 @@ __device__ __forceinline__ u32x4 shift_bytes(u32x4 v, int s)
 // 16 bytes of a row of K at k, from any address (the hardware takes 16-byte
 // loads at any byte), zeros past K.  A chunk across the end is the row's last
 // 16 bytes shifted down, so that it, too, is one load and no branch.
+struct RowEnd {
+    u32x4 v;  // as loaded
+    int s;
+
+    __device__ __forceinline__ void load(const int8_t* row, int k, int K)
+    {
+        struct __attribute__((packed, aligned(1))) Any {
+            u32x4 v;
+        };
+        if (K >= 16) {
+            const int over = k - (K - 16);
+            s = over < 0 ? 0 : (over < 16 ? over : 16);
+            v = ((const Any*)(row + (over < 0 ? k : K - 16)))->v;
+            return;
+        }
+        s = 0;
+        v = u32x4{0, 0, 0, 0};
+        for (int i = 0; k + i < K; ++i)
+            v[i >> 2] |= (u32)(uint8_t)row[k + i] << (8 * (i & 3));
+    }
+    __device__ __forceinline__ u32x4 bytes() const { return shift_bytes(v, s); }
+};
+
 __device__ __forceinline__ u32x4 load16_row(const int8_t* row, int k, int K)
 {
-    struct __attribute__((packed, aligned(1))) Any {
-        u32x4 v;
-    };
-    if (K >= 16) {
-        const int over = k - (K - 16);
-        const int s = over < 0 ? 0 : (over < 16 ? over : 16);
-        return shift_bytes(((const Any*)(row + (over < 0 ? k : K - 16)))->v, s);
-    }
-    u32x4 v = {0, 0, 0, 0};
-    for (int i = 0; k + i < K; ++i)
-        v[i >> 2] |= (u32)(uint8_t)row[k + i] << (8 * (i & 3));
-    return v;
+    RowEnd e;
+    e.load(row, k, K);
+    return e.bytes();
 }
 
 // A row, and 16-byte chunks of it from whole dwords: the hardware takes 16-byte
@@ -84,6 +98,7 @@ struct Row16 {
         x = s ? 16 : 12;
         p = row - s;
     }
+    __device__ __forceinline__ const int8_t* row() const { return p + s; }
     // of a whole chunk (k + 16 <= K), as it was loaded
     __device__ __forceinline__ Chunk load(int k) const
     {
@@ -98,7 +113,7 @@ struct Row16 {
     // across or past the row's end: zeros past K, nothing to shift
     __device__ __forceinline__ Chunk load_end(int k, int K) const
     {
-        return Chunk{load16_row(p + s, k, K), 0};
+        return Chunk{load16_row(row(), k, K), 0};
     }
     static __device__ __forceinline__ u32x4 bytes(const Chunk& c, u32 s)
     {

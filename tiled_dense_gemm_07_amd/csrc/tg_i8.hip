@@ -93,16 +93,21 @@ struct I8Tile {
              (const void*)&tg::i8_dma_kernel<tg::DT_BF16, BM, BN, BK, WGM, WGN, NS, OCC>}, \
             BM, BN, WGM* WGN * 64, PER_CU, T0, ONE, FULL                                   \
     }
-// Kernels for any layout, smaller tiles first.
-#define TG_I8_ANY(BM, BN, PD)                                                  \
+// Kernels for any layout.  Fitted to 156 shapes of odd K (M 17 to 4096): the
+// choice is 0.2% on average above the fastest of the three (15% at most).
+#define TG_I8_ANY(BM, BN, PD, T0, ROUND)                                       \
     {                                                                          \
         "i8_any_" #BM "x" #BN,                                                 \
             {(const void*)&tg::i8_any_kernel<tg::DT_F32, BM, BN, PD>,          \
              (const void*)&tg::i8_any_kernel<tg::DT_F16, BM, BN, PD>,          \
              (const void*)&tg::i8_any_kernel<tg::DT_BF16, BM, BN, PD>},        \
-            BM, BN, 256, 0, 0.0f, 0.0f, 0.0f                                   \
+            BM, BN, 256, 1, T0, ROUND, ROUND                                   \
     }
-const I8Tile kAny[] = {TG_I8_ANY(64, 64, 4), TG_I8_ANY(128, 128, 1)};
+const I8Tile kAny[] = {
+    TG_I8_ANY(64, 64, 2, 3.97f, 0.490f),
+    TG_I8_ANY(64, 128, 1, 5.11f, 0.687f),
+    TG_I8_ANY(128, 128, 1, 6.84f, 0.970f),
+};
 
 const I8Tile kTiles[] = {
     TG_I8_TILE(32, 64, 256, 1, 2, 4, 1, 1, 3.68f, 0.182f, 0.261f),
@@ -153,33 +158,37 @@ struct I8Pick {
 // at most).  Above: the cheapest tile.
 // Rows that do not start at 16-byte boundaries, or K % 16 != 0, leave the
 // streaming kernel, which takes any address (M = 32, 4096 x 4095, levels of
-// linear_i8: 11.4 us, and 26.3 with tiles; 64 x 8192 x 8191: 57.5 and 48.4), and
-// the tiles for any layout: 128 x 128 where they fill most of the card (1024 x
-// 4096 x 4095: 39.7 us, more than 50 with 64 x 64), else 64 x 64 (256 x 4096 x
-// 4095: 24.3 us, more than 36 with 128 x 128).
+// linear_i8: 11.4 us, and 24.8 with tiles; 64 x 8192 x 8191: 57.5 and 47), and
+// the tiles for any layout (256 x 4096 x 4095: 23.2 us with 64 x 64, 30.4 with 64
+// x 128; 512 x 4096 x 4095: 34.8 and 29.0; 4096 x 4096 x 4095: 127 with 128 x
+// 128, 174 with 64 x 128).
+float tile_cost(const I8Tile& t, int64_t M, int64_t N, int64_t K)
+{
+    const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
+    return t.t0 + (float)ceil_div(K, 128) *
+                      (tiles <= 256 ? t.one : t.full * (float)ceil_div(tiles, 256 * t.per_cu));
+}
+
 I8Pick pick_i8(int64_t M, int64_t N, int64_t K, bool aligned, int shift)
 {
     const I8Stream s = stream_i8(M, N, K, shift);
-    if (M <= 16)
-        return {nullptr, s.tokens};
-    float best = M <= 128 ? s.cost : 1e30f;
     I8Pick p{nullptr, s.tokens};
-    if (!aligned) {
-        const int64_t tiles = ceil_div(M, 64) * ceil_div(N, 64);
-        if (best < 3.0f + 4.9e-3f * (float)(K * ceil_div(tiles, 256)))
-            return p;
-        return {ceil_div(M, 128) * ceil_div(N, 128) > 160 ? &kAny[1] : &kAny[0], 0};
-    }
-    for (const I8Tile& t : kTiles) {
-        const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
-        const float strips = (float)ceil_div(K, 128);
-        const float c = t.t0 + strips * (tiles <= 256 ? t.one
-                                                      : t.full * (float)ceil_div(tiles, 256 * t.per_cu));
+    if (M <= 16)
+        return p;
+    float best = M <= 128 ? s.cost : 1e30f;
+    const auto consider = [&](const I8Tile& t) {
+        const float c = tile_cost(t, M, N, K);
         if (c < best) {
             best = c;
             p = {&t, 0};
         }
-    }
+    };
+    if (aligned)
+        for (const I8Tile& t : kTiles)
+            consider(t);
+    else
+        for (const I8Tile& t : kAny)
+            consider(t);
     return p;
 }
 

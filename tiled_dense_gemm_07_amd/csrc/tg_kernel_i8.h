@@ -23,10 +23,16 @@
 //
 // i8_any_kernel: any sizes, strides and addresses (LDS-DMA copies want aligned
 // ones).  Strips of 128 bytes of k go through registers: 16-byte loads at any
-// byte, PD strips ahead, into a two-stage LDS ring.  Measured: 1000 x 1001 x
-// 1003 8.6 us with 64 x 64 tiles and four strips ahead (8.9 with two); 4096 x
-// 4096 x 4095 124 us with 128 x 128 tiles and one strip ahead (180 with two: the
-// registers halve the waves).  Bound by the latency of its loads.
+// byte, PD strips ahead, into a two-stage LDS ring.  Measured (W from HBM): 1000
+// x 1001 x 1003 8.0 us with 64 x 64 tiles, 512 x 4096 x 4095 29 us with 64 x 128,
+// 4096 x 4096 x 4095 127 us with 128 x 128.  Bound by the unit's path to L2: 128
+// bytes of a row that starts anywhere lie in two lines, so 11 bytes reach a
+// unit's registers in a cycle where the aligned copies above bring 22 (the same
+// with rows at dwords, 4092 for 4095: 10 to 20% less time).  Not kept: strips of
+// 256 bytes, three lines for two (256 x 4096 x 4095 21.4 us for 23.2, but 1000 x
+// 1001 x 1003 9.4: half the workgroups fit); whole dwords and a shift, as the
+// streaming kernel does (no gain here: the lines count); 256 x 128 tiles, four
+// strips ahead (within 5%).
 #pragma once
 
 #include "tg_i8.h"
@@ -129,21 +135,86 @@ __device__ __forceinline__ void i8_store_staged(const i32x16 (&acc)[FM][FN], con
     }
 }
 
-// BM x BN tiles, four waves in a 2 x 2 grid.  PD: strips whose loads are in
-// flight or in registers.  One barrier for each strip: a strip is written to
-// the stage that the strip two before it used, which every wave has read by the
-// barrier of the strip between them.
+// BM x BN tiles, four waves in a 2 x 2 grid.  Each step reads a strip's fragments
+// from one LDS stage, multiplies, writes the next strip into the other, which
+// every wave has read by the barrier of the step before, and issues the loads of
+// the strip PD steps on.  The row's end, if it is not a whole strip, is loaded
+// first and multiplied last, so that no load in the loop needs a branch.
 template <int DT, int BM, int BN, int PD>
 struct I8Any {
     static constexpr int BK = 128;
     static constexpr int WTM = BM / 2, WTN = BN / 2;
     static constexpr int FM = WTM / 32, FN = WTN / 32;
     static constexpr int JA = BM / 32, JB = BN / 32;  // chunks of a thread and strip
+    static constexpr int JN = JA > JB ? JA : JB;
     static constexpr int STAGE = (BM + BN) * BK;
+    using Row = Row16<false>;
 
     struct Strip {
-        u32x4 a[JA], b[JB];
+        typename Row::Chunk a[JA], b[JB];
     };
+    struct Rows {
+        Row a[JA], b[JB];
+    };
+
+    static __device__ __forceinline__ void load(Strip& s, const Rows& r, int k)
+    {
+#pragma unroll
+        for (int j = 0; j < JA; ++j)
+            s.a[j] = r.a[j].load(k);
+#pragma unroll
+        for (int j = 0; j < JB; ++j)
+            s.b[j] = r.b[j].load(k);
+    }
+
+    static __device__ __forceinline__ void write(const Strip& s, const Rows& r, lds_char* stage,
+                                                 const u32 (&st)[JN])
+    {
+#pragma unroll
+        for (int j = 0; j < JA; ++j)
+            *(lds_u32x4*)(stage + st[j]) = Row::bytes(s.a[j], r.a[j].s);
+#pragma unroll
+        for (int j = 0; j < JB; ++j)
+            *(lds_u32x4*)(stage + BM * BK + st[j]) = Row::bytes(s.b[j], r.b[j].s);
+    }
+
+    static __device__ __forceinline__ void multiply(i32x16 (&acc)[FM][FN], const lds_char* stage,
+                                                    int lane, int wm0, int wn0)
+    {
+        i32x4 fa[BK / 32][FM], fb[BK / 32][FN];
+#pragma unroll
+        for (int s = 0; s < BK / 32; ++s) {
+            const int ch = 2 * s + (lane >> 5);
+#pragma unroll
+            for (int f = 0; f < FM; ++f) {
+                const int r = wm0 + 32 * f + (lane & 31);
+                fa[s][f] = __builtin_bit_cast(
+                    i32x4, *(const lds_u32x4*)(stage + r * BK + ((ch ^ swz8(r)) << 4)));
+            }
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                const int r = wn0 + 32 * f + (lane & 31);
+                fb[s][f] = __builtin_bit_cast(
+                    i32x4, *(const lds_u32x4*)(stage + BM * BK + r * BK + ((ch ^ swz8(r)) << 4)));
+            }
+        }
+        if constexpr (FM * FN <= 2)  // all reads before the first MFMA waits for one
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < BK / 32; ++s)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int k = 0; k < FN; ++k)
+                    acc[i][k] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[s][k], fa[s][i],
+                                                                     acc[i][k], 0, 0, 0);
+    }
+
+    // the LDS writes and reads of all waves, but not the loads in flight
+    static __device__ __forceinline__ void publish()
+    {
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
 
     static __device__ __forceinline__ void run(const I8Params& p)
     {
@@ -159,38 +230,17 @@ struct I8Any {
         // thread t moves chunk t % 8 of rows t / 8 + 32 j; rows past the end
         // read the last row again (their results are not stored)
         const int c = tid & 7;
-        const int8_t *a[JA], *b[JB];
-        u32 st[JA > JB ? JA : JB];
+        Rows rows;
+        u32 st[JN];
 #pragma unroll
-        for (int j = 0; j < (JA > JB ? JA : JB); ++j) {
+        for (int j = 0; j < JN; ++j) {
             const int r = (tid >> 3) + 32 * j;
             st[j] = r * BK + ((c ^ swz8(r)) << 4);
             if (j < JA)
-                a[j] = p.A + (int64_t)(m0 + r < p.M ? m0 + r : p.M - 1) * p.lda;
+                rows.a[j].at(p.A + (int64_t)(m0 + r < p.M ? m0 + r : p.M - 1) * p.lda);
             if (j < JB)
-                b[j] = p.W + (int64_t)(n0 + r < p.N ? n0 + r : p.N - 1) * p.ldw;
+                rows.b[j].at(p.W + (int64_t)(n0 + r < p.N ? n0 + r : p.N - 1) * p.ldw);
         }
-        const auto load = [&](Strip& s, int t) {
-            struct __attribute__((packed, aligned(1))) Any {
-                u32x4 v;
-            };
-            const int k = t * BK + 16 * c;
-            if ((t + 1) * BK <= p.K) {  // uniform
-#pragma unroll
-                for (int j = 0; j < JA; ++j)
-                    s.a[j] = ((const Any*)(a[j] + k))->v;
-#pragma unroll
-                for (int j = 0; j < JB; ++j)
-                    s.b[j] = ((const Any*)(b[j] + k))->v;
-            } else if (t * BK < p.K) {
-#pragma unroll
-                for (int j = 0; j < JA; ++j)
-                    s.a[j] = load16_row(a[j], k, p.K);
-#pragma unroll
-                for (int j = 0; j < JB; ++j)
-                    s.b[j] = load16_row(b[j], k, p.K);
-            }
-        };
         i32x16 acc[FM][FN];
 #pragma unroll
         for (int i = 0; i < FM; ++i)
@@ -200,54 +250,56 @@ struct I8Any {
                 for (int r = 0; r < 16; ++r)
                     acc[i][j][r] = 0;
 
+        const int KW = p.K / BK;  // whole strips
         const int KT = (p.K + BK - 1) / BK;
-        Strip S[PD];
+        RowEnd ea[JA], eb[JB];
+        if (KT > KW) {
 #pragma unroll
-        for (int j = 0; j < PD; ++j)
-            load(S[j], j);
-        for (int t0 = 0; t0 < KT; t0 += PD) {
+            for (int j = 0; j < JA; ++j)
+                ea[j].load(rows.a[j].row(), KW * BK + 16 * c, p.K);
 #pragma unroll
-            for (int j = 0; j < PD; ++j) {
-                const int t = t0 + j;
-                if (t >= KT)
-                    break;  // uniform
-                lds_char* stage = sm + (t & 1) * STAGE;
+            for (int j = 0; j < JB; ++j)
+                eb[j].load(rows.b[j].row(), KW * BK + 16 * c, p.K);
+        }
+        const auto write_end = [&](lds_char* stage) {
 #pragma unroll
-                for (int i = 0; i < JA; ++i)
-                    *(lds_u32x4*)(stage + st[i]) = S[j].a[i];
+            for (int j = 0; j < JA; ++j)
+                *(lds_u32x4*)(stage + st[j]) = ea[j].bytes();
 #pragma unroll
-                for (int i = 0; i < JB; ++i)
-                    *(lds_u32x4*)(stage + BM * BK + st[i]) = S[j].b[i];
-                load(S[j], t + PD);
-                // the LDS writes of all waves, but not the loads in flight
-                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            for (int j = 0; j < JB; ++j)
+                *(lds_u32x4*)(stage + BM * BK + st[j]) = eb[j].bytes();
+        };
+        if (KW > 0) {
+            // loads past the last whole strip read it again
+            const auto at = [&](int t) { return (t < KW ? t : KW - 1) * BK + 16 * c; };
+            Strip S[PD];
 #pragma unroll
-                for (int s = 0; s < BK / 32; ++s) {
-                    i32x4 fa[FM], fb[FN];
-                    const int ch = 2 * s + (lane >> 5);
+            for (int j = 0; j < PD; ++j)
+                load(S[j], rows, at(j));
+            write(S[0], rows, sm, st);
+            load(S[0], rows, at(PD));
+            publish();
+            for (int t0 = 0; t0 < KT; t0 += PD) {
 #pragma unroll
-                    for (int f = 0; f < FM; ++f) {
-                        const int r = wm0 + 32 * f + (lane & 31);
-                        fa[f] = __builtin_bit_cast(
-                            i32x4, *(const lds_u32x4*)(stage + r * BK + ((ch ^ swz8(r)) << 4)));
-                    }
-#pragma unroll
-                    for (int f = 0; f < FN; ++f) {
-                        const int r = wn0 + 32 * f + (lane & 31);
-                        fb[f] = __builtin_bit_cast(
-                            i32x4, *(const lds_u32x4*)(stage + BM * BK + r * BK +
-                                                       ((ch ^ swz8(r)) << 4)));
-                    }
-#pragma unroll
-                    for (int i = 0; i < FM; ++i)
-#pragma unroll
-                        for (int k = 0; k < FN; ++k)
-                            acc[i][k] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[k], fa[i],
-                                                                             acc[i][k], 0, 0, 0);
+                for (int j = 0; j < PD; ++j) {
+                    const int t = t0 + j;
+                    if (t >= KT)
+                        break;  // uniform
+                    multiply(acc, sm + (t & 1) * STAGE, lane, wm0, wn0);
+                    if (t + 1 < KW)
+                        write(S[(j + 1) % PD], rows, sm + ((t + 1) & 1) * STAGE, st);
+                    else
+                        write_end(sm + ((t + 1) & 1) * STAGE);
+                    load(S[(j + 1) % PD], rows, at(t + 1 + PD));
+                    publish();
                 }
             }
+        } else if (KT > 0) {
+            write_end(sm);
+            publish();
+            multiply(acc, sm, lane, wm0, wn0);
         }
-        __syncthreads();  // the last strips' reads, before the results take their place
+        __syncthreads();  // the last strip's reads, before the results take their place
         constexpr int ES = DT == DT_F32 ? 4 : 2;
         static_assert(4 * 32 * WTN * ES <= 2 * STAGE, "a 32-row stripe for each wave");
         i8_store_staged<DT, FM, FN>(acc, p, m0 + wm0, n0 + wn0, lane, sm + w * (32 * WTN * ES));
@@ -255,7 +307,8 @@ struct I8Any {
 };
 
 template <int DT, int BM, int BN, int PD>
-__global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void i8_any_kernel(I8Params p)
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(2))) void
+i8_any_kernel(I8Params p)
 {
     GemmParams rec{};
     rec.stamps = p.stamps;
