@@ -319,9 +319,11 @@ tg_status tg_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t l
  * quantised as by tg_quant_i8 and W in 8 bits as in tg_gemm_i8.
  *   X: [M][K] of `dtype`, row stride ldx; C: [M][N] of `dtype`, row stride ldc.
  *   workspace: device memory, 16-byte aligned, of at least the size
- *     tg_linear_i8_workspace_size reports (it holds the levels and scales; 0
- *     bytes, and NULL, where the call needs none).  Its contents need not be
- *     kept between calls; calls that share it must not run concurrently.
+ *     tg_linear_i8_workspace_size reports for these sizes (it holds the levels
+ *     and scales and, for some sizes with K % 16 != 0, W with its rows at
+ *     16-byte boundaries; 0 bytes, and NULL, where the call needs none).  Its
+ *     contents need not be kept between calls; calls that share it must not
+ *     run concurrently.
  *   The result has the bits of tg_quant_i8 followed by tg_gemm_i8.
  * Errors: as for those; TG_ERR_WORKSPACE when the workspace is NULL, smaller
  *   than needed or not 16-byte aligned; TG_ERR_ALIAS also when it overlaps an

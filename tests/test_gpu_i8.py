@@ -157,6 +157,7 @@ def test_product_few_tokens(M, N, K, pad):
                                        (2100, 2300, 515, 0), (2100, 2300, 512, 1),
                                        (2100, 2300, 130, 2), (600, 3000, 100, 0),
                                        (2000, 2050, 770, 0), (2000, 2050, 768, 3),
+                                       (2050, 4100, 390, 0), (2050, 4100, 384, 1),
                                        (700, 900, 9, 0)])
 def test_product_any_layout_tiles(M, N, K, pad):
     """Every tile of the kernels for any layout: rows with and without an end of
@@ -368,6 +369,30 @@ def test_linear_rows_at_any_byte(M, N, K, dtype):
         got = binding.linear_i8(x, strided(W, pad, shift), sw, bias=b)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+@TYPES
+@pytest.mark.parametrize("M,N,K", [(300, 300, 2050), (1030, 2000, 1001), (1030, 301, 510),
+                                   (257, 100, 5001), (200, 70, 9007), (130, 40, 33001)])
+def test_linear_copies_weights(M, N, K, dtype):
+    """Sizes where the rows of W are copied to 16-byte boundaries in the
+    workspace: the bits of the product on W as it is, whatever the workspace
+    held, and nothing past the workspace written."""
+    r = np.random.Generator(np.random.PCG64(M + N + K))
+    x = activations(r, M, K, dtype)
+    _, _, W, sw, b = make_product(1, N, K, 3)
+    W, sw, b = dev(W), dev(sw), dev(b)
+    q, s = binding.quant_i8(x)
+    want = binding.gemm_i8(q, s, W, sw, bias=b, out_dtype=torch_dtype(dtype))
+    need = binding.linear_i8_workspace_size(M, N, K, dtype)
+    assert need >= (M + N) * K
+    for pad, shift in ((0, 0), (1, 0), ((-K) % 16, 0), (5, 3)):
+        say("linear_i8 %dx%dx%d %s pad=%d shift=%d" % (M, N, K, DNAME[dtype], pad, shift))
+        ws = torch.full((need + 64,), 0x7F, dtype=torch.uint8, device=DEV)
+        got = binding.linear_i8(x, strided(W, pad, shift), sw, bias=b, workspace=ws[:need])
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        assert bool((ws[need:] == 0x7F).all())
 
 
 def test_linear_workspace_contents_do_not_matter():

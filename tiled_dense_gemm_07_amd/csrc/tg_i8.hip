@@ -60,7 +60,14 @@ tg_status launch_quant(const tg::QuantParams& p, int dtype, hipStream_t stream)
         k = odd ? quant_kernel<tg::DT_BF16, true>(p.K, &threads, &rows)
                 : quant_kernel<tg::DT_BF16, false>(p.K, &threads, &rows);
     tg::QuantParams q = p;
-    return tg::launch_kernel(k, ceil_div(p.M, rows), 1, threads, &q, stream, "quant_i8");
+    int64_t grid = ceil_div(p.M, rows);
+    q.first = (tg::u32)grid;
+    if (p.N > 0) {
+        q.rows = 4 * threads / (p.kq / 16);
+        q.rows = q.rows < 1 ? 1 : q.rows;
+        grid += ceil_div(p.N, q.rows);
+    }
+    return tg::launch_kernel(k, grid, 1, threads, &q, stream, "quant_i8");
 }
 
 constexpr int64_t kMaxStride = kMaxDim / 256;  // of A and W: a tile's offsets fit 31 bits
@@ -149,6 +156,7 @@ I8Stream stream_i8(int64_t M, int64_t N, int64_t K, int shift)
 struct I8Pick {
     const I8Tile* tile;  // NULL: the streaming kernel
     int tokens;          // its workgroup's
+    float cost;
 };
 
 // Up to 16 tokens: the streaming kernel (M = 1, 8192 x 8192: 14.6 us, and 18.4
@@ -172,16 +180,15 @@ float tile_cost(const I8Tile& t, int64_t M, int64_t N, int64_t K)
 I8Pick pick_i8(int64_t M, int64_t N, int64_t K, bool aligned, int shift)
 {
     const I8Stream s = stream_i8(M, N, K, shift);
-    I8Pick p{nullptr, s.tokens};
+    I8Pick p{nullptr, s.tokens, s.cost};
     if (M <= 16)
         return p;
-    float best = M <= 128 ? s.cost : 1e30f;
+    if (M > 128)
+        p.cost = 1e30f;
     const auto consider = [&](const I8Tile& t) {
         const float c = tile_cost(t, M, N, K);
-        if (c < best) {
-            best = c;
-            p = {&t, 0};
-        }
+        if (c < p.cost)
+            p = {&t, 0, c};
     };
     if (aligned)
         for (const I8Tile& t : kTiles)
@@ -220,6 +227,21 @@ tg_status launch_i8(tg::I8Params p, hipStream_t stream)
               32 * p.ldc * es <= kMaxDim;
     return tg::launch_kernel(k.tile->kernel[p.dt_out], (int64_t)p.tiles_m * p.tiles_n, 1,
                              k.tile->threads, &p, stream, k.tile->name);
+}
+
+// tg_linear_i8 with K % 16 != 0: whether W's rows are copied to 16-byte
+// boundaries, for the LDS-DMA tiles, by the launch that quantises.  Measured
+// with the copy and without, both launches: 256 x 1024 x 4095 15.8 us and 20.3,
+// 1000 x 4096 x 4095 29.1 and 40.1, 4096 x 4096 x 4095 73.0 and 118, 64 x 4096 x
+// 4095 18.3 and 18.9, 256 x 8192 x 1023 15.3 and 13.4; by this rule 0.4% above
+// the better of the two on average over 86 shapes (7% at most).
+bool pack_linear(int64_t M, int64_t N, int64_t K)
+{
+    if (K % 16 == 0 || K < 16 || M <= 16)
+        return false;
+    const float copy = 1.5f + (float)N * (float)K / 3e6f;
+    return pick_i8(M, N, ceil_div(K, 16) * 16, true, 0).cost + copy <
+           pick_i8(M, N, K, false, 1).cost;
 }
 
 // tg_linear_i8 in one launch: up to 8 tokens (a wave or more to a row), whose
@@ -287,7 +309,14 @@ tg_status tg_quant_i8(int64_t M, int64_t K, tg_dtype dtype, const void* X, int64
                ss = span1(s, M, 4);
     if (overlap(x, q) || overlap(x, ss) || overlap(q, ss))
         return TG_ERR_ALIAS;
-    tg::QuantParams p{X, Q, s, (int)M, (int)K, ldx, ldq, (int)K};
+    tg::QuantParams p{};
+    p.X = X;
+    p.Q = Q;
+    p.s = s;
+    p.M = (int)M;
+    p.K = p.kq = (int)K;
+    p.ldx = ldx;
+    p.ldq = ldq;
     return launch_quant(p, dtype, (hipStream_t)stream);
 }
 
@@ -340,10 +369,11 @@ tg_status tg_linear_i8_workspace_size(int64_t M, int64_t N, int64_t K, tg_dtype 
         return TG_ERR_BAD_DTYPE;
     if (tg_status st = check_dims(M, N, K))
         return st;
-    // scales, then rows of levels padded to whole 16-byte chunks
+    // scales, then rows of levels (and of W) padded to whole 16-byte chunks
     *bytes = M == 0 || N == 0 || fused_linear(M, K)
                  ? 0
-                 : (size_t)(ceil_div(4 * M, 256) * 256 + M * ceil_div(K, 16) * 16);
+                 : (size_t)(ceil_div(4 * M, 256) * 256 +
+                            (M + (pack_linear(M, N, K) ? N : 0)) * ceil_div(K, 16) * 16);
     return TG_OK;
 }
 
@@ -391,7 +421,24 @@ tg_status tg_linear_i8(int64_t M, int64_t N, int64_t K, tg_dtype dtype, const vo
     const int64_t ldq = ceil_div(K, 16) * 16;
     float* sa = (float*)workspace;
     int8_t* A = (int8_t*)workspace + ceil_div(4 * M, 256) * 256;
-    tg::QuantParams q{X, A, sa, (int)M, (int)K, ldx, ldq, (int)ldq};
+    tg::QuantParams q{};
+    q.X = X;
+    q.Q = A;
+    q.s = sa;
+    q.M = (int)M;
+    q.K = (int)K;
+    q.ldx = ldx;
+    q.ldq = ldq;
+    q.kq = (int)ldq;
+    if (pack_linear(M, N, K)) {
+        q.W = W;
+        q.Wq = A + M * ldq;
+        q.ldw = ldw;
+        q.N = (int)N;
+        p.W = q.Wq;
+        p.ldw = ldq;
+        p.K = (int)ldq;  // zeros past K in both
+    }
     if (tg_status st = launch_quant(q, dtype, (hipStream_t)stream))
         return st;
     p.A = A;

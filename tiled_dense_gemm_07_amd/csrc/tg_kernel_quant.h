@@ -5,6 +5,8 @@
 // x 8192 30.7 us (201 MB, 6.5 TB/s, part of it from the last-level cache), 16 x
 // 8192 2.7 us, which is launch and latency.  The correction of the quotient
 // (three operations an element) hides under the loads.
+// tg_linear_i8 may have the same launch copy W's rows to 16-byte boundaries, in
+// workgroups after those of the activations: 4096 x 4095 6 to 7 us more.
 #pragma once
 
 #include "tg_rows.h"
@@ -18,7 +20,47 @@ struct QuantParams {
     int M, K;
     int64_t ldx, ldq;
     int kq;  // columns of Q to write: past K, zeros
+    // Rows of 8-bit weights that the workgroups from `first` on copy, `rows`
+    // each, to rows of kq bytes, zeros past K (none: first is the grid).
+    const int8_t* W;
+    int8_t* Wq;
+    int64_t ldw;
+    int N, rows;
+    u32 first;
 };
+
+// Copies rows of W from any address to 16-byte boundaries, a chunk to a thread,
+// four of them in flight (K >= 16).
+template <int NT>
+__device__ __forceinline__ void pack_rows(const QuantParams& p, int block)
+{
+    struct __attribute__((packed, aligned(1))) Any {
+        u32x4 v;
+    };
+    constexpr int U = 4;
+    const int n0 = block * p.rows;
+    const int8_t* W = p.W + (int64_t)n0 * p.ldw;
+    u32x4* to = (u32x4*)(p.Wq + (int64_t)n0 * p.kq);
+    const int per = p.kq / 16;
+    const int rows = p.N - n0 < p.rows ? p.N - n0 : p.rows;
+    const int total = rows * per;
+    for (int i0 = threadIdx.x; i0 < total; i0 += U * NT) {
+        u32x4 v[U];
+        int s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * NT < total ? i0 + u * NT : total - 1;
+            const int n = i / per, k = 16 * (i - n * per);
+            const int over = k - (p.K - 16);  // a chunk across the end, as load16_row
+            s[u] = over < 0 ? 0 : over;
+            v[u] = ((const Any*)(W + n * p.ldw + (over < 0 ? k : p.K - 16)))->v;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * NT < total)
+                to[i0 + u * NT] = shift_bytes(v[u], s[u]);
+    }
+}
 
 template <int DT>
 __device__ __forceinline__ void quant_chunk(const Raw8<DT>& r, const RowLevels& L, int8_t* row,
@@ -51,6 +93,10 @@ template <int DT, int NT, int TPR, int NC, bool ODD>
 __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void quant_i8_kernel(QuantParams p)
 {
     __shared__ u32 slot[16];
+    if (blockIdx.x >= p.first) {
+        pack_rows<NT>(p, (int)(blockIdx.x - p.first));
+        return;
+    }
     const int t = threadIdx.x % TPR;
     const u32 row =
         blockIdx.x * (NT / TPR) + (u32)__builtin_amdgcn_readfirstlane((int)(threadIdx.x / TPR));
