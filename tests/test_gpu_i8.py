@@ -170,6 +170,31 @@ def test_product_any_layout_tiles(M, N, K, pad):
     check_product(values(C, BF16), A, sa, W, sw, b, BF16, True)
 
 
+@pytest.mark.parametrize("M,N,K", [(4100, 4096, 1024), (4096, 4097, 1008), (4000, 4300, 640),
+                                   (16385, 1024, 1024), (1000, 16640, 1024)])
+def test_product_in_two_launches(M, N, K):
+    """A few rows or columns more than whole rounds of the largest tiles."""
+    assert " + " in binding.query_config(4, M, N, K)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(M + N + K)
+    A = torch.randint(-128, 128, (M, K), dtype=torch.int8, device=DEV, generator=g)
+    W = torch.randint(-128, 128, (N, K), dtype=torch.int8, device=DEV, generator=g)
+    sa = 2.0 ** torch.randint(-6, 2, (M,), device=DEV, generator=g).float()
+    sw = 2.0 ** torch.randint(-9, -3, (N,), device=DEV, generator=g).float()
+    b = torch.randint(-4, 5, (N,), device=DEV, generator=g).float()
+    say("gemm_i8 %dx%dx%d" % (M, N, K))
+    for bias in (None, b):
+        C = binding.gemm_i8(A, sa, W, sw, bias=bias, out_dtype=torch.float32, epilogue="relu")
+        torch.cuda.synchronize()
+        # sums up to 2^24 and scales that are powers of two: exact in fp32 but
+        # for the bias, one rounding of the sum
+        want = (A.cpu().float() @ W.cpu().float().t()).double()
+        want = want * sa.cpu().double()[:, None] * sw.cpu().double()
+        if bias is not None:
+            want = want + b.cpu().double()
+        assert torch.equal(C.cpu(), want.clamp(min=0).float())
+
+
 def test_product_largest_sums():
     """The largest magnitudes the sum can take: 128 * 128 * K near 2^31."""
     for M, K in ((3, 131071), (70, 131056)):

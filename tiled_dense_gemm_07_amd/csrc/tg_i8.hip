@@ -157,6 +157,7 @@ struct I8Pick {
     const I8Tile* tile;  // NULL: the streaming kernel
     int tokens;          // its workgroup's
     float cost;
+    int64_t m1, n1;  // of the first launch; a second one takes what is left of M or N
 };
 
 // Up to 16 tokens: the streaming kernel (M = 1, 8192 x 8192: 14.6 us, and 18.4
@@ -177,18 +178,37 @@ float tile_cost(const I8Tile& t, int64_t M, int64_t N, int64_t K)
                       (tiles <= 256 ? t.one : t.full * (float)ceil_div(tiles, 256 * t.per_cu));
 }
 
-I8Pick pick_i8(int64_t M, int64_t N, int64_t K, bool aligned, int shift)
+// Where the last round of 256 x 256 tiles is less than half full, the rounds before
+// it and, in a second launch, whatever is best for the rows or columns left, if
+// that costs a tenth less (4096 x 4224 x 4096: 68 us, 90 in one launch; 4096 x
+// 4097 x 1024: 31 and 38; 6000 x 6000 x 2000: 90 and 99).  Not for the smaller
+// tiles, whose last workgroups find the paths to L2 free (1088 x 4096 x 4096 with
+// 128 x 128: 30 us, 27.5 in one launch).
+I8Pick pick_i8(int64_t M, int64_t N, int64_t K, bool aligned, int shift, bool one_launch = false)
 {
     const I8Stream s = stream_i8(M, N, K, shift);
-    I8Pick p{nullptr, s.tokens, s.cost};
+    I8Pick p{nullptr, s.tokens, s.cost, M, N};
     if (M <= 16)
         return p;
     if (M > 128)
         p.cost = 1e30f;
+    const auto take = [&](const I8Tile& t, float cost, int64_t m1, int64_t n1) {
+        if (cost < p.cost)
+            p = {&t, 0, cost, m1, n1};
+    };
     const auto consider = [&](const I8Tile& t) {
-        const float c = tile_cost(t, M, N, K);
-        if (c < p.cost)
-            p = {&t, 0, c};
+        take(t, tile_cost(t, M, N, K), M, N);
+        const int64_t tm = ceil_div(M, t.bm), tn = ceil_div(N, t.bn), round = 256 * t.per_cu;
+        const int64_t left = tm * tn % round, whole = tm * tn - left;
+        if (one_launch || t.bm < 256 || whole == 0 || left == 0 || 2 * left >= round)
+            return;
+        const int64_t n1 = whole / tm * t.bn, m1 = whole / tn * t.bm;
+        if (n1 > 0)
+            take(t, 1.1f * (tile_cost(t, M, n1, K) +
+                            pick_i8(M, N - n1, K, aligned, shift, true).cost), M, n1);
+        if (m1 > 0)
+            take(t, 1.1f * (tile_cost(t, m1, N, K) +
+                            pick_i8(M - m1, N, K, aligned, shift, true).cost), m1, N);
     };
     if (aligned)
         for (const I8Tile& t : kTiles)
@@ -203,13 +223,8 @@ I8Pick pick_i8(int64_t M, int64_t N, int64_t K, bool aligned, int shift)
 // boundaries.
 bool dma_rows(const void* p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && ld % 16 == 0; }
 
-tg_status launch_i8(tg::I8Params p, hipStream_t stream)
+tg_status launch_pick(tg::I8Params p, const I8Pick& k, int shift, hipStream_t stream)
 {
-    p.stamps = tg::clock_stamps();
-    const int es = tg::dtype_size(p.dt_out);
-    const bool aligned = p.K > 0 && p.K % 16 == 0 && dma_rows(p.A, p.lda) && dma_rows(p.W, p.ldw);
-    const int shift = shift_i8(p.A, p.lda, p.W, p.ldw);
-    const I8Pick k = pick_i8(p.M, p.N, p.K, aligned, shift);
     if (!k.tile) {
         static const void* const kernels[3][2] = {
             {(const void*)&tg::i8_gemv_kernel<1, 8, 0>, (const void*)&tg::i8_gemv_kernel<2, 8, 0>},
@@ -220,6 +235,7 @@ tg_status launch_i8(tg::I8Params p, hipStream_t stream)
                                  512, &p, stream, "i8_gemv", 8 * mt * 1024);
     }
     // Tile order: patches of 4 tile rows, as the 16-bit kernels' largest tiles.
+    const int es = tg::dtype_size(p.dt_out);
     p.group_m = tg::swizzle_override() > 0 ? tg::swizzle_override() : 4;
     p.tiles_m = (int)ceil_div(p.M, k.tile->bm);
     p.tiles_n = (int)ceil_div(p.N, k.tile->bn);
@@ -227,6 +243,32 @@ tg_status launch_i8(tg::I8Params p, hipStream_t stream)
               32 * p.ldc * es <= kMaxDim;
     return tg::launch_kernel(k.tile->kernel[p.dt_out], (int64_t)p.tiles_m * p.tiles_n, 1,
                              k.tile->threads, &p, stream, k.tile->name);
+}
+
+tg_status launch_i8(tg::I8Params p, hipStream_t stream)
+{
+    p.stamps = tg::clock_stamps();
+    const bool aligned = p.K > 0 && p.K % 16 == 0 && dma_rows(p.A, p.lda) && dma_rows(p.W, p.ldw);
+    const int shift = shift_i8(p.A, p.lda, p.W, p.ldw);
+    const I8Pick k = pick_i8(p.M, p.N, p.K, aligned, shift);
+    tg::I8Params rest = p;
+    p.M = (int)k.m1;
+    p.N = (int)k.n1;
+    if (tg_status st = launch_pick(p, k, shift, stream))
+        return st;
+    if (rest.M == p.M && rest.N == p.N)
+        return TG_OK;
+    const int64_t m = rest.M == p.M ? 0 : p.M, n = rest.N == p.N ? 0 : p.N;
+    rest.M -= (int)m;
+    rest.N -= (int)n;
+    rest.A += m * p.lda;
+    rest.sa += m;
+    rest.W += n * p.ldw;
+    rest.sw += n;
+    rest.bias = p.bias ? p.bias + n : nullptr;
+    rest.C = (char*)p.C + (m * p.ldc + n) * tg::dtype_size(p.dt_out);
+    rest.stamps = nullptr;  // the record is the first launch's
+    return launch_pick(rest, pick_i8(rest.M, rest.N, rest.K, aligned, shift, true), shift, stream);
 }
 
 // tg_linear_i8 with K % 16 != 0: whether W's rows are copied to 16-byte
@@ -281,13 +323,24 @@ namespace tg {
 
 void describe_i8(int64_t M, int64_t N, int64_t K, char* buf, size_t len)
 {
-    const I8Pick k = pick_i8(M, N, K, K > 0 && K % 16 == 0, shift_i8(nullptr, K, nullptr, K));
-    if (!k.tile)
-        snprintf(buf, len, "i8_gemv_%d grid=%lldx%lld threads=512", k.tokens,
-                 (long long)ceil_div(N, 16), (long long)ceil_div(M, k.tokens));
-    else
-        snprintf(buf, len, "%s grid=%lld threads=%d", k.tile->name,
-                 (long long)(ceil_div(M, k.tile->bm) * ceil_div(N, k.tile->bn)), k.tile->threads);
+    const bool aligned = K > 0 && K % 16 == 0;
+    const int shift = shift_i8(nullptr, K, nullptr, K);
+    const auto one = [&](const I8Pick& k, int64_t m, int64_t n, char* to, size_t room) {
+        return k.tile ? snprintf(to, room, "%s grid=%lld threads=%d", k.tile->name,
+                                 (long long)(ceil_div(m, k.tile->bm) * ceil_div(n, k.tile->bn)),
+                                 k.tile->threads)
+                      : snprintf(to, room, "i8_gemv_%d grid=%lldx%lld threads=512", k.tokens,
+                                 (long long)ceil_div(n, 16), (long long)ceil_div(m, k.tokens));
+    };
+    const I8Pick k = pick_i8(M, N, K, aligned, shift);
+    int at = one(k, k.m1, k.n1, buf, len);
+    if (k.m1 == M && k.n1 == N)
+        return;
+    const int64_t m = k.m1 == M ? M : M - k.m1, n = k.n1 == N ? N : N - k.n1;
+    if (at >= 0 && (size_t)at < len)
+        at += snprintf(buf + at, len - at, " + ");
+    if (at >= 0 && (size_t)at < len)
+        one(pick_i8(m, n, K, aligned, shift, true), m, n, buf + at, len - at);
 }
 
 }  // namespace tg
