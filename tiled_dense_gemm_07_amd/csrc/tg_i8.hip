@@ -125,10 +125,19 @@ const I8Tile kTiles[] = {
     TG_I8_TILE(256, 256, 128, 2, 4, 2, 2, 1, 6.00f, 1.250f, 1.820f),
 };
 
+float tile_cost(const I8Tile& t, int64_t M, int64_t N, int64_t K)
+{
+    const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
+    return t.t0 + (float)ceil_div(K, 128) *
+                      (tiles <= 256 ? t.one : t.full * (float)ceil_div(tiles, 256 * t.per_cu));
+}
+
 // Rows of W (1), or of A or both (2), that do not start at dwords.
 int shift_i8(const void* A, int64_t lda, const void* W, int64_t ldw)
 {
-    const auto off = [](const void* p, int64_t ld) { return (((uintptr_t)p | (uint64_t)ld) & 3) != 0; };
+    const auto off = [](const void* p, int64_t ld) {
+        return (((uintptr_t)p | (uint64_t)ld) & 3) != 0;
+    };
     return off(A, lda) ? 2 : (off(W, ldw) ? 1 : 0);
 }
 
@@ -171,13 +180,6 @@ struct I8Pick {
 // the tiles for any layout (256 x 4096 x 4095: 23.2 us with 64 x 64, 30.4 with 64
 // x 128; 512 x 4096 x 4095: 34.8 and 29.0; 4096 x 4096 x 4095: 127 with 128 x
 // 128, 174 with 64 x 128).
-float tile_cost(const I8Tile& t, int64_t M, int64_t N, int64_t K)
-{
-    const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
-    return t.t0 + (float)ceil_div(K, 128) *
-                      (tiles <= 256 ? t.one : t.full * (float)ceil_div(tiles, 256 * t.per_cu));
-}
-
 // Where the last round of 256 x 256 tiles is less than half full, the rounds before
 // it and, in a second launch, whatever is best for the rows or columns left, if
 // that costs a tenth less (4096 x 4224 x 4096: 68 us, 90 in one launch; 4096 x
