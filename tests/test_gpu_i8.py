@@ -452,7 +452,8 @@ def test_linear_rows_that_are_not_finite():
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 256, 1024), (16, 256, 1024), (64, 256, 512),
-                                   (300, 512, 512)])
+                                   (300, 512, 512), (300, 300, 2050), (8, 100, 1003),
+                                   (4100, 4096, 1024)])
 def test_stream_and_graph(M, N, K):
     """On a side stream, and captured and replayed with new inputs between
     eager calls: the same bits as the eager call on the null stream."""
