@@ -347,7 +347,8 @@ tg_status tg_linear_i8_workspace_size(int64_t M, int64_t N, int64_t K, tg_dtype 
  *   x, x_out: [T][D] of `xtype`; y, h: [T][D] of `btype`; gate: [ceil(T /
  *     gate_rows)][D], w_post, w_pre: [D], of `btype`, dense.  (xtype, btype):
  *     equal, or TG_F32 with TG_F16 or TG_BF16.  Row strides in elements.
- *   y NULL: there is no block before; x_out must be NULL, h = norm(x) * w_pre.
+ *   y NULL: there is no block before; x_out must be NULL, h = norm(x) * w_pre
+ *     (alpha has no part in it).
  *   post_norm 0: y[t] stands in place of norm(y[t]) * w_post (w_post NULL).
  *   gate, w_post, w_pre NULL: ones.
  *   h, hq: either, both or (x_out not NULL) neither.  hq: int8 [T][D] with
@@ -396,7 +397,8 @@ tg_status tg_block_norm(const tg_block_norm_args* args, tg_stream_t stream);
 
 /*
  * Gradients of tg_block_norm (h as h; the 8-bit h has none).  In: x_new, the
- * x_out of the forward call (its x when y is NULL), y, gate, gate_rows,
+ * x_out of the forward call (its x when y is NULL: dx is then the gradient at
+ * x_new, whatever alpha is), y, gate, gate_rows,
  * w_post, w_pre, alpha, post_norm and the saved r_post, r_pre; the gradients
  * dx_new at x_out and dh at h (either may be NULL: zeros).  Out, each NULL if
  * not wanted:

@@ -693,7 +693,7 @@ def block_norm(x, y=None, gate=None, gate_rows=None, w_post=None, w_pre=None, al
         x' = alpha x + gate * norm(y) * w_post,   h = norm(x') * w_pre
 
     x [T, D]: residual stream; y [T, D]: output of the block before (None: x'
-    is x); gate [G, D], one row for gate_rows tokens.  out: "h" (h in y's
+    is x, whatever alpha is); gate [G, D], one row for gate_rows tokens.  out: "h" (h in y's
     type, x's without y), "i8" (h as int8 levels with scales hs) or None (x'
     only).  x_out may be x.  save: also return the norms' reciprocal roots
     for :func:`block_norm_backward`.  Returns a BlockNorm(x, h, hs, r_post,

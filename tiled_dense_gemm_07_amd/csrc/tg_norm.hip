@@ -338,7 +338,7 @@ tg_status tg_block_norm_backward(const tg_block_norm_grad_args* a, void* workspa
     p.D = (int)D;
     p.Dp = (int)g.Dp;
     p.post = a->y && a->post_norm;
-    p.alpha = a->alpha;
+    p.alpha = a->y ? a->alpha : 1.0f;  // without y, x' is x
     const Pick k = pick_backward(D, a->xtype, a->btype);
     if (tg_status s = tg::launch_kernel(k.kernel, g.P, 1, k.threads, &p, (hipStream_t)stream,
                                         "block_norm_grad"))
