@@ -6,7 +6,8 @@ from __future__ import annotations
 import pytest
 
 from gpu_helpers import say
-from test_gpu_block_norm import DNAME, EPS, by_pair, check_backward, check_forward, operands, run_backward
+from test_gpu_block_norm import (DEV, DNAME, EPS, by_pair, check_backward, check_forward,
+                                 operands, run_backward)
 from tiled_dense_gemm_07_amd import binding
 
 torch = pytest.importorskip("torch")
@@ -39,3 +40,33 @@ def test_norm_alone_has_no_alpha(xt, bt):
     same = run_backward(s, f, xt, bt, 0, 1.0, False)
     torch.cuda.synchronize()
     assert torch.equal(g.dx, same.dx) and torch.equal(g.dw_pre, same.dw_pre)
+
+
+# --------------------------------------------------------------------------
+# empty batches and empty rows
+# --------------------------------------------------------------------------
+def dirty(n):
+    """Leaves n freed blocks of NaN for the allocator's next requests."""
+    junk = [torch.full((4, 64), float("nan"), device=DEV) for _ in range(n)]
+    torch.cuda.synchronize()
+    del junk
+
+
+@pytest.mark.parametrize("shape", [(64,), (1, 64)], ids=["vector", "row"])
+@pytest.mark.parametrize("gate_rows", [4])
+def test_no_tokens_with_a_shared_gate(shape, gate_rows):
+    """T = 0: a gate that every token shares is taken as for any other T, and its
+    gradient, a sum over no tokens, is zero."""
+    x = torch.zeros((0, 64), dtype=torch.bfloat16, device=DEV)
+    gate = torch.ones(shape, dtype=torch.bfloat16, device=DEV)
+    w, r = x.new_ones(64), torch.zeros(0, device=DEV)
+    say("block_norm T = 0, shared gate %s, gate_rows %s" % (shape, gate_rows))
+    f = binding.block_norm(x, y=x, gate=gate, gate_rows=gate_rows, w_post=w, w_pre=w)
+    assert f.x.shape == (0, 64) and f.h.shape == (0, 64)
+    dirty(8)
+    g = binding.block_norm_backward(x, x, x, y=x, gate=gate, gate_rows=gate_rows, w_post=w,
+                                    w_pre=w, r_post=r, r_pre=r)
+    torch.cuda.synchronize()
+    assert g.dgate.shape == shape and g.dgate.dtype == torch.float32
+    for t in (g.dgate, g.dw_post, g.dw_pre):
+        assert bool((t == 0).all())

@@ -801,7 +801,7 @@ def block_norm_backward(x_new, dx_new=None, dh=None, y=None, gate=None, gate_row
         a.dx_new, a.lddx_new = dx_new.data_ptr(), _rows("dx_new", dx_new, shape, xt)
     if T == 0:  # sums over no tokens; nothing is launched
         with torch.cuda.stream(stream):
-            for g in (dw_post, dw_pre):
+            for g in (dgate, dw_post, dw_pre):
                 if g is not None:
                     g.zero_()
     lib = load_library()
