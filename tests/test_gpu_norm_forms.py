@@ -53,7 +53,7 @@ def dirty(n):
 
 
 @pytest.mark.parametrize("shape", [(64,), (1, 64)], ids=["vector", "row"])
-@pytest.mark.parametrize("gate_rows", [4])
+@pytest.mark.parametrize("gate_rows", [None, 4])
 def test_no_tokens_with_a_shared_gate(shape, gate_rows):
     """T = 0: a gate that every token shares is taken as for any other T, and its
     gradient, a sum over no tokens, is zero."""
@@ -70,3 +70,12 @@ def test_no_tokens_with_a_shared_gate(shape, gate_rows):
     assert g.dgate.shape == shape and g.dgate.dtype == torch.float32
     for t in (g.dgate, g.dw_post, g.dw_pre):
         assert bool((t == 0).all())
+
+
+def test_no_tokens_through_a_stack():
+    from tiled_dense_gemm_07_amd.int8_block import Int8Stack
+
+    stack = Int8Stack(64, 128, 2)
+    x = torch.zeros((0, 64), dtype=torch.bfloat16, device=DEV)
+    say("int8 stack of no tokens")
+    assert stack.serve(x).shape == (0, 64)

@@ -39,3 +39,29 @@ def test_reference_gradients_by_differences(alone, alpha):
         d = (loss({**v, k: v[k] + e * step}) - loss({**v, k: v[k] - e * step})) / (2 * e)
         # the difference's own error: e^2 times third derivatives, and 2^-52 / e
         assert abs(d - (g[name] * step).sum()) <= 1e-6 * max(1.0, abs(d)), name
+
+
+class FakeGate:
+    """What the argument check asks of a gate on the GPU."""
+
+    is_cuda, dtype = True, "bf16"
+
+    def __init__(self, *shape):
+        self.shape = shape
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x1000
+
+
+def test_shared_gate_of_no_tokens():
+    for shape in ((16,), (1, 16)):
+        for rows in (None, 0, 4):
+            p, per = binding._gate_arg(FakeGate(*shape), rows, 0, 16, "bf16")
+            assert p == 0x1000 and per >= 1
+    p, per = binding._gate_arg(FakeGate(0, 16), None, 0, 16, "bf16")
+    assert per == 1
+    with pytest.raises(ValueError, match="gate must be"):
+        binding._gate_arg(FakeGate(15), None, 0, 16, "bf16")

@@ -675,7 +675,7 @@ def _gate_arg(gate, gate_rows, T, D, dtype):
     if not gate_rows:
         if G != 1 and G != T:
             raise ValueError("gate_rows is needed: gate has %d rows for %d tokens" % (G, T))
-        gate_rows = T if G == 1 else 1
+        gate_rows = max(T, 1) if G == 1 else 1
     if not gate.is_cuda or not gate.is_contiguous():
         raise ValueError("gate must be a dense GPU tensor")
     if gate.dtype != dtype:
