@@ -360,8 +360,8 @@ tg_status tg_linear_i8_workspace_size(int64_t M, int64_t N, int64_t K, tg_dtype 
  * Sums and intermediate values are fp32; x_out is rounded to xtype, and h is
  * computed from the rounded x_out, so that the call equals one that computes
  * x_out and one that computes h from it, bit for bit.
- * D <= 32768, T <= 2^30.  T == 0 or D == 0: nothing is launched.  A row of
- * zeros with eps 0 has no norm (NaN).
+ * D <= 32768, T <= 2^30.  T == 0 or D == 0: nothing is launched (with D == 0, hs,
+ * r_post and r_pre are not written).  A row of zeros with eps 0 has no norm (NaN).
  * Errors: TG_ERR_BAD_DTYPE, TG_ERR_BAD_SHAPE (sizes, strides below D,
  *   gate_rows < 1 with a gate), TG_ERR_NULL_POINTER (x, or nothing to write,
  *   or hq without hs or the reverse, x_out NULL with y), TG_ERR_BAD_LAYOUT (x_out, gate, w_post

@@ -79,3 +79,25 @@ def test_no_tokens_through_a_stack():
     x = torch.zeros((0, 64), dtype=torch.bfloat16, device=DEV)
     say("int8 stack of no tokens")
     assert stack.serve(x).shape == (0, 64)
+
+
+@pytest.mark.parametrize("residual", [False, True])
+def test_rows_of_no_elements(residual):
+    """D = 0: 8-bit h has the scale quant_i8 gives an empty row, the product
+    taken from it is its bias, and the norms' r is NaN (the mean of nothing)."""
+    x = torch.zeros((5, 0), dtype=torch.bfloat16, device=DEV)
+    dirty(8)
+    say("block_norm D = 0")
+    f = binding.block_norm(x, y=x if residual else None, out="i8", save=True)
+    s = torch.full((5,), float("nan"), device=DEV)
+    g = binding.block_norm(x, y=x if residual else None, out="i8", hs=s)
+    torch.cuda.synchronize()
+    assert f.h.shape == (5, 0) and bool((f.hs == 2.0 ** -126).all())
+    assert g.hs is s and bool((s == 2.0 ** -126).all())
+    assert bool((binding.quant_i8(x)[1] == f.hs).all())
+    assert bool(f.r_pre.isnan().all()) and (not residual or bool(f.r_post.isnan().all()))
+    w = torch.zeros((7, 0), dtype=torch.int8, device=DEV)
+    b = torch.arange(7, device=DEV, dtype=torch.float32)
+    c = binding.gemm_i8(f.h, f.hs, w, torch.ones(7, device=DEV), bias=b)
+    torch.cuda.synchronize()
+    assert bool((c.float() == b).all())

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import math
 import os
 
 import numpy as np
@@ -744,6 +745,11 @@ def block_norm(x, y=None, gate=None, gate_rows=None, w_post=None, w_pre=None, al
             r_pre = _empty((T,), torch.float32, x, stream)
             a.r_pre = r_pre.data_ptr()
     _one_device(x, y, gate, w_post, w_pre, x_out, h, hs)
+    if D == 0:  # nothing is launched: the scale of an empty row, a mean of nothing
+        with torch.cuda.stream(stream):
+            for t, v in ((hs, 2.0 ** -126), (r_post, math.nan), (r_pre, math.nan)):
+                if t is not None:
+                    t.fill_(v)
     _check(load_library().tg_block_norm(ctypes.byref(a), _stream_ptr(x.device, stream)))
     return BlockNorm(x if x_out is None else x_out, h, hs, r_post, r_pre)
 
