@@ -65,3 +65,15 @@ def test_shared_gate_of_no_tokens():
     assert per == 1
     with pytest.raises(ValueError, match="gate must be"):
         binding._gate_arg(FakeGate(15), None, 0, 16, "bf16")
+
+
+def test_buffers_that_a_call_would_not_write():
+    """h without an output for it, and scales without levels, are refused: their
+    old contents would stand in the result."""
+    torch = pytest.importorskip("torch")
+    x, s = torch.zeros(4, 16), torch.zeros(4)
+    with pytest.raises(ValueError, match="h is not written"):
+        binding.block_norm(x, y=x, out=None, h=x)
+    for out in ("h", None):
+        with pytest.raises(ValueError, match="hs is not written"):
+            binding.block_norm(x, y=x, out=out, hs=s)

@@ -702,6 +702,10 @@ def block_norm(x, y=None, gate=None, gate_rows=None, w_post=None, w_pre=None, al
     torch = _torch()
     if out not in ("h", "i8", None):
         raise ValueError("out must be 'h', 'i8' or None")
+    if out is None and h is not None:
+        raise ValueError("h is not written with out None")
+    if out != "i8" and hs is not None:
+        raise ValueError("hs is not written without out 'i8'")
     ldx = _rows("x", x)
     shape = x.shape
     T, D = shape
