@@ -5,7 +5,7 @@ from __future__ import annotations
 
 import pytest
 
-from gpu_helpers import say
+from gpu_helpers import BF16, say
 from test_gpu_block_norm import (DEV, DNAME, EPS, by_pair, check_backward, check_forward,
                                  operands, run_backward)
 from tiled_dense_gemm_07_amd import binding
@@ -101,3 +101,49 @@ def test_rows_of_no_elements(residual):
     c = binding.gemm_i8(f.h, f.hs, w, torch.ones(7, device=DEV), bias=b)
     torch.cuda.synchronize()
     assert bool((c.float() == b).all())
+
+
+# --------------------------------------------------------------------------
+# the plain residual
+# --------------------------------------------------------------------------
+@by_pair
+@pytest.mark.parametrize("D", [1, 513, 1000, 2047, 4096, 4099, 8200, 16384, 32767])
+def test_plain_residual(D, xt, bt):
+    """h, 8-bit h and the gradients of x' = alpha x + y, few rows and (in parts,
+    with several rows to a team) many."""
+    for T, alpha in ((3, 1.0), (700 if D <= 1000 else 19, 0.75)):
+        s = operands(T, D, xt, bt, 0, False, D + T)
+        say("block_norm x + y %dx%d %s/%s" % (T, D, DNAME[xt], DNAME[bt]))
+        kw = dict(y=s["y"], w_pre=s["w_pre"], alpha=alpha, eps=EPS, post_norm=False)
+        f = binding.block_norm(s["x"], save=True, **kw)
+        q = binding.block_norm(s["x"], out="i8", **kw)
+        torch.cuda.synchronize()
+        assert f.r_post is None and torch.equal(f.x, q.x)
+        check_forward(s, f, xt, bt, 0, alpha, False)
+        check_forward(s, q, xt, bt, 0, alpha, False)
+        say("block_norm_backward x + y %dx%d %s/%s" % (T, D, DNAME[xt], DNAME[bt]))
+        g = run_backward(s, f, xt, bt, 0, alpha, False)
+        torch.cuda.synchronize()
+        assert g.dgate is None and g.dw_post is None
+        check_backward(s, f, g, xt, bt, 0, alpha, False)
+
+
+# --------------------------------------------------------------------------
+# the example's training step
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("tokens", [1, 40, 333])
+def test_boundary_step_values(tokens):
+    """The stack's training step of one boundary, every output, against the
+    64-bit forms."""
+    from tiled_dense_gemm_07_amd.int8_block import Int8Stack
+
+    D, alpha = 512, 0.9
+    stack = Int8Stack(D, 1024, 2, alpha=alpha)
+    s = operands(tokens, D, BF16, BF16, 0, False, 51)
+    a, b = stack.layers[1], stack.layers[0]
+    s.update(gate=a["gate"][None], w_post=a["w_post"], w_pre=b["w_pre"])
+    say("int8 stack boundary step, %d tokens" % tokens)
+    f, g = stack.boundary_step(s["x"], s["y"], s["dx_new"], s["dh"], layer=1)
+    torch.cuda.synchronize()
+    check_forward(s, f, BF16, BF16, tokens, alpha, True)
+    check_backward(s, f, g, BF16, BF16, tokens, alpha, True)
