@@ -352,9 +352,12 @@ tg_status tg_linear_i8_workspace_size(int64_t M, int64_t N, int64_t K, tg_dtype 
  *   post_norm 0: y[t] stands in place of norm(y[t]) * w_post (w_post NULL).
  *   gate, w_post, w_pre NULL: ones.
  *   h, hq: either, both or (x_out not NULL) neither.  hq: int8 [T][D] with
- *     fp32 scales hs [T]: h quantised as by tg_quant_i8 from its fp32 values,
- *     which tg_gemm_i8 takes as A and sa.  (A value within an fp32 rounding of
- *     the border between two levels may get either.)
+ *     fp32 scales hs [T], as tg_gemm_i8 takes them as A and sa: h quantised as
+ *     by tg_quant_i8.  The levels are the exact ones of norm(x_out) * w_pre, ties
+ *     to even: r is one factor of the row and has no part in them, nor has any
+ *     rounding of h.  (Only where x_out and w_pre are both fp32 may a value
+ *     within a 64-bit rounding of the border between two levels get either, and in
+ *     a row whose scale is the least one a value within an fp32 rounding of it.)
  *   r_post, r_pre: fp32 [T] or NULL: the norms' r, for the gradients.
  *   x_out may be x itself (same address and stride).
  * Sums and intermediate values are fp32; x_out is rounded to xtype, and h is

@@ -3,10 +3,11 @@ forms."""
 
 from __future__ import annotations
 
+import numpy as np
 import pytest
 
-from gpu_helpers import BF16, say
-from test_gpu_block_norm import (DEV, DNAME, EPS, by_pair, check_backward, check_forward,
+from gpu_helpers import BF16, F32, say
+from test_gpu_block_norm import (DEV, DNAME, EPS, by_pair, check_backward, check_forward, f64,
                                  operands, run_backward)
 from tiled_dense_gemm_07_amd import binding
 
@@ -147,3 +148,71 @@ def test_boundary_step_values(tokens):
     torch.cuda.synchronize()
     check_forward(s, f, BF16, BF16, tokens, alpha, True)
     check_backward(s, f, g, BF16, BF16, tokens, alpha, True)
+
+
+# --------------------------------------------------------------------------
+# exact levels
+# --------------------------------------------------------------------------
+def exact_levels(xo, w):
+    """Levels of h = xo r w from its definition, round(127 xo w / max |xo w|):
+    r, one factor for a row, is not in them.  64 bits of significand: 127 xo w
+    is exact but for fp32 with fp32.  Also how far a quotient is from a tie."""
+    u = xo.astype(np.longdouble) * w.astype(np.longdouble)
+    q = 127 * u / np.abs(u).max(axis=1, keepdims=True)
+    level = np.rint(q)
+    return level.astype(np.float64), np.abs(0.5 - np.abs(q - level)).astype(np.float64)
+
+
+@by_pair
+@pytest.mark.parametrize("T,D", [(400, 1000), (30, 4099), (7, 20000)])
+def test_levels_of_h_are_exact(T, D, xt, bt):
+    """Ties to even and quotients next to a tie, whatever fp32 makes of r and h;
+    only fp32 x' with fp32 weights (55 bits) may differ, within 64-bit
+    roundings of a tie."""
+    s = operands(T, D, xt, bt, 0, True, 41)
+    half = torch.arange(127, device=DEV) + 0.5  # 127 +- (k + 1/2): ties
+    for i in range(T // 4):
+        s["x"][4 * i] = 0
+        s["x"][4 * i, 1] = 127.0 * 2.0 ** (i % 9 - 4)
+        s["x"][4 * i, 10:137] = (half * 2.0 ** (i % 9 - 4)).to(s["x"].dtype)
+    for w in (s["w_pre"], torch.full_like(s["w_pre"], 1.25), None):
+        say("block_norm exact levels %dx%d %s/%s" % (T, D, DNAME[xt], DNAME[bt]))
+        if w is None and bt != xt:
+            continue  # without y and weights the block's type is x's
+        f = binding.block_norm(s["x"], w_pre=w, eps=EPS, out="i8")
+        g = binding.block_norm(s["x"], y=s["y"], w_post=s["w_post"], w_pre=w, eps=EPS, out="i8")
+        torch.cuda.synchronize()
+        for o in (f, g):
+            want, margin = exact_levels(f64(o.x, xt), np.ones(D) if w is None else f64(w, bt))
+            got = o.h.cpu().numpy().astype(np.float64)
+            sure = margin > 2.0 ** -40 if (xt, bt) == (F32, F32) else True
+            assert not ((got != want) & sure).any(), int(((got != want) & sure).sum())
+
+
+def test_levels_below_the_least_scale():
+    """Rows whose largest |h| is under 127 2^-126 are quantised with that; and x'
+    far above its row's rms beside weights next to it."""
+    D = 256
+    x = torch.ones((3, D), device=DEV)
+    w = torch.full((D,), 0.25, device=DEV) * 2.0 ** -120
+    w[::2] *= 3.0
+    say("block_norm levels of tiny h")
+    f = binding.block_norm(x, w_pre=w, eps=0.0, out="i8")  # r = 1
+    torch.cuda.synchronize()
+    want = np.rint(f64(w, F32) * 2.0 ** 126)  # 16 and 48 of 127
+    assert sorted(set(want)) == [16.0, 48.0]
+    assert np.array_equal(f.h.cpu().numpy(), np.tile(want, (3, 1)))
+    assert bool((f.hs == 2.0 ** -126).all())
+    x[:, 0] = 300.0
+    w[0] = 2.0 ** -129
+    w[1::2] = -2.0 ** -122
+    f = binding.block_norm(x, w_pre=w, eps=0.0, out="i8")
+    torch.cuda.synchronize()
+    r = 1.0 / np.sqrt((300.0 ** 2 + D - 1) / D)
+    want = np.rint(f64(x, F32)[0] * f64(w, F32) * r * 2.0 ** 126)
+    assert sorted(set(want)) == [-1.0, 2.0, 3.0]
+    assert np.array_equal(f.h.cpu().numpy(), np.tile(want, (3, 1)))
+    # no norm (0 / 0): a scale of NaN
+    f = binding.block_norm(x * 0, eps=0.0, out="i8")
+    torch.cuda.synchronize()
+    assert not bool(f.h.any()) and bool(f.hs.isnan().all())

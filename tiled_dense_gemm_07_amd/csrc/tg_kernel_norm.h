@@ -7,6 +7,11 @@
 // Sums, norms and every intermediate value are fp32; x' is rounded to its
 // stored type before h is computed from it, so that h, and the gradients
 // taken from the stored x', belong to the x' the caller holds.
+// 8-bit h has the exact levels of x' r2 w_pre: r2 cancels in them, so they are
+// taken from x' w_pre (bf16: 16 bits, which fp32 divides exactly; else 64 bits next
+// to a tie, tg_rows.h).  Against levels of h in fp32: bf16 8192 x 4096 and 4096 x
+// 8192 the same time, fp32 x' with bf16 4096 x 8192 68.3 and 69.3 us, 2048 x 16384
+// 85 and 92 (one workgroup to a unit, whose arithmetic no other one's loads hide).
 // Bound by memory: bf16 8192 x 4096 with h 44.6 us in a trace (268 MB, 6.0 TB/s,
 // part of it from the last-level cache; a large copy reaches 5.2); one row of
 // 4096 2.7 us, which is launch, two reductions and latency.
@@ -31,6 +36,7 @@ template <int XT, int BT, int NT, int TPR, int NC, bool ODD>
 __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void block_norm_kernel(NormParams p)
 {
     __shared__ u32 slots[3][16];
+    __shared__ float rest[16];
     const int t = threadIdx.x % TPR;
     const int row = (int)blockIdx.x * (NT / TPR) +
                     __builtin_amdgcn_readfirstlane((int)(threadIdx.x / TPR));
@@ -114,50 +120,119 @@ __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void block_norm_
     const float r2 = __builtin_amdgcn_rsqf(s[0] * inv_d + p.eps);
     if (p.r_pre && t == 0)
         p.r_pre[row] = r2;
-    float h[NC][8];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            h[c][i] = get8<XT>(rx[c], i) * r2;
-        if (p.w_pre) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                h[c][i] *= get8<BT>(rw[c], i);
-        }
-    }
     if (p.h) {
         const Row<BT, ODD> out(p.h, row, p.ldh, p.D);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
+            float h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                h[i] = get8<XT>(rx[c], i) * r2;
+            if (p.w_pre) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    h[i] *= get8<BT>(rw[c], i);
+            }
             Raw8<BT> r;
-            put8<BT>(r, h[c]);
+            put8<BT>(r, h);
             out.store(r, at(c));
         }
     }
     if (p.hq) {
-        u32 m[1] = {0};
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const u32 b = __builtin_bit_cast(u32, h[c][i]) & 0x7FFFFFFFu;
-                if (at(c) + i < p.D)
-                    m[0] = b > m[0] ? b : m[0];
-            }
-        row_all<MaxOp, TPR, 1>(m, slots[2]);
-        RowLevels L;
-        L.of_amax(m[0]);
+        // h = u f, f (1 to 2) being what r2 has beyond a power of two: the levels
+        // are those of u = (x' pow) w, which r2 and its roundings have no part in
+        const u32 rb = __builtin_bit_cast(u32, r2);
+        const float pow = __builtin_bit_cast(float, rb & 0x7F800000u);
+        const float f = __builtin_bit_cast(float, (rb & 0x007FFFFFu) | 0x3F800000u);
+        const auto xp = [&](int c, int i) { return get8<XT>(rx[c], i) * pow; };
+        const auto w = [&](int c, int i) { return p.w_pre ? get8<BT>(rw[c], i) : 1.0f; };
+        const auto v = [&](int c, int i) { return xp(c, i) * w(c, i); };  // u in fp32
+        const auto bits = [](float x) { return __builtin_bit_cast(u32, x) & 0x7FFFFFFFu; };
+        // the largest |v|, of all and of each chunk (zeros past the end; NaN
+        // there, with r2 infinite or NaN, only in a row without a norm)
+        u32 m[1] = {0}, top[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            int q[8];
+            top[c] = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                q[i] = L.level(h[c][i]);
-            store_levels(p.hq + row * p.ldhq, at(c), p.D - at(c), q);
+                top[c] = MaxOp::of(top[c], bits(v(c, i)));
+            m[0] = MaxOp::of(top[c], m[0]);
         }
-        if (t == 0)
-            p.hs[row] = L.scale;
+        const auto store = [&](float scale, const auto& levels) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                int q[8];
+                levels(c, q);
+                store_levels(p.hq + row * p.ldhq, at(c), p.D - at(c), q);
+            }
+            if (t == 0)
+                p.hs[row] = scale;
+        };
+        if constexpr (XT == DT_BF16) {  // u has 16 bits
+            row_all<MaxOp, TPR, 1>(m, slots[2]);
+            RowLevels L;
+            L.of_amax(m[0], f);
+            store(L.scale, [&](int c, int (&q)[8]) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    q[i] = L.level(v(c, i));
+            });
+        } else {
+            const auto unpack_again = [&] {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    repack<XT>(rx[c]);
+                    repack<BT>(rw[c]);
+                }
+            };
+            unpack_again();
+            float e = 0.0f;
+            if constexpr (XT == DT_F16) {  // u has 22 bits, 127 u too many
+                row_all<MaxOp, TPR, 1>(m, slots[2]);
+            } else {
+                // the largest |u| is among those that round to the largest |v|
+                m[0] = wave_all<MaxOp>(m[0]);
+                e = -__builtin_inff();
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    if (top[c] == m[0]) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (bits(v(c, i)) == m[0])
+                                e = fmaxf(e, __builtin_fmaf(fabsf(xp(c, i)), fabsf(w(c, i)),
+                                                            -fabsf(v(c, i))));
+                    }
+                e = __builtin_bit_cast(float, wave_all<MaxFloatOp>(__builtin_bit_cast(u32, e)));
+                if constexpr (TPR > 64) {
+                    if ((threadIdx.x & 63) == 0) {
+                        slots[2][t >> 6] = m[0];
+                        rest[t >> 6] = e;
+                    }
+                    __syncthreads();
+#pragma unroll
+                    for (int j = 0; j < TPR / 64; ++j)
+                        m[0] = MaxOp::of(m[0], slots[2][j]);
+                    e = -__builtin_inff();
+#pragma unroll
+                    for (int j = 0; j < TPR / 64; ++j)
+                        e = slots[2][j] == m[0] ? fmaxf(e, rest[j]) : e;
+                }
+            }
+            unpack_again();
+            WideLevels L;
+            L.of_amax(m[0], e, f);
+            if (L.ok)
+                store(L.scale, [&](int c, int (&q)[8]) {
+                    L.levels([&](int i) { return xp(c, i); }, [&](int i) { return w(c, i); }, q);
+                });
+            else
+                store(L.scale, [](int, int (&q)[8]) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        q[i] = 0;
+                });
+        }
     }
 }
 

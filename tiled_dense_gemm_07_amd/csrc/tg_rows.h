@@ -208,6 +208,14 @@ struct MaxOp {  // of bit patterns: for magnitudes, NaN > Inf > finite
     static __device__ __forceinline__ u32 of(u32 a, u32 b) { return a > b ? a : b; }
 };
 
+struct MaxFloatOp {
+    static __device__ __forceinline__ u32 of(u32 a, u32 b)
+    {
+        return __builtin_bit_cast(
+            u32, fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+    }
+};
+
 template <class Op>
 __device__ __forceinline__ u32 wave_all(u32 v)
 {
@@ -275,22 +283,24 @@ struct RowLevels {
     float a, ra;  // a (times the same power of two), and its reciprocal
     bool ok;
 
-    __device__ __forceinline__ void of_amax(u32 bits)
+    // bits: of the largest |v|; f: a factor of the whole row (1 to 2) that v lacks
+    __device__ __forceinline__ void of_amax(u32 bits, float f = 1.0f)
     {
+        constexpr float least = 127.0f * 0x1p-126f;
         ok = bits < 0x7F800000u;
-        float m = __builtin_bit_cast(float, bits);
-        m = ok ? fmaxf(m, 127.0f * 0x1p-126f) : 1.0f;
-        scale = ok ? m / 127.0f : __builtin_nanf("");
+        float m = ok ? __builtin_bit_cast(float, bits) : 1.0f;
+        scale = ok ? fmaxf(m * f, least) / 127.0f : __builtin_nanf("");
+        m = m * f < least ? least / f : m;
         const bool big = m > 0x1p100f;
         c = big ? 127.0f * 0x1p-32f : 127.0f;
         a = big ? m * 0x1p-32f : m;
         ra = 1.0f / a;
     }
 
-    // One Newton step corrects the quotient to its rounded value.  For 16-bit
-    // v, 127 v is exact and a quotient that is no tie lies more than 2^-13
-    // (relative) from one: the level is the exact one.  For v computed in
-    // fp32 a quotient within an fp32 rounding of a tie may go either way.
+    // One Newton step corrects the quotient to its rounded value.  For v of 16
+    // significant bits or fewer (a product of two bf16 values has 16), 127 v is exact,
+    // and a quotient that is no tie lies 2^-23 (relative) or more from one, twice
+    // half a step: the level is the exact one.
     __device__ __forceinline__ int level(float v) const
     {
         const float x = v * c;
@@ -309,6 +319,49 @@ struct RowLevels {
         q = __builtin_fma(__builtin_fma(-q, d, x), r, q);   // to about 2^-46
         q = __builtin_fma(__builtin_fma(-q, d, x), r, q);   // rounded
         return ok ? (int)__builtin_rint(q) : 0;
+    }
+};
+
+// The same for u = x w of more bits, v = u rounded to fp32; f as above.  The fp32
+// quotient of v is within 127 * 4 roundings, less than 2^-14, of the exact one and
+// decides all levels but those that near to a tie, one of 8192.  Those are
+// taken in 64 bits: 127 u is exact (but for a product of two fp32 values, 55
+// bits), a quotient that is no tie lies more than 2^-48 (relative) from one, and
+// the corrected one within 2^-52 of the exact one.
+struct WideLevels {
+    float scale, c;  // c: 127 / a
+    double a;        // max|u|, or what stands for it where the scale is the least
+    bool ok;
+
+    // bits: of the largest |v|; e: what the largest |u| has beyond it
+    __device__ __forceinline__ void of_amax(u32 bits, float e, float f)
+    {
+        constexpr float least = 127.0f * 0x1p-126f;
+        ok = bits < 0x7F800000u;
+        const float m = ok ? __builtin_bit_cast(float, bits) : 1.0f;
+        scale = ok ? fmaxf(m * f, least) / 127.0f : __builtin_nanf("");
+        a = m * f < least ? (double)(least / f) : (double)m + (double)e;
+        c = 127.0f / (float)a;
+    }
+    // Levels of eight elements x(i), w(i) of a row that is ok.
+    template <class X, class W>
+    __device__ __forceinline__ void levels(const X& x, const W& w, int (&q)[8]) const
+    {
+        float off = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float v = x(i) * w(i) * c, n = __builtin_rintf(v);
+            off = fmaxf(off, fabsf(v - n));
+            q[i] = (int)n;
+        }
+        if (off > 0.5f - 0x1p-14f) {
+            const double ra = 1.0 / a;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const double u = 127.0 * ((double)x(i) * (double)w(i)), y = u * ra;
+                q[i] = (int)__builtin_rint(__builtin_fma(__builtin_fma(-y, a, u), ra, y));
+            }
+        }
     }
 };
 
