@@ -6,7 +6,7 @@ from __future__ import annotations
 import numpy as np
 import pytest
 
-from gpu_helpers import BF16, F32, say
+from gpu_helpers import BF16, F32, say, torch_dtype
 from test_gpu_block_norm import (DEV, DNAME, EPS, by_pair, check_backward, check_forward, f64,
                                  operands, run_backward)
 from tiled_dense_gemm_07_amd import binding
@@ -216,3 +216,18 @@ def test_levels_below_the_least_scale():
     f = binding.block_norm(x * 0, eps=0.0, out="i8")
     torch.cuda.synchronize()
     assert not bool(f.h.any()) and bool(f.hs.isnan().all())
+
+
+@pytest.mark.parametrize("xt,bt", [(BF16, BF16), (F32, BF16), (F32, F32)])
+def test_levels_of_h_past_fp32(xt, bt):
+    """An h beyond fp32 is an infinity: the scale NaN and zero levels, also where
+    the factor that r has beyond a power of two is what takes it there."""
+    x = torch.ones((2, 256), dtype=torch_dtype(xt), device=DEV)
+    x[:, 3] = 8.0  # r = 0.896 = 1.79 / 2, h up to 7.17 w, 4 w without the 1.79
+    w = torch.full((256,), 0.8e38, dtype=torch_dtype(bt), device=DEV)
+    say("block_norm h past fp32 %s/%s" % (DNAME[xt], DNAME[bt]))
+    f = binding.block_norm(x, w_pre=w, eps=EPS, out="i8")
+    g = binding.block_norm(x, w_pre=w * 0.5, eps=EPS, out="i8")
+    torch.cuda.synchronize()
+    assert bool(f.hs.isnan().all()) and not bool(f.h.any())
+    assert bool(g.hs.isfinite().all()) and bool((g.h[:, 3] == 127).all())

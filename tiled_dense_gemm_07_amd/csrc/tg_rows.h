@@ -287,8 +287,9 @@ struct RowLevels {
     __device__ __forceinline__ void of_amax(u32 bits, float f = 1.0f)
     {
         constexpr float least = 127.0f * 0x1p-126f;
-        ok = bits < 0x7F800000u;
-        float m = ok ? __builtin_bit_cast(float, bits) : 1.0f;
+        float m = __builtin_bit_cast(float, bits);
+        ok = m * f < __builtin_inff();
+        m = ok ? m : 1.0f;
         scale = ok ? fmaxf(m * f, least) / 127.0f : __builtin_nanf("");
         m = m * f < least ? least / f : m;
         const bool big = m > 0x1p100f;
@@ -337,8 +338,9 @@ struct WideLevels {
     __device__ __forceinline__ void of_amax(u32 bits, float e, float f)
     {
         constexpr float least = 127.0f * 0x1p-126f;
-        ok = bits < 0x7F800000u;
-        const float m = ok ? __builtin_bit_cast(float, bits) : 1.0f;
+        float m = __builtin_bit_cast(float, bits);
+        ok = m * f < __builtin_inff();
+        m = ok ? m : 1.0f;
         scale = ok ? fmaxf(m * f, least) / 127.0f : __builtin_nanf("");
         a = m * f < least ? (double)(least / f) : (double)m + (double)e;
         c = 127.0f / (float)a;
