@@ -11,15 +11,15 @@
 // swizzles and fragment addresses are those of its k-contiguous operands, and
 // a fragment (16 bytes of one row for each lane) is the operand of
 // v_mfma_i32_32x32x32_i8, which does twice the 16-bit instruction's work.
-// Measured: 8192^3 bf16 out 410-445 us (2.5-2.7 POP/s; power-limited, 1.57 GHz
-// and 81% of the matrix rate at that clock with real data, 308 us and 2.28 GHz
-// with zeros), 4096^3 57-60 us.  256 x 8192 x 8192: 24.5 us; its copies alone
-// take 18.5 us from L2 and the last-level cache and 28 us from HBM, through LDS
-// or registers alike, so what bounds grids of small tiles is the unit's path to
-// L2 (62 GB/s of 85).  Not kept: the sums of k split over wave groups (same
-// time: LDS reads are not the bound), and a dword of each row touched ahead to
-// bring its line into L2 (a third slower: the lines touched count, not the
-// bytes).
+// Measured: 8192^3 bf16 out 444-466 us (2.4-2.5 POP/s; back to back on the same
+// data 410, at 1.57 GHz, power-limited, and 81% of the matrix rate at that clock;
+// 308 us and 2.28 GHz with zeros), 4096^3 56-60 us.  256 x 8192 x 8192: 24.5 us;
+// its copies alone take 18.5 us from L2 and the last-level cache and 28 us from
+// HBM, through LDS or registers alike, so what bounds grids of small tiles is the
+// unit's path to L2 (62 GB/s of 85).  Not kept: the sums of k split over wave
+// groups (same time: LDS reads are not the bound), and a dword of each row touched
+// ahead to bring its line into L2 (a third slower: the lines touched count, not
+// the bytes).
 //
 // i8_any_kernel: any sizes, strides and addresses (LDS-DMA copies want aligned
 // ones).  Strips of 128 bytes of k go through registers: 16-byte loads at any

@@ -248,14 +248,21 @@ __global__ __attribute__((amdgpu_flat_work_group_size(NT, NT))) void block_norm_
 // consecutive rows: whole groups of rows that share a gate row (parts == 0; a
 // group to a team), or one of the `parts` of a group (its rows to the teams in
 // turn).
-// Column sums stay in registers over those rows, are added over the teams in
-// LDS, and leave one partial row of each in the workspace, which
-// block_norm_columns_kernel adds in a fixed order.
+// Column sums stay in registers over those rows (NC = 1: all but the fp32 / fp32
+// kernel of 1024 threads, which spills 30), are added over the teams in LDS, and
+// leave one partial row of each in the workspace, which block_norm_columns_kernel
+// adds in a fixed order.
 // Bound by memory: bf16 8192 x 4096 with 2048-token gates 83 us (403 MB and 8 MB
 // of partial sums, 5.0 TB/s) and 5.5 us for the columns.  512 workgroups of half
 // the threads took as long and left twice the partial sums (12.7 us for the
 // columns).  The unpacked values of a row are not kept over its reduction but
 // unpacked again (repack): kept, they spill.
+// NC = 2 and 4 (D > 8192) hold 24 NC column sums a lane beside their row, in 128
+// registers: 89 to 237 and 436 to 722 of them are spilled, and the row loop goes
+// through scratch memory.  2048 x 16384: bf16 134 to 143 us (2.8 to 3.0 TB/s), fp32
+// with bf16 210 to 220, fp32 474 to 486; 1024 x 32768: 447 to 468, 612 to 632 and 950
+// to 975 (0.8 to 1 TB/s).  The sums would have to go to LDS, or a row to two
+// workgroups.
 // --------------------------------------------------------------------------
 struct NormGradParams {
     const void *x_new, *y, *gate, *w_post, *w_pre, *dx_new, *dh;
@@ -374,7 +381,8 @@ block_norm_grad_kernel(NormGradParams p)
     GradRow<XT, BT, NC> R;
     // The next row's loads in flight during this one's arithmetic, where 128
     // registers hold two rows; spilled ones cost far more than the overlap
-    // gives (4096 x 8192 fp32 383 us so, 186 with one row at a time).
+    // gives (4096 x 8192 fp32 383 us so, 186 with one row at a time).  With NC > 1
+    // not even one row fits (see above).
     constexpr bool AHEAD = NC == 1 && (TPR < 1024 || (XT != DT_F32 && !ODD));
     const bool own_gate = whole && p.gate;  // each group's gate with its first row
     if (AHEAD && row < r1)

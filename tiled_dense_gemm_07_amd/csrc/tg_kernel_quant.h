@@ -2,9 +2,11 @@
 // One pass over memory: a team of TPR threads holds a row of up to 8 NC TPR
 // elements in registers between the search for its largest magnitude and the
 // conversion.  Longer rows (NC = 0) are read twice.  Bound by memory: bf16 8192
-// x 8192 30.7 us (201 MB, 6.5 TB/s, part of it from the last-level cache), 16 x
-// 8192 2.7 us, which is launch and latency.  The correction of the quotient
-// (three operations an element) hides under the loads.
+// x 8192 30.7 us (201 MB, 6.5 TB/s, part of it from the last-level cache; three
+// inputs in turn 36, 5.6 TB/s), 16 x 8192 2.7 us, which is launch and latency.  The
+// correction of the quotient (three operations an element) hides under the loads,
+// and so do the 64-bit levels of fp32 inputs: three inputs in turn 8192 x 8192 61.8
+// us, 8192 x 4096 31.2, 8192 x 1024 8.6 (5.4, 5.4 and 4.9 TB/s).
 // tg_linear_i8 may have the same launch copy W's rows to 16-byte boundaries, in
 // workgroups after those of the activations: 4096 x 4095 6 to 7 us more.
 #pragma once

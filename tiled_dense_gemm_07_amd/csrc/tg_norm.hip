@@ -13,7 +13,7 @@ using tg::Span;
 using tg::span;
 using tg::span1;
 
-constexpr int64_t kMaxD = 32768;    // a row's registers: 1024 threads of 32 elements
+constexpr int64_t kMaxD = 32768;    // 1024 threads of 32 elements
 constexpr int64_t kMaxT = 1 << 30;  // sums of two row numbers fit 31 bits
 
 bool types_ok(int xt, int bt)
@@ -81,7 +81,9 @@ Pick pick_forward(int64_t D, int xt, int bt)
 }
 
 // One workgroup to a compute unit: 1024 threads (128 registers each) in teams,
-// or 512 where both types are fp32, whose rows take twice the registers.
+// or 512 where both types are fp32, whose rows take twice the registers.  From D
+// = 8193 on (both fp32: 4097) the registers do not hold a thread's sums and row,
+// and some are spilled (tg_kernel_norm.h has the times).
 template <int XT, int BT, bool ODD>
 Pick pick_backward_of(int64_t D)
 {

@@ -275,7 +275,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], u32* slot)
 // Quantisation of a row to 8-bit levels: q = 127 v / a with ties to even, a =
 // the row's largest magnitude (at least 127 * 2^-126, so that the scale
 // a / 127 is never subnormal).  A row with an infinity or NaN gets the scale
-// NaN and zero levels: whatever is computed from it is NaN.
+// NaN and zero levels: a product taken from it is NaN (zero after a ReLU).
 // --------------------------------------------------------------------------
 struct RowLevels {
     float scale;  // a / 127, rounded
@@ -299,9 +299,10 @@ struct RowLevels {
     }
 
     // One Newton step corrects the quotient to its rounded value.  For v of 16
-    // significant bits or fewer (a product of two bf16 values has 16), 127 v is exact,
-    // and a quotient that is no tie lies 2^-23 (relative) or more from one, twice
-    // half a step: the level is the exact one.
+    // significant bits or fewer (a product of two bf16 values has 16), 127 v is exact
+    // and a quotient that is no tie lies a whole step of fp32 or more from one (with
+    // steps of v and a of 2^i and 2^j, 254 v and (2 k + 1) a differ by one at least):
+    // the level is the exact one.
     __device__ __forceinline__ int level(float v) const
     {
         const float x = v * c;

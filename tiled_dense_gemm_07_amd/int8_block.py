@@ -9,6 +9,10 @@ Serving, per layer (weights quantised once per channel):
     x     = alpha x + gate * norm(y) * w_post   block_norm, together with the next
                                             layer's norm: x and h in one pass
 
+A token that is not finite keeps its infinities and NaN in the residual stream
+only: in 8 bits its row has the scale NaN, and the ReLU after the first product
+takes NaN to zero.
+
 Training runs the same boundary with h in the block's type and takes its
 gradients (block_norm_backward).
 
