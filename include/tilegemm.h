@@ -457,6 +457,206 @@ tg_status tg_block_norm_backward(const tg_block_norm_grad_args* args, void* work
 tg_status tg_block_norm_backward_workspace_size(const tg_block_norm_grad_args* args,
                                                 size_t* bytes);
 
+/*
+ * Microscaled blocks (OCP MX v1.0): 32 consecutive elements of 4 bits (E2M1) or
+ * 8 bits (E4M3) share one power of two P.  For a block with the largest
+ * magnitude a,
+ *   P = 2^(floor(log2 a) - emax), at least 2^-127   (emax: 2 for E2M1, 8 for E4M3),
+ *   element = x / P rounded to the format, ties to even, at most its largest
+ *     magnitude (6; 448),
+ * and the scale byte is P's exponent + 127.  A block that holds an infinity or
+ * NaN gets the scale byte 255 (NaN) and zero elements: every product taken from
+ * it is NaN (with TG_EPI_RELU zero).  A block of zeros gets the scale byte 0.
+ *
+ * tg_quant_mx writes X's blocks along its rows (Q, S), along its columns as rows
+ * of the transpose (Qt, St), or both from one read (NULL: not wanted).
+ *   X: [M][K] of `dtype`, row stride ldx in elements, any alignment.
+ *   Q: codes of [M][Kp] elements, Kp = K rounded up to a multiple of 128, zeros
+ *     past K: uint8 [M][Kp / 2], two E2M1 codes to a byte (even k in bits 3:0),
+ *     or uint8 [M][Kp] of E4M3;  S: uint8 [M][Kp / 32].
+ *   Qt: codes of [K][Mp] elements, Mp = M rounded up likewise, zeros past M;
+ *     St: uint8 [K][Mp / 32].
+ *   These are the operands of tg_gemm_mx (Aq, As or Wq, Ws, with its K the Kp
+ *   here) and the weights of tg_linear_mx.
+ * tg_dequant_mx writes the values that Q and S stand for, rounded once to `dtype`:
+ *   X: [M][K], row stride ldx.
+ * M or K == 0: nothing is launched.
+ * Errors: TG_ERR_BAD_DTYPE (also fmt), TG_ERR_BAD_SHAPE (negative, above 2^29 - 1,
+ *   or a stride below K), TG_ERR_NULL_POINTER (X, neither Q nor Qt, or codes
+ *   without scales or the reverse), TG_ERR_NO_CONFIG (codes not 16-byte or
+ *   scales not 4-byte aligned), TG_ERR_ALIAS (an output overlaps X or another),
+ *   TG_ERR_HIP.
+ */
+tg_status tg_quant_mx(int64_t M, int64_t K, tg_dtype dtype, const void* X, int64_t ldx,
+                      tg_mx_format fmt, uint8_t* Q, uint8_t* S, uint8_t* Qt, uint8_t* St,
+                      tg_stream_t stream);
+tg_status tg_dequant_mx(int64_t M, int64_t K, tg_mx_format fmt, const uint8_t* Q, const uint8_t* S,
+                        tg_dtype dtype, void* X, int64_t ldx, tg_stream_t stream);
+
+/*
+ * Linear layer with 4-bit weights: C = epilogue(Q(X) W^T + bias), the rows of X
+ * brought to blocks of format `fmt` within the call, as by tg_quant_mx.
+ *   X: [M][K] of `dtype`, row stride ldx; bias: fp32 [N] or NULL; C: [M][N] of
+ *   `dtype`, row stride ldc.  Strides in elements, any alignment.
+ *   Wq, Ws: E2M1 weights [N][Kp] as tg_quant_mx writes them (Kp: K rounded up to
+ *     a multiple of 128); what they hold past K has no part in C as long as its
+ *     scale bytes are not 255.
+ *   The product is that of tg_gemm_mx (whose arithmetic on E4M3 holds here, too),
+ *   the bias is added in fp32 and C rounded once; sums are taken in an order that
+ *   depends on the sizes only.
+ *   workspace: device memory, 16-byte aligned, of at least the size
+ *     tg_linear_mx_workspace_size reports for these sizes (it holds X's codes
+ *     and scales; 0 bytes, and NULL, where the call needs none).  Its contents
+ *     need not be kept between calls; calls that share it must not run
+ *     concurrently.
+ *   K == 0: C = epilogue(bias); X, Wq and Ws may be NULL then.
+ * Errors: TG_ERR_BAD_DTYPE (also fmt), TG_ERR_BAD_EPILOGUE, TG_ERR_BAD_SHAPE
+ *   (also a stride below its row length, K > 8388479), TG_ERR_NULL_POINTER,
+ *   TG_ERR_NO_CONFIG (Wq not 16-byte or Ws not 4-byte aligned),
+ *   TG_ERR_WORKSPACE, TG_ERR_ALIAS (C or the workspace overlaps an operand or
+ *   each other), TG_ERR_HIP.
+ */
+tg_status tg_linear_mx(int64_t M, int64_t N, int64_t K, tg_dtype dtype, const void* X, int64_t ldx,
+                       tg_mx_format fmt, const uint8_t* Wq, const uint8_t* Ws, const float* bias,
+                       void* C, int64_t ldc, tg_epilogue epi, void* workspace,
+                       size_t workspace_bytes, tg_stream_t stream);
+tg_status tg_linear_mx_workspace_size(int64_t M, int64_t N, int64_t K, tg_dtype dtype,
+                                      tg_mx_format fmt, size_t* bytes);
+
+/*
+ * Gradients of the linear layer Y = X W^T + bias with both products in blocks, each
+ * operand quantised along the axis that is summed (Q(.) to `fmt`, Q4(.) to E2M1):
+ *   dX[M][K] = Q(dY) Q4(W)       blocks along N,
+ *   dW[N][K] = Q(dY)^T Q4(X)     blocks along M,
+ *   dbias[N] = sum_m dY[m][n]    from dY as given, fp32, in a fixed order.
+ * The roundings of the quantisation are passed over (their gradient is taken to be
+ * that of the value itself).  dY is the gradient before the ReLU, if there is one.
+ *   dY: [M][N], X, dX: [M][K] of `dtype`; W, dW: [N][K] of `wtype`, which is
+ *   `dtype` or TG_F32 (W as the optimiser holds it, not in 4 bits).  Row strides in
+ *   elements, any alignment.  dX, dW, dbias: NULL if not wanted; dX needs W, dW
+ *   needs X.
+ *   workspace: as for tg_linear_mx, of the size that
+ *     tg_linear_mx_backward_workspace_size reports for the same arguments.
+ * With no tokens dW and dbias are zero, with N == 0 dX is.
+ * Errors: TG_ERR_NULL_POINTER (an input that an output needs, or no output),
+ *   TG_ERR_BAD_DTYPE, TG_ERR_BAD_SHAPE (also a size above 8388479),
+ *   TG_ERR_WORKSPACE, TG_ERR_ALIAS (an output or the workspace overlaps an input
+ *   or another output), TG_ERR_HIP.
+ */
+typedef struct {
+    int64_t M, N, K;
+    tg_dtype dtype, wtype;
+    tg_mx_format fmt;
+    const void* dY;
+    int64_t lddy;
+    const void* X;
+    int64_t ldx;
+    const void* W;
+    int64_t ldw;
+    void* dX;
+    int64_t lddx;
+    void* dW;
+    int64_t lddw;
+    float* dbias;
+} tg_linear_mx_grad_args;
+
+tg_status tg_linear_mx_backward(const tg_linear_mx_grad_args* args, void* workspace,
+                                size_t workspace_bytes, tg_stream_t stream);
+tg_status tg_linear_mx_backward_workspace_size(const tg_linear_mx_grad_args* args,
+                                               size_t* bytes);
+
+/*
+ * Norm of every query and key head with the rotation to its token's position, in
+ * one pass.  For a head x of D values at position t,
+ *   y = x r * w,  r = 1 / sqrt(mean(x^2) + eps),
+ *   out = y with pair i of its first R values (a, b) turned to
+ *     (a cos[t][i] - b sin[t][i], a sin[t][i] + b cos[t][i]);
+ * pair i is (i, i + R / 2), or (2 i, 2 i + 1) with `interleaved`; values past R
+ * are not turned.
+ *   q: Hq heads of T tokens: values of token t, head h at q + t q_t + h q_h
+ *     (strides in elements; slices of one projection's output, or heads that
+ *     hold their tokens); k: Hk heads, likewise.  No heads of a kind: its
+ *     pointers may be NULL.
+ *   w_q, w_k: [D] of `dtype`, or NULL: ones.
+ *   cos, sin: fp32 [P][R / 2], dense; positions: int64 [T], or NULL: token t is at
+ *     position t.  Values turned by a position outside [0, P) are NaN; tables are
+ *     not read out of range.
+ *   q_out, k_out: of `dtype`; may be q and k themselves (same address and strides).
+ * Sums and intermediate values are fp32, one rounding to `dtype`.
+ * D <= 1024, T <= 2^30, Hq and Hk <= 65536.
+ * Errors: TG_ERR_BAD_DTYPE, TG_ERR_BAD_SHAPE (sizes, R odd or above D, strides
+ *   negative, heads of an output that overlap, P < T without positions, P < 1
+ *   with R), TG_ERR_NULL_POINTER, TG_ERR_ALIAS (an output overlaps an input,
+ *   except in place, or the other output), TG_ERR_HIP.
+ */
+typedef struct {
+    int64_t T, Hq, Hk, D, R;
+    tg_dtype dtype;
+    const void* q;
+    int64_t q_t, q_h;
+    const void* k;
+    int64_t k_t, k_h;
+    const void* w_q;
+    const void* w_k;
+    const float* cos;
+    const float* sin;
+    int64_t P;
+    const int64_t* positions;
+    float eps;
+    int interleaved;
+    void* q_out;
+    int64_t q_out_t, q_out_h;
+    void* k_out;
+    int64_t k_out_t, k_out_h;
+} tg_head_norm_rope_args;
+
+tg_status tg_head_norm_rope(const tg_head_norm_rope_args* args, tg_stream_t stream);
+
+/*
+ * Gradients of tg_head_norm_rope.  In: its inputs, q and k as they were, and the
+ * gradients dq_out and dk_out at its outputs.  Out: dq, dk of `dtype`; dw_q, dw_k
+ * [D] in fp32, sums over all tokens and heads in a fixed order (NULL: not wanted;
+ * zero for no tokens).
+ *   workspace: device memory, 16-byte aligned, of at least the size
+ *     tg_head_norm_rope_backward_workspace_size reports for the same arguments; it
+ *     holds partial sums.  Its contents need not be kept; calls that share it must
+ *     not run concurrently.
+ * Errors: as tg_head_norm_rope; TG_ERR_BAD_LAYOUT (dw_q, dw_k without w_q, w_k);
+ *   TG_ERR_ALIAS (an output or the workspace overlaps an input or another output;
+ *   there is no in-place form); TG_ERR_WORKSPACE.
+ */
+typedef struct {
+    int64_t T, Hq, Hk, D, R;
+    tg_dtype dtype;
+    const void* q;
+    int64_t q_t, q_h;
+    const void* k;
+    int64_t k_t, k_h;
+    const void* w_q;
+    const void* w_k;
+    const float* cos;
+    const float* sin;
+    int64_t P;
+    const int64_t* positions;
+    float eps;
+    int interleaved;
+    const void* dq_out;
+    int64_t dq_out_t, dq_out_h;
+    const void* dk_out;
+    int64_t dk_out_t, dk_out_h;
+    void* dq;
+    int64_t dq_t, dq_h;
+    void* dk;
+    int64_t dk_t, dk_h;
+    float* dw_q;
+    float* dw_k;
+} tg_head_norm_rope_grad_args;
+
+tg_status tg_head_norm_rope_backward(const tg_head_norm_rope_grad_args* args, void* workspace,
+                                     size_t workspace_bytes, tg_stream_t stream);
+tg_status tg_head_norm_rope_backward_workspace_size(const tg_head_norm_rope_grad_args* args,
+                                                    size_t* bytes);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* tg_status_str(tg_status s);
 

@@ -1,0 +1,318 @@
+"""Host-side checks of the microscaled linear path and of the head norms (no GPU
+needed, no kernel launched): every invalid-argument path returns its status
+before any HIP call, workspace sizes, the binding's refusals, and the tests' own
+64-bit forms against differences and independent values."""
+
+import ctypes
+
+import pytest
+import torch
+
+import mx_heads_reference as ref
+from tiled_dense_gemm_07_amd import binding
+
+OK, NULLP, SHAPE, DTYPE, EPI, ALIAS, NOCFG, HIP, BADL, WSP, SCRATCH = range(11)
+# fake, well-separated device addresses: validation never dereferences them
+P = [0x10000000 * (i + 1) for i in range(20)]
+F32, F16, BF16 = 0, 1, 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return binding.load_library()
+
+
+def quant(lib, M=4, K=40, dt=BF16, X=P[0], ldx=None, fmt=0, Q=P[1], S=P[2], Qt=P[3], St=P[4]):
+    return lib.tg_quant_mx(M, K, dt, X, K if ldx is None else ldx, fmt, Q, S, Qt, St, None)
+
+
+def test_quant_argument_errors(lib):
+    assert quant(lib, dt=3) == DTYPE
+    assert quant(lib, fmt=2) == DTYPE
+    for k in ("M", "K"):
+        assert quant(lib, **{k: -1}) == SHAPE
+        assert quant(lib, **{k: 1 << 29}) == SHAPE
+    assert quant(lib, ldx=39) == SHAPE
+    for k in ("X", "Q", "S", "Qt", "St"):
+        assert quant(lib, **{k: None}) == NULLP
+    assert quant(lib, Q=None, S=None, Qt=None, St=None) == NULLP
+    for k, at in (("Q", 1), ("S", 2), ("Qt", 3), ("St", 4)):
+        assert quant(lib, **{k: P[at] + (8 if k[0] == "Q" else 2)}) == NOCFG
+        assert quant(lib, **{k: P[0] + 16}) == ALIAS
+    assert quant(lib, S=P[1] + 4) == ALIAS
+    assert quant(lib, Qt=P[1] + 16) == ALIAS
+    assert quant(lib, M=0, X=None, Q=None, S=None, Qt=None, St=None) == OK
+    assert quant(lib, K=0, X=None, Q=None, S=None, Qt=None, St=None) == OK
+
+
+def dequant(lib, M=4, K=40, fmt=0, Q=P[0], S=P[1], dt=BF16, X=P[2], ldx=None):
+    return lib.tg_dequant_mx(M, K, fmt, Q, S, dt, X, K if ldx is None else ldx, None)
+
+
+def test_dequant_argument_errors(lib):
+    assert dequant(lib, dt=3) == DTYPE
+    assert dequant(lib, fmt=-1) == DTYPE
+    assert dequant(lib, M=-1) == SHAPE
+    assert dequant(lib, K=1 << 29) == SHAPE
+    assert dequant(lib, ldx=39) == SHAPE
+    for k in ("Q", "S", "X"):
+        assert dequant(lib, **{k: None}) == NULLP
+    assert dequant(lib, Q=P[0] + 4) == NOCFG
+    assert dequant(lib, S=P[1] + 1) == NOCFG
+    assert dequant(lib, X=P[0]) == ALIAS
+    assert dequant(lib, X=P[1] + 8) == ALIAS
+    assert dequant(lib, M=0, Q=None, S=None, X=None) == OK
+
+
+def linear(lib, M=32, N=8, K=40, dt=BF16, X=P[0], ldx=None, fmt=0, Wq=P[1], Ws=P[2], bias=None,
+           C=P[3], ldc=None, epi=0, ws=P[4], wn=1 << 20):
+    return lib.tg_linear_mx(M, N, K, dt, X, K if ldx is None else ldx, fmt, Wq, Ws, bias, C,
+                            N if ldc is None else ldc, epi, ws, wn, None)
+
+
+def test_linear_argument_errors(lib):
+    assert linear(lib, dt=-1) == DTYPE
+    assert linear(lib, fmt=2) == DTYPE
+    assert linear(lib, epi=2) == EPI
+    for k in ("M", "N", "K"):
+        assert linear(lib, **{k: -1}) == SHAPE
+        assert linear(lib, **{k: 1 << 31}) == SHAPE
+    assert linear(lib, K=8388480) == SHAPE
+    assert linear(lib, ldx=39) == SHAPE
+    assert linear(lib, ldc=7) == SHAPE
+    for k in ("X", "Wq", "Ws", "C"):
+        assert linear(lib, **{k: None}) == NULLP
+    assert linear(lib, Wq=P[1] + 8) == NOCFG
+    assert linear(lib, Ws=P[2] + 2) == NOCFG
+    assert linear(lib, ws=None) == WSP
+    assert linear(lib, ws=P[4] + 8) == WSP
+    need = binding.linear_mx_workspace_size(32, 8, 40, BF16)
+    assert need > 0 and linear(lib, wn=need - 1) == WSP
+    for at in (P[0] + 80, P[1] + 16, P[2] + 4):
+        assert linear(lib, C=at) == ALIAS
+    assert linear(lib, C=P[4] + 32) == ALIAS
+    assert linear(lib, bias=P[3] + 4) == ALIAS
+    assert linear(lib, ws=P[0] + 16) == ALIAS
+    assert linear(lib, M=0, X=None, Wq=None, Ws=None, C=None, ws=None) == OK
+    assert linear(lib, N=0, X=None, Wq=None, Ws=None, C=None, ws=None) == OK
+
+
+def test_linear_workspace_size(lib):
+    size = binding.linear_mx_workspace_size
+    assert size(0, 8, 40, BF16) == size(8, 0, 40, BF16) == size(8, 8, 0, BF16) == 0
+    assert size(1, 1024, 1024, BF16) == 0  # one launch
+    for fmt, per in ((0, 64), (1, 128)):
+        assert size(100, 64, 100, BF16, fmt) >= 100 * (per + 4)
+    assert lib.tg_linear_mx_workspace_size(4, 4, 4, BF16, 0, None) == NULLP
+    out = ctypes.c_size_t(0)
+    assert lib.tg_linear_mx_workspace_size(4, 4, 4, BF16, 7, ctypes.byref(out)) == DTYPE
+    assert lib.tg_linear_mx_workspace_size(-4, 4, 4, BF16, 0, ctypes.byref(out)) == SHAPE
+
+
+def grad_args(**kw):
+    a = binding.LinearMxGradArgs()
+    d = dict(M=40, N=48, K=56, dtype=BF16, wtype=BF16, fmt=0, dY=P[0], lddy=48, X=P[1], ldx=56,
+             W=P[2], ldw=56, dX=P[3], lddx=56, dW=P[4], lddw=56, dbias=P[5])
+    d.update(kw)
+    for k, v in d.items():
+        setattr(a, k, v)
+    return a
+
+
+def grad(lib, ws=P[6], wn=1 << 20, **kw):
+    return lib.tg_linear_mx_backward(ctypes.byref(grad_args(**kw)), ws, wn, None)
+
+
+def test_linear_backward_argument_errors(lib):
+    assert lib.tg_linear_mx_backward(None, None, 0, None) == NULLP
+    assert grad(lib, dtype=3) == DTYPE
+    assert grad(lib, dtype=F32, wtype=BF16) == DTYPE
+    assert grad(lib, wtype=F16) == DTYPE
+    assert grad(lib, fmt=2) == DTYPE
+    for k in ("M", "N", "K"):
+        assert grad(lib, **{k: -1}) == SHAPE
+        assert grad(lib, **{k: 8388480}) == SHAPE
+    for k, n in (("lddy", 48), ("ldx", 56), ("ldw", 56), ("lddx", 56), ("lddw", 56)):
+        assert grad(lib, **{k: n - 1}) == SHAPE
+    assert grad(lib, dY=None) == NULLP
+    assert grad(lib, W=None) == NULLP
+    assert grad(lib, X=None) == NULLP
+    assert grad(lib, dX=None, dW=None, dbias=None) == NULLP
+    assert grad(lib, ws=None) == WSP
+    assert grad(lib, ws=P[6] + 4) == WSP
+    out = ctypes.c_size_t(0)
+    assert lib.tg_linear_mx_backward_workspace_size(ctypes.byref(grad_args()),
+                                                    ctypes.byref(out)) == OK
+    assert out.value > 0 and grad(lib, wn=out.value - 1) == WSP
+    assert lib.tg_linear_mx_backward_workspace_size(ctypes.byref(grad_args()), None) == NULLP
+    for k, at in (("dX", P[0]), ("dX", P[1] + 8), ("dW", P[2]), ("dW", P[3] + 4), ("dbias", P[4]),
+                  ("dX", P[6])):
+        assert grad(lib, **{k: at}) == ALIAS
+    assert grad(lib, M=0, K=0, dY=None, X=None, W=None, dbias=None) == OK
+    assert grad(lib, N=0, K=0, dY=None, X=None, W=None) == OK
+
+
+def head_args(cls=binding.HeadNormRopeArgs, **kw):
+    a = cls()
+    T, Hq, Hk, D = (kw.get(k, v) for k, v in (("T", 8), ("Hq", 4), ("Hk", 2), ("D", 64)))
+    d = dict(T=T, Hq=Hq, Hk=Hk, D=D, R=64, dtype=BF16, q=P[0], k=P[1], w_q=P[2], w_k=P[3],
+             cos=P[4], sin=P[5], P=100, positions=P[6], eps=1e-6, interleaved=0)
+    names = [("q", Hq), ("k", Hk)]
+    if cls is binding.HeadNormRopeArgs:
+        d.update(q_out=P[7], k_out=P[8])
+        names += [("q_out", Hq), ("k_out", Hk)]
+    else:
+        d.update(dq_out=P[7], dk_out=P[8], dq=P[9], dk=P[10], dw_q=P[11], dw_k=P[12])
+        names += [("dq_out", Hq), ("dk_out", Hk), ("dq", Hq), ("dk", Hk)]
+    for n, H in names:
+        d[n + "_t"], d[n + "_h"] = H * D, D
+    d.update(kw)
+    for k, v in d.items():
+        setattr(a, k, v)
+    return a
+
+
+def heads(lib, **kw):
+    return lib.tg_head_norm_rope(ctypes.byref(head_args(**kw)), None)
+
+
+def test_heads_argument_errors(lib):
+    assert lib.tg_head_norm_rope(None, None) == NULLP
+    assert heads(lib, dtype=3) == DTYPE
+    for kw in (dict(T=-1), dict(T=(1 << 30) + 1), dict(Hq=-1), dict(Hk=65537), dict(D=0),
+               dict(D=1025), dict(R=63), dict(R=66), dict(R=-2), dict(P=-1), dict(P=0),
+               dict(P=7, positions=None), dict(q_t=-1), dict(k_h=-1), dict(q_t=1 << 60),
+               dict(q_out_h=63), dict(q_out_t=255), dict(k_out_t=1 << 50)):
+        assert heads(lib, **kw) == SHAPE, kw
+    for k in ("q", "k", "cos", "sin", "q_out", "k_out"):
+        assert heads(lib, **{k: None}) == NULLP, k
+    for k, at in (("q_out", P[0] + 128), ("q_out", P[1]), ("k_out", P[2]), ("k_out", P[3]),
+                  ("q_out", P[4]), ("k_out", P[5]), ("q_out", P[6]), ("k_out", P[7])):
+        assert heads(lib, **{k: at}) == ALIAS, (k, at)
+    assert heads(lib, T=0, q=None, k=None, cos=None, sin=None, q_out=None, k_out=None) == OK
+    assert heads(lib, Hq=0, Hk=0, q=None, k=None, q_out=None, k_out=None) == OK
+
+
+def test_heads_slices_of_one_buffer_do_not_alias(lib):
+    # q, k, out in column slices of one row-strided buffer are apart; one value
+    # further they are not.  (The launch itself is made to fail.)
+    import os
+
+    old = os.environ.get("TG_FAULT")
+    os.environ["TG_FAULT"] = "launch"
+    try:
+        row = 64 * 12
+        base = dict(q=P[0], q_t=row, k=P[0] + 2 * 256, k_t=row, q_out=P[0] + 2 * 384, q_out_t=row,
+                    k_out=P[0] + 2 * 640, k_out_t=row)
+        assert heads(lib, **base) == HIP
+        assert heads(lib, **dict(base, k_out=P[0] + 2 * 639)) == ALIAS
+        assert heads(lib, **dict(base, q_out=P[0], k_out=P[0] + 2 * 256)) == HIP  # in place
+        assert heads(lib, **dict(base, q_out=P[0], q_out_t=row + 64)) == ALIAS
+        # heads that hold their tokens: [H][T][D]
+        assert heads(lib, q_t=64, q_h=512, q_out_t=64, q_out_h=512) == HIP
+        assert heads(lib, q_out_t=64, q_out_h=100) == SHAPE  # such heads overlap
+        # a head shared by every token or by all heads, as an input
+        assert heads(lib, q_t=0, k_h=0) == HIP
+        assert heads(lib, q_out_t=0) == SHAPE
+    finally:
+        if old is None:
+            del os.environ["TG_FAULT"]
+        else:
+            os.environ["TG_FAULT"] = old
+
+
+def heads_grad(lib, ws=P[13], wn=1 << 20, **kw):
+    a = head_args(binding.HeadNormRopeGradArgs, **kw)
+    return lib.tg_head_norm_rope_backward(ctypes.byref(a), ws, wn, None)
+
+
+def test_heads_backward_argument_errors(lib):
+    assert lib.tg_head_norm_rope_backward(None, None, 0, None) == NULLP
+    assert heads_grad(lib, dtype=-1) == DTYPE
+    for kw in (dict(T=-1), dict(D=1025), dict(R=1), dict(dq_out_t=-1), dict(dk_out_h=-5),
+               dict(dq_h=1), dict(dk_t=3)):
+        assert heads_grad(lib, **kw) == SHAPE, kw
+    for k in ("q", "k", "cos", "sin", "dq_out", "dk_out", "dq", "dk"):
+        assert heads_grad(lib, **{k: None}) == NULLP, k
+    assert heads_grad(lib, w_q=None) == BADL
+    assert heads_grad(lib, w_k=None) == BADL
+    assert heads_grad(lib, ws=None) == WSP
+    assert heads_grad(lib, ws=P[13] + 8) == WSP
+    assert heads_grad(lib, wn=0) == WSP
+    for k, at in (("dq", P[0]), ("dq", P[7]), ("dk", P[8]), ("dk", P[1]), ("dw_q", P[9]),
+                  ("dw_k", P[11]), ("dq", P[13]), ("dw_q", P[4])):
+        assert heads_grad(lib, **{k: at}) == ALIAS, (k, at)
+    out = ctypes.c_size_t(0)
+    a = head_args(binding.HeadNormRopeGradArgs)
+    size = lib.tg_head_norm_rope_backward_workspace_size
+    assert size(ctypes.byref(a), None) == NULLP
+    assert size(None, ctypes.byref(out)) == NULLP
+    assert size(ctypes.byref(a), ctypes.byref(out)) == OK and out.value > 0
+    a = head_args(binding.HeadNormRopeGradArgs, dw_q=None, dw_k=None)
+    assert size(ctypes.byref(a), ctypes.byref(out)) == OK and out.value == 0
+
+
+def test_binding_refusals_without_a_gpu():
+    x = torch.zeros((4, 64))
+    w = torch.zeros((4, 64), dtype=torch.uint8)
+    for f in (lambda: binding.quant_mx(x), lambda: binding.dequant_mx(w, w[:, :4]),
+              lambda: binding.linear_mx(x, w, w[:, :4]),
+              lambda: binding.linear_mx_backward(x, X=x), lambda: binding.linear_mx_backward(x),
+              lambda: binding.quant_mx(x, fmt=5), lambda: binding.quant_mx(x, sides="rows+"),
+              lambda: binding.head_norm_rope(x.view(2, 2, 64)),
+              lambda: binding.head_norm_rope_backward(x.view(2, 2, 64), None, x.view(2, 2, 64))):
+        with pytest.raises(ValueError):
+            f()
+
+
+# --------------------------------------------------------------------------
+# The references themselves.
+# --------------------------------------------------------------------------
+def test_reference_quantiser_values():
+    # one block by hand: the largest, 7, falls into the highest octave [4, 8) as it is
+    x = torch.zeros((1, 32))
+    x[0, :12] = torch.tensor([7.0, 6.9, 5.0, 2.5, -2.4, 0.25, 0.26, -0.75, 1.25, 3.5, -0.1, 1.75])
+    c, s = ref.quantise(x, ref.E2M1)
+    assert s[0, 0] == 127 and list(s[0, 1:]) == [0, 0, 0]
+    v = ref.values(c, s, ref.E2M1)[0, :12]
+    assert v.tolist() == [6.0, 6.0, 4.0, 2.0, -2.0, 0.0, 0.5, -1.0, 1.0, 4.0, 0.0, 2.0]
+    c, s = ref.quantise(x * 2.0 ** 40, ref.E4M3)
+    assert s[0, 0] == 127 + 40 + 2 - 8
+    v = ref.values(c, s, ref.E4M3)[0, :12] * 2.0 ** -40
+    assert v.tolist() == [7.0, 7.0, 5.0, 2.5, -2.5, 0.25, 0.25, -0.75, 1.25, 3.5, -0.1015625, 1.75]
+    x[0, 3] = float("inf")
+    c, s = ref.quantise(x, ref.E2M1)
+    assert s[0, 0] == 255 and int(c[0].abs().sum()) == 0
+
+
+def test_reference_formats_hold_their_own_values():
+    for fmt in (ref.E2M1, ref.E4M3):
+        t = ref.table(fmt)
+        x = torch.stack([t, -t], dim=1).reshape(-1)
+        x = torch.nn.functional.pad(x, (0, -x.numel() % 31)).view(-1, 31)
+        x = torch.cat([x, torch.full((x.shape[0], 1), float(t[-1]))], dim=1)
+        c, s = ref.quantise(x, fmt)
+        assert torch.equal(ref.values(c, s, fmt)[:, :32], x)
+        assert torch.equal(ref.unpack(ref.pack(c, fmt), fmt), c)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,R", [(8, 8), (7, 4), (6, 0)])
+def test_reference_head_gradients_by_differences(D, R, interleaved):
+    g = torch.Generator().manual_seed(D + R)
+    T, H, eps = 3, 2, 1e-3
+    x, d = (torch.randn((T, H, D), generator=g, dtype=torch.float64) for _ in range(2))
+    w = torch.randn((D,), generator=g, dtype=torch.float64)
+    cos, sin = ref.tables(T, R // 2)
+    f = lambda x, w: float((ref.heads_forward(x, w, cos, sin, R, eps, interleaved)[0] * d).sum())
+    dx, dw, _, _ = ref.heads_backward(d, x, w, cos, sin, R, eps, interleaved)
+    h = 1e-6
+    for i in range(0, x.numel(), 5):
+        e = torch.zeros_like(x).view(-1)
+        e[i] = h
+        e = e.view_as(x)
+        assert abs((f(x + e, w) - f(x - e, w)) / (2 * h) - float(dx.view(-1)[i])) < 1e-7
+    for i in range(D):
+        e = torch.zeros_like(w)
+        e[i] = h
+        assert abs((f(x, w + e) - f(x, w - e)) / (2 * h) - float(dw[i])) < 1e-7

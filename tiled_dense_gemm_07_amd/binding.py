@@ -34,7 +34,10 @@ EXPORTS = ("tg_gemm", "tg_gemm_ex", "tg_dequant_gemm_w4", "tg_status_str", "tg_q
            "tg_gemm_splitk_workspace_size", "tg_gemm_splitk_config", "tg_gemm_splitk_noalloc",
            "tg_set_clock_stamps", "tg_set_swizzle_override", "tg_config_occupancy",
            "tg_quant_i8", "tg_gemm_i8", "tg_linear_i8", "tg_linear_i8_workspace_size",
-           "tg_block_norm", "tg_block_norm_backward", "tg_block_norm_backward_workspace_size")
+           "tg_block_norm", "tg_block_norm_backward", "tg_block_norm_backward_workspace_size",
+           "tg_quant_mx", "tg_dequant_mx", "tg_linear_mx", "tg_linear_mx_workspace_size",
+           "tg_linear_mx_backward", "tg_linear_mx_backward_workspace_size", "tg_head_norm_rope",
+           "tg_head_norm_rope_backward", "tg_head_norm_rope_backward_workspace_size")
 TG_SPLITK_SCRATCH_BYTES = 16 * 1024 * 1024
 
 _lib = None
@@ -70,10 +73,52 @@ class BlockNormGradArgs(ctypes.Structure):
                 ("dw_post", ctypes.c_void_p), ("dw_pre", ctypes.c_void_p)]
 
 
+class LinearMxGradArgs(ctypes.Structure):
+    """tg_linear_mx_grad_args."""
+
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("wtype", ctypes.c_int), ("fmt", ctypes.c_int),
+                ("dY", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("X", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("W", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+                ("dX", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dW", ctypes.c_void_p),
+                ("lddw", ctypes.c_int64), ("dbias", ctypes.c_void_p)]
+
+
+def _head_fields(*tail):
+    f = [(n, ctypes.c_int64) for n in ("T", "Hq", "Hk", "D", "R")] + [("dtype", ctypes.c_int)]
+    for n in ("q", "k"):
+        f += [(n, ctypes.c_void_p), (n + "_t", ctypes.c_int64), (n + "_h", ctypes.c_int64)]
+    f += [(n, ctypes.c_void_p) for n in ("w_q", "w_k", "cos", "sin")]
+    f += [("P", ctypes.c_int64), ("positions", ctypes.c_void_p), ("eps", ctypes.c_float),
+          ("interleaved", ctypes.c_int)]
+    for n in tail:
+        f += [(n, ctypes.c_void_p), (n + "_t", ctypes.c_int64), (n + "_h", ctypes.c_int64)]
+    return f
+
+
+class HeadNormRopeArgs(ctypes.Structure):
+    """tg_head_norm_rope_args."""
+
+    _fields_ = _head_fields("q_out", "k_out")
+
+
+class HeadNormRopeGradArgs(ctypes.Structure):
+    """tg_head_norm_rope_grad_args."""
+
+    _fields_ = _head_fields("dq_out", "dk_out", "dq", "dk") + [("dw_q", ctypes.c_void_p),
+                                                              ("dw_k", ctypes.c_void_p)]
+
+
 # Result of block_norm: the new residual stream, h (block type, or int8 levels
 # with their scales hs), and the norms' reciprocal roots (None unless saved).
 BlockNorm = collections.namedtuple("BlockNorm", "x h hs r_post r_pre")
 BlockNormGrad = collections.namedtuple("BlockNormGrad", "dx dy dgate dw_post dw_pre")
+# Result of quant_mx: codes and scales of the blocks along the rows, and of those
+# along the columns (None unless asked for).
+QuantMx = collections.namedtuple("QuantMx", "q s qt st")
+LinearMxGrad = collections.namedtuple("LinearMxGrad", "dx dw dbias")
+HeadNormRope = collections.namedtuple("HeadNormRope", "q k")
+HeadNormRopeGrad = collections.namedtuple("HeadNormRopeGrad", "dq dk dw_q dw_k")
 
 
 class TileGemmError(RuntimeError):
@@ -159,6 +204,23 @@ def load_library():
                                            p]
     lib.tg_block_norm_backward_workspace_size.argtypes = [ctypes.POINTER(BlockNormGradArgs),
                                                           size_p]
+    lib.tg_quant_mx.argtypes = [i64, i64, c_int, p, i64, c_int, p, p, p, p, p]
+    lib.tg_dequant_mx.argtypes = [i64, i64, c_int, p, p, c_int, p, i64, p]
+    lib.tg_linear_mx.argtypes = [i64, i64, i64, c_int, p, i64, c_int, p, p, p, p, i64, c_int, p,
+                                 ctypes.c_size_t, p]
+    lib.tg_linear_mx_workspace_size.argtypes = [i64, i64, i64, c_int, c_int, size_p]
+    lib.tg_linear_mx_backward.argtypes = [ctypes.POINTER(LinearMxGradArgs), p, ctypes.c_size_t, p]
+    lib.tg_linear_mx_backward_workspace_size.argtypes = [ctypes.POINTER(LinearMxGradArgs), size_p]
+    lib.tg_head_norm_rope.argtypes = [ctypes.POINTER(HeadNormRopeArgs), p]
+    lib.tg_head_norm_rope_backward.argtypes = [ctypes.POINTER(HeadNormRopeGradArgs), p,
+                                               ctypes.c_size_t, p]
+    lib.tg_head_norm_rope_backward_workspace_size.argtypes = [
+        ctypes.POINTER(HeadNormRopeGradArgs), size_p]
+    for name in ("tg_quant_mx", "tg_dequant_mx", "tg_linear_mx", "tg_linear_mx_workspace_size",
+                 "tg_linear_mx_backward", "tg_linear_mx_backward_workspace_size",
+                 "tg_head_norm_rope", "tg_head_norm_rope_backward",
+                 "tg_head_norm_rope_backward_workspace_size"):
+        getattr(lib, name).restype = c_int
     for name in ("tg_quant_i8", "tg_gemm_i8", "tg_linear_i8", "tg_linear_i8_workspace_size",
                  "tg_block_norm", "tg_block_norm_backward",
                  "tg_block_norm_backward_workspace_size"):
@@ -830,6 +892,325 @@ def block_norm_backward(x_new, dx_new=None, dh=None, y=None, gate=None, gate_row
     _one_device(x_new, dx_new, dh, y, gate, w_post, w_pre, r_post, r_pre, workspace)
     _check(lib.tg_block_norm_backward(ref, wp, wn, _stream_ptr(x_new.device, stream)))
     return BlockNormGrad(dx, dy, dgate, dw_post, dw_pre)
+
+
+# --------------------------------------------------------------------------
+# Microscaled linear path, and norms of query and key heads with rotation.
+# --------------------------------------------------------------------------
+def _call(device, entry, *args):
+    """entry(*args) with `device` current: the null stream is the current device's."""
+    torch = _torch()
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            _check(entry(*args))
+    else:
+        _check(entry(*args))
+
+
+def _workspace(workspace, need, like, stream):
+    """(tensor, pointer, bytes) of the caller's workspace, or of one allocated for `need` bytes."""
+    if workspace is not None:
+        _require_gpu_tensor("workspace", workspace)
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if not need:
+        return None, None, 0
+    workspace = _empty((need,), _torch().uint8, like, stream)
+    return workspace, workspace.data_ptr(), need
+
+
+def _mx_format(fmt):
+    if fmt not in (TG_MX_E2M1, TG_MX_E4M3):
+        raise ValueError("format must be TG_MX_E2M1 or TG_MX_E4M3")
+    return fmt
+
+
+def _mx_shapes(rows, cols, fmt):
+    """Shapes of the codes and scales of [rows, cols] elements."""
+    padded = -(-cols // 128) * 128
+    return (rows, padded // 2 if fmt == TG_MX_E2M1 else padded), (rows, padded // 32)
+
+
+def _mx_dense(name, t, shape):
+    torch = _torch()
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s must be a dense GPU tensor" % name)
+    if t.dtype != torch.uint8:
+        raise TypeError("%s must be uint8, got %s" % (name, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), tuple(t.shape)))
+    return t.data_ptr()
+
+
+def quant_mx(X, fmt=TG_MX_E2M1, sides="rows", q=None, s=None, qt=None, st=None, stream=None):
+    """X [M, K] (fp32, fp16 or bf16) to microscaled blocks of 32 elements
+    (tg_quant_mx).  sides: "rows" (q, s: blocks along the rows), "columns" (qt,
+    st: blocks along the columns, as rows of the transpose) or "both", from one
+    read.  q: uint8 [M, Kp / 2] (E2M1, two codes to a byte) or [M, Kp] (E4M3), s:
+    uint8 [M, Kp / 32], Kp = K rounded up to a multiple of 128; qt and st likewise
+    with M and K exchanged.  Returns a QuantMx(q, s, qt, st), None where not
+    asked for."""
+    torch = _torch()
+    if sides not in ("rows", "columns", "both"):
+        raise ValueError("sides must be 'rows', 'columns' or 'both'")
+    _mx_format(fmt)
+    ldx = _rows("X", X)
+    M, K = X.shape
+    ptr = [None] * 4
+    if sides != "columns":
+        sq, ss = _mx_shapes(M, K, fmt)
+        q = _empty(sq, torch.uint8, X, stream) if q is None else q
+        s = _empty(ss, torch.uint8, X, stream) if s is None else s
+        ptr[:2] = _mx_dense("q", q, sq), _mx_dense("s", s, ss)
+    elif q is not None or s is not None:
+        raise ValueError("q and s are not written with sides 'columns'")
+    if sides != "rows":
+        sq, ss = _mx_shapes(K, M, fmt)
+        qt = _empty(sq, torch.uint8, X, stream) if qt is None else qt
+        st = _empty(ss, torch.uint8, X, stream) if st is None else st
+        ptr[2:] = _mx_dense("qt", qt, sq), _mx_dense("st", st, ss)
+    elif qt is not None or st is not None:
+        raise ValueError("qt and st are not written with sides 'rows'")
+    _one_device(X, q, s, qt, st)
+    _call(X.device, load_library().tg_quant_mx, M, K, _dtype_code(X), X.data_ptr(), ldx, fmt, *ptr,
+          _stream_ptr(X.device, stream))
+    return QuantMx(q, s, qt, st)
+
+
+def dequant_mx(q, s, fmt=TG_MX_E2M1, K=None, dtype=None, X=None, stream=None):
+    """The values that codes q and scales s stand for (tg_dequant_mx): [M, K] of
+    `dtype` (bfloat16 unless X or dtype says otherwise).  K: the columns wanted,
+    whose number rounded up to a multiple of 128 is that of q (None: all)."""
+    torch = _torch()
+    _mx_format(fmt)
+    if q.dim() != 2:
+        raise ValueError("q must be 2-D")
+    M = q.shape[0]
+    if K is None:
+        K = q.shape[1] * (2 if fmt == TG_MX_E2M1 else 1)
+    sq, ss = _mx_shapes(M, K, fmt)
+    pq, ps = _mx_dense("q", q, sq), _mx_dense("s", s, ss)
+    if X is None:
+        X = _empty((M, K), dtype or torch.bfloat16, q, stream)
+    elif dtype is not None and X.dtype != dtype:
+        raise TypeError("X must be %s, got %s" % (dtype, X.dtype))
+    ldx = _rows("X", X, (M, K))
+    _one_device(q, s, X)
+    _call(q.device, load_library().tg_dequant_mx, M, K, fmt, pq, ps, _dtype_code(X), X.data_ptr(),
+          ldx, _stream_ptr(q.device, stream))
+    return X
+
+
+def linear_mx_workspace_size(M: int, N: int, K: int, dtype: int, fmt: int = TG_MX_E2M1) -> int:
+    """Workspace bytes :func:`linear_mx` needs (0: none)."""
+    out = ctypes.c_size_t(0)
+    _check(load_library().tg_linear_mx_workspace_size(M, N, K, dtype, fmt, ctypes.byref(out)))
+    return out.value
+
+
+def linear_mx(X, Wq, Ws, bias=None, fmt=TG_MX_E2M1, C=None, epilogue=None, workspace=None,
+              stream=None):
+    """C = epilogue(Q(X) @ W^T + bias) with the rows of X [M, K] (fp32, fp16 or
+    bf16) brought to microscaled blocks of `fmt` within the call and W in 4 bits:
+    Wq uint8 [N, Kp / 2], Ws uint8 [N, Kp / 32], the q and s of
+    quant_mx(W) (Kp: K rounded up to a multiple of 128).  bias: fp32 [N]; C [M, N]
+    of X's dtype.  workspace: a uint8 device tensor of at least
+    :func:`linear_mx_workspace_size` bytes (allocated here when None and needed)."""
+    _mx_format(fmt)
+    ldx = _rows("X", X)
+    M, K = X.shape
+    if Wq.dim() != 2:
+        raise ValueError("Wq must be 2-D")
+    N = Wq.shape[0]
+    sq, ss = _mx_shapes(N, K, TG_MX_E2M1)
+    pq, ps = _mx_dense("Wq", Wq, sq), _mx_dense("Ws", Ws, ss)
+    if C is None:
+        C = _empty((M, N), X.dtype, X, stream)
+    ldc = _rows("C", C, (M, N), X.dtype)
+    dt = _dtype_code(X)
+    need = linear_mx_workspace_size(M, N, K, dt, fmt) if workspace is None else 0
+    workspace, wp, wn = _workspace(workspace, need, X, stream)
+    pb = _vector("bias", bias, N, _torch().float32)
+    _one_device(X, Wq, Ws, bias, C, workspace)
+    _call(X.device, load_library().tg_linear_mx, M, N, K, dt, X.data_ptr(), ldx, fmt, pq, ps, pb,
+          C.data_ptr(), ldc, _epi_code(epilogue), wp, wn, _stream_ptr(X.device, stream))
+    return C
+
+
+def linear_mx_backward(dY, X=None, W=None, fmt=TG_MX_E2M1, dbias=False, workspace=None,
+                       stream=None):
+    """Gradients of Y = X @ W^T + bias with both products in microscaled blocks
+    (tg_linear_mx_backward): dx = Q(dY) @ Q4(W) where W [N, K] is given, dw =
+    Q(dY)^T @ Q4(X) where X [M, K] is given, and with dbias the sums of dY's
+    columns.  dY [M, N] goes to blocks of `fmt`, W and X to 4 bits, along the
+    axis that is summed.  W: dY's type, or fp32 (not in 4 bits).  Returns a
+    LinearMxGrad(dx, dw, dbias): dx of dY's type, dw of W's (dY's without W), dbias
+    fp32; None where not asked for."""
+    torch = _torch()
+    _mx_format(fmt)
+    a = LinearMxGradArgs()
+    a.lddy = _rows("dY", dY)
+    M, N = dY.shape
+    if X is None and W is None and not dbias:
+        raise ValueError("nothing to compute: X, W or dbias is needed")
+    K = 0
+    for name, t, rows in (("X", X, M), ("W", W, N)):
+        if t is None:
+            continue
+        if t.dim() != 2 or t.shape[0] != rows or (name == "W" and X is not None
+                                                  and t.shape[1] != K):
+            raise ValueError("%s must have %d rows%s, got %s"
+                             % (name, rows, " of X's length" if name == "W" else "",
+                                tuple(t.shape)))
+        K = t.shape[1]
+    wtype = dY.dtype if W is None else W.dtype
+    a.M, a.N, a.K, a.fmt = M, N, K, fmt
+    a.dtype = a.wtype = _dtype_code(dY)
+    a.dY = dY.data_ptr()
+    dx = dw = db = None
+    if W is not None:
+        if wtype not in (dY.dtype, torch.float32):
+            raise TypeError("W must be %s or float32, got %s" % (dY.dtype, wtype))
+        a.wtype = _dtype_code(W)
+        a.W, a.ldw = W.data_ptr(), _rows("W", W)
+        dx = _empty((M, K), dY.dtype, dY, stream)
+        a.dX, a.lddx = dx.data_ptr(), K
+    if X is not None:
+        a.X, a.ldx = X.data_ptr(), _rows("X", X, None, dY.dtype)
+        dw = _empty((N, K), wtype, dY, stream)
+        a.dW, a.lddw = dw.data_ptr(), K
+    if dbias:
+        db = _empty((N,), torch.float32, dY, stream)
+        a.dbias = db.data_ptr()
+    lib = load_library()
+    need = ctypes.c_size_t(0)
+    if workspace is None:
+        _check(lib.tg_linear_mx_backward_workspace_size(ctypes.byref(a), ctypes.byref(need)))
+    workspace, wp, wn = _workspace(workspace, need.value, dY, stream)
+    _one_device(dY, X, W, workspace)
+    _call(dY.device, lib.tg_linear_mx_backward, ctypes.byref(a), wp, wn,
+          _stream_ptr(dY.device, stream))
+    return LinearMxGrad(dx, dw, db)
+
+
+def _set_heads(a, field, name, t, T=None, H=None, D=None, dtype=None):
+    """Puts the heads t [T, H, D] into `field` of the argument struct, with its
+    strides of tokens and heads."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    size = t.shape
+    if len(size) != 3 or any(w is not None and g != w for g, w in zip(size, (T, H, D))):
+        raise ValueError("%s must be [tokens, heads, values]%s, got %s"
+                         % (name, "" if T is None else " = %s" % [T, H, D], tuple(size)))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    st, sh, unit = t.stride()
+    if unit != 1 and size[2] > 1:
+        raise ValueError("%s must have unit stride along a head" % name)
+    setattr(a, field, t.data_ptr())
+    setattr(a, field + "_t", st)
+    setattr(a, field + "_h", sh)
+
+
+def _heads_args(a, q, k, w_q, w_k, cos, sin, positions, eps, interleaved):
+    """Fills what the forward and the backward call share; returns (T, Hq, Hk, D)."""
+    torch = _torch()
+    _set_heads(a, "q", "q", q)
+    T, Hq, D = q.shape
+    Hk = 0
+    if k is not None:
+        Hk = k.shape[1] if k.dim() == 3 else None
+        _set_heads(a, "k", "k", k, T, Hk, D, q.dtype)
+    elif w_k is not None:
+        raise ValueError("w_k without k")
+    a.T, a.Hq, a.Hk, a.D, a.dtype = T, Hq, Hk, D, _dtype_code(q)
+    a.w_q = _vector("w_q", w_q, D, q.dtype)
+    a.w_k = _vector("w_k", w_k, D, q.dtype)
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    if cos is not None:
+        for name, t in (("cos", cos), ("sin", sin)):
+            if not t.is_cuda or not t.is_contiguous() or t.dim() != 2 or t.shape != cos.shape:
+                raise ValueError("%s must be a dense GPU tensor [positions, pairs]" % name)
+            if t.dtype != torch.float32:
+                raise TypeError("%s must be torch.float32, got %s" % (name, t.dtype))
+        a.P, a.R = cos.shape[0], 2 * cos.shape[1]
+        if a.R > D:
+            raise ValueError("cos has %d pairs for heads of %d values" % (cos.shape[1], D))
+        if positions is None and a.R > 0 and a.P < T:
+            raise ValueError("positions are needed: tables of %d positions for %d tokens"
+                             % (a.P, T))
+        a.cos, a.sin = cos.data_ptr(), sin.data_ptr()
+    if positions is not None:
+        a.positions = _vector("positions", positions, T, torch.int64)
+    a.eps, a.interleaved = eps, bool(interleaved)
+    return T, Hq, Hk, D
+
+
+def head_norm_rope(q, k=None, w_q=None, w_k=None, cos=None, sin=None, positions=None, eps=1e-6,
+                   interleaved=False, q_out=None, k_out=None, stream=None):
+    """Every head of q [T, Hq, D] and k [T, Hk, D] normed, times w_q or w_k [D]
+    (None: ones), and its first 2 * cos.shape[1] values turned to the token's
+    position (tg_head_norm_rope): cos and sin fp32 [P, pairs], positions int64 [T]
+    (None: token t is at position t).  Pairs are half the turned values apart, or
+    neighbours with interleaved.  q and k may have any strides of tokens and
+    heads (slices of one projection's output); q_out and k_out may be q and k.
+    Returns a HeadNormRope(q, k)."""
+    a = HeadNormRopeArgs()
+    T, Hq, Hk, D = _heads_args(a, q, k, w_q, w_k, cos, sin, positions, eps, interleaved)
+    if q_out is None:
+        q_out = _empty((T, Hq, D), q.dtype, q, stream)
+    _set_heads(a, "q_out", "q_out", q_out, T, Hq, D, q.dtype)
+    if k is not None:
+        if k_out is None:
+            k_out = _empty((T, Hk, D), q.dtype, q, stream)
+        _set_heads(a, "k_out", "k_out", k_out, T, Hk, D, q.dtype)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _one_device(q, k, w_q, w_k, cos, sin, positions, q_out, k_out)
+    _call(q.device, load_library().tg_head_norm_rope, ctypes.byref(a),
+          _stream_ptr(q.device, stream))
+    return HeadNormRope(q_out, k_out)
+
+
+def head_norm_rope_backward(dq_out, dk_out, q, k=None, w_q=None, w_k=None, cos=None, sin=None,
+                            positions=None, eps=1e-6, interleaved=False, workspace=None,
+                            stream=None):
+    """Gradients of :func:`head_norm_rope` from those at its outputs; q and k as
+    the forward call had them (not its outputs).  Returns a HeadNormRopeGrad(dq,
+    dk, dw_q, dw_k): dq and dk [T, H, D] of q's type, dw_q and dw_k [D] fp32, None
+    where there is no such input."""
+    torch = _torch()
+    a = HeadNormRopeGradArgs()
+    T, Hq, Hk, D = _heads_args(a, q, k, w_q, w_k, cos, sin, positions, eps, interleaved)
+    if (k is None) != (dk_out is None):
+        raise ValueError("dk_out and k go together")
+    _set_heads(a, "dq_out", "dq_out", dq_out, T, Hq, D, q.dtype)
+    dq = _empty((T, Hq, D), q.dtype, q, stream)
+    _set_heads(a, "dq", "dq", dq)
+    dk = dw_q = dw_k = None
+    if k is not None:
+        _set_heads(a, "dk_out", "dk_out", dk_out, T, Hk, D, q.dtype)
+        dk = _empty((T, Hk, D), q.dtype, q, stream)
+        _set_heads(a, "dk", "dk", dk)
+    if w_q is not None and w_k is not None:  # one allocation for both
+        dw_q, dw_k = _empty((2, D), torch.float32, q, stream).unbind(0)
+    elif w_q is not None:
+        dw_q = _empty((D,), torch.float32, q, stream)
+    elif w_k is not None:
+        dw_k = _empty((D,), torch.float32, q, stream)
+    if dw_q is not None:
+        a.dw_q = dw_q.data_ptr()
+    if dw_k is not None:
+        a.dw_k = dw_k.data_ptr()
+    lib = load_library()
+    need = ctypes.c_size_t(0)
+    if workspace is None:
+        _check(lib.tg_head_norm_rope_backward_workspace_size(ctypes.byref(a), ctypes.byref(need)))
+    workspace, wp, wn = _workspace(workspace, need.value, q, stream)
+    _one_device(q, dq_out, dk_out, k, w_q, w_k, cos, sin, positions, workspace)
+    _call(q.device, lib.tg_head_norm_rope_backward, ctypes.byref(a), wp, wn,
+          _stream_ptr(q.device, stream))
+    return HeadNormRopeGrad(dq, dk, dw_q, dw_k)
 
 
 def query_config(op: int, M: int, N: int, K: int, dtype: int = TG_BF16, trans_a: bool = False,

@@ -1,0 +1,460 @@
+// Linear layer in microscaled blocks (tg_linear_mx, tg_linear_mx_backward):
+//   C[m][n] = epilogue(sum_k a(m, k) w(n, k) + bias[n]),
+// a in E2M1 or E4M3 and w in E2M1, each 32 k of a row with one power of two;
+// fp32 accumulation, one rounding to C's type.
+//
+// mx_linear_kernel: the tiles and main loops of tg_kernel_mx.h and
+// tg_kernel_mx2.h, with bias, any C type and any C rows in the epilogue.
+//
+// mx_stream_kernel: for few tokens the time is that of streaming W once, so W
+// goes from memory straight into the operand registers of
+// v_mfma_scale_f32_16x16x128_f8f6f4, with no LDS on its way.
+//  * Lane layout of that instruction (measured with an in-bounds probe): lane l
+//    supplies row l % 16 and, with g = l / 16, the scale byte of k-block g and, in
+//    E2M1, that block's 16 bytes; in E4M3 its bytes 0 .. 15 are k = 16 g .. and
+//    16 .. 31 are k = 64 + 16 g ..; it holds results of column l % 16 (second
+//    operand), rows 4 g + 0 .. 3.
+//  * A workgroup owns 16 rows of W and 16 MT tokens, and all of k; its NW waves
+//    take runs of 256 k in turn: two instructions of 16 rows' 64 bytes each, a
+//    whole cache line of every row, and 8 scale bytes of it.
+//  * The loads of a wave's next run are issued before the MFMAs of this one.
+//  * The waves' sums are added in LDS, in the waves' order.
+//  * Rows past M or N read the last row again; their results are not stored.
+//  * FUSED: the activations are given in 16 or 32 bits and every workgroup
+//    quantises them itself, into LDS, while its first loads of W are in flight:
+//    one launch instead of two.
+#pragma once
+
+#include "tg_kernel_mx2.h"
+#include "tg_mx.h"
+
+namespace tg {
+
+struct MxLinearParams {
+    GemmParams g;  // A, As, B (W), Bs, C, M, N, K (padded), tiles, relu, c_vec, group_m, stamps
+    const float* bias;  // [N] or NULL
+    int64_t ldc;
+};
+
+__device__ __forceinline__ float mx_result(float v, float bias, int relu)
+{
+    v += bias;
+    return (relu && !(v > 0.0f)) ? 0.0f : v;
+}
+
+// Results of one wave's FM x FN blocks (lane l holds row l % 32 and, for element
+// 4 q + e, column 8 q + 4 (l / 32) + e of a block) through its own LDS region
+// `st` (32 rows of FN * 32 results), 32 rows at a time: rounded, written as
+// 16-byte chunks (chunk c of row r at c ^ (r % CH)), read back and stored 16
+// bytes to a lane, so that a store instruction writes runs of whole rows.  c_vec:
+// whole aligned chunks and 32 rows within 31 bits of offset; other C rows take
+// unaligned stores, and the chunk across column N single ones.
+template <int DT, int FM, int FN>
+__device__ __forceinline__ void mx_store_staged(const f32x16 (&acc)[FM][FN],
+                                                const MxLinearParams& p, int mw0, int nw0,
+                                                int lane, lds_char* st)
+{
+    constexpr int ES = DT == DT_F32 ? 4 : 2;
+    constexpr int EPC = 16 / ES;
+    constexpr int ROWB = FN * 32 * ES;
+    constexpr int CH = ROWB / 16;
+    constexpr int RPI = 64 / CH;  // rows of a store instruction
+    static_assert((CH & (CH - 1)) == 0 && CH >= 4 && CH <= 64, "rows of 64 to 1024 bytes");
+    const GemmParams& g = p.g;
+    const int lr = lane & 31, h = lane >> 5;
+    f32x4 bs[FN][4];
+#pragma unroll
+    for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int n = nw0 + fn * 32 + 8 * q + 4 * h + e;
+                bs[fn][q][e] = p.bias ? p.bias[n < g.N ? n : g.N - 1] : 0.0f;
+            }
+    const int c = lane % CH;
+    const int n = nw0 + EPC * c;
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = mx_result(acc[fm][fn][4 * q + e], bs[fn][q][e], g.relu);
+                if constexpr (DT == DT_F32) {
+                    const int ch = 8 * fn + 2 * q + h;
+                    *(lds_u32x4*)(st + lr * ROWB + ((ch ^ (lr & (CH - 1))) << 4)) =
+                        __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
+                } else {
+                    const int ch = 4 * fn + q;
+                    *(lds_u32x2*)(st + lr * ROWB + ((ch ^ (lr & (CH - 1))) << 4) + 8 * h) =
+                        u32x2{pack2(v[0], v[1], DT), pack2(v[2], v[3], DT)};
+                }
+            }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // own region: no barrier needed
+        const auto rs =
+            make_rsrc((char*)g.C + ((int64_t)(mw0 + fm * 32) * p.ldc + nw0) * ES, 0x7FFFFFFFu);
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += RPI) {
+            const int r = r0 + lane / CH;
+            const int m = mw0 + fm * 32 + r;
+            const u32x4 v = *(const lds_u32x4*)(st + r * ROWB + ((c ^ (r & (CH - 1))) << 4));
+            if (m >= g.M || n >= g.N)
+                continue;
+            if (g.c_vec) {
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    v, rs, (int)((u32)(r * (int)p.ldc + EPC * c) * (u32)ES), 0, kStoreThrough);
+                continue;
+            }
+            char* to = (char*)g.C + ((int64_t)m * p.ldc + n) * ES;
+            if (n + EPC <= g.N) {
+                struct __attribute__((packed, aligned(ES))) Any {
+                    u32x4 v;
+                };
+                ((Any*)to)->v = v;
+            } else {
+#pragma unroll
+                for (int e = 0; e < EPC; ++e)
+                    if (n + e < g.N) {
+                        const u32 w = v[e * ES / 4];
+                        if constexpr (DT == DT_F32)
+                            ((u32*)to)[e] = w;
+                        else
+                            ((uint16_t*)to)[e] = (uint16_t)(w >> (16 * (e & 1)));
+                    }
+            }
+        }
+    }
+}
+
+// G: DmaMx or DmaMx2 of a tile.
+template <class G, int DT>
+__device__ __forceinline__ void mx_linear_run(const MxLinearParams& p, int group_m)
+{
+    constexpr int NW = G::NW, WTM = G::WTM, WTN = G::WTN, FM = G::FM, FN = G::FN;
+    constexpr int WGN = G::BNT / WTN;
+    constexpr int ES = DT == DT_F32 ? 4 : 2;
+    static_assert(NW * 32 * WTN * ES <= G::LDS_BYTES, "32 staged rows to a wave");
+    __shared__ __attribute__((aligned(1024))) char smem[G::LDS_BYTES];
+    lds_char* sm = (lds_char*)smem;
+    const u32 smem0 = lds_offset(smem);
+    const GemmParams& g = p.g;
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int wm = w / WGN, wn = w % WGN;
+    const TileCoord tc = tile_of(blockIdx.x, g.tiles_m, g.tiles_n, group_of(g, group_m));
+    const int m0 = tc.m * G::BMT, n0 = tc.n * G::BNT;
+    const int KT = (g.K + G::BK - 1) / G::BK;
+    typename G::Lane L;
+    G::setup(L, g, m0, n0, w, lane, wm, wn);
+    f32x16 acc[FM][FN];
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                acc[fm][fn][r] = 0.0f;
+    switch (w) {
+    case 0:
+        G::template main_loop<0>(acc, L, sm, g, m0, n0, KT, smem0);
+        break;
+    case 1:
+        G::template main_loop<1>(acc, L, sm, g, m0, n0, KT, smem0);
+        break;
+    case 2:
+        G::template main_loop<2>(acc, L, sm, g, m0, n0, KT, smem0);
+        break;
+    case 3:
+        G::template main_loop<3>(acc, L, sm, g, m0, n0, KT, smem0);
+        break;
+    case 4:
+        G::template main_loop<4 % NW>(acc, L, sm, g, m0, n0, KT, smem0);
+        break;
+    case 5:
+        G::template main_loop<5 % NW>(acc, L, sm, g, m0, n0, KT, smem0);
+        break;
+    case 6:
+        G::template main_loop<6 % NW>(acc, L, sm, g, m0, n0, KT, smem0);
+        break;
+    default:
+        G::template main_loop<7 % NW>(acc, L, sm, g, m0, n0, KT, smem0);
+        break;
+    }
+    wait_all_barrier();  // every wave's copies landed and reads done
+    mx_store_staged<DT, FM, FN>(acc, p, m0 + wm * WTM, n0 + wn * WTN, lane,
+                                sm + w * (32 * WTN * ES));
+}
+
+// A tile's kernel; K a whole number of strips of 128 (of 1024 with MX2).
+template <bool MX2, int DT, int AFMT, int BM, int BN, int WGM, int WGN, int NS>
+struct MxTileOf;
+template <int DT, int AFMT, int BM, int BN, int WGM, int WGN, int NS>
+struct MxTileOf<false, DT, AFMT, BM, BN, WGM, WGN, NS>
+    : DmaMx<AFMT, BM, BN, WGM, WGN, NS, 4, false> {
+    static constexpr int BMT = BM, BNT = BN;
+    static constexpr int OCC = MxOcc<AFMT, BM, BN, WGM * WGN>::value;
+};
+template <int DT, int AFMT, int BM, int BN, int WGM, int WGN, int NS>
+struct MxTileOf<true, DT, AFMT, BM, BN, WGM, WGN, NS> : DmaMx2<AFMT, BM, BN, WGM, WGN, 4> {
+    static constexpr int BMT = BM, BNT = BN;
+    static constexpr int OCC = WGM * WGN > 4 ? 2 : 1;
+};
+
+template <bool MX2, int DT, int AFMT, int BM, int BN, int WGM, int WGN, int NS>
+__global__ __attribute__((
+    amdgpu_flat_work_group_size(WGM * WGN * 64, WGM * WGN * 64),
+    amdgpu_waves_per_eu(MxTileOf<MX2, DT, AFMT, BM, BN, WGM, WGN, NS>::OCC,
+                        MxTileOf<MX2, DT, AFMT, BM, BN, WGM, WGN, NS>::OCC))) void
+mx_linear_kernel(MxLinearParams p)
+{
+    const ClockStamp clk = stamp_begin(p.g);
+    mx_linear_run<MxTileOf<MX2, DT, AFMT, BM, BN, WGM, WGN, NS>, DT>(p, 4);
+    stamp_end(p.g, clk);
+}
+
+// --------------------------------------------------------------------------
+// Few tokens.
+// --------------------------------------------------------------------------
+struct MxStreamParams {
+    MxLinearParams l;
+    int dt_out;
+    const void* X;  // FUSED: activations [M][ldx], Kx columns
+    int64_t ldx;
+    int Kx;
+};
+
+template <int DTX, int AFMT, int MT, int NW, bool FUSED>
+struct MxStream {
+    static constexpr bool A8 = AFMT == MX_E4M3;
+    static constexpr int RUN = 256;
+    static constexpr int TOKENS = 16 * MT;
+
+    // FUSED: LDS bytes of a token's codes, 16 apart from a multiple of the bank
+    // line so that the rows of a fragment read spread, and of its scales.
+    static __host__ __device__ __forceinline__ int code_row(int Kp)
+    {
+        return (int)mx_bytes<AFMT>(Kp) + 16;
+    }
+    static __host__ __device__ __forceinline__ int lds_bytes(int M, int Kp)
+    {
+        const int a = FUSED ? M * (code_row(Kp) + Kp / 32) : 0, r = NW * MT * 1024;
+        return a > r ? a : r;
+    }
+
+    struct Run {
+        u32x4 w[2];
+        u32x2 ws;
+        u32x4 a[FUSED ? 1 : MT][2][A8 ? 2 : 1];
+        u32x2 as[FUSED ? 1 : MT];
+    };
+    struct Rows {
+        const uint8_t *w, *ws;
+        const uint8_t *a[MT], *as[MT];
+    };
+
+    // Steps of 128 k of the run at k0 that exist (the last run may have one).
+    static __device__ __forceinline__ void load(Run& R, const Rows& at, int k0, int steps, int g)
+    {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (s >= steps)
+                break;
+            R.w[s] = *(const u32x4*)(at.w + k0 / 2 + 64 * s + 16 * g);
+            R.ws[s] = *(const u32*)(at.ws + k0 / 32 + 4 * s);
+            if constexpr (!FUSED) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const uint8_t* a = at.a[m] + mx_bytes<AFMT>(k0 + 128 * s) + 16 * g;
+                    R.a[m][s][0] = *(const u32x4*)a;
+                    if constexpr (A8)
+                        R.a[m][s][1] = *(const u32x4*)(a + 64);
+                    R.as[m][s] = *(const u32*)(at.as[m] + k0 / 32 + 4 * s);
+                }
+            }
+        }
+    }
+
+    static __device__ __forceinline__ void multiply(f32x4 (&acc)[MT], const Run& R,
+                                                    const uint8_t* codes, const uint8_t* scales,
+                                                    int k0, int steps, int g)
+    {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (s >= steps)
+                break;
+            const u32x4 w = R.w[s];
+            const i32x8 wop = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                u32x4 lo, hi;
+                u32 as;
+                if constexpr (FUSED) {
+                    const uint8_t* a = codes + mx_bytes<AFMT>(k0 + 128 * s) + 16 * g;
+                    lo = *(const u32x4*)a;
+                    hi = A8 ? *(const u32x4*)(a + (A8 ? 64 : 0)) : u32x4{0, 0, 0, 0};
+                    as = *(const u32*)(scales + k0 / 32 + 4 * s);
+                } else {
+                    lo = R.a[m][s][0];
+                    hi = A8 ? R.a[m][s][A8 ? 1 : 0] : u32x4{0, 0, 0, 0};
+                    as = R.as[m][s];
+                }
+                const i32x8 aop = {(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
+                                   (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+                acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    wop, aop, acc[m], MX_E2M1, AFMT, 0, (int)(R.ws[s] >> (8 * g)), 0,
+                    (int)(as >> (8 * g)));
+            }
+        }
+    }
+
+    // The M tokens' blocks into LDS: rows of code_row(Kp) bytes, then the scales.
+    static __device__ __forceinline__ void quantise(const MxStreamParams& p, uint8_t* codes,
+                                                    uint8_t* scales)
+    {
+        const int Kp = p.l.g.K, per = Kp / 8, row_b = code_row(Kp);
+        for (int m = 0; m < p.l.g.M; ++m) {
+            const char* src = elem_ptr<DTX>(p.X, m * p.ldx);
+            for (int u = threadIdx.x; u < per; u += NW * 64) {  // whole quads: per % 16 == 0
+                Raw8<DTX> r;
+                load8<DTX>(r, src, 8 * u, p.Kx - 8 * u);
+                u32 t = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    t = MaxOp::of(t, __builtin_bit_cast(u32, get8<DTX>(r, i)) & 0x7FFFFFFFu);
+                MxScale s;
+                s.of_amax<AFMT>(mx_block_max<4>(t));
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = s.ok ? get8<DTX>(r, i) : 0.0f;
+                uint8_t* to = codes + m * row_b + mx_bytes<AFMT>(8 * u);
+                if constexpr (A8)
+                    *(u32x2*)to = u32x2{mx_codes8(v[0], v[1], v[2], v[3], s.p),
+                                        mx_codes8(v[4], v[5], v[6], v[7], s.p)};
+                else
+                    *(u32*)to = mx_codes4(v, s.p);
+                if ((u & 3) == 0)
+                    scales[m * (Kp / 32) + u / 4] = (uint8_t)s.byte;
+            }
+        }
+    }
+
+    static __device__ __forceinline__ void run(const MxStreamParams& p)
+    {
+        extern __shared__ __attribute__((aligned(16))) uint8_t mx_lds[];
+        const GemmParams& gp = p.l.g;
+        const int tid = threadIdx.x;
+        const int lane = tid & 63;
+        const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int m0 = (int)blockIdx.y * TOKENS, n0 = (int)blockIdx.x * 16;
+        const int ln = lane & 15, g = lane >> 4;
+        const int K = gp.K;
+        Rows at;
+        {
+            const int64_t n = n0 + ln < gp.N ? n0 + ln : gp.N - 1;
+            at.w = (const uint8_t*)gp.B + n * (K / 2);
+            at.ws = (const uint8_t*)gp.Bs + n * (K / 32);
+        }
+        const uint8_t *codes = nullptr, *scales = nullptr;
+        if constexpr (FUSED) {
+            const int m = ln < gp.M ? ln : gp.M - 1;
+            codes = mx_lds + m * code_row(K);
+            scales = mx_lds + gp.M * code_row(K) + m * (K / 32);
+        } else {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const int t = m0 + 16 * i + ln;
+                const int64_t m = t < gp.M ? t : gp.M - 1;
+                at.a[i] = (const uint8_t*)gp.A + m * mx_bytes<AFMT>(K);
+                at.as[i] = (const uint8_t*)gp.As + m * (K / 32);
+            }
+        }
+        f32x4 acc[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const int whole = K / RUN, rest = K % RUN / 128;  // runs, and steps of a partial one
+        Run R;
+        int r = w;
+        if (r < whole)
+            load(R, at, r * RUN, 2, g);
+        if constexpr (FUSED) {
+            quantise(p, mx_lds, mx_lds + gp.M * code_row(K));
+            __syncthreads();
+        }
+        while (r < whole) {
+            const int next = r + NW;
+            Run S = R;
+            if (next < whole)
+                load(R, at, next * RUN, 2, g);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(acc, S, codes, scales, r * RUN, 2, g);
+            r = next;
+        }
+        if (rest > 0 && w == whole % NW) {
+            load(R, at, whole * RUN, 1, g);
+            multiply(acc, R, codes, scales, whole * RUN, 1, g);
+        }
+        float* red = (float*)mx_lds;
+        if constexpr (FUSED)
+            __syncthreads();  // the codes' last reads
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            *(f32x4*)&red[(w * MT + m) * 256 + lane * 4] = acc[m];
+        __syncthreads();
+        for (int o = tid; o < MT * 256; o += NW * 64) {
+            float s = 0.0f;
+#pragma unroll
+            for (int v = 0; v < NW; ++v)
+                s += red[v * MT * 256 + o];
+            const int l = (o >> 2) & 63;
+            const int m = m0 + 16 * (o >> 8) + (l & 15);
+            const int n = n0 + 4 * (l >> 4) + (o & 3);
+            if (m < gp.M && n < gp.N) {
+                const float v = mx_result(s, p.l.bias ? p.l.bias[n] : 0.0f, gp.relu);
+                const int64_t c = (int64_t)m * p.l.ldc + n;
+                if (p.dt_out == DT_F32)
+                    ((float*)gp.C)[c] = v;
+                else
+                    ((uint16_t*)gp.C)[c] = cvt1(v, p.dt_out);
+            }
+        }
+    }
+};
+
+template <int DTX, int AFMT, int MT, int NW, bool FUSED>
+__global__ __attribute__((amdgpu_flat_work_group_size(NW * 64, NW * 64))) void
+mx_stream_kernel(MxStreamParams p)
+{
+    const ClockStamp clk = stamp_begin(p.l.g);
+    MxStream<DTX, AFMT, MT, NW, FUSED>::run(p);
+    stamp_end(p.l.g, clk);
+}
+
+// C = epilogue(bias) where K is 0.
+struct MxFillParams {
+    const float* bias;
+    void* C;
+    int64_t ldc;
+    int M, N, dt, relu;
+};
+
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void
+mx_fill_kernel(MxFillParams p)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)p.M * p.N)
+        return;
+    const int64_t m = i / p.N, n = i - m * p.N;
+    const float v = mx_result(0.0f, p.bias ? p.bias[n] : 0.0f, p.relu);
+    if (p.dt == DT_F32)
+        ((float*)p.C)[m * p.ldc + n] = v;
+    else
+        ((uint16_t*)p.C)[m * p.ldc + n] = cvt1(v, p.dt);
+}
+
+}  // namespace tg

@@ -1,0 +1,516 @@
+// Entry points of the microscaled linear path: quantisation to blocks and back,
+// the linear layer with its activations quantised within the call, and its
+// gradients.  Arguments are checked before any HIP call; the kernel is chosen by
+// sizes and alignment.
+#include <hip/hip_runtime.h>
+
+#include "tg_host.h"
+#include "tg_kernel_mx_linear.h"
+#include "tg_kernel_mx_quant.h"
+
+namespace {
+
+using tg::ceil_div;
+using tg::kMaxDim;
+using tg::mx_padded;
+using tg::overlap;
+using tg::Span;
+using tg::span;
+using tg::span1;
+
+constexpr int64_t kMaxLen = kMaxDim / 256;  // of a summed axis: a tile's offsets fit 31 bits
+
+bool fmt_ok(int f) { return f == TG_MX_E2M1 || f == TG_MX_E4M3; }
+int64_t code_bytes(int fmt, int64_t n) { return fmt == TG_MX_E4M3 ? n : n / 2; }
+bool misaligned(const void* codes, const void* scales)
+{
+    return ((uintptr_t)codes & 15) != 0 || ((uintptr_t)scales & 3) != 0;
+}
+
+// Calls f with type and format as compile-time constants.
+template <class F>
+auto by_type(int dt, int fmt, const F& f)
+{
+    using std::integral_constant;
+    using E2 = integral_constant<int, tg::MX_E2M1>;
+    using E4 = integral_constant<int, tg::MX_E4M3>;
+    const bool e4 = fmt == TG_MX_E4M3;
+    if (dt == TG_F32)
+        return e4 ? f(integral_constant<int, tg::DT_F32>{}, E4{})
+                  : f(integral_constant<int, tg::DT_F32>{}, E2{});
+    if (dt == TG_F16)
+        return e4 ? f(integral_constant<int, tg::DT_F16>{}, E4{})
+                  : f(integral_constant<int, tg::DT_F16>{}, E2{});
+    return e4 ? f(integral_constant<int, tg::DT_BF16>{}, E4{})
+              : f(integral_constant<int, tg::DT_BF16>{}, E2{});
+}
+
+// --------------------------------------------------------------------------
+// Quantisation.
+// --------------------------------------------------------------------------
+constexpr int kUnits = 2;  // of a thread, in flight together
+
+tg::u32 unit_magic(int64_t Kp)
+{
+    const uint64_t per = (uint64_t)Kp / 8;
+    return per >= 256 * kUnits ? 0 : (tg::u32)((((uint64_t)1 << 32) + per - 1) / per);
+}
+
+const void* columns_kernel(int dt, int fmt, bool rows, bool cols, bool sums)
+{
+    return by_type(dt, fmt, [&](auto D, auto F) -> const void* {
+        constexpr int DT = decltype(D)::value, FMT = decltype(F)::value;
+        if (!cols)
+            return rows ? (const void*)&tg::mx_columns_kernel<DT, FMT, true, false, true>
+                        : (const void*)&tg::mx_columns_kernel<DT, FMT, false, false, true>;
+        if (sums)
+            return rows ? (const void*)&tg::mx_columns_kernel<DT, FMT, true, true, true>
+                        : (const void*)&tg::mx_columns_kernel<DT, FMT, false, true, true>;
+        return rows ? (const void*)&tg::mx_columns_kernel<DT, FMT, true, true, false>
+                    : (const void*)&tg::mx_columns_kernel<DT, FMT, false, true, false>;
+    });
+}
+
+// Blocks along the rows (Q), the columns (Qt), or both from one read; sums: the
+// columns' sums over each 128 rows.
+tg_status launch_quant(int64_t M, int64_t K, int dt, const void* X, int64_t ldx, int fmt,
+                       uint8_t* Q, uint8_t* S, uint8_t* Qt, uint8_t* St, float* sums,
+                       hipStream_t stream)
+{
+    tg::MxQuantParams p{};
+    p.X = X;
+    p.ldx = ldx;
+    p.M = (int)M;
+    p.K = (int)K;
+    p.Kp = (int)mx_padded(K);
+    p.Mp = (int)mx_padded(M);
+    p.Q = Q;
+    p.S = S;
+    p.Qt = Qt;
+    p.St = St;
+    p.sums = sums;
+    p.magic = unit_magic(p.Kp);
+    if (!Qt && !sums) {
+        const void* k = by_type(dt, fmt, [](auto D, auto F) {
+            return (const void*)&tg::mx_rows_kernel<decltype(D)::value, decltype(F)::value, kUnits>;
+        });
+        return tg::launch_kernel(k, ceil_div(M * (p.Kp / 8), 256 * kUnits), 1, 256, &p, stream,
+                                 "mx_rows");
+    }
+    const int64_t across = dt == TG_F32 ? 128 : 256;  // columns of a workgroup
+    return tg::launch_kernel(columns_kernel(dt, fmt, Q != nullptr, Qt != nullptr, sums != nullptr),
+                             ceil_div(p.Mp, 256) * ceil_div(K, across), 1, 256, &p, stream,
+                             "mx_columns");
+}
+
+// --------------------------------------------------------------------------
+// Product of two matrices of blocks.
+// --------------------------------------------------------------------------
+struct Tile {
+    const char* name;
+    const void* kernel[3];  // by C's type
+    int bm, bn, threads, strip;  // K has to be a multiple of strip
+    float t0, one, full;
+    int per_cu;
+};
+
+#define TG_MX_TILE(MX2, AFMT, BM, BN, WGM, WGN, NS, STRIP, PER_CU, T0, ONE, FULL)                 \
+    {                                                                                             \
+        "mx_linear_" #AFMT "_" #BM "x" #BN "_w" #WGM "x" #WGN "_s" #NS "_k" #STRIP,               \
+            {(const void*)&tg::mx_linear_kernel<MX2, tg::DT_F32, tg::AFMT, BM, BN, WGM, WGN, NS>, \
+             (const void*)&tg::mx_linear_kernel<MX2, tg::DT_F16, tg::AFMT, BM, BN, WGM, WGN, NS>, \
+             (const void*)&tg::mx_linear_kernel<MX2, tg::DT_BF16, tg::AFMT, BM, BN, WGM, WGN,     \
+                                                NS>},                                             \
+            BM, BN, WGM* WGN * 64, STRIP, T0, ONE, FULL, PER_CU                                   \
+    }
+
+const Tile kTiles2[] = {
+    TG_MX_TILE(false, MX_E2M1, 64, 64, 2, 2, 4, 128, 2, 3.3f, 0.2f, 0.4f),
+    TG_MX_TILE(false, MX_E2M1, 128, 128, 2, 2, 4, 128, 1, 3.5f, 0.3f, 0.6f),
+    TG_MX_TILE(false, MX_E2M1, 256, 256, 2, 4, 4, 128, 1, 6.0f, 0.8f, 0.9f),
+    TG_MX_TILE(true, MX_E2M1, 256, 256, 2, 4, 2, 1024, 1, 6.0f, 0.7f, 0.8f),
+};
+const Tile kTiles4[] = {
+    TG_MX_TILE(false, MX_E4M3, 64, 64, 2, 2, 4, 128, 2, 3.3f, 0.2f, 0.4f),
+    TG_MX_TILE(false, MX_E4M3, 128, 128, 2, 2, 4, 128, 1, 3.5f, 0.35f, 0.7f),
+    TG_MX_TILE(false, MX_E4M3, 256, 256, 2, 4, 3, 128, 1, 6.0f, 1.1f, 1.2f),
+    TG_MX_TILE(true, MX_E4M3, 128, 256, 2, 2, 2, 1024, 1, 6.0f, 0.6f, 0.7f),
+};
+
+float tile_cost(const Tile& t, int64_t M, int64_t N, int64_t K)
+{
+    const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
+    return t.t0 + (float)(K / 128) *
+                      (tiles <= 256 ? t.one : t.full * (float)ceil_div(tiles, 256 * t.per_cu));
+}
+
+const Tile* pick_tile(int64_t M, int64_t N, int64_t K, int fmt)
+{
+    const Tile* best = nullptr;
+    float cost = 0.0f;
+    for (const Tile& t : fmt == TG_MX_E4M3 ? kTiles4 : kTiles2) {
+        if (K % t.strip != 0)
+            continue;
+        const float c = tile_cost(t, M, N, K);
+        if (!best || c < cost) {
+            best = &t;
+            cost = c;
+        }
+    }
+    return best;
+}
+
+template <int DTX, bool FUSED>
+const void* stream_kernel(int fmt, int mt)
+{
+    if (fmt == TG_MX_E4M3)
+        return mt == 2 && !FUSED
+                   ? (const void*)&tg::mx_stream_kernel<DTX, tg::MX_E4M3, FUSED ? 1 : 2, 8, FUSED>
+                   : (const void*)&tg::mx_stream_kernel<DTX, tg::MX_E4M3, 1, 8, FUSED>;
+    return mt == 2 && !FUSED
+               ? (const void*)&tg::mx_stream_kernel<DTX, tg::MX_E2M1, FUSED ? 1 : 2, 8, FUSED>
+               : (const void*)&tg::mx_stream_kernel<DTX, tg::MX_E2M1, 1, 8, FUSED>;
+}
+
+struct Product {
+    int64_t M, N, K;  // K padded
+    int fmt, dt;
+    const uint8_t *A, *As, *W, *Ws;
+    const float* bias;
+    void* C;
+    int64_t ldc;
+    bool relu;
+};
+
+tg::MxLinearParams product_params(const Product& q)
+{
+    tg::MxLinearParams p{};
+    p.g.A = q.A;
+    p.g.As = q.As;
+    p.g.B = q.W;
+    p.g.Bs = q.Ws;
+    p.g.C = q.C;
+    p.g.M = (int)q.M;
+    p.g.N = (int)q.N;
+    p.g.K = (int)q.K;
+    p.g.relu = q.relu;
+    p.g.stamps = tg::clock_stamps();
+    p.bias = q.bias;
+    p.ldc = q.ldc;
+    return p;
+}
+
+tg_status launch_product(const Product& q, hipStream_t stream)
+{
+    tg::MxLinearParams p = product_params(q);
+    if (q.M <= 32) {
+        const int mt = q.M <= 16 ? 1 : 2;
+        tg::MxStreamParams s{p, q.dt, nullptr, 0, 0};
+        return tg::launch_kernel(stream_kernel<tg::DT_F32, false>(q.fmt, mt), ceil_div(q.N, 16),
+                                 ceil_div(q.M, 16 * mt), 512, &s, stream, "mx_stream",
+                                 8 * mt * 1024);
+    }
+    const Tile* t = pick_tile(q.M, q.N, q.K, q.fmt);
+    const int es = tg::dtype_size(q.dt);
+    p.g.group_m = tg::swizzle_override() > 0 ? tg::swizzle_override() : 4;
+    p.g.tiles_m = (int)ceil_div(q.M, t->bm);
+    p.g.tiles_n = (int)ceil_div(q.N, t->bn);
+    p.g.c_vec = ((uintptr_t)q.C & 15) == 0 && q.ldc * es % 16 == 0 && q.N * es % 16 == 0 &&
+                32 * q.ldc * es <= kMaxDim;
+    return tg::launch_kernel(t->kernel[q.dt], (int64_t)p.g.tiles_m * p.g.tiles_n, 1, t->threads, &p,
+                             stream, t->name);
+}
+
+tg_status launch_fill(int64_t M, int64_t N, int dt, const float* bias, void* C, int64_t ldc,
+                      bool relu, hipStream_t stream)
+{
+    if (M == 0 || N == 0)
+        return TG_OK;
+    tg::MxFillParams p{bias, C, ldc, (int)M, (int)N, dt, relu};
+    return tg::launch_kernel((const void*)&tg::mx_fill_kernel, ceil_div(M * N, 256), 1, 256, &p,
+                             stream, "mx_fill");
+}
+
+// --------------------------------------------------------------------------
+// The linear layer.
+// --------------------------------------------------------------------------
+// In one launch: a few tokens, whose quantisation in every workgroup takes less
+// than a launch of its own would.
+bool fused_linear(int64_t M, int64_t K) { return M <= 8 && K > 0 && M * K <= 16384; }
+
+size_t linear_bytes(int64_t M, int64_t N, int64_t K, int fmt)
+{
+    if (M == 0 || N == 0 || K == 0 || fused_linear(M, K))
+        return 0;
+    const int64_t Kp = mx_padded(K);
+    return (size_t)(ceil_div(M * (Kp / 32), 256) * 256 + M * code_bytes(fmt, Kp));
+}
+
+tg_status check_linear(int64_t M, int64_t N, int64_t K, int dtype, int fmt)
+{
+    if (!tg::dtype_ok(dtype) || !fmt_ok(fmt))
+        return TG_ERR_BAD_DTYPE;
+    if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxLen - 128)
+        return TG_ERR_BAD_SHAPE;
+    return TG_OK;
+}
+
+// How a backward call lays out its workspace, in bytes from its start; parts
+// that are not needed are empty.
+struct GradPlan {
+    int64_t Mp, Np;
+    bool dx, dw, db;
+    int64_t dy, dys, dyt, dyts, wt, wts, xt, xts, sums, bytes;
+};
+
+GradPlan grad_plan(const tg_linear_mx_grad_args& a)
+{
+    GradPlan g{};
+    g.Mp = mx_padded(a.M);
+    g.Np = mx_padded(a.N);
+    const bool any = a.M > 0 && a.N > 0;
+    g.dx = a.dX && any && a.K > 0;
+    g.dw = a.dW && any && a.K > 0;
+    g.db = a.dbias && any;
+    const auto take = [&](bool need, int64_t n) {
+        const int64_t at = g.bytes;
+        g.bytes += need ? ceil_div(n, 256) * 256 : 0;
+        return at;
+    };
+    g.dy = take(g.dx, a.M * code_bytes(a.fmt, g.Np));
+    g.dys = take(g.dx, a.M * (g.Np / 32));
+    g.dyt = take(g.dw, a.N * code_bytes(a.fmt, g.Mp));
+    g.dyts = take(g.dw, a.N * (g.Mp / 32));
+    g.wt = take(g.dx, a.K * (g.Np / 2));
+    g.wts = take(g.dx, a.K * (g.Np / 32));
+    g.xt = take(g.dw, a.K * (g.Mp / 2));
+    g.xts = take(g.dw, a.K * (g.Mp / 32));
+    g.sums = take(g.db, g.Mp / 128 * a.N * 4);
+    return g;
+}
+
+tg_status check_grad(const tg_linear_mx_grad_args* a)
+{
+    if (!a)
+        return TG_ERR_NULL_POINTER;
+    if (!tg::dtype_ok(a->dtype) || !tg::dtype_ok(a->wtype) || !fmt_ok(a->fmt) ||
+        (a->wtype != a->dtype && a->wtype != TG_F32))
+        return TG_ERR_BAD_DTYPE;
+    const int64_t most = kMaxLen - 128;
+    if (a->M < 0 || a->N < 0 || a->K < 0 || a->M > most || a->N > most || a->K > most)
+        return TG_ERR_BAD_SHAPE;
+    const auto bad = [](const void* p, int64_t ld, int64_t n) { return p && ld < n; };
+    if (bad(a->dY, a->lddy, a->N) || bad(a->X, a->ldx, a->K) || bad(a->W, a->ldw, a->K) ||
+        bad(a->dX, a->lddx, a->K) || bad(a->dW, a->lddw, a->K))
+        return TG_ERR_BAD_SHAPE;
+    return TG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+tg_status tg_quant_mx(int64_t M, int64_t K, tg_dtype dtype, const void* X, int64_t ldx,
+                      tg_mx_format fmt, uint8_t* Q, uint8_t* S, uint8_t* Qt, uint8_t* St,
+                      tg_stream_t stream)
+{
+    if (!tg::dtype_ok(dtype) || !fmt_ok(fmt))
+        return TG_ERR_BAD_DTYPE;
+    if (M < 0 || K < 0 || M > kMaxDim / 4 || K > kMaxDim / 4 || ldx < K)
+        return TG_ERR_BAD_SHAPE;
+    if (M == 0 || K == 0)
+        return TG_OK;
+    if (!X || (!Q && !Qt) || !Q != !S || !Qt != !St)
+        return TG_ERR_NULL_POINTER;
+    if (misaligned(Q, S) || misaligned(Qt, St))
+        return TG_ERR_NO_CONFIG;
+    const int64_t Kp = mx_padded(K), Mp = mx_padded(M);
+    const Span x = span(X, M, K, ldx, tg::dtype_size(dtype));
+    const Span out[] = {span1(Q, M * code_bytes(fmt, Kp), 1), span1(S, M * (Kp / 32), 1),
+                        span1(Qt, K * code_bytes(fmt, Mp), 1), span1(St, K * (Mp / 32), 1)};
+    for (int o = 0; o < 4; ++o) {
+        if (overlap(out[o], x))
+            return TG_ERR_ALIAS;
+        for (int i = 0; i < o; ++i)
+            if (overlap(out[o], out[i]))
+                return TG_ERR_ALIAS;
+    }
+    return launch_quant(M, K, dtype, X, ldx, fmt, Q, S, Qt, St, nullptr, (hipStream_t)stream);
+}
+
+tg_status tg_dequant_mx(int64_t M, int64_t K, tg_mx_format fmt, const uint8_t* Q, const uint8_t* S,
+                        tg_dtype dtype, void* X, int64_t ldx, tg_stream_t stream)
+{
+    if (!tg::dtype_ok(dtype) || !fmt_ok(fmt))
+        return TG_ERR_BAD_DTYPE;
+    if (M < 0 || K < 0 || M > kMaxDim / 4 || K > kMaxDim / 4 || ldx < K)
+        return TG_ERR_BAD_SHAPE;
+    if (M == 0 || K == 0)
+        return TG_OK;
+    if (!X || !Q || !S)
+        return TG_ERR_NULL_POINTER;
+    if (misaligned(Q, S))
+        return TG_ERR_NO_CONFIG;
+    const int64_t Kp = mx_padded(K);
+    const Span x = span(X, M, K, ldx, tg::dtype_size(dtype));
+    if (overlap(x, span1(Q, M * code_bytes(fmt, Kp), 1)) || overlap(x, span1(S, M * (Kp / 32), 1)))
+        return TG_ERR_ALIAS;
+    tg::MxDequantParams p{Q, S, X, ldx, (int)M, (int)K, (int)Kp, unit_magic(Kp)};
+    const void* k = by_type(dtype, fmt, [](auto D, auto F) {
+        return (const void*)&tg::mx_dequant_kernel<decltype(D)::value, decltype(F)::value, kUnits>;
+    });
+    return tg::launch_kernel(k, ceil_div(M * (Kp / 8), 256 * kUnits), 1, 256, &p,
+                             (hipStream_t)stream, "mx_dequant");
+}
+
+tg_status tg_linear_mx_workspace_size(int64_t M, int64_t N, int64_t K, tg_dtype dtype,
+                                      tg_mx_format fmt, size_t* bytes)
+{
+    if (!bytes)
+        return TG_ERR_NULL_POINTER;
+    if (tg_status s = check_linear(M, N, K, dtype, fmt))
+        return s;
+    *bytes = linear_bytes(M, N, K, fmt);
+    return TG_OK;
+}
+
+tg_status tg_linear_mx(int64_t M, int64_t N, int64_t K, tg_dtype dtype, const void* X, int64_t ldx,
+                       tg_mx_format fmt, const uint8_t* Wq, const uint8_t* Ws, const float* bias,
+                       void* C, int64_t ldc, tg_epilogue epi, void* workspace,
+                       size_t workspace_bytes, tg_stream_t stream)
+{
+    if (tg_status s = check_linear(M, N, K, dtype, fmt))
+        return s;
+    if (epi != TG_EPI_NONE && epi != TG_EPI_RELU)
+        return TG_ERR_BAD_EPILOGUE;
+    if (ldx < K || ldc < N)
+        return TG_ERR_BAD_SHAPE;
+    if (M == 0 || N == 0)
+        return TG_OK;
+    if (!C || (K > 0 && (!X || !Wq || !Ws)))
+        return TG_ERR_NULL_POINTER;
+    const int64_t Kp = mx_padded(K);
+    if (K > 0 && misaligned(Wq, Ws))
+        return TG_ERR_NO_CONFIG;
+    const size_t need = linear_bytes(M, N, K, fmt);
+    if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 15)))
+        return TG_ERR_WORKSPACE;
+    const int es = tg::dtype_size(dtype);
+    const Span in[] = {span(X, M, K, ldx, es), span1(Wq, N * (Kp / 2), 1),
+                       span1(Ws, N * (Kp / 32), 1), span1(bias, N, 4)};
+    const Span c = span(C, M, N, ldc, es), ws = span1(workspace, (int64_t)need, 1);
+    for (const Span& i : in)
+        if (overlap(c, i) || overlap(ws, i))
+            return TG_ERR_ALIAS;
+    if (overlap(c, ws))
+        return TG_ERR_ALIAS;
+    const hipStream_t hs = (hipStream_t)stream;
+    const bool relu = epi == TG_EPI_RELU;
+    if (K == 0)
+        return launch_fill(M, N, dtype, bias, C, ldc, relu, hs);
+    Product q{M, N, Kp, fmt, dtype, nullptr, nullptr, Wq, Ws, bias, C, ldc, relu};
+    if (fused_linear(M, K)) {
+        tg::MxStreamParams s{product_params(q), (int)dtype, X, ldx, (int)K};
+        const void* k = dtype == TG_F32   ? stream_kernel<tg::DT_F32, true>(fmt, 1)
+                        : dtype == TG_F16 ? stream_kernel<tg::DT_F16, true>(fmt, 1)
+                                          : stream_kernel<tg::DT_BF16, true>(fmt, 1);
+        const int lds =
+            fmt == TG_MX_E4M3
+                ? tg::MxStream<tg::DT_F32, tg::MX_E4M3, 1, 8, true>::lds_bytes((int)M, (int)Kp)
+                : tg::MxStream<tg::DT_F32, tg::MX_E2M1, 1, 8, true>::lds_bytes((int)M, (int)Kp);
+        return tg::launch_kernel(k, ceil_div(N, 16), 1, 512, &s, hs, "mx_linear_stream",
+                                 (unsigned)lds);
+    }
+    uint8_t* As = (uint8_t*)workspace;
+    uint8_t* A = As + ceil_div(M * (Kp / 32), 256) * 256;
+    if (tg_status s = launch_quant(M, K, dtype, X, ldx, fmt, A, As, nullptr, nullptr, nullptr, hs))
+        return s;
+    q.A = A;
+    q.As = As;
+    return launch_product(q, hs);
+}
+
+tg_status tg_linear_mx_backward_workspace_size(const tg_linear_mx_grad_args* a, size_t* bytes)
+{
+    if (!bytes)
+        return TG_ERR_NULL_POINTER;
+    if (tg_status s = check_grad(a))
+        return s;
+    *bytes = (size_t)grad_plan(*a).bytes;
+    return TG_OK;
+}
+
+tg_status tg_linear_mx_backward(const tg_linear_mx_grad_args* a, void* workspace,
+                                size_t workspace_bytes, tg_stream_t stream)
+{
+    if (tg_status s = check_grad(a))
+        return s;
+    const int64_t M = a->M, N = a->N, K = a->K;
+    const bool out = (a->dX && M > 0 && K > 0) || (a->dW && N > 0 && K > 0) || (a->dbias && N > 0);
+    if (!a->dX && !a->dW && !a->dbias && N > 0 && (M > 0 || K > 0))
+        return TG_ERR_NULL_POINTER;
+    if (!out)
+        return TG_OK;
+    const GradPlan g = grad_plan(*a);
+    if (((g.dx || g.dw || g.db) && !a->dY) || (g.dx && !a->W) || (g.dw && !a->X))
+        return TG_ERR_NULL_POINTER;
+    if (g.bytes > 0 &&
+        (!workspace || workspace_bytes < (size_t)g.bytes || ((uintptr_t)workspace & 15)))
+        return TG_ERR_WORKSPACE;
+    const int es = tg::dtype_size(a->dtype), wes = tg::dtype_size(a->wtype);
+    const Span in[] = {span(a->dY, M, N, a->lddy, es), span(a->X, M, K, a->ldx, es),
+                       span(a->W, N, K, a->ldw, wes)};
+    const Span outs[] = {span(a->dX, M, K, a->lddx, es), span(a->dW, N, K, a->lddw, wes),
+                         span1(a->dbias, N, 4), span1(workspace, g.bytes, 1)};
+    for (int o = 0; o < 4; ++o) {
+        for (const Span& i : in)
+            if (overlap(outs[o], i))
+                return TG_ERR_ALIAS;
+        for (int i = 0; i < o; ++i)
+            if (overlap(outs[o], outs[i]))
+                return TG_ERR_ALIAS;
+    }
+    const hipStream_t hs = (hipStream_t)stream;
+    uint8_t* ws = (uint8_t*)workspace;
+    if (g.dx || g.dw || g.db) {
+        if (tg_status s = launch_quant(M, N, a->dtype, a->dY, a->lddy, a->fmt,
+                                       g.dx ? ws + g.dy : nullptr, g.dx ? ws + g.dys : nullptr,
+                                       g.dw ? ws + g.dyt : nullptr, g.dw ? ws + g.dyts : nullptr,
+                                       g.db ? (float*)(ws + g.sums) : nullptr, hs))
+            return s;
+    }
+    if (g.dx) {
+        if (tg_status s = launch_quant(N, K, a->wtype, a->W, a->ldw, TG_MX_E2M1, nullptr, nullptr,
+                                       ws + g.wt, ws + g.wts, nullptr, hs))
+            return s;
+        const Product q{M,          K,          g.Np,        a->fmt,  a->dtype, ws + g.dy,
+                        ws + g.dys, ws + g.wt,  ws + g.wts,  nullptr, a->dX,    a->lddx,
+                        false};
+        if (tg_status s = launch_product(q, hs))
+            return s;
+    } else if (a->dX) {
+        if (tg_status s = launch_fill(M, K, a->dtype, nullptr, a->dX, a->lddx, false, hs))
+            return s;
+    }
+    if (g.dw) {
+        if (tg_status s = launch_quant(M, K, a->dtype, a->X, a->ldx, TG_MX_E2M1, nullptr, nullptr,
+                                       ws + g.xt, ws + g.xts, nullptr, hs))
+            return s;
+        const Product q{N,           K,          g.Mp,        a->fmt,  a->wtype, ws + g.dyt,
+                        ws + g.dyts, ws + g.xt,  ws + g.xts,  nullptr, a->dW,    a->lddw,
+                        false};
+        if (tg_status s = launch_product(q, hs))
+            return s;
+    } else if (a->dW) {
+        if (tg_status s = launch_fill(N, K, a->wtype, nullptr, a->dW, a->lddw, false, hs))
+            return s;
+    }
+    if (g.db) {
+        tg::MxSumParams p{(const float*)(ws + g.sums), a->dbias, (int)(g.Mp / 128), (int)N};
+        return tg::launch_kernel((const void*)&tg::mx_sums_kernel, ceil_div(N, 256), 1, 256, &p, hs,
+                                 "mx_sums");
+    }
+    return a->dbias ? launch_fill(1, N, TG_F32, nullptr, a->dbias, N, false, hs) : TG_OK;
+}
+
+}  // extern "C"
