@@ -195,10 +195,10 @@ GradPlan grad_plan(const tg_head_norm_rope_grad_args& a)
     GradPlan g{};
     g.k = pick(a.dtype, a.D, a.R, a.interleaved != 0, true);
     const int64_t uq = a.T * ceil_div(a.Hq, g.k.per_wave), uk = a.T * ceil_div(a.Hk, g.k.per_wave);
-    g.per = ceil_div(uq + uk, 4 * 1024);
+    g.per = ceil_div(uq + uk, 4096);  // four waves to a SIMD
     g.per = g.per < 1 ? 1 : g.per;
-    g.blocks[0] = ceil_div(uq, 4 * g.per);
-    g.blocks[1] = ceil_div(uk, 4 * g.per);
+    g.blocks[0] = ceil_div(uq, tg::kHeadsGradWaves * g.per);
+    g.blocks[1] = ceil_div(uk, tg::kHeadsGradWaves * g.per);
     g.bytes = (size_t)((a.dw_q ? g.blocks[0] : 0) + (a.dw_k ? g.blocks[1] : 0)) * a.D * 4;
     return g;
 }
@@ -336,13 +336,13 @@ tg_status tg_head_norm_rope_backward(const tg_head_norm_rope_grad_args* a, void*
         side(0, a->dq_out, a->dq_out_t, a->dq_out_h, a->dq, a->dq_t, a->dq_h, a->dw_q);
         side(1, a->dk_out, a->dk_out_t, a->dk_out_h, a->dk, a->dk_t, a->dk_h, a->dw_k);
         p.per = (int)g.per;
-        if (tg_status s = tg::launch_kernel(g.k.kernel, g.blocks[0] + g.blocks[1], 1, 256, &p, hs,
-                                            "heads_grad"))
+        if (tg_status s = tg::launch_kernel(g.k.kernel, g.blocks[0] + g.blocks[1], 1,
+                                            64 * tg::kHeadsGradWaves, &p, hs, "heads_grad"))
             return s;
     }
     if (!a->dw_q && !a->dw_k)
         return TG_OK;
-    return tg::launch_kernel((const void*)&tg::heads_sums_kernel, ceil_div(a->D, 32), 2, 256, &sums,
+    return tg::launch_kernel((const void*)&tg::heads_sums_kernel, ceil_div(a->D, 8), 2, 256, &sums,
                              hs, "heads_sums");
 }
 

@@ -319,13 +319,17 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void heads_ker
 // Backward.  A workgroup takes the units of one side; its waves' sums of dw are
 // added over the wave's heads, then over the waves, and written to its row of
 // partial sums, which heads_sums_kernel adds in order.
+constexpr int kHeadsGradWaves = 8;
+
 template <int DT, int V, int G, int NC, bool INTER>
-__global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void
+__global__ __attribute__((amdgpu_flat_work_group_size(64 * kHeadsGradWaves,
+                                                      64 * kHeadsGradWaves))) void
 heads_grad_kernel(HeadsParams p)
 {
+    constexpr int NW = kHeadsGradWaves;
     using Lane = HeadLane<DT, V, G, NC, INTER>;
     constexpr int NG = 64 / G;
-    __shared__ float red[4][NC * 2 * V * G];
+    __shared__ float red[NW][NC * 2 * V * G];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int sd = (int)blockIdx.x >= p.s[0].blocks;
@@ -333,7 +337,7 @@ heads_grad_kernel(HeadsParams p)
     const int block = (int)blockIdx.x - (sd ? p.s[0].blocks : 0);
     const Lane L(p, lane % G);
     const int64_t total = (int64_t)p.T * s.units;
-    const int64_t u0 = ((int64_t)block * 4 + w) * p.per;
+    const int64_t u0 = ((int64_t)block * NW + w) * p.per;
     const int64_t left = total - u0;
     const int n = left <= 0 ? 0 : (left < p.per ? (int)left : p.per);
     int token = (int)(u0 / s.units), at = (int)(u0 - (int64_t)token * s.units);
@@ -412,17 +416,28 @@ heads_grad_kernel(HeadsParams p)
                 red[w][(c * 2 * V + e) * G + lane] = acc[c][e];
         }
     __syncthreads();
-    if (threadIdx.x >= G)
-        return;
+    // value o of the head is in the lane and register that hold it; each thread
+    // adds one, over the waves
+    for (int i = threadIdx.x; i < NC * 2 * V * G; i += 64 * NW) {
+        const int j = i % G, r = i / G;
+        const Lane l(p, j);
+        int o = p.D;
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int e = 0; e < 2 * V; ++e) {
-            const int o = e < V ? L.oa[c] + e : L.ob[c] + e - V;
-            const int k = (c * 2 * V + e) * G + lane;
-            if ((e < V ? L.oa[c] : L.ob[c]) < p.D)
-                s.part[(int64_t)block * p.D + o] = red[0][k] + red[1][k] + red[2][k] + red[3][k];
+            for (int e = 0; e < 2 * V; ++e)
+                if (r == c * 2 * V + e) {
+                    const int base = e < V ? l.oa[c] : l.ob[c];
+                    o = base < p.D ? base + e % V : p.D;
+                }
+        if (o < p.D) {
+            float s8 = red[0][i];
+#pragma unroll
+            for (int v = 1; v < NW; ++v)
+                s8 += red[v][i];
+            s.part[(int64_t)block * p.D + o] = s8;
         }
+    }
 }
 
 struct HeadSums {
@@ -432,25 +447,33 @@ struct HeadSums {
     int D;
 };
 
-// dw of one side (blockIdx.y), 32 values to a workgroup: eight rows of partial
-// sums at a time, then the eight sums, in order.
+// dw of one side (blockIdx.y), 8 values to a workgroup: 32 rows of partial sums at
+// a time, four of them in flight, then the 32 sums, in order.
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void
 heads_sums_kernel(HeadSums p)
 {
-    __shared__ float red[8][32];
+    __shared__ float red[32][8];
     const int side = (int)blockIdx.y;
-    const int c = threadIdx.x & 31, t = threadIdx.x >> 5;
-    const int k = (int)blockIdx.x * 32 + c;
-    const float* part = p.part[side];
+    const int c = threadIdx.x & 7, t = threadIdx.x >> 3;
+    const int k = (int)blockIdx.x * 8 + c;
+    const bool there = p.out[side] && k < p.D;
+    const int n = there ? p.blocks[side] : 0;
+    const float* part = p.part[side] + k;
     float s = 0.0f;
-    if (p.out[side] && k < p.D)
-        for (int b = t; b < p.blocks[side]; b += 8)
-            s += part[(int64_t)b * p.D + k];
+    for (int b0 = t; b0 < n; b0 += 128) {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = b0 + 32 * i < n ? part[(int64_t)(b0 + 32 * i) * p.D] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s += v[i];
+    }
     red[t][c] = s;
     __syncthreads();
-    if (t == 0 && p.out[side] && k < p.D) {
+    if (t == 0 && there) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i)
+        for (int i = 1; i < 32; ++i)
             s += red[i][c];
         p.out[side][k] = s;
     }

@@ -321,24 +321,15 @@ struct MxStream {
             for (int u = threadIdx.x; u < per; u += NW * 64) {  // whole quads: per % 16 == 0
                 Raw8<DTX> r;
                 load8<DTX>(r, src, 8 * u, p.Kx - 8 * u);
-                u32 t = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    t = MaxOp::of(t, __builtin_bit_cast(u32, get8<DTX>(r, i)) & 0x7FFFFFFFu);
-                MxScale s;
-                s.of_amax<AFMT>(mx_block_max<4>(t));
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] = s.ok ? get8<DTX>(r, i) : 0.0f;
+                u32 byte;
+                const u32x2 w = mx_codes<DTX, AFMT>(r, byte);
                 uint8_t* to = codes + m * row_b + mx_bytes<AFMT>(8 * u);
                 if constexpr (A8)
-                    *(u32x2*)to = u32x2{mx_codes8(v[0], v[1], v[2], v[3], s.p),
-                                        mx_codes8(v[4], v[5], v[6], v[7], s.p)};
+                    *(u32x2*)to = w;
                 else
-                    *(u32*)to = mx_codes4(v, s.p);
+                    *(u32*)to = w[0];
                 if ((u & 3) == 0)
-                    scales[m * (Kp / 32) + u / 4] = (uint8_t)s.byte;
+                    scales[m * (Kp / 32) + u / 4] = (uint8_t)byte;
             }
         }
     }

@@ -4,16 +4,17 @@
 // a block.
 //
 // mx_columns_kernel: blocks along the columns, written as rows of the transpose,
-// and on request those along the rows from the same read.  A lane holds a block
-// of 32 rows by the columns of one 16-byte load (8 of 16 bits, 4 of 32) in
-// registers, so that no value crosses lanes: its codes of a column are 16 or 32
-// consecutive bytes of the transpose, and its columns of a row a part of that
-// row's block, whose largest magnitude is found over 4 or 8 lanes.  A wave takes
-// 128 rows (four lanes down) by 16 lanes across; the four waves of a workgroup
-// two by two, so that its writes are whole cache lines.
+// and on request those along the rows from the same read.  A lane holds 32 rows of
+// four columns in registers, so that no value crosses lanes: its codes of a column
+// are 16 or 32 consecutive bytes of the transpose, and its part of a row an eighth
+// of that row's block, whose largest magnitude is found over 8 lanes.  A wave takes
+// 128 rows (four lanes down) by 64 columns (16 lanes across); the four waves of a
+// workgroup two by two, and neighbouring workgroups stay on one XCD, whose L2 joins
+// their parts of cache lines.
 #pragma once
 
 #include "tg_mx.h"
+#include "tg_sched.h"
 
 namespace tg {
 
@@ -25,6 +26,7 @@ struct MxQuantParams {
     uint8_t *Q, *S;    // along the rows
     uint8_t *Qt, *St;  // along the columns
     float* sums;       // [Mp / 128][K]: the columns' sums over each 128 rows
+    int tiles_m, tiles_n;  // workgroups down and across (columns kernel)
     u32 magic;         // ceil(2^32 / (Kp / 8)), for the row of a unit
 };
 
@@ -54,48 +56,62 @@ mx_rows_kernel(MxQuantParams p)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const uint64_t at = first + threadIdx.x + 256 * u;
-        u32 m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            m = MaxOp::of(m, __builtin_bit_cast(u32, get8<DT>(r[u], i)) & 0x7FFFFFFFu);
-        MxScale s;
-        s.of_amax<FMT>(mx_block_max<4>(m));
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = s.ok ? get8<DT>(r[u], i) : 0.0f;
+        u32 byte;
+        const u32x2 w = mx_codes<DT, FMT>(r[u], byte);
         if (at >= total)
             continue;
         if constexpr (FMT == MX_E2M1)
-            ((u32*)p.Q)[at] = mx_codes4(v, s.p);
+            ((u32*)p.Q)[at] = w[0];
         else
-            ((u32x2*)p.Q)[at] = u32x2{mx_codes8(v[0], v[1], v[2], v[3], s.p),
-                                      mx_codes8(v[4], v[5], v[6], v[7], s.p)};
+            ((u32x2*)p.Q)[at] = w;
         if ((threadIdx.x & 3) == 0)
-            p.S[at / 4] = (uint8_t)s.byte;
+            p.S[at / 4] = (uint8_t)byte;
     }
 }
 
-// The columns of one 16-byte load.
+// Four consecutive elements of a row.
 template <int DT>
 struct MxLane {
-    static constexpr int V = DT == DT_F32 ? 4 : 8;
-    u32x4 v;
+    static constexpr int NW = DT == DT_F32 ? 4 : 2;  // words
+    static constexpr int ES = DT == DT_F32 ? 4 : 2;
+    u32 v[NW];
 
-    // left: columns that exist from `p` on
-    __device__ __forceinline__ void load(const char* p, int left)
+    __device__ __forceinline__ void load(const char* p)
     {
-        constexpr int ES = DT == DT_F32 ? 4 : 2;
+        typedef __attribute__((ext_vector_type(NW))) u32 Vec;
         struct __attribute__((packed, aligned(ES))) Any {
-            u32x4 v;
+            Vec v;
         };
-        if (left >= V) {
-            v = ((const Any*)p)->v;
-            return;
-        }
-        v = u32x4{0, 0, 0, 0};
+        const Vec w = ((const Any*)p)->v;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < NW; ++i)
+            v[i] = w[i];
+    }
+    // Drops the first s elements (0 to 4), zeros from above.
+    __device__ __forceinline__ void drop(int s)
+    {
+        if constexpr (DT == DT_F32) {
+            const bool one = s & 1, two = s & 2;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = one ? (i < 3 ? v[i < 3 ? i + 1 : 3] : 0u) : v[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = s >= 4 ? 0u : (two ? (i < 2 ? v[i < 2 ? i + 2 : 3] : 0u) : v[i]);
+        } else {
+            const uint64_t w = s >= 4 ? 0 : ((uint64_t)v[1] << 32 | v[0]) >> (16 * (s & 3));
+            v[0] = (u32)w;
+            v[1] = (u32)(w >> 32);
+        }
+    }
+    // Of a row of fewer than four elements.
+    __device__ __forceinline__ void load_few(const char* p, int left)
+    {
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+            v[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
             if (i < left) {
                 if constexpr (DT == DT_F32)
                     v[i] = ((const u32*)p)[i];
@@ -105,10 +121,8 @@ struct MxLane {
     }
     __device__ __forceinline__ float get(int i) const
     {
-        if constexpr (DT == DT_F32) {
-            const u32 w = v[i];
-            return __builtin_bit_cast(float, w);
-        }
+        if constexpr (DT == DT_F32)
+            return __builtin_bit_cast(float, v[i]);
         const u32 w = v[i >> 1];
         if constexpr (DT == DT_BF16)
             return __builtin_bit_cast(float, (i & 1) ? (w & 0xFFFF0000u) : (w << 16));
@@ -116,25 +130,42 @@ struct MxLane {
     }
 };
 
-// Magnitudes as stored, two of 16 bits to a word: their order is that of their
-// bit patterns, NaN above infinity.
+// Keeps the compiler from holding the rows' unpacked values across this point.
 template <int DT>
-__device__ __forceinline__ u32 mx_max_word(u32 m, u32 w)
+__device__ __forceinline__ void mx_repack(MxLane<DT> (&x)[32])
 {
-    if constexpr (DT == DT_F32)
-        return MaxOp::of(m, w & 0x7FFFFFFFu);
-    typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
-    return __builtin_bit_cast(u32, __builtin_elementwise_max(
-                                       __builtin_bit_cast(u16x2, m),
-                                       __builtin_bit_cast(u16x2, w & 0x7FFF7FFFu)));
+    if constexpr (DT != DT_F32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            asm volatile("" : "+v"(x[i].v[0]), "+v"(x[i].v[1]));
+    }
+    __builtin_amdgcn_sched_barrier(0);
 }
-// The fp32 bit pattern of magnitude i of such words.
-template <int DT>
-__device__ __forceinline__ u32 mx_bits(const u32x4& m, int i)
+
+// Codes of element j of eight rows x[0 .. 7], to a dword (E2M1) or two.
+template <int DT, int FMT>
+__device__ __forceinline__ u32x2 mx_column_codes(const MxLane<DT>* x, int j, const MxScale& s)
 {
-    MxLane<DT> l;
-    l.v = m;
-    return __builtin_bit_cast(u32, l.get(i));
+    u32x2 w;
+    if constexpr (FMT == MX_E2M1 && DT != DT_F32) {
+        // pairs of rows as the instruction takes them
+        const u32 sel = (j & 1) ? 0x07060302u : 0x05040100u;
+        const auto pair = [&](int i) {
+            return __builtin_amdgcn_perm(x[i + 1].v[j >> 1], x[i].v[j >> 1], sel);
+        };
+        w = u32x2{mx_codes4_16<DT>(pair(0), pair(2), pair(4), pair(6), s.p), 0u};
+    } else {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = x[e].get(j);
+        if constexpr (FMT == MX_E2M1)
+            w = u32x2{mx_codes4(v, s.p), 0u};
+        else
+            w = u32x2{mx_codes8(v[0], v[1], v[2], v[3], s.p),
+                      mx_codes8(v[4], v[5], v[6], v[7], s.p)};
+    }
+    return s.ok ? w : u32x2{0u, 0u};
 }
 
 template <int DT, int FMT, bool ROWS, bool COLS, bool SUMS>
@@ -142,15 +173,13 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void
 mx_columns_kernel(MxQuantParams p)
 {
     using Lane = MxLane<DT>;
-    constexpr int V = Lane::V, CL = 16, TC = CL * V;  // a wave's columns
-    constexpr int ES = DT == DT_F32 ? 4 : 2;
+    constexpr int V = 4, CL = 16, TC = CL * V;  // a wave's columns
+    constexpr int ES = Lane::ES;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int tiles = (p.K + 2 * TC - 1) / (2 * TC);  // workgroups across
-    const int wg = (int)blockIdx.x;
-    const int mt = wg / tiles;
-    const int m0 = mt * 256 + (w >> 1) * 128;
-    const int c0 = (wg - mt * tiles) * 2 * TC + (w & 1) * TC;
+    const TileCoord tc = tile_of((int)blockIdx.x, p.tiles_m, p.tiles_n, 1);
+    const int m0 = tc.m * 256 + (w >> 1) * 128;
+    const int c0 = tc.n * 2 * TC + (w & 1) * TC;
     if (m0 >= p.Mp || c0 >= p.Kp)
         return;  // whole waves, and no barrier follows
     const int cl = lane & (CL - 1), b = lane / CL;
@@ -160,12 +189,23 @@ mx_columns_kernel(MxQuantParams p)
         const char* at = (const char*)p.X + ((int64_t)m * p.ldx + c) * ES;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            x[i].load(at + (int64_t)i * p.ldx * ES, V);
+            x[i].load(at + (int64_t)i * p.ldx * ES);
+    } else if (p.K >= V) {
+        // across an edge: the row's last four elements shifted down, the last
+        // row again for rows that are not there
+        const int over = c - (p.K - V);
+        const char* at = (const char*)p.X + (int64_t)(over > 0 ? p.K - V : c) * ES;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            x[i].load(at + (int64_t)(m + i < p.M ? m + i : p.M - 1) * p.ldx * ES);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            x[i].drop(m + i < p.M ? (over < 0 ? 0 : (over < V ? over : V)) : V);
     } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            x[i].load((const char*)p.X + ((int64_t)(m + i) * p.ldx + c) * ES,
-                      m + i < p.M ? p.K - c : 0);
+            x[i].load_few((const char*)p.X + (int64_t)(m + i) * p.ldx * ES,
+                          m + i < p.M && c == 0 ? p.K : 0);
     }
     if constexpr (SUMS) {
         float s[V];
@@ -185,74 +225,95 @@ mx_columns_kernel(MxQuantParams p)
                 if (c + j < p.K)
                     to[j] = s[j];
         }
+        mx_repack(x);
     }
     if constexpr (COLS) {
-        u32x4 top = {0, 0, 0, 0};
+        u32 top[Lane::NW];
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int j = 0; j < Lane::NW; ++j) {
+            top[j] = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int i = 0; i < 32; ++i)
                 top[j] = mx_max_word<DT>(top[j], x[i].v[j]);
+        }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             MxScale s;
-            s.of_amax<FMT>(mx_bits<DT>(top, j));
-            const int64_t at = (int64_t)(c + j) * p.Mp + m;
+            s.of_amax<FMT>(mx_bits<DT>(top[DT == DT_F32 ? j : j >> 1], j & 1));
             u32x4 q[FMT == MX_E2M1 ? 1 : 2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = s.ok ? x[8 * i + e].get(j) : 0.0f;
+                const u32x2 k = mx_column_codes<DT, FMT>(x + 8 * i, j, s);
                 if constexpr (FMT == MX_E2M1) {
-                    q[0][i] = mx_codes4(v, s.p);
+                    q[0][i] = k[0];
                 } else {
-                    q[i >> 1][(i & 1) * 2] = mx_codes8(v[0], v[1], v[2], v[3], s.p);
-                    q[i >> 1][(i & 1) * 2 + 1] = mx_codes8(v[4], v[5], v[6], v[7], s.p);
+                    q[i >> 1][(i & 1) * 2] = k[0];
+                    q[i >> 1][(i & 1) * 2 + 1] = k[1];
                 }
             }
             if (c + j < p.K) {
+                const int64_t at = (int64_t)(c + j) * p.Mp + m;
                 u32x4* to = (u32x4*)(p.Qt + mx_bytes<FMT>(at));
                 to[0] = q[0];
                 if constexpr (FMT == MX_E4M3)
                     to[1] = q[1];
                 p.St[at / 32] = (uint8_t)s.byte;
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
+        mx_repack(x);
     }
     if constexpr (ROWS) {
-        const int rows = p.M - m;
+        // Eight lanes hold a row's block.  Of E2M1 a lane's codes of two rows are
+        // half dwords: neighbours exchange them, so that each stores a whole one of
+        // one row.  Of eight rows' scales each of the eight lanes stores one.
+        const int odd = lane & 1, l8 = lane & 7;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            u32 t = 0;
+        for (int i0 = 0; i0 < 32; i0 += 8) {
+            u32 byte = 0;
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                t = MaxOp::of(t, __builtin_bit_cast(u32, x[i].get(j)) & 0x7FFFFFFFu);
-            MxScale s;
-            s.of_amax<FMT>(mx_block_max<32 / V>(t));
-            float v[8];
+            for (int i = i0; i < i0 + 8; i += 2) {
+                u32 code[2];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = s.ok && j < V ? x[i].get(j < V ? j : 0) : 0.0f;
-            if (i >= rows)
-                continue;
-            const int64_t at = (int64_t)(m + i) * p.Kp + c;
-            uint8_t* to = p.Q + mx_bytes<FMT>(at);
-            if constexpr (FMT == MX_E2M1) {
-                if constexpr (V == 8)
-                    *(u32*)to = mx_codes4(v, s.p);
-                else
-                    *(uint16_t*)to = (uint16_t)mx_codes4(v, s.p);
-            } else {
-                if constexpr (V == 8)
-                    *(u32x2*)to = u32x2{mx_codes8(v[0], v[1], v[2], v[3], s.p),
-                                        mx_codes8(v[4], v[5], v[6], v[7], s.p)};
-                else
-                    *(u32*)to = mx_codes8(v[0], v[1], v[2], v[3], s.p);
+                for (int h = 0; h < 2; ++h) {
+                    const Lane& r = x[i + h];
+                    u32 t = 0;
+#pragma unroll
+                    for (int j = 0; j < Lane::NW; ++j)
+                        t = mx_max_word<DT>(t, r.v[j]);
+                    if constexpr (DT != DT_F32)
+                        t = MaxOp::of(mx_bits<DT>(t, false), mx_bits<DT>(t, true));
+                    MxScale s;
+                    s.of_amax<FMT>(mx_block_max<8>(t));
+                    byte = i + h - i0 == l8 ? s.byte : byte;
+                    if constexpr (FMT == MX_E4M3) {
+                        code[h] = mx_codes8(r.get(0), r.get(1), r.get(2), r.get(3), s.p);
+                    } else if constexpr (DT == DT_F32) {
+                        const float v[8] = {r.get(0), r.get(1), r.get(2), r.get(3), 0, 0, 0, 0};
+                        code[h] = mx_codes4(v, s.p) & 0xFFFFu;
+                    } else {
+                        code[h] = mx_codes4_16<DT>(r.v[0], r.v[1], 0u, 0u, s.p) & 0xFFFFu;
+                    }
+                    code[h] = s.ok ? code[h] : 0u;
+                }
+                if constexpr (FMT == MX_E4M3) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (m + i + h < p.M)
+                            *(u32*)(p.Q + (int64_t)(m + i + h) * p.Kp + c) = code[h];
+                } else {
+                    const u32 give = odd ? code[0] : code[1], keep = odd ? code[1] : code[0];
+                    const u32 got = dpp<0xB1>(give);
+                    const u32 word = odd ? got | keep << 16 : keep | got << 16;
+                    const int row = m + i + odd;
+                    if (row < p.M)
+                        *(u32*)(p.Q + ((int64_t)row * p.Kp + (c & ~7)) / 2) = word;
+                }
             }
-            if ((cl & (32 / V - 1)) == 0)
-                p.S[at / 32] = (uint8_t)s.byte;
+            const int row = m + i0 + l8;
+            if (row < p.M)
+                p.S[((int64_t)row * p.Kp + c) / 32] = (uint8_t)byte;
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
@@ -264,15 +325,26 @@ struct MxSumParams {
     int parts, K;
 };
 
-__global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void
+__global__ __attribute__((amdgpu_flat_work_group_size(64, 64))) void
 mx_sums_kernel(MxSumParams p)
 {
-    const int k = (int)(blockIdx.x * 256 + threadIdx.x);
+    const int k = (int)(blockIdx.x * 64 + threadIdx.x);
     if (k >= p.K)
         return;
     float s = 0.0f;
-    for (int i = 0; i < p.parts; ++i)
-        s += p.part[(int64_t)i * p.K + k];
+    const float* at = p.part + k;
+    int i = 0;
+    for (; i + 8 <= p.parts; i += 8) {  // eight loads in flight, added in order
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = at[(int64_t)(i + j) * p.K];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            s += v[j];
+    }
+    for (; i < p.parts; ++i)
+        s += at[(int64_t)i * p.K];
     p.out[k] = s;
 }
 

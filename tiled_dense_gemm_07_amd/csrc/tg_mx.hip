@@ -97,10 +97,10 @@ tg_status launch_quant(int64_t M, int64_t K, int dt, const void* X, int64_t ldx,
         return tg::launch_kernel(k, ceil_div(M * (p.Kp / 8), 256 * kUnits), 1, 256, &p, stream,
                                  "mx_rows");
     }
-    const int64_t across = dt == TG_F32 ? 128 : 256;  // columns of a workgroup
+    p.tiles_m = (int)ceil_div(p.Mp, 256);
+    p.tiles_n = (int)ceil_div(K, 128);
     return tg::launch_kernel(columns_kernel(dt, fmt, Q != nullptr, Qt != nullptr, sums != nullptr),
-                             ceil_div(p.Mp, 256) * ceil_div(K, across), 1, 256, &p, stream,
-                             "mx_columns");
+                             (int64_t)p.tiles_m * p.tiles_n, 1, 256, &p, stream, "mx_columns");
 }
 
 // --------------------------------------------------------------------------
@@ -507,7 +507,7 @@ tg_status tg_linear_mx_backward(const tg_linear_mx_grad_args* a, void* workspace
     }
     if (g.db) {
         tg::MxSumParams p{(const float*)(ws + g.sums), a->dbias, (int)(g.Mp / 128), (int)N};
-        return tg::launch_kernel((const void*)&tg::mx_sums_kernel, ceil_div(N, 256), 1, 256, &p, hs,
+        return tg::launch_kernel((const void*)&tg::mx_sums_kernel, ceil_div(N, 64), 1, 64, &p, hs,
                                  "mx_sums");
     }
     return a->dbias ? launch_fill(1, N, TG_F32, nullptr, a->dbias, N, false, hs) : TG_OK;
