@@ -8,14 +8,15 @@
 //
 // Bound by memory: every value is read and written once.  A group of G lanes
 // holds a head; lane j has pairs j V .. j V + V - 1 (and, where a head has more,
-// those G V further): the V values of 16 bytes that are their first members and
-// the V that are their second, so that a turn crosses no lanes (members half
-// of R apart; neighbours are 2 V consecutive values).  Values past R form such
-// pairs, too, half of what is left apart, and are not turned.  Where sizes do
-// not divide so, V is 1.
-// A unit is one token and 64 / G heads of one kind, to a wave; a wave takes
-// consecutive units, so that a token's cosines and sines are loaded once and its
-// position is uniform.
+// those G V further): the V values that are their first members and the V that are
+// their second, so that a turn crosses no lanes (members half of R apart;
+// neighbours are 2 V consecutive values).  Values past R form such pairs, too, half
+// of what is left apart, and are not turned.  Where sizes do not divide so, V is 1.
+// A unit is one token and 64 / G heads of one kind, to a wave, so that a token's
+// position is uniform and what addresses it scalar.
+// Measured (bf16, 8192 tokens of 32 + 8 heads of 128, slices of one buffer): forward
+// 30 us (5.6 TB/s, what a large copy reaches), backward 45 us and 4.6 for the sums of
+// dw (5.6 TB/s); one token 2.5 us, which is launch and latency.
 #pragma once
 
 #include "tg_rows.h"
@@ -41,49 +42,54 @@ struct HeadsParams {
     int T, D, R, P;
     int interleaved;
     int per;  // units of a wave
-    float eps;
+    float eps, inv_d;  // inv_d: 1 / D
 };
 
-// V values as stored, 16 bytes or one value.
+// V values as stored (one, or whole words).
 template <int DT, int V>
 struct HeadRaw {
     static constexpr int ES = DT == DT_F32 ? 4 : 2;
     static constexpr bool WIDE = V > 1;
-    u32x4 v;  // WIDE, else v[0]
+    static constexpr int NW = WIDE ? V * ES / 4 : 1;
+    typedef __attribute__((ext_vector_type(NW))) u32 Words;
+    struct __attribute__((packed, aligned(ES))) Any {
+        Words v;
+    };
+    u32 v[NW];
 
-    __device__ __forceinline__ void load(const char* p, bool there)
+    __device__ __forceinline__ void load(const char* p)
     {
-        struct __attribute__((packed, aligned(ES))) Any {
-            u32x4 v;
-        };
-        v = u32x4{0, 0, 0, 0};
-        if (!there)
-            return;
-        if constexpr (WIDE)
-            v = ((const Any*)p)->v;
-        else if constexpr (DT == DT_F32)
-            v[0] = *(const u32*)p;
+        Words w;
+        if constexpr (WIDE || DT == DT_F32)
+            w = ((const Any*)p)->v;
         else
-            v[0] = *(const uint16_t*)p;
+            w = (Words)(u32) * (const uint16_t*)p;
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+            v[i] = w[i];
+    }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+            v[i] = 0;
     }
     __device__ __forceinline__ void store(char* p) const
     {
-        struct __attribute__((packed, aligned(ES))) Any {
-            u32x4 v;
-        };
-        if constexpr (WIDE)
-            ((Any*)p)->v = v;
-        else if constexpr (DT == DT_F32)
-            *(u32*)p = v[0];
-        else
+        if constexpr (WIDE || DT == DT_F32) {
+            Words w;
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                w[i] = v[i];
+            ((Any*)p)->v = w;
+        } else {
             *(uint16_t*)p = (uint16_t)v[0];
+        }
     }
     __device__ __forceinline__ float get(int i) const
     {
-        if constexpr (DT == DT_F32) {
-            const u32 w = v[i];
-            return __builtin_bit_cast(float, w);
-        }
+        if constexpr (DT == DT_F32)
+            return __builtin_bit_cast(float, v[i]);
         const u32 w = v[i >> 1];
         if constexpr (DT == DT_BF16)
             return __builtin_bit_cast(float, (i & 1) ? (w & 0xFFFF0000u) : (w << 16));
@@ -98,7 +104,7 @@ struct HeadRaw {
                 v[i] = __builtin_bit_cast(u32, f[i]);
         } else if constexpr (WIDE) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < NW; ++i)
                 v[i] = pack2(f[2 * i], f[2 * i + 1], DT);
         } else {
             v[0] = cvt1(f[0], DT);
@@ -135,6 +141,7 @@ template <int DT, int V, int G, int NC, bool INTER>
 struct HeadLane {
     using Raw = HeadRaw<DT, V>;
     static constexpr int ES = DT == DT_F32 ? 4 : 2;
+    static constexpr int NG = 64 / G;
     struct Values {
         Raw a[NC], b[NC];
     };
@@ -144,12 +151,14 @@ struct HeadLane {
     int oa[NC], ob[NC];  // places of the first and the second members; past D: none
     int i0[NC];          // first pair
     int D, R;
+    int g;  // which of the unit's heads
 
-    __device__ __forceinline__ HeadLane(const HeadsParams& p, int j) : D(p.D), R(p.R)
+    __device__ __forceinline__ HeadLane(const HeadsParams& p, int lane)
+        : D(p.D), R(p.R), g(lane / G)
     {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int i = (j + c * G) * V;
+            const int i = (lane % G + c * G) * V;
             i0[c] = i;
             if (V == 1 ? p.interleaved != 0 : INTER) {
                 oa[c] = 2 * i;
@@ -165,28 +174,39 @@ struct HeadLane {
             }
         }
     }
-    __device__ __forceinline__ void load(Values& v, const void* base, int64_t at, bool there) const
+    // The first of a unit's heads: `at` is the unit's place in its token.
+    static __device__ __forceinline__ char* first_head(const void* base, int64_t st, int64_t sh,
+                                                       int token, int at)
     {
-        const char* p = (const char*)base + at * ES;
+        return (char*)base + (token * st + (int64_t)(at * NG) * sh) * ES;
+    }
+    // Bytes from there to the lane's head; the host sees to it that they fit.
+    static __device__ __forceinline__ u32 head_offset(int64_t sh, int head)
+    {
+        return (u32)head * (u32)sh * (u32)ES;
+    }
+    // No load stands in a branch, so that all of them are in flight together: places
+    // past D read the head's first values, which have no part in anything.
+    __device__ __forceinline__ void load(Values& v, const char* p, u32 off) const
+    {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            v.a[c].load(p + oa[c] * ES, there && oa[c] < D);
-            v.b[c].load(p + ob[c] * ES, there && ob[c] < D);
+            v.a[c].load(p + (off + (u32)(oa[c] < D ? oa[c] * ES : 0)));
+            v.b[c].load(p + (off + (u32)(ob[c] < D ? ob[c] * ES : 0)));
         }
     }
-    __device__ __forceinline__ void store(void* base, int64_t at, const float (&f)[NC][2 * V]) const
+    __device__ __forceinline__ void store(char* p, u32 off, const float (&f)[NC][2 * V]) const
     {
-        char* p = (char*)base + at * ES;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             Raw r;
             if (oa[c] < D) {
                 r.put(&f[c][0]);
-                r.store(p + oa[c] * ES);
+                r.store(p + (off + (u32)(oa[c] * ES)));
             }
             if (ob[c] < D) {
                 r.put(&f[c][V]);
-                r.store(p + ob[c] * ES);
+                r.store(p + (off + (u32)(ob[c] * ES)));
             }
         }
     }
@@ -207,57 +227,117 @@ struct HeadLane {
     {
         return INTER && V > 1 ? 2 * i + 1 : V + i;
     }
-    // The token's cosines and sines; NaN for a position that the tables lack.
-    __device__ __forceinline__ void turn(Turn& t, const HeadsParams& p, int token) const
+    // Sum over the head of x y.  A chunk of several pairs is in the head as a whole
+    // or not at all.
+    __device__ __forceinline__ float dot(const float (&x)[NC][2 * V],
+                                         const float (&y)[NC][2 * V]) const
     {
-        const int64_t pos = p.pos ? p.pos[token] : token;
-        const bool in = pos >= 0 && pos < p.P;
-        const int64_t row = (in ? pos : 0) * (R / 2);
+        float t = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            float ta = 0.0f, tb = 0.0f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                ta = __builtin_fmaf(x[c][e], y[c][e], ta);
+                tb = __builtin_fmaf(x[c][V + e], y[c][V + e], tb);
+            }
+            if constexpr (V > 1)
+                t += oa[c] < D ? ta + tb : 0.0f;
+            else
+                t += (oa[c] < D ? ta : 0.0f) + (ob[c] < D ? tb : 0.0f);
+        }
+        return group_sum<G>(t);
+    }
+    // 1 / sqrt(mean of x^2 + eps): the instruction is good to a step, but takes
+    // subnormal numbers for zero.
+    __device__ __forceinline__ float root(const float (&x)[NC][2 * V], const HeadsParams& p) const
+    {
+        const float v = dot(x, x) * p.inv_d + p.eps;
+        const bool tiny = v < 0x1p-96f;
+        return __builtin_amdgcn_rsqf(tiny ? v * 0x1p96f : v) * (tiny ? 0x1p48f : 1.0f);
+    }
+    // The weights, ones where there are none.
+    __device__ __forceinline__ void weights(float (&w)[NC][2 * V], const void* base) const
+    {
+        if (base) {
+            Values v;
+            load(v, (const char*)base, 0);
+            unpack(v, w);
+            return;
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int e = 0; e < 2 * V; ++e)
+                w[c][e] = 1.0f;
+    }
+    // The token's position: read-only to the kernel, hence by the scalar path, whose
+    // waits are apart from those of vector loads and stores.
+    static __device__ __forceinline__ int64_t position(const HeadsParams& p, int token)
+    {
+        typedef const __attribute__((address_space(4))) int64_t Const;
+        return p.pos ? ((Const*)(uintptr_t)p.pos)[token] : token;
+    }
+    // Its cosines and sines as loaded, and as they are used: NaN for a position that
+    // the tables lack, no turn for values past R.
+    __device__ __forceinline__ void load(Turn& t, const HeadsParams& p, int64_t pos) const
+    {
+        if (R == 0)
+            return;
+        const int64_t row = (pos >= 0 && pos < p.P ? pos : 0) * (R / 2);
+        const char *pc = (const char*)(p.cos + row), *ps = (const char*)(p.sin + row);
+        typedef __attribute__((ext_vector_type(V))) float Vec;
         struct __attribute__((packed, aligned(4))) Any {
-            f32x4 v;
+            Vec v;
         };
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const bool turned = i0[c] < R / 2;
-            const float *pc = p.cos + row + i0[c], *ps = p.sin + row + i0[c];
+            const u32 off = (u32)(i0[c] < R / 2 ? i0[c] : 0) * 4u;
+            const Vec vc = ((const Any*)(pc + off))->v, vs = ((const Any*)(ps + off))->v;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                t.c[c][i] = 1.0f;
-                t.s[c][i] = 0.0f;
-            }
-            if (!turned)
-                continue;
-            if constexpr (V > 1) {
-#pragma unroll
-                for (int i = 0; i < V; i += 4) {
-                    const f32x4 vc = ((const Any*)(pc + i))->v, vs = ((const Any*)(ps + i))->v;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        t.c[c][i + e] = in ? vc[e] : __builtin_nanf("");
-                        t.s[c][i + e] = in ? vs[e] : __builtin_nanf("");
-                    }
-                }
-            } else {
-                t.c[c][0] = in ? *pc : __builtin_nanf("");
-                t.s[c][0] = in ? *ps : __builtin_nanf("");
+                t.c[c][i] = vc[i];
+                t.s[c][i] = vs[i];
             }
         }
     }
+    __device__ __forceinline__ void settle(Turn& t, const HeadsParams& p, int64_t pos) const
+    {
+        const bool in = pos >= 0 && pos < p.P;
+        if (in && R == D)
+            return;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const bool turned = i0[c] < R / 2;
+                t.c[c][i] = turned ? (in ? t.c[c][i] : __builtin_nanf("")) : 1.0f;
+                t.s[c][i] = turned ? (in ? t.s[c][i] : __builtin_nanf("")) : 0.0f;
+            }
+    }
+    // Turned to the token's position, or back.
+    template <bool BACK>
+    static __device__ __forceinline__ void turn(float (&x)[NC][2 * V], const Turn& t)
+    {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float a = x[c][first(e)], b = x[c][second(e)];
+                const float k = t.c[c][e], n = BACK ? -t.s[c][e] : t.s[c][e];
+                x[c][first(e)] = a * k - b * n;
+                x[c][second(e)] = a * n + b * k;
+            }
+    }
 };
-
-__device__ __forceinline__ float head_root(float sum, int D, float eps)
-{
-    return 1.0f / sqrtf(sum / (float)D + eps);
-}
 
 template <int DT, int V, int G, int NC, bool INTER>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void heads_kernel(HeadsParams p)
 {
     using Lane = HeadLane<DT, V, G, NC, INTER>;
     constexpr int NG = 64 / G;
-    const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const Lane L(p, lane % G);
+    const Lane L(p, threadIdx.x & 63);
     const int units = p.s[0].units + p.s[1].units;
     const int64_t total = (int64_t)p.T * units;
     const int64_t u0 = ((int64_t)blockIdx.x * 4 + w) * p.per;
@@ -267,48 +347,37 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void heads_ker
     const int64_t left = total - u0;
     const int n = left < p.per ? (int)left : p.per;
     typename Lane::Turn t;
-    typename Lane::Values wv;
+    float wf[NC][2 * V];
     int have = -1, side = -1;
     for (int i = 0; i < n; ++i) {
         const int sd = at >= p.s[0].units;
         const HeadSide& s = p.s[sd];
-        const int h = (at - (sd ? p.s[0].units : 0)) * NG + lane / G;
-        const bool there = h < s.H;
+        const int a = at - (sd ? p.s[0].units : 0);
+        const bool there = a * NG + L.g < s.H;
         typename Lane::Values xv;
-        L.load(xv, s.x, token * s.xt + h * s.xh, there);
+        L.load(xv, Lane::first_head(s.x, s.xt, s.xh, token, a),
+               Lane::head_offset(s.xh, there ? L.g : 0));
         if (have != token) {
-            L.turn(t, p, token);
+            const int64_t pos = Lane::position(p, token);
+            L.load(t, p, pos);
+            L.settle(t, p, pos);
             have = token;
         }
         if (side != sd) {
-            if (s.w)
-                L.load(wv, s.w, 0, true);
+            L.weights(wf, s.w);
             side = sd;
         }
-        float x[NC][2 * V], wf[NC][2 * V];
+        float x[NC][2 * V];
         Lane::unpack(xv, x);
-        Lane::unpack(wv, wf);
-        float ss = 0.0f;
+        const float r = L.root(x, p);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int e = 0; e < 2 * V; ++e)
-                ss += x[c][e] * x[c][e];
-        const float r = head_root(group_sum<G>(ss), p.D, p.eps);
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-#pragma unroll
-            for (int e = 0; e < 2 * V; ++e)
-                x[c][e] = s.w ? x[c][e] * r * wf[c][e] : x[c][e] * r;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float a = x[c][Lane::first(e)], b = x[c][Lane::second(e)];
-                x[c][Lane::first(e)] = a * t.c[c][e] - b * t.s[c][e];
-                x[c][Lane::second(e)] = a * t.s[c][e] + b * t.c[c][e];
-            }
-        }
+                x[c][e] = x[c][e] * r * wf[c][e];
+        Lane::template turn<false>(x, t);
         if (there)
-            L.store(s.out, token * s.ot + h * s.oh, x);
+            L.store(Lane::first_head(s.out, s.ot, s.oh, token, a), Lane::head_offset(s.oh, L.g), x);
         if (++at == units) {
             at = 0;
             ++token;
@@ -335,73 +404,93 @@ heads_grad_kernel(HeadsParams p)
     const int sd = (int)blockIdx.x >= p.s[0].blocks;
     const HeadSide& s = p.s[sd];
     const int block = (int)blockIdx.x - (sd ? p.s[0].blocks : 0);
-    const Lane L(p, lane % G);
-    const int64_t total = (int64_t)p.T * s.units;
-    const int64_t u0 = ((int64_t)block * NW + w) * p.per;
-    const int64_t left = total - u0;
-    const int n = left <= 0 ? 0 : (left < p.per ? (int)left : p.per);
-    int token = (int)(u0 / s.units), at = (int)(u0 - (int64_t)token * s.units);
-    float acc[NC][2 * V];
+    const Lane L(p, lane);
+    float acc[NC][2 * V], wf[NC][2 * V];
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int e = 0; e < 2 * V; ++e)
             acc[c][e] = 0.0f;
-    typename Lane::Turn t;
-    typename Lane::Values wv;
-    if (s.w)
-        L.load(wv, s.w, 0, true);
-    int have = -1;
-    for (int i = 0; i < n; ++i) {
-        const int h = at * NG + lane / G;
-        const bool there = h < s.H;
-        typename Lane::Values xv, dv;
-        L.load(xv, s.x, token * s.xt + h * s.xh, there);
-        L.load(dv, s.d, token * s.dt + h * s.dh, there);
-        if (have != token) {
-            L.turn(t, p, token);
-            have = token;
+    L.weights(wf, s.w);
+    // A unit's loads are issued a unit ahead, all together and before the stores of
+    // the one at hand: vector loads and stores are waited for in the order in which
+    // they were issued.  Its position is read two units ahead.
+    struct Unit {
+        typename Lane::Values x, d;
+        typename Lane::Turn t;
+        int64_t pos;
+        int token, at;
+    };
+    const auto fetch = [&](Unit& n) {
+        const int g = n.at * NG + L.g < s.H ? L.g : 0;
+        L.load(n.x, Lane::first_head(s.x, s.xt, s.xh, n.token, n.at), Lane::head_offset(s.xh, g));
+        L.load(n.d, Lane::first_head(s.d, s.dt, s.dh, n.token, n.at), Lane::head_offset(s.dh, g));
+        L.load(n.t, p, n.pos);
+    };
+    // Unit u of this side is unit u % units of token u / units; a step adds
+    // (step_t, step_a) to the two.
+    const int step = s.blocks * NW, step_t = step / s.units, step_a = step - step_t * s.units;
+    int token = (block * NW + w) / s.units, at = (block * NW + w) - token * s.units;
+    const auto next = [&](Unit& n) {
+        n.token = token < p.T ? token : p.T - 1;
+        n.at = token < p.T ? at : 0;
+        n.pos = Lane::position(p, n.token);
+        at += step_a;
+        token += step_t;
+        if (at >= s.units) {
+            at -= s.units;
+            ++token;
         }
-        float x[NC][2 * V], d[NC][2 * V], wf[NC][2 * V];
-        Lane::unpack(xv, x);
-        Lane::unpack(dv, d);
-        Lane::unpack(wv, wf);
-        float ss = 0.0f;
+    };
+    int count = 0;  // the wave's units
+    {
+        const int64_t total = (int64_t)p.T * s.units, u0 = block * NW + w;
+        count = u0 < total ? (int)((total - u0 + step - 1) / step) : 0;
+    }
+    Unit n1, n2;
+    if (count > 0) {
+        next(n1);
+        fetch(n1);
+        next(n2);
+    }
+    for (int i = 0; i < count; ++i) {
+        Unit n = n1;
+        n1 = n2;
+        if (i + 1 < count)
+            fetch(n1);
+        next(n2);
+        L.settle(n.t, p, n.pos);
+        const bool there = n.at * NG + L.g < s.H;
+        if (n.at * NG + NG > s.H && !there) {
+            // a head that is not there (another one was read): no part in dw
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                n.d.a[c].clear();
+                n.d.b[c].clear();
+            }
+        }
+        float x[NC][2 * V], d[NC][2 * V];
+        Lane::unpack(n.x, x);
+        Lane::unpack(n.d, d);
+        const float r = L.root(x, p);
+        Lane::template turn<true>(d, n.t);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int e = 0; e < 2 * V; ++e)
-                ss += x[c][e] * x[c][e];
-        const float r = head_root(group_sum<G>(ss), p.D, p.eps);
-        float dot = 0.0f;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float a = d[c][Lane::first(e)], b = d[c][Lane::second(e)];
-                d[c][Lane::first(e)] = a * t.c[c][e] + b * t.s[c][e];
-                d[c][Lane::second(e)] = b * t.c[c][e] - a * t.s[c][e];
-            }
 #pragma unroll
             for (int e = 0; e < 2 * V; ++e) {
                 x[c][e] *= r;
-                acc[c][e] += there ? d[c][e] * x[c][e] : 0.0f;
-                d[c][e] = s.w ? d[c][e] * wf[c][e] : d[c][e];
-                dot += d[c][e] * x[c][e];
+                acc[c][e] = __builtin_fmaf(d[c][e], x[c][e], acc[c][e]);
+                d[c][e] *= wf[c][e];
             }
-        }
-        const float m = group_sum<G>(dot) / (float)p.D;
+        const float m = L.dot(d, x) * p.inv_d;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int e = 0; e < 2 * V; ++e)
-                d[c][e] = r * (d[c][e] - x[c][e] * m);
+                d[c][e] = r * __builtin_fmaf(-x[c][e], m, d[c][e]);
         if (there)
-            L.store(s.out, token * s.ot + h * s.oh, d);
-        if (++at == s.units) {
-            at = 0;
-            ++token;
-        }
+            L.store(Lane::first_head(s.out, s.ot, s.oh, n.token, n.at),
+                    Lane::head_offset(s.oh, L.g), d);
     }
     if (!s.part)
         return;  // the whole workgroup
@@ -419,8 +508,8 @@ heads_grad_kernel(HeadsParams p)
     // value o of the head is in the lane and register that hold it; each thread
     // adds one, over the waves
     for (int i = threadIdx.x; i < NC * 2 * V * G; i += 64 * NW) {
-        const int j = i % G, r = i / G;
-        const Lane l(p, j);
+        const int r = i / G;
+        const Lane l(p, i % G);
         int o = p.D;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -431,11 +520,11 @@ heads_grad_kernel(HeadsParams p)
                     o = base < p.D ? base + e % V : p.D;
                 }
         if (o < p.D) {
-            float s8 = red[0][i];
+            float t = red[0][i];
 #pragma unroll
             for (int v = 1; v < NW; ++v)
-                s8 += red[v][i];
-            s.part[(int64_t)block * p.D + o] = s8;
+                t += red[v][i];
+            s.part[(int64_t)block * p.D + o] = t;
         }
     }
 }
@@ -448,7 +537,7 @@ struct HeadSums {
 };
 
 // dw of one side (blockIdx.y), 8 values to a workgroup: 32 rows of partial sums at
-// a time, four of them in flight, then the 32 sums, in order.
+// a time, sixteen of them in flight, then the 32 sums, in order.
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void
 heads_sums_kernel(HeadSums p)
 {
@@ -460,14 +549,16 @@ heads_sums_kernel(HeadSums p)
     const int n = there ? p.blocks[side] : 0;
     const float* part = p.part[side] + k;
     float s = 0.0f;
-    for (int b0 = t; b0 < n; b0 += 128) {
-        float v[4];
+    for (int b0 = t; b0 < n; b0 += 512) {
+        float v[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = b0 + 32 * i < n ? part[(int64_t)(b0 + 32 * i) * p.D] : 0.0f;
+        for (int i = 0; i < 16; ++i) {
+            const int b = b0 + 32 * i;
+            v[i] = part[(int64_t)(b < n ? b : t) * p.D];
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            s += v[i];
+        for (int i = 0; i < 16; ++i)
+            s += b0 + 32 * i < n ? v[i] : 0.0f;
     }
     red[t][c] = s;
     __syncthreads();
