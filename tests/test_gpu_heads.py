@@ -165,6 +165,25 @@ def test_far_positions_and_extreme_values():
     assert not torch.isnan(out.k).any()
 
 
+def test_heads_far_apart():
+    # heads more than 32 bits of bytes from the first of their unit
+    T, H, D, far = 3, 8, 64, 640 * 2 ** 20 // 2
+    x = torch.empty(((H - 1) * far + T * D,), dtype=BF16, device="cuda")
+    q = x.as_strided((T, H, D), (D, far, 1))
+    _, k, wq, wk, cos, sin, pos = case(T, H, 2, D, D, BF16)
+    q.copy_(rand((T, H, D), 3, BF16))
+    a = binding.head_norm_rope(q, k, wq, wk, cos, sin, pos, EPS)
+    b = binding.head_norm_rope(q.contiguous(), k, wq, wk, cos, sin, pos, EPS)
+    want, err = ref.heads_forward(q, wq, cos[pos], sin[pos], D, EPS, False)
+    for got in (a.q, b.q):
+        ref.assert_close(got, want, err, BF16)
+    d = rand((T, H, D), 4, BF16)
+    g = binding.head_norm_rope_backward(d, k, q, k, wq, wk, cos, sin, pos, EPS)
+    dx, dw, ex, ew = ref.heads_backward(d, q, wq, cos[pos], sin[pos], D, EPS, False)
+    ref.assert_close(g.dq, dx, ex, BF16)
+    ref.assert_close(g.dw_q, dw, ew, F32)
+
+
 def test_nothing():
     q = torch.zeros((0, 4, 64), dtype=BF16, device="cuda")
     w = torch.ones((64,), dtype=BF16, device="cuda")

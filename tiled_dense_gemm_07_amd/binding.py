@@ -13,8 +13,10 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import functools
 import math
 import os
+import struct
 
 import numpy as np
 
@@ -211,11 +213,10 @@ def load_library():
     lib.tg_linear_mx_workspace_size.argtypes = [i64, i64, i64, c_int, c_int, size_p]
     lib.tg_linear_mx_backward.argtypes = [ctypes.POINTER(LinearMxGradArgs), p, ctypes.c_size_t, p]
     lib.tg_linear_mx_backward_workspace_size.argtypes = [ctypes.POINTER(LinearMxGradArgs), size_p]
-    lib.tg_head_norm_rope.argtypes = [ctypes.POINTER(HeadNormRopeArgs), p]
-    lib.tg_head_norm_rope_backward.argtypes = [ctypes.POINTER(HeadNormRopeGradArgs), p,
-                                               ctypes.c_size_t, p]
-    lib.tg_head_norm_rope_backward_workspace_size.argtypes = [
-        ctypes.POINTER(HeadNormRopeGradArgs), size_p]
+    # the argument structs packed (bytes) or by reference
+    lib.tg_head_norm_rope.argtypes = [p, p]
+    lib.tg_head_norm_rope_backward.argtypes = [p, p, ctypes.c_size_t, p]
+    lib.tg_head_norm_rope_backward_workspace_size.argtypes = [p, size_p]
     for name in ("tg_quant_mx", "tg_dequant_mx", "tg_linear_mx", "tg_linear_mx_workspace_size",
                  "tg_linear_mx_backward", "tg_linear_mx_backward_workspace_size",
                  "tg_head_norm_rope", "tg_head_norm_rope_backward",
@@ -897,14 +898,36 @@ def block_norm_backward(x_new, dx_new=None, dh=None, y=None, gate=None, gate_row
 # --------------------------------------------------------------------------
 # Microscaled linear path, and norms of query and key heads with rotation.
 # --------------------------------------------------------------------------
-def _call(device, entry, *args):
-    """entry(*args) with `device` current: the null stream is the current device's."""
-    torch = _torch()
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            _check(entry(*args))
+_current_device = None
+
+
+def _call(t, entry, *args):
+    """entry(*args, stream) on t's device, made current: the null stream is the current
+    device's.  The last argument is the caller's stream or None."""
+    global _current_device
+    if _current_device is None:
+        torch = _torch()
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    device = t.device
+    stream = _stream_ptr(device, args[-1])
+    if _current_device() == device.index:
+        status = entry(*args[:-1], stream)
     else:
-        _check(entry(*args))
+        with _torch().cuda.device(device):
+            status = entry(*args[:-1], stream)
+    if status:
+        _check(status)
+
+
+def _same_device(first, *others):
+    """Raises unless every tensor (None: none) is on first's GPU."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("operands must be GPU tensors")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError("operands must be on one device: %s and %s"
+                             % (first.device, t.device))
 
 
 def _workspace(workspace, need, like, stream):
@@ -931,13 +954,13 @@ def _mx_shapes(rows, cols, fmt):
 
 
 def _mx_dense(name, t, shape):
-    torch = _torch()
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError("%s must be a dense GPU tensor" % name)
-    if t.dtype != torch.uint8:
+    """Device pointer of the dense uint8 tensor t."""
+    if t.dtype != _torch().uint8:
         raise TypeError("%s must be uint8, got %s" % (name, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be dense" % name)
     return t.data_ptr()
 
 
@@ -970,9 +993,8 @@ def quant_mx(X, fmt=TG_MX_E2M1, sides="rows", q=None, s=None, qt=None, st=None, 
         ptr[2:] = _mx_dense("qt", qt, sq), _mx_dense("st", st, ss)
     elif qt is not None or st is not None:
         raise ValueError("qt and st are not written with sides 'rows'")
-    _one_device(X, q, s, qt, st)
-    _call(X.device, load_library().tg_quant_mx, M, K, _dtype_code(X), X.data_ptr(), ldx, fmt, *ptr,
-          _stream_ptr(X.device, stream))
+    _same_device(X, q, s, qt, st)
+    _call(X, load_library().tg_quant_mx, M, K, _dtype_code(X), X.data_ptr(), ldx, fmt, *ptr, stream)
     return QuantMx(q, s, qt, st)
 
 
@@ -994,12 +1016,13 @@ def dequant_mx(q, s, fmt=TG_MX_E2M1, K=None, dtype=None, X=None, stream=None):
     elif dtype is not None and X.dtype != dtype:
         raise TypeError("X must be %s, got %s" % (dtype, X.dtype))
     ldx = _rows("X", X, (M, K))
-    _one_device(q, s, X)
-    _call(q.device, load_library().tg_dequant_mx, M, K, fmt, pq, ps, _dtype_code(X), X.data_ptr(),
-          ldx, _stream_ptr(q.device, stream))
+    _same_device(q, s, X)
+    _call(q, load_library().tg_dequant_mx, M, K, fmt, pq, ps, _dtype_code(X), X.data_ptr(), ldx,
+          stream)
     return X
 
 
+@functools.lru_cache(maxsize=4096)
 def linear_mx_workspace_size(M: int, N: int, K: int, dtype: int, fmt: int = TG_MX_E2M1) -> int:
     """Workspace bytes :func:`linear_mx` needs (0: none)."""
     out = ctypes.c_size_t(0)
@@ -1028,11 +1051,13 @@ def linear_mx(X, Wq, Ws, bias=None, fmt=TG_MX_E2M1, C=None, epilogue=None, works
     ldc = _rows("C", C, (M, N), X.dtype)
     dt = _dtype_code(X)
     need = linear_mx_workspace_size(M, N, K, dt, fmt) if workspace is None else 0
-    workspace, wp, wn = _workspace(workspace, need, X, stream)
-    pb = _vector("bias", bias, N, _torch().float32)
-    _one_device(X, Wq, Ws, bias, C, workspace)
-    _call(X.device, load_library().tg_linear_mx, M, N, K, dt, X.data_ptr(), ldx, fmt, pq, ps, pb,
-          C.data_ptr(), ldc, _epi_code(epilogue), wp, wn, _stream_ptr(X.device, stream))
+    wp, wn = None, 0
+    if need or workspace is not None:
+        workspace, wp, wn = _workspace(workspace, need, X, stream)
+    pb = None if bias is None else _vector("bias", bias, N, _torch().float32)
+    _same_device(X, Wq, Ws, bias, C, workspace)
+    _call(X, load_library().tg_linear_mx, M, N, K, dt, X.data_ptr(), ldx, fmt, pq, ps, pb,
+          C.data_ptr(), ldc, _epi_code(epilogue), wp, wn, stream)
     return C
 
 
@@ -1086,64 +1111,68 @@ def linear_mx_backward(dY, X=None, W=None, fmt=TG_MX_E2M1, dbias=False, workspac
     if workspace is None:
         _check(lib.tg_linear_mx_backward_workspace_size(ctypes.byref(a), ctypes.byref(need)))
     workspace, wp, wn = _workspace(workspace, need.value, dY, stream)
-    _one_device(dY, X, W, workspace)
-    _call(dY.device, lib.tg_linear_mx_backward, ctypes.byref(a), wp, wn,
-          _stream_ptr(dY.device, stream))
+    _same_device(dY, X, W, workspace)
+    _call(dY, lib.tg_linear_mx_backward, ctypes.byref(a), wp, wn, stream)
     return LinearMxGrad(dx, dw, db)
 
 
-def _set_heads(a, field, name, t, T=None, H=None, D=None, dtype=None):
-    """Puts the heads t [T, H, D] into `field` of the argument struct, with its
-    strides of tokens and heads."""
-    if not t.is_cuda:
-        raise ValueError("%s must be a GPU tensor" % name)
-    size = t.shape
-    if len(size) != 3 or any(w is not None and g != w for g, w in zip(size, (T, H, D))):
-        raise ValueError("%s must be [tokens, heads, values]%s, got %s"
-                         % (name, "" if T is None else " = %s" % [T, H, D], tuple(size)))
-    if dtype is not None and t.dtype != dtype:
+# The argument structs of the head norms, field by field as HeadNormRopeArgs and
+# HeadNormRopeGradArgs have them: packing takes a fraction of setting their fields.
+_HEADS_ARGS = struct.Struct("@5qiP2qP2q4PqPfiP2qP2q")
+_HEADS_GRAD_ARGS = struct.Struct("@5qiP2qP2q4PqPfiP2qP2qP2qP2q2P")
+
+
+def _heads(name, t, shape, dtype):
+    """(pointer, stride of tokens, stride of heads) of the heads t."""
+    if t.shape != shape:
+        raise ValueError("%s must be [tokens, heads, values] = %s, got %s"
+                         % (name, list(shape), tuple(t.shape)))
+    if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     st, sh, unit = t.stride()
-    if unit != 1 and size[2] > 1:
+    if unit != 1 and shape[2] > 1:
         raise ValueError("%s must have unit stride along a head" % name)
-    setattr(a, field, t.data_ptr())
-    setattr(a, field + "_t", st)
-    setattr(a, field + "_h", sh)
+    return t.data_ptr(), st, sh
 
 
-def _heads_args(a, q, k, w_q, w_k, cos, sin, positions, eps, interleaved):
-    """Fills what the forward and the backward call share; returns (T, Hq, Hk, D)."""
+def _heads_args(q, k, w_q, w_k, cos, sin, positions, eps, interleaved):
+    """(shape of q, shape of k, the packed fields that the forward and the backward call
+    share)."""
     torch = _torch()
-    _set_heads(a, "q", "q", q)
-    T, Hq, D = q.shape
-    Hk = 0
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3:
+        raise ValueError("q must be [tokens, heads, values], got %s" % (tuple(shape),))
+    T, Hq, D = shape
+    at_q, at_k, kshape = _heads("q", q, shape, dtype), (0, 0, 0), (T, 0, D)
     if k is not None:
-        Hk = k.shape[1] if k.dim() == 3 else None
-        _set_heads(a, "k", "k", k, T, Hk, D, q.dtype)
+        if k.dim() != 3:
+            raise ValueError("k must be [tokens, heads, values], got %s" % (tuple(k.shape),))
+        kshape = (T, k.shape[1], D)
+        at_k = _heads("k", k, kshape, dtype)
     elif w_k is not None:
         raise ValueError("w_k without k")
-    a.T, a.Hq, a.Hk, a.D, a.dtype = T, Hq, Hk, D, _dtype_code(q)
-    a.w_q = _vector("w_q", w_q, D, q.dtype)
-    a.w_k = _vector("w_k", w_k, D, q.dtype)
-    if (cos is None) != (sin is None):
+    R = P = pc = ps = 0
+    if cos is not None and sin is not None:
+        size = cos.shape
+        if len(size) != 2 or sin.shape != size or not (cos.is_contiguous() and sin.is_contiguous()):
+            raise ValueError("cos and sin must be dense tensors [positions, pairs]")
+        if cos.dtype != torch.float32 or sin.dtype != torch.float32:
+            raise TypeError("cos and sin must be torch.float32, got %s and %s"
+                            % (cos.dtype, sin.dtype))
+        P, R = size[0], 2 * size[1]
+        if R > D:
+            raise ValueError("cos has %d pairs for heads of %d values" % (size[1], D))
+        if positions is None and R > 0 and P < T:
+            raise ValueError("positions are needed: tables of %d positions for %d tokens" % (P, T))
+        pc, ps = cos.data_ptr(), sin.data_ptr()
+    elif cos is not None or sin is not None:
         raise ValueError("cos and sin go together")
-    if cos is not None:
-        for name, t in (("cos", cos), ("sin", sin)):
-            if not t.is_cuda or not t.is_contiguous() or t.dim() != 2 or t.shape != cos.shape:
-                raise ValueError("%s must be a dense GPU tensor [positions, pairs]" % name)
-            if t.dtype != torch.float32:
-                raise TypeError("%s must be torch.float32, got %s" % (name, t.dtype))
-        a.P, a.R = cos.shape[0], 2 * cos.shape[1]
-        if a.R > D:
-            raise ValueError("cos has %d pairs for heads of %d values" % (cos.shape[1], D))
-        if positions is None and a.R > 0 and a.P < T:
-            raise ValueError("positions are needed: tables of %d positions for %d tokens"
-                             % (a.P, T))
-        a.cos, a.sin = cos.data_ptr(), sin.data_ptr()
-    if positions is not None:
-        a.positions = _vector("positions", positions, T, torch.int64)
-    a.eps, a.interleaved = eps, bool(interleaved)
-    return T, Hq, Hk, D
+    return shape, kshape, (
+        T, Hq, kshape[1], D, R, _dtype_code(q), *at_q, *at_k,
+        0 if w_q is None else _vector("w_q", w_q, D, dtype),
+        0 if w_k is None else _vector("w_k", w_k, D, dtype), pc, ps, P,
+        0 if positions is None else _vector("positions", positions, T, torch.int64), eps,
+        bool(interleaved))
 
 
 def head_norm_rope(q, k=None, w_q=None, w_k=None, cos=None, sin=None, positions=None, eps=1e-6,
@@ -1155,20 +1184,20 @@ def head_norm_rope(q, k=None, w_q=None, w_k=None, cos=None, sin=None, positions=
     neighbours with interleaved.  q and k may have any strides of tokens and
     heads (slices of one projection's output); q_out and k_out may be q and k.
     Returns a HeadNormRope(q, k)."""
-    a = HeadNormRopeArgs()
-    T, Hq, Hk, D = _heads_args(a, q, k, w_q, w_k, cos, sin, positions, eps, interleaved)
+    _same_device(q, k, w_q, w_k, cos, sin, positions, q_out, k_out)
+    qs, ks, args = _heads_args(q, k, w_q, w_k, cos, sin, positions, eps, interleaved)
+    dtype = q.dtype
     if q_out is None:
-        q_out = _empty((T, Hq, D), q.dtype, q, stream)
-    _set_heads(a, "q_out", "q_out", q_out, T, Hq, D, q.dtype)
+        q_out = _empty(qs, dtype, q, stream)
+    at_k = (0, 0, 0)
     if k is not None:
         if k_out is None:
-            k_out = _empty((T, Hk, D), q.dtype, q, stream)
-        _set_heads(a, "k_out", "k_out", k_out, T, Hk, D, q.dtype)
+            k_out = _empty(ks, dtype, q, stream)
+        at_k = _heads("k_out", k_out, ks, dtype)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _one_device(q, k, w_q, w_k, cos, sin, positions, q_out, k_out)
-    _call(q.device, load_library().tg_head_norm_rope, ctypes.byref(a),
-          _stream_ptr(q.device, stream))
+    _call(q, load_library().tg_head_norm_rope,
+          _HEADS_ARGS.pack(*args, *_heads("q_out", q_out, qs, dtype), *at_k), stream)
     return HeadNormRope(q_out, k_out)
 
 
@@ -1180,36 +1209,32 @@ def head_norm_rope_backward(dq_out, dk_out, q, k=None, w_q=None, w_k=None, cos=N
     dk, dw_q, dw_k): dq and dk [T, H, D] of q's type, dw_q and dw_k [D] fp32, None
     where there is no such input."""
     torch = _torch()
-    a = HeadNormRopeGradArgs()
-    T, Hq, Hk, D = _heads_args(a, q, k, w_q, w_k, cos, sin, positions, eps, interleaved)
     if (k is None) != (dk_out is None):
         raise ValueError("dk_out and k go together")
-    _set_heads(a, "dq_out", "dq_out", dq_out, T, Hq, D, q.dtype)
-    dq = _empty((T, Hq, D), q.dtype, q, stream)
-    _set_heads(a, "dq", "dq", dq)
-    dk = dw_q = dw_k = None
-    if k is not None:
-        _set_heads(a, "dk_out", "dk_out", dk_out, T, Hk, D, q.dtype)
-        dk = _empty((T, Hk, D), q.dtype, q, stream)
-        _set_heads(a, "dk", "dk", dk)
+    _same_device(q, dq_out, dk_out, k, w_q, w_k, cos, sin, positions, workspace)
+    qs, ks, args = _heads_args(q, k, w_q, w_k, cos, sin, positions, eps, interleaved)
+    dtype, D = q.dtype, qs[2]
+    none = (0, 0, 0)
+    dq = _empty(qs, dtype, q, stream)
+    dk = None if k is None else _empty(ks, dtype, q, stream)
+    dw_q = dw_k = None
     if w_q is not None and w_k is not None:  # one allocation for both
         dw_q, dw_k = _empty((2, D), torch.float32, q, stream).unbind(0)
     elif w_q is not None:
         dw_q = _empty((D,), torch.float32, q, stream)
     elif w_k is not None:
         dw_k = _empty((D,), torch.float32, q, stream)
-    if dw_q is not None:
-        a.dw_q = dw_q.data_ptr()
-    if dw_k is not None:
-        a.dw_k = dw_k.data_ptr()
+    packed = _HEADS_GRAD_ARGS.pack(
+        *args, *_heads("dq_out", dq_out, qs, dtype),
+        *(none if k is None else _heads("dk_out", dk_out, ks, dtype)),
+        dq.data_ptr(), qs[1] * D, D, *(none if k is None else (dk.data_ptr(), ks[1] * D, D)),
+        0 if dw_q is None else dw_q.data_ptr(), 0 if dw_k is None else dw_k.data_ptr())
     lib = load_library()
     need = ctypes.c_size_t(0)
     if workspace is None:
-        _check(lib.tg_head_norm_rope_backward_workspace_size(ctypes.byref(a), ctypes.byref(need)))
+        _check(lib.tg_head_norm_rope_backward_workspace_size(packed, ctypes.byref(need)))
     workspace, wp, wn = _workspace(workspace, need.value, q, stream)
-    _one_device(q, dq_out, dk_out, k, w_q, w_k, cos, sin, positions, workspace)
-    _call(q.device, lib.tg_head_norm_rope_backward, ctypes.byref(a), wp, wn,
-          _stream_ptr(q.device, stream))
+    _call(q, lib.tg_head_norm_rope_backward, packed, wp, wn, stream)
     return HeadNormRopeGrad(dq, dk, dw_q, dw_k)
 
 

@@ -32,9 +32,11 @@ Pick pick_of(bool grad)
 }
 
 template <int DT, bool INTER>
-Pick pick_wide(int64_t chunks, bool grad)
+Pick pick_wide(int64_t chunks, bool grad, bool far)
 {
     constexpr int V = 4;
+    if (far && chunks <= 64)
+        return pick_of<DT, V, 64, 1, INTER>(grad);
     if (chunks <= 4)
         return pick_of<DT, V, 4, 1, INTER>(grad);
     if (chunks <= 8)
@@ -52,12 +54,15 @@ Pick pick_wide(int64_t chunks, bool grad)
 // them (eight of 16 bits, 8192 tokens of 40 heads of 128: forward 30.0 us either way,
 // backward 50.2 and 45.1 with four, whose registers hold another wave to a SIMD).
 template <int DT>
-Pick pick_type(int64_t D, int64_t R, bool inter, bool grad)
+Pick pick_type(int64_t D, int64_t R, bool inter, bool grad, bool far)
 {
     constexpr int V = 4;
     const int64_t pairs = (D + 1) / 2;
     if (D % (2 * V) == 0 && R % (2 * V) == 0)
-        return inter ? pick_wide<DT, true>(pairs / V, grad) : pick_wide<DT, false>(pairs / V, grad);
+        return inter ? pick_wide<DT, true>(pairs / V, grad, far)
+                     : pick_wide<DT, false>(pairs / V, grad, far);
+    if (far && pairs <= 64)
+        return pick_of<DT, 1, 64, 1, false>(grad);
     if (pairs <= 16)
         return pick_of<DT, 1, 16, 1, false>(grad);
     if (pairs <= 32)
@@ -71,14 +76,23 @@ Pick pick_type(int64_t D, int64_t R, bool inter, bool grad)
     return pick_of<DT, 1, 64, 8, false>(grad);
 }
 
-Pick pick(int dt, int64_t D, int64_t R, bool inter, bool grad)
+// apart: the largest stride of heads; a unit's heads are within 32 bits of bytes, or
+// one head is a unit.
+Pick pick(int dt, int64_t D, int64_t R, bool inter, bool grad, int64_t apart)
 {
-    if (dt == TG_F32)
-        return pick_type<tg::DT_F32>(D, R, inter, grad);
-    if (dt == TG_F16)
-        return pick_type<tg::DT_F16>(D, R, inter, grad);
-    return pick_type<tg::DT_BF16>(D, R, inter, grad);
+    const auto of = [&](bool far) {
+        if (dt == TG_F32)
+            return pick_type<tg::DT_F32>(D, R, inter, grad, far);
+        if (dt == TG_F16)
+            return pick_type<tg::DT_F16>(D, R, inter, grad, far);
+        return pick_type<tg::DT_BF16>(D, R, inter, grad, far);
+    };
+    const Pick k = of(false);
+    const int64_t most = ((int64_t)1 << 32) / tg::dtype_size(dt) - kMaxHeadD;
+    return (k.per_wave - 1) * apart > most ? of(true) : k;
 }
+
+int64_t larger(int64_t a, int64_t b) { return a > b ? a : b; }
 
 // Byte range of T tokens of H heads of D values.  Tokens that hold their heads
 // are the rows of a strided matrix, and so are heads that hold their tokens;
@@ -197,7 +211,9 @@ struct GradPlan {
 GradPlan grad_plan(const tg_head_norm_rope_grad_args& a)
 {
     GradPlan g{};
-    g.k = pick(a.dtype, a.D, a.R, a.interleaved != 0, true);
+    g.k = pick(a.dtype, a.D, a.R, a.interleaved != 0, true,
+               larger(larger(larger(a.q_h, a.k_h), larger(a.dq_out_h, a.dk_out_h)),
+                      larger(a.dq_h, a.dk_h)));
     const int64_t uq = a.T * ceil_div(a.Hq, g.k.per_wave), uk = a.T * ceil_div(a.Hk, g.k.per_wave);
     // All workgroups resident at once, shared out by the sides' units; a wave has at
     // least one unit.  (8192 tokens of 40 heads of 128 in bf16: 45 us; one workgroup
@@ -246,7 +262,8 @@ tg_status tg_head_norm_rope(const tg_head_norm_rope_args* a, tg_stream_t stream)
                 return TG_ERR_ALIAS;
     if (overlap(out[0], out[1]))
         return TG_ERR_ALIAS;
-    const Pick k = pick(a->dtype, a->D, a->R, a->interleaved != 0, false);
+    const Pick k = pick(a->dtype, a->D, a->R, a->interleaved != 0, false,
+                        larger(larger(a->q_h, a->k_h), larger(a->q_out_h, a->k_out_h)));
     tg::HeadsParams p = params(c, a->eps, a->interleaved, k.per_wave);
     p.s[0].out = a->q_out;
     p.s[0].ot = a->q_out_t;
