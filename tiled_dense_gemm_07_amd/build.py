@@ -17,7 +17,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtilegemm.so")
 SOURCES = ["tg_api.hip", "tg_gemm_f32.hip", "tg_gemm_f16.hip", "tg_gemm_bf16.hip",
            "tg_dequant_w4.hip", "tg_gemm_mx.hip", "tg_gemm_sp24.hip", "tg_i8.hip", "tg_norm.hip",
-           "tg_mx.hip", "tg_heads.hip"]
+           "tg_mx.hip", "tg_mx_e2m1.hip", "tg_mx_e4m3.hip", "tg_heads.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-Wall",

@@ -36,12 +36,6 @@ struct MxLinearParams {
     int64_t ldc;
 };
 
-__device__ __forceinline__ float mx_result(float v, float bias, int relu)
-{
-    v += bias;
-    return (relu && !(v > 0.0f)) ? 0.0f : v;
-}
-
 // Results of one wave's FM x FN blocks (lane l holds row l % 32 and, for element
 // 4 q + e, column 8 q + 4 (l / 32) + e of a block) through its own LDS region
 // `st` (32 rows of FN * 32 results), 32 rows at a time: rounded, written as
@@ -189,30 +183,123 @@ __device__ __forceinline__ void mx_linear_run(const MxLinearParams& p, int group
                                 sm + w * (32 * WTN * ES));
 }
 
-// A tile's kernel; K a whole number of strips of 128 (of 1024 with MX2).
-template <bool MX2, int DT, int AFMT, int BM, int BN, int WGM, int WGN, int NS>
+// The 256-k strips of tg_kernel_mx2.h for any K that is a whole number of 128: after
+// its groups of four strips come up to three single ones, and the first two steps of
+// a last one.  What the copies of that one bring from past a row's end (the next
+// row, zeros past the last) is not multiplied.
+template <int AFMT, int BM, int BN, int WGM, int WGN>
+struct DmaMx2Any : DmaMx2<AFMT, BM, BN, WGM, WGN, 4> {
+    using Base = DmaMx2<AFMT, BM, BN, WGM, WGN, 4>;
+    using typename Base::Frag;
+    using typename Base::Lane;
+    using typename Base::Res;
+    using typename Base::Scales;
+    using typename Base::StripOff;
+    static constexpr int FM = Base::FM, FN = Base::FN, NM = Base::NM, NRD = Base::NRD;
+
+    // Steps 0 and 1 of the strip in stage ST, whose step 0 is in F[0].
+    template <int ST, int CUR>
+    static __device__ __forceinline__ void half(f32x16 (&acc)[FM][FN], Frag (&F)[2],
+                                                const Scales (&SC)[2], const Lane& L, lds_char* sm)
+    {
+#pragma unroll
+        for (int i = 0; i < NRD; ++i)
+            Base::template read_one<ST, 1>(F[1], L, sm, i);
+#pragma unroll
+        for (int i = 0; i < NM; ++i)
+            Base::template mfma_one<0>(acc, F[0], SC[CUR], L, i);
+#pragma unroll
+        for (int i = 0; i < NM; ++i)
+            Base::template mfma_one<1>(acc, F[1], SC[CUR], L, i);
+    }
+
+    template <int W>
+    static __device__ __forceinline__ void main_loop(f32x16 (&acc)[FM][FN], const Lane& L,
+                                                     lds_char* sm, const GemmParams& p, int m0,
+                                                     int n0, int, u32 smem0)
+    {
+        const Res res = Base::band_res(p, m0, n0);
+#pragma unroll
+        for (int d = 0; d < Base::JS; ++d)
+            Base::template issue_chunk<W>(L, res, p, 0, d, smem0);
+        {
+            const StripOff o0 = Base::strip_off(p, 0), o1 = Base::strip_off(p, 1);
+#pragma unroll
+            for (int d = 0; d < Base::NCOPY; ++d) {
+                Base::template issue_copy<0, W>(L, res, o0, d, smem0);
+                if (Base::cpos(d, W) < Base::STEPS)
+                    Base::template issue_copy<1, W>(L, res, o1, d, smem0);
+            }
+        }
+        wait_all_barrier();
+        Frag F[2];
+        Scales SC[2];
+        Base::template read_scales<0>(SC[0], L, sm, 0);
+#pragma unroll
+        for (int i = 0; i < NRD; ++i)
+            Base::template read_one<0, 0>(F[0], L, sm, i);
+        const int whole = p.K / 256;
+        const bool rest = p.K % 256 != 0;
+        int t = 0;
+        for (; t + 4 <= whole; t += 4) {
+            Base::template strip<0, 0, W>(acc, F, SC, L, res, sm, p, t, smem0);
+            Base::template strip<1, 1, W>(acc, F, SC, L, res, sm, p, t + 1, smem0);
+            Base::template strip<0, 2, W>(acc, F, SC, L, res, sm, p, t + 2, smem0);
+            Base::template strip<1, 3, W>(acc, F, SC, L, res, sm, p, t + 3, smem0);
+        }
+        if (t < whole) {
+            Base::template strip<0, 0, W>(acc, F, SC, L, res, sm, p, t, smem0);
+            if (t + 1 < whole) {
+                Base::template strip<1, 1, W>(acc, F, SC, L, res, sm, p, t + 1, smem0);
+                if (t + 2 < whole) {
+                    Base::template strip<0, 2, W>(acc, F, SC, L, res, sm, p, t + 2, smem0);
+                    if (rest)
+                        half<1, 1>(acc, F, SC, L, sm);
+                } else if (rest) {
+                    half<0, 0>(acc, F, SC, L, sm);
+                }
+            } else if (rest) {
+                half<1, 1>(acc, F, SC, L, sm);
+            }
+        } else if (rest) {
+            half<0, 0>(acc, F, SC, L, sm);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+};
+
+// A tile's kernel.  KIND 0: strips of 128 k; 1: of 256, K a whole number of 1024; 2:
+// of 256, any K.
+enum { MX_S128 = 0, MX_S256_1024 = 1, MX_S256 = 2 };
+template <int KIND, int DT, int AFMT, int BM, int BN, int WGM, int WGN, int NS>
 struct MxTileOf;
 template <int DT, int AFMT, int BM, int BN, int WGM, int WGN, int NS>
-struct MxTileOf<false, DT, AFMT, BM, BN, WGM, WGN, NS>
+struct MxTileOf<MX_S128, DT, AFMT, BM, BN, WGM, WGN, NS>
     : DmaMx<AFMT, BM, BN, WGM, WGN, NS, 4, false> {
     static constexpr int BMT = BM, BNT = BN;
     static constexpr int OCC = MxOcc<AFMT, BM, BN, WGM * WGN>::value;
 };
 template <int DT, int AFMT, int BM, int BN, int WGM, int WGN, int NS>
-struct MxTileOf<true, DT, AFMT, BM, BN, WGM, WGN, NS> : DmaMx2<AFMT, BM, BN, WGM, WGN, 4> {
+struct MxTileOf<MX_S256_1024, DT, AFMT, BM, BN, WGM, WGN, NS>
+    : DmaMx2<AFMT, BM, BN, WGM, WGN, 4> {
+    static constexpr int BMT = BM, BNT = BN;
+    static constexpr int OCC = WGM * WGN > 4 ? 2 : 1;
+};
+template <int DT, int AFMT, int BM, int BN, int WGM, int WGN, int NS>
+struct MxTileOf<MX_S256, DT, AFMT, BM, BN, WGM, WGN, NS> : DmaMx2Any<AFMT, BM, BN, WGM, WGN> {
     static constexpr int BMT = BM, BNT = BN;
     static constexpr int OCC = WGM * WGN > 4 ? 2 : 1;
 };
 
-template <bool MX2, int DT, int AFMT, int BM, int BN, int WGM, int WGN, int NS>
+template <int KIND, int DT, int AFMT, int BM, int BN, int WGM, int WGN, int NS>
 __global__ __attribute__((
     amdgpu_flat_work_group_size(WGM * WGN * 64, WGM * WGN * 64),
-    amdgpu_waves_per_eu(MxTileOf<MX2, DT, AFMT, BM, BN, WGM, WGN, NS>::OCC,
-                        MxTileOf<MX2, DT, AFMT, BM, BN, WGM, WGN, NS>::OCC))) void
+    amdgpu_waves_per_eu(MxTileOf<KIND, DT, AFMT, BM, BN, WGM, WGN, NS>::OCC,
+                        MxTileOf<KIND, DT, AFMT, BM, BN, WGM, WGN, NS>::OCC))) void
 mx_linear_kernel(MxLinearParams p)
 {
     const ClockStamp clk = stamp_begin(p.g);
-    mx_linear_run<MxTileOf<MX2, DT, AFMT, BM, BN, WGM, WGN, NS>, DT>(p, 4);
+    mx_linear_run<MxTileOf<KIND, DT, AFMT, BM, BN, WGM, WGN, NS>, DT>(p, 4);
     stamp_end(p.g, clk);
 }
 
@@ -227,11 +314,13 @@ struct MxStreamParams {
     int Kx;
 };
 
-template <int DTX, int AFMT, int MT, int NW, bool FUSED>
+// NT groups of 16 rows of W and MT of 16 tokens to a workgroup; runs of ST steps of
+// 128 k (ST 4: a row's scale bytes of a run are one 16-byte load).
+template <int DTX, int AFMT, int NT, int MT, int ST, int NW, bool FUSED>
 struct MxStream {
     static constexpr bool A8 = AFMT == MX_E4M3;
-    static constexpr int RUN = 256;
-    static constexpr int TOKENS = 16 * MT;
+    static constexpr int RUN = 128 * ST;
+    static constexpr int TOKENS = 16 * MT, ROWS = 16 * NT;
 
     // FUSED: LDS bytes of a token's codes, 16 apart from a multiple of the bank
     // line so that the rows of a fragment read spread, and of its scales.
@@ -241,53 +330,74 @@ struct MxStream {
     }
     static __host__ __device__ __forceinline__ int lds_bytes(int M, int Kp)
     {
-        const int a = FUSED ? M * (code_row(Kp) + Kp / 32) : 0, r = NW * MT * 1024;
+        const int a = FUSED ? M * (code_row(Kp) + Kp / 32) : 0, r = NW * NT * MT * 1024;
         return a > r ? a : r;
     }
 
     struct Run {
-        u32x4 w[2];
-        u32x2 ws;
-        u32x4 a[FUSED ? 1 : MT][2][A8 ? 2 : 1];
-        u32x2 as[FUSED ? 1 : MT];
+        u32x4 w[NT][ST];
+        u32 ws[NT][ST];
+        u32x4 a[FUSED ? 1 : MT][ST][A8 ? 2 : 1];
+        u32 as[FUSED ? 1 : MT][ST];
     };
     struct Rows {
-        const uint8_t *w, *ws;
+        const uint8_t *w[NT], *ws[NT];
         const uint8_t *a[MT], *as[MT];
     };
 
-    // Steps of 128 k of the run at k0 that exist (the last run may have one).
-    static __device__ __forceinline__ void load(Run& R, const Rows& at, int k0, int steps, int g)
+    static __device__ __forceinline__ void load_scales(u32 (&s)[ST], const uint8_t* p, bool whole)
+    {
+        if constexpr (ST == 4) {
+            if (whole) {
+                struct __attribute__((packed, aligned(4))) Any {
+                    u32x4 v;
+                };
+                const u32x4 v = ((const Any*)p)->v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[i] = v[i];
+                return;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < ST; ++i)
+            s[i] = whole || i == 0 ? ((const u32*)p)[i] : 0;
+    }
+    // A whole run at k0, or its first step.
+    static __device__ __forceinline__ void load(Run& R, const Rows& at, int k0, bool whole, int g)
     {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if (s >= steps)
-                break;
-            R.w[s] = *(const u32x4*)(at.w + k0 / 2 + 64 * s + 16 * g);
-            R.ws[s] = *(const u32*)(at.ws + k0 / 32 + 4 * s);
-            if constexpr (!FUSED) {
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const uint8_t* a = at.a[m] + mx_bytes<AFMT>(k0 + 128 * s) + 16 * g;
-                    R.a[m][s][0] = *(const u32x4*)a;
-                    if constexpr (A8)
-                        R.a[m][s][1] = *(const u32x4*)(a + 64);
-                    R.as[m][s] = *(const u32*)(at.as[m] + k0 / 32 + 4 * s);
-                }
+            for (int s = 0; s < ST; ++s)
+                if (whole || s == 0)
+                    R.w[n][s] = *(const u32x4*)(at.w[n] + k0 / 2 + 64 * s + 16 * g);
+            load_scales(R.ws[n], at.ws[n] + k0 / 32, whole);
+        }
+        if constexpr (!FUSED) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+#pragma unroll
+                for (int s = 0; s < ST; ++s)
+                    if (whole || s == 0) {
+                        const uint8_t* a = at.a[m] + mx_bytes<AFMT>(k0 + 128 * s) + 16 * g;
+                        R.a[m][s][0] = *(const u32x4*)a;
+                        if constexpr (A8)
+                            R.a[m][s][1] = *(const u32x4*)(a + 64);
+                    }
+                load_scales(R.as[m], at.as[m] + k0 / 32, whole);
             }
         }
     }
 
-    static __device__ __forceinline__ void multiply(f32x4 (&acc)[MT], const Run& R,
+    static __device__ __forceinline__ void multiply(f32x4 (&acc)[NT][MT], const Run& R,
                                                     const uint8_t* codes, const uint8_t* scales,
-                                                    int k0, int steps, int g)
+                                                    int k0, bool whole, int g)
     {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if (s >= steps)
+        for (int s = 0; s < ST; ++s) {
+            if (!whole && s > 0)
                 break;
-            const u32x4 w = R.w[s];
-            const i32x8 wop = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 u32x4 lo, hi;
@@ -304,9 +414,14 @@ struct MxStream {
                 }
                 const i32x8 aop = {(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
                                    (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-                acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    wop, aop, acc[m], MX_E2M1, AFMT, 0, (int)(R.ws[s] >> (8 * g)), 0,
-                    (int)(as >> (8 * g)));
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const u32x4 w = R.w[n][s];
+                    const i32x8 wop = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+                    acc[n][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        wop, aop, acc[n][m], MX_E2M1, AFMT, 0, (int)(R.ws[n][s] >> (8 * g)), 0,
+                        (int)(as >> (8 * g)));
+                }
             }
         }
     }
@@ -315,21 +430,33 @@ struct MxStream {
     static __device__ __forceinline__ void quantise(const MxStreamParams& p, uint8_t* codes,
                                                     uint8_t* scales)
     {
-        const int Kp = p.l.g.K, per = Kp / 8, row_b = code_row(Kp);
-        for (int m = 0; m < p.l.g.M; ++m) {
-            const char* src = elem_ptr<DTX>(p.X, m * p.ldx);
-            for (int u = threadIdx.x; u < per; u += NW * 64) {  // whole quads: per % 16 == 0
-                Raw8<DTX> r;
-                load8<DTX>(r, src, 8 * u, p.Kx - 8 * u);
+        // eight elements to a thread, four times at once; whole quads: per % 16 == 0
+        constexpr int NT_ = NW * 64, U = 4;
+        const int Kp = p.l.g.K, per = Kp / 8, row_b = code_row(Kp), total = p.l.g.M * per;
+        for (int u0 = threadIdx.x; u0 < total; u0 += U * NT_) {
+            Raw8<DTX> r[U];
+            int row[U], k[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int u = u0 + i * NT_;
+                row[i] = u / per;
+                k[i] = 8 * (u - row[i] * per);
+                if (u < total)
+                    load8<DTX>(r[i], elem_ptr<DTX>(p.X, row[i] * p.ldx), k[i], p.Kx - k[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (u0 + i * NT_ >= total)
+                    break;
                 u32 byte;
-                const u32x2 w = mx_codes<DTX, AFMT>(r, byte);
-                uint8_t* to = codes + m * row_b + mx_bytes<AFMT>(8 * u);
+                const u32x2 w = mx_codes<DTX, AFMT>(r[i], byte);
+                uint8_t* to = codes + row[i] * row_b + mx_bytes<AFMT>(k[i]);
                 if constexpr (A8)
                     *(u32x2*)to = w;
                 else
                     *(u32*)to = w[0];
-                if ((u & 3) == 0)
-                    scales[m * (Kp / 32) + u / 4] = (uint8_t)byte;
+                if ((k[i] & 31) == 0)
+                    scales[row[i] * (Kp / 32) + k[i] / 32] = (uint8_t)byte;
             }
         }
     }
@@ -341,14 +468,16 @@ struct MxStream {
         const int tid = threadIdx.x;
         const int lane = tid & 63;
         const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-        const int m0 = (int)blockIdx.y * TOKENS, n0 = (int)blockIdx.x * 16;
+        const int m0 = (int)blockIdx.y * TOKENS, n0 = (int)blockIdx.x * ROWS;
         const int ln = lane & 15, g = lane >> 4;
         const int K = gp.K;
         Rows at;
-        {
-            const int64_t n = n0 + ln < gp.N ? n0 + ln : gp.N - 1;
-            at.w = (const uint8_t*)gp.B + n * (K / 2);
-            at.ws = (const uint8_t*)gp.Bs + n * (K / 32);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int r = n0 + 16 * i + ln;
+            const int64_t n = r < gp.N ? r : gp.N - 1;
+            at.w[i] = (const uint8_t*)gp.B + n * (K / 2);
+            at.ws[i] = (const uint8_t*)gp.Bs + n * (K / 32);
         }
         const uint8_t *codes = nullptr, *scales = nullptr;
         if constexpr (FUSED) {
@@ -364,15 +493,18 @@ struct MxStream {
                 at.as[i] = (const uint8_t*)gp.As + m * (K / 32);
             }
         }
-        f32x4 acc[MT];
+        f32x4 acc[NT][MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-            acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const int whole = K / RUN, rest = K % RUN / 128;  // runs, and steps of a partial one
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                acc[n][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        // whole runs w, w + NW, ...; the steps of a partial one go to the waves after
+        const int whole = K / RUN, rest = K % RUN / 128;
         Run R;
         int r = w;
         if (r < whole)
-            load(R, at, r * RUN, 2, g);
+            load(R, at, r * RUN, true, g);
         if constexpr (FUSED) {
             quantise(p, mx_lds, mx_lds + gp.M * code_row(K));
             __syncthreads();
@@ -381,30 +513,38 @@ struct MxStream {
             const int next = r + NW;
             Run S = R;
             if (next < whole)
-                load(R, at, next * RUN, 2, g);
+                load(R, at, next * RUN, true, g);
             __builtin_amdgcn_sched_barrier(0);
-            multiply(acc, S, codes, scales, r * RUN, 2, g);
+            multiply(acc, S, codes, scales, r * RUN, true, g);
             r = next;
         }
-        if (rest > 0 && w == whole % NW) {
-            load(R, at, whole * RUN, 1, g);
-            multiply(acc, R, codes, scales, whole * RUN, 1, g);
+        if constexpr (ST > 1) {
+            const int step = (w - whole % NW + NW) % NW;
+            if (step < rest) {
+                load(R, at, whole * RUN + 128 * step, false, g);
+                multiply(acc, R, codes, scales, whole * RUN + 128 * step, false, g);
+            }
         }
         float* red = (float*)mx_lds;
         if constexpr (FUSED)
             __syncthreads();  // the codes' last reads
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-            *(f32x4*)&red[(w * MT + m) * 256 + lane * 4] = acc[m];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                *(f32x4*)&red[((w * NT + n) * MT + m) * 256 + lane * 4] = acc[n][m];
         __syncthreads();
-        for (int o = tid; o < MT * 256; o += NW * 64) {
+        // element e of lane l: token l % 16, row 4 (l / 16) + e of its block; threads
+        // go along the rows
+        for (int o = tid; o < NT * MT * 256; o += NW * 64) {
+            const int nr = o % ROWS, mr = o / ROWS;
+            const int at_r = ((nr >> 4) * MT + (mr >> 4)) * 256 +
+                             (((nr & 15) >> 2) * 16 + (mr & 15)) * 4 + (nr & 3);
             float s = 0.0f;
 #pragma unroll
             for (int v = 0; v < NW; ++v)
-                s += red[v * MT * 256 + o];
-            const int l = (o >> 2) & 63;
-            const int m = m0 + 16 * (o >> 8) + (l & 15);
-            const int n = n0 + 4 * (l >> 4) + (o & 3);
+                s += red[v * NT * MT * 256 + at_r];
+            const int m = m0 + mr, n = n0 + nr;
             if (m < gp.M && n < gp.N) {
                 const float v = mx_result(s, p.l.bias ? p.l.bias[n] : 0.0f, gp.relu);
                 const int64_t c = (int64_t)m * p.l.ldc + n;
@@ -417,35 +557,13 @@ struct MxStream {
     }
 };
 
-template <int DTX, int AFMT, int MT, int NW, bool FUSED>
+template <int DTX, int AFMT, int NT, int MT, int ST, int NW, bool FUSED>
 __global__ __attribute__((amdgpu_flat_work_group_size(NW * 64, NW * 64))) void
 mx_stream_kernel(MxStreamParams p)
 {
     const ClockStamp clk = stamp_begin(p.l.g);
-    MxStream<DTX, AFMT, MT, NW, FUSED>::run(p);
+    MxStream<DTX, AFMT, NT, MT, ST, NW, FUSED>::run(p);
     stamp_end(p.l.g, clk);
-}
-
-// C = epilogue(bias) where K is 0.
-struct MxFillParams {
-    const float* bias;
-    void* C;
-    int64_t ldc;
-    int M, N, dt, relu;
-};
-
-__global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void
-mx_fill_kernel(MxFillParams p)
-{
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)p.M * p.N)
-        return;
-    const int64_t m = i / p.N, n = i - m * p.N;
-    const float v = mx_result(0.0f, p.bias ? p.bias[n] : 0.0f, p.relu);
-    if (p.dt == DT_F32)
-        ((float*)p.C)[m * p.ldc + n] = v;
-    else
-        ((uint16_t*)p.C)[m * p.ldc + n] = cvt1(v, p.dt);
 }
 
 }  // namespace tg

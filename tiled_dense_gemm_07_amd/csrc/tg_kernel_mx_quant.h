@@ -416,4 +416,26 @@ mx_dequant_kernel(MxDequantParams p)
     }
 }
 
+// C = epilogue(bias) where K is 0.
+struct MxFillParams {
+    const float* bias;
+    void* C;
+    int64_t ldc;
+    int M, N, dt, relu;
+};
+
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void
+mx_fill_kernel(MxFillParams p)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)p.M * p.N)
+        return;
+    const int64_t m = i / p.N, n = i - m * p.N;
+    const float v = mx_result(0.0f, p.bias ? p.bias[n] : 0.0f, p.relu);
+    if (p.dt == DT_F32)
+        ((float*)p.C)[m * p.ldc + n] = v;
+    else
+        ((uint16_t*)p.C)[m * p.ldc + n] = cvt1(v, p.dt);
+}
+
 }  // namespace tg

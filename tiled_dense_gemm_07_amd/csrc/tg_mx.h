@@ -152,4 +152,11 @@ __device__ __forceinline__ u32x2 mx_codes(const Raw8<DT>& r, u32& byte)
     return s.ok ? w : u32x2{0u, 0u};
 }
 
+// A sum of products to the layer's result.
+__device__ __forceinline__ float mx_result(float v, float bias, int relu)
+{
+    v += bias;
+    return (relu && !(v > 0.0f)) ? 0.0f : v;
+}
+
 }  // namespace tg

@@ -7,6 +7,7 @@
 #include "tg_host.h"
 #include "tg_kernel_mx_linear.h"
 #include "tg_kernel_mx_quant.h"
+#include "tg_mx_kernels.h"
 
 namespace {
 
@@ -106,70 +107,35 @@ tg_status launch_quant(int64_t M, int64_t K, int dt, const void* X, int64_t ldx,
 // --------------------------------------------------------------------------
 // Product of two matrices of blocks.
 // --------------------------------------------------------------------------
-struct Tile {
-    const char* name;
-    const void* kernel[3];  // by C's type
-    int bm, bn, threads, strip;  // K has to be a multiple of strip
-    float t0, one, full;
-    int per_cu;
-};
+using tg::MxKernel;
 
-#define TG_MX_TILE(MX2, AFMT, BM, BN, WGM, WGN, NS, STRIP, PER_CU, T0, ONE, FULL)                 \
-    {                                                                                             \
-        "mx_linear_" #AFMT "_" #BM "x" #BN "_w" #WGM "x" #WGN "_s" #NS "_k" #STRIP,               \
-            {(const void*)&tg::mx_linear_kernel<MX2, tg::DT_F32, tg::AFMT, BM, BN, WGM, WGN, NS>, \
-             (const void*)&tg::mx_linear_kernel<MX2, tg::DT_F16, tg::AFMT, BM, BN, WGM, WGN, NS>, \
-             (const void*)&tg::mx_linear_kernel<MX2, tg::DT_BF16, tg::AFMT, BM, BN, WGM, WGN,     \
-                                                NS>},                                             \
-            BM, BN, WGM* WGN * 64, STRIP, T0, ONE, FULL, PER_CU                                   \
-    }
-
-const Tile kTiles2[] = {
-    TG_MX_TILE(false, MX_E2M1, 64, 64, 2, 2, 4, 128, 2, 3.3f, 0.2f, 0.4f),
-    TG_MX_TILE(false, MX_E2M1, 128, 128, 2, 2, 4, 128, 1, 3.5f, 0.3f, 0.6f),
-    TG_MX_TILE(false, MX_E2M1, 256, 256, 2, 4, 4, 128, 1, 6.0f, 0.8f, 0.9f),
-    TG_MX_TILE(true, MX_E2M1, 256, 256, 2, 4, 2, 1024, 1, 6.0f, 0.7f, 0.8f),
-};
-const Tile kTiles4[] = {
-    TG_MX_TILE(false, MX_E4M3, 64, 64, 2, 2, 4, 128, 2, 3.3f, 0.2f, 0.4f),
-    TG_MX_TILE(false, MX_E4M3, 128, 128, 2, 2, 4, 128, 1, 3.5f, 0.35f, 0.7f),
-    TG_MX_TILE(false, MX_E4M3, 256, 256, 2, 4, 3, 128, 1, 6.0f, 1.1f, 1.2f),
-    TG_MX_TILE(true, MX_E4M3, 128, 256, 2, 2, 2, 1024, 1, 6.0f, 0.6f, 0.7f),
-};
-
-float tile_cost(const Tile& t, int64_t M, int64_t N, int64_t K)
+float kernel_cost(const MxKernel& k, int64_t M, int64_t N, int64_t K)
 {
-    const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
-    return t.t0 + (float)(K / 128) *
-                      (tiles <= 256 ? t.one : t.full * (float)ceil_div(tiles, 256 * t.per_cu));
+    const int64_t groups = ceil_div(M, k.bm) * ceil_div(N, k.bn);
+    const float strips = (float)(K / 128);
+    return k.t0 + (groups <= 256 ? strips * k.one
+                                 : (float)ceil_div(groups, 256 * k.per_cu) *
+                                       (k.round + strips * k.full));
 }
 
-const Tile* pick_tile(int64_t M, int64_t N, int64_t K, int fmt)
+// The cheapest; up to 16 tokens among the streaming kernels (1 x 14336 x 4096 in E4M3
+// 10.2 us, 15.5 with 64 x 64 tiles), above 256 among the tiles.
+const MxKernel* pick_kernel(int64_t M, int64_t N, int64_t K, int fmt)
 {
-    const Tile* best = nullptr;
+    const MxKernel* best = nullptr;
     float cost = 0.0f;
-    for (const Tile& t : fmt == TG_MX_E4M3 ? kTiles4 : kTiles2) {
-        if (K % t.strip != 0)
+    const tg::MxKernels all =
+        fmt == TG_MX_E4M3 ? tg::mx_kernels_e4m3() : tg::mx_kernels_e2m1();
+    for (const MxKernel* k = all.begin; k != all.end; ++k) {
+        if (K % k->strip != 0 || (k->lds ? M > 256 : M <= 16))
             continue;
-        const float c = tile_cost(t, M, N, K);
+        const float c = kernel_cost(*k, M, N, K);
         if (!best || c < cost) {
-            best = &t;
+            best = k;
             cost = c;
         }
     }
     return best;
-}
-
-template <int DTX, bool FUSED>
-const void* stream_kernel(int fmt, int mt)
-{
-    if (fmt == TG_MX_E4M3)
-        return mt == 2 && !FUSED
-                   ? (const void*)&tg::mx_stream_kernel<DTX, tg::MX_E4M3, FUSED ? 1 : 2, 8, FUSED>
-                   : (const void*)&tg::mx_stream_kernel<DTX, tg::MX_E4M3, 1, 8, FUSED>;
-    return mt == 2 && !FUSED
-               ? (const void*)&tg::mx_stream_kernel<DTX, tg::MX_E2M1, FUSED ? 1 : 2, 8, FUSED>
-               : (const void*)&tg::mx_stream_kernel<DTX, tg::MX_E2M1, 1, 8, FUSED>;
 }
 
 struct Product {
@@ -203,22 +169,19 @@ tg::MxLinearParams product_params(const Product& q)
 tg_status launch_product(const Product& q, hipStream_t stream)
 {
     tg::MxLinearParams p = product_params(q);
-    if (q.M <= 32) {
-        const int mt = q.M <= 16 ? 1 : 2;
+    const MxKernel* k = pick_kernel(q.M, q.N, q.K, q.fmt);
+    const int64_t tm = ceil_div(q.M, k->bm), tn = ceil_div(q.N, k->bn);
+    if (k->lds) {
         tg::MxStreamParams s{p, q.dt, nullptr, 0, 0};
-        return tg::launch_kernel(stream_kernel<tg::DT_F32, false>(q.fmt, mt), ceil_div(q.N, 16),
-                                 ceil_div(q.M, 16 * mt), 512, &s, stream, "mx_stream",
-                                 8 * mt * 1024);
+        return tg::launch_kernel(k->kernel[0], tn, tm, k->threads, &s, stream, k->name, k->lds);
     }
-    const Tile* t = pick_tile(q.M, q.N, q.K, q.fmt);
     const int es = tg::dtype_size(q.dt);
     p.g.group_m = tg::swizzle_override() > 0 ? tg::swizzle_override() : 4;
-    p.g.tiles_m = (int)ceil_div(q.M, t->bm);
-    p.g.tiles_n = (int)ceil_div(q.N, t->bn);
+    p.g.tiles_m = (int)tm;
+    p.g.tiles_n = (int)tn;
     p.g.c_vec = ((uintptr_t)q.C & 15) == 0 && q.ldc * es % 16 == 0 && q.N * es % 16 == 0 &&
                 32 * q.ldc * es <= kMaxDim;
-    return tg::launch_kernel(t->kernel[q.dt], (int64_t)p.g.tiles_m * p.g.tiles_n, 1, t->threads, &p,
-                             stream, t->name);
+    return tg::launch_kernel(k->kernel[q.dt], tm * tn, 1, k->threads, &p, stream, k->name);
 }
 
 tg_status launch_fill(int64_t M, int64_t N, int dt, const float* bias, void* C, int64_t ldc,
@@ -235,12 +198,19 @@ tg_status launch_fill(int64_t M, int64_t N, int dt, const float* bias, void* C, 
 // The linear layer.
 // --------------------------------------------------------------------------
 // In one launch: a few tokens, whose quantisation in every workgroup takes less
-// than a launch of its own would.
-bool fused_linear(int64_t M, int64_t K) { return M <= 8 && K > 0 && M * K <= 16384; }
+// than a launch of its own would.  Measured with both launches and with one: 1 x 1024
+// x 1024 4.2 us and 2.9, 8 x 4096 x 1024 4.7 and 3.4, 8 x 2048 x 2048 5.2 and 4.0, 4 x
+// 8192 x 8192 15.0 and 13.6, 8 x 4096 x 4096 7.3 and 7.0, 6 x 1024 x 8192 8.1 and 9.3;
+// with more than two workgroups to a compute unit half as much: 4 x 14336 x 4096 12.5
+// and 11.8, 6 x 14336 x 4096 12.3 and 13.7.
+bool fused_linear(int64_t M, int64_t N, int64_t K)
+{
+    return M <= 16 && K > 0 && M * K <= (N <= 8192 ? 32768 : 16384);
+}
 
 size_t linear_bytes(int64_t M, int64_t N, int64_t K, int fmt)
 {
-    if (M == 0 || N == 0 || K == 0 || fused_linear(M, K))
+    if (M == 0 || N == 0 || K == 0 || fused_linear(M, N, K))
         return 0;
     const int64_t Kp = mx_padded(K);
     return (size_t)(ceil_div(M * (Kp / 32), 256) * 256 + M * code_bytes(fmt, Kp));
@@ -409,15 +379,14 @@ tg_status tg_linear_mx(int64_t M, int64_t N, int64_t K, tg_dtype dtype, const vo
     if (K == 0)
         return launch_fill(M, N, dtype, bias, C, ldc, relu, hs);
     Product q{M, N, Kp, fmt, dtype, nullptr, nullptr, Wq, Ws, bias, C, ldc, relu};
-    if (fused_linear(M, K)) {
+    if (fused_linear(M, N, K)) {
         tg::MxStreamParams s{product_params(q), (int)dtype, X, ldx, (int)K};
-        const void* k = dtype == TG_F32   ? stream_kernel<tg::DT_F32, true>(fmt, 1)
-                        : dtype == TG_F16 ? stream_kernel<tg::DT_F16, true>(fmt, 1)
-                                          : stream_kernel<tg::DT_BF16, true>(fmt, 1);
-        const int lds =
-            fmt == TG_MX_E4M3
-                ? tg::MxStream<tg::DT_F32, tg::MX_E4M3, 1, 8, true>::lds_bytes((int)M, (int)Kp)
-                : tg::MxStream<tg::DT_F32, tg::MX_E2M1, 1, 8, true>::lds_bytes((int)M, (int)Kp);
+        int lds = 0;
+        const void* k = by_type(dtype, fmt, [&](auto D, auto F) {
+            constexpr int DT = decltype(D)::value, FMT = decltype(F)::value;
+            lds = tg::MxStream<DT, FMT, 1, 1, 2, 8, true>::lds_bytes((int)M, (int)Kp);
+            return (const void*)&tg::mx_stream_kernel<DT, FMT, 1, 1, 2, 8, true>;
+        });
         return tg::launch_kernel(k, ceil_div(N, 16), 1, 512, &s, hs, "mx_linear_stream",
                                  (unsigned)lds);
     }
