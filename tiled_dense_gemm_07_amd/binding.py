@@ -1143,20 +1143,32 @@ def _heads_args(q, k, w_q, w_k, cos, sin, positions, eps, interleaved):
     if len(shape) != 3:
         raise ValueError("q must be [tokens, heads, values], got %s" % (tuple(shape),))
     T, Hq, D = shape
-    at_q, at_k, kshape = _heads("q", q, shape, dtype), (0, 0, 0), (T, 0, D)
+    q_t, q_h, unit = q.stride()
+    if unit != 1 and D > 1:
+        raise ValueError("q must have unit stride along a head")
+    at_k, Hk = (0, 0, 0), 0
     if k is not None:
         if k.dim() != 3:
             raise ValueError("k must be [tokens, heads, values], got %s" % (tuple(k.shape),))
-        kshape = (T, k.shape[1], D)
-        at_k = _heads("k", k, kshape, dtype)
+        Hk = k.shape[1]
+        at_k = _heads("k", k, (T, Hk, D), dtype)
     elif w_k is not None:
         raise ValueError("w_k without k")
-    R = P = pc = ps = 0
+    pq = pk = 0
+    if w_q is not None:
+        if w_q.dtype != dtype or w_q.shape != (D,) or not w_q.is_contiguous():
+            raise ValueError("w_q must be a dense vector of %d values of %s" % (D, dtype))
+        pq = w_q.data_ptr()
+    if w_k is not None:
+        if w_k.dtype != dtype or w_k.shape != (D,) or not w_k.is_contiguous():
+            raise ValueError("w_k must be a dense vector of %d values of %s" % (D, dtype))
+        pk = w_k.data_ptr()
+    R = P = pc = ps = pp = 0
     if cos is not None and sin is not None:
-        size = cos.shape
+        size, f32 = cos.shape, torch.float32
         if len(size) != 2 or sin.shape != size or not (cos.is_contiguous() and sin.is_contiguous()):
             raise ValueError("cos and sin must be dense tensors [positions, pairs]")
-        if cos.dtype != torch.float32 or sin.dtype != torch.float32:
+        if cos.dtype != f32 or sin.dtype != f32:
             raise TypeError("cos and sin must be torch.float32, got %s and %s"
                             % (cos.dtype, sin.dtype))
         P, R = size[0], 2 * size[1]
@@ -1167,12 +1179,14 @@ def _heads_args(q, k, w_q, w_k, cos, sin, positions, eps, interleaved):
         pc, ps = cos.data_ptr(), sin.data_ptr()
     elif cos is not None or sin is not None:
         raise ValueError("cos and sin go together")
-    return shape, kshape, (
-        T, Hq, kshape[1], D, R, _dtype_code(q), *at_q, *at_k,
-        0 if w_q is None else _vector("w_q", w_q, D, dtype),
-        0 if w_k is None else _vector("w_k", w_k, D, dtype), pc, ps, P,
-        0 if positions is None else _vector("positions", positions, T, torch.int64), eps,
-        bool(interleaved))
+    if positions is not None:
+        if positions.dtype != torch.int64:
+            raise TypeError("positions must be torch.int64, got %s" % positions.dtype)
+        if positions.shape != (T,) or not positions.is_contiguous():
+            raise ValueError("positions must be a dense vector of %d values" % T)
+        pp = positions.data_ptr()
+    return shape, (T, Hk, D), (T, Hq, Hk, D, R, _dtype_code(q), q.data_ptr(), q_t, q_h, *at_k, pq,
+                               pk, pc, ps, P, pp, eps, bool(interleaved))
 
 
 def head_norm_rope(q, k=None, w_q=None, w_k=None, cos=None, sin=None, positions=None, eps=1e-6,
@@ -1186,18 +1200,22 @@ def head_norm_rope(q, k=None, w_q=None, w_k=None, cos=None, sin=None, positions=
     Returns a HeadNormRope(q, k)."""
     _same_device(q, k, w_q, w_k, cos, sin, positions, q_out, k_out)
     qs, ks, args = _heads_args(q, k, w_q, w_k, cos, sin, positions, eps, interleaved)
-    dtype = q.dtype
+    dtype, D = q.dtype, qs[2]
+    at_k = (0, 0, 0)
     if q_out is None:
         q_out = _empty(qs, dtype, q, stream)
-    at_k = (0, 0, 0)
+        at_q = (q_out.data_ptr(), qs[1] * D, D)
+    else:
+        at_q = _heads("q_out", q_out, qs, dtype)
     if k is not None:
         if k_out is None:
             k_out = _empty(ks, dtype, q, stream)
-        at_k = _heads("k_out", k_out, ks, dtype)
+            at_k = (k_out.data_ptr(), ks[1] * D, D)
+        else:
+            at_k = _heads("k_out", k_out, ks, dtype)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _call(q, load_library().tg_head_norm_rope,
-          _HEADS_ARGS.pack(*args, *_heads("q_out", q_out, qs, dtype), *at_k), stream)
+    _call(q, load_library().tg_head_norm_rope, _HEADS_ARGS.pack(*args, *at_q, *at_k), stream)
     return HeadNormRope(q_out, k_out)
 
 

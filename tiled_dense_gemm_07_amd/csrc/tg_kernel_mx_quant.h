@@ -168,16 +168,16 @@ __device__ __forceinline__ u32x2 mx_column_codes(const MxLane<DT>* x, int j, con
     return s.ok ? w : u32x2{0u, 0u};
 }
 
+// Workgroup `block` of p's tiles_m x tiles_n.
 template <int DT, int FMT, bool ROWS, bool COLS, bool SUMS>
-__global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void
-mx_columns_kernel(MxQuantParams p)
+__device__ __forceinline__ void mx_columns(const MxQuantParams& p, int block)
 {
     using Lane = MxLane<DT>;
     constexpr int V = 4, CL = 16, TC = CL * V;  // a wave's columns
     constexpr int ES = Lane::ES;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const TileCoord tc = tile_of((int)blockIdx.x, p.tiles_m, p.tiles_n, 1);
+    const TileCoord tc = tile_of(block, p.tiles_m, p.tiles_n, 1);
     const int m0 = tc.m * 256 + (w >> 1) * 128;
     const int c0 = tc.n * 2 * TC + (w & 1) * TC;
     if (m0 >= p.Mp || c0 >= p.Kp)
@@ -318,17 +318,23 @@ mx_columns_kernel(MxQuantParams p)
     }
 }
 
-// Sums of the columns' partial sums, in order.
+template <int DT, int FMT, bool ROWS, bool COLS, bool SUMS>
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void
+mx_columns_kernel(MxQuantParams p)
+{
+    mx_columns<DT, FMT, ROWS, COLS, SUMS>(p, (int)blockIdx.x);
+}
+
+// Sums of the columns' partial sums, in order, 256 to a workgroup.
 struct MxSumParams {
     const float* part;  // [parts][K]
     float* out;         // [K]
     int parts, K;
 };
 
-__global__ __attribute__((amdgpu_flat_work_group_size(64, 64))) void
-mx_sums_kernel(MxSumParams p)
+__device__ __forceinline__ void mx_sums(const MxSumParams& p, int block)
 {
-    const int k = (int)(blockIdx.x * 64 + threadIdx.x);
+    const int k = block * 256 + (int)threadIdx.x;
     if (k >= p.K)
         return;
     float s = 0.0f;
@@ -346,6 +352,27 @@ mx_sums_kernel(MxSumParams p)
     for (; i < p.parts; ++i)
         s += at[(int64_t)i * p.K];
     p.out[k] = s;
+}
+
+// The rest of a backward pass' quantisation in one launch: the columns of two
+// matrices to E2M1 (workgroups up to end[0] and up to end[1]), and the sums of the
+// columns of a third that an earlier launch left in parts.
+struct MxRestParams {
+    MxQuantParams q[2];
+    MxSumParams sums;
+    int end[2];
+};
+
+template <int DT>
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void
+mx_rest_kernel(MxRestParams p)
+{
+    const int b = (int)blockIdx.x;
+    if (b < p.end[1])
+        mx_columns<DT, MX_E2M1, false, true, false>(b < p.end[0] ? p.q[0] : p.q[1],
+                                                    b < p.end[0] ? b : b - p.end[0]);
+    else
+        mx_sums(p.sums, b - p.end[1]);
 }
 
 struct MxDequantParams {

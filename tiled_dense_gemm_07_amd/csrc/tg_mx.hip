@@ -54,7 +54,7 @@ constexpr int kUnits = 2;  // of a thread, in flight together
 tg::u32 unit_magic(int64_t Kp)
 {
     const uint64_t per = (uint64_t)Kp / 8;
-    return per >= 256 * kUnits ? 0 : (tg::u32)((((uint64_t)1 << 32) + per - 1) / per);
+    return per == 0 || per >= 256 * kUnits ? 0 : (tg::u32)((((uint64_t)1 << 32) + per - 1) / per);
 }
 
 const void* columns_kernel(int dt, int fmt, bool rows, bool cols, bool sums)
@@ -74,9 +74,8 @@ const void* columns_kernel(int dt, int fmt, bool rows, bool cols, bool sums)
 
 // Blocks along the rows (Q), the columns (Qt), or both from one read; sums: the
 // columns' sums over each 128 rows.
-tg_status launch_quant(int64_t M, int64_t K, int dt, const void* X, int64_t ldx, int fmt,
-                       uint8_t* Q, uint8_t* S, uint8_t* Qt, uint8_t* St, float* sums,
-                       hipStream_t stream)
+tg::MxQuantParams quant_params(int64_t M, int64_t K, const void* X, int64_t ldx, uint8_t* Q,
+                               uint8_t* S, uint8_t* Qt, uint8_t* St, float* sums)
 {
     tg::MxQuantParams p{};
     p.X = X;
@@ -91,17 +90,44 @@ tg_status launch_quant(int64_t M, int64_t K, int dt, const void* X, int64_t ldx,
     p.St = St;
     p.sums = sums;
     p.magic = unit_magic(p.Kp);
-    if (!Qt && !sums) {
+    p.tiles_m = (int)ceil_div(p.Mp, 256);
+    p.tiles_n = (int)ceil_div(K, 128);
+    return p;
+}
+
+tg_status launch_quant(tg::MxQuantParams p, int dt, int fmt, hipStream_t stream)
+{
+    if (!p.Qt && !p.sums) {
         const void* k = by_type(dt, fmt, [](auto D, auto F) {
             return (const void*)&tg::mx_rows_kernel<decltype(D)::value, decltype(F)::value, kUnits>;
         });
-        return tg::launch_kernel(k, ceil_div(M * (p.Kp / 8), 256 * kUnits), 1, 256, &p, stream,
-                                 "mx_rows");
+        return tg::launch_kernel(k, ceil_div((int64_t)p.M * (p.Kp / 8), 256 * kUnits), 1, 256, &p,
+                                 stream, "mx_rows");
     }
-    p.tiles_m = (int)ceil_div(p.Mp, 256);
-    p.tiles_n = (int)ceil_div(K, 128);
-    return tg::launch_kernel(columns_kernel(dt, fmt, Q != nullptr, Qt != nullptr, sums != nullptr),
+    return tg::launch_kernel(columns_kernel(dt, fmt, p.Q != nullptr, p.Qt != nullptr,
+                                            p.sums != nullptr),
                              (int64_t)p.tiles_m * p.tiles_n, 1, 256, &p, stream, "mx_columns");
+}
+
+// Columns of up to two matrices of one type to E2M1 (those with Qt), and the sums
+// (those with an output).
+tg_status launch_rest(const tg::MxQuantParams& a, const tg::MxQuantParams& b,
+                      const tg::MxSumParams& sums, int dt, hipStream_t stream)
+{
+    const auto groups = [](const tg::MxQuantParams& q) {
+        return q.Qt ? (int64_t)q.tiles_m * q.tiles_n : 0;
+    };
+    const int64_t e0 = groups(a), e1 = e0 + groups(b),
+                  all = e1 + (sums.out ? ceil_div(sums.K, 256) : 0);
+    if (all == 0)
+        return TG_OK;
+    if (all > kMaxDim)
+        return TG_ERR_BAD_SHAPE;
+    tg::MxRestParams p{{a, b}, sums, {(int)e0, (int)e1}};
+    const void* k = dt == TG_F32   ? (const void*)&tg::mx_rest_kernel<tg::DT_F32>
+                    : dt == TG_F16 ? (const void*)&tg::mx_rest_kernel<tg::DT_F16>
+                                   : (const void*)&tg::mx_rest_kernel<tg::DT_BF16>;
+    return tg::launch_kernel(k, all, 1, 256, &p, stream, "mx_rest");
 }
 
 // --------------------------------------------------------------------------
@@ -305,7 +331,8 @@ tg_status tg_quant_mx(int64_t M, int64_t K, tg_dtype dtype, const void* X, int64
             if (overlap(out[o], out[i]))
                 return TG_ERR_ALIAS;
     }
-    return launch_quant(M, K, dtype, X, ldx, fmt, Q, S, Qt, St, nullptr, (hipStream_t)stream);
+    return launch_quant(quant_params(M, K, X, ldx, Q, S, Qt, St, nullptr), dtype, fmt,
+                        (hipStream_t)stream);
 }
 
 tg_status tg_dequant_mx(int64_t M, int64_t K, tg_mx_format fmt, const uint8_t* Q, const uint8_t* S,
@@ -392,7 +419,8 @@ tg_status tg_linear_mx(int64_t M, int64_t N, int64_t K, tg_dtype dtype, const vo
     }
     uint8_t* As = (uint8_t*)workspace;
     uint8_t* A = As + ceil_div(M * (Kp / 32), 256) * 256;
-    if (tg_status s = launch_quant(M, K, dtype, X, ldx, fmt, A, As, nullptr, nullptr, nullptr, hs))
+    if (tg_status s = launch_quant(quant_params(M, K, X, ldx, A, As, nullptr, nullptr, nullptr),
+                                   dtype, fmt, hs))
         return s;
     q.A = A;
     q.As = As;
@@ -442,16 +470,26 @@ tg_status tg_linear_mx_backward(const tg_linear_mx_grad_args* a, void* workspace
     const hipStream_t hs = (hipStream_t)stream;
     uint8_t* ws = (uint8_t*)workspace;
     if (g.dx || g.dw || g.db) {
-        if (tg_status s = launch_quant(M, N, a->dtype, a->dY, a->lddy, a->fmt,
-                                       g.dx ? ws + g.dy : nullptr, g.dx ? ws + g.dys : nullptr,
-                                       g.dw ? ws + g.dyt : nullptr, g.dw ? ws + g.dyts : nullptr,
-                                       g.db ? (float*)(ws + g.sums) : nullptr, hs))
+        const auto at = [ws](bool wanted, int64_t o) { return wanted ? ws + o : nullptr; };
+        if (tg_status s = launch_quant(
+                quant_params(M, N, a->dY, a->lddy, at(g.dx, g.dy), at(g.dx, g.dys),
+                             at(g.dw, g.dyt), at(g.dw, g.dyts), (float*)at(g.db, g.sums)),
+                a->dtype, a->fmt, hs))
             return s;
+        const tg::MxQuantParams w = quant_params(N, K, a->W, a->ldw, nullptr, nullptr,
+                                                 at(g.dx, g.wt), at(g.dx, g.wts), nullptr),
+                                x = quant_params(M, K, a->X, a->ldx, nullptr, nullptr,
+                                                 at(g.dw, g.xt), at(g.dw, g.xts), nullptr);
+        const tg::MxSumParams sums{(const float*)(ws + g.sums), g.db ? a->dbias : nullptr,
+                                   (int)(g.Mp / 128), (int)N};
+        const bool one = a->wtype == a->dtype;
+        if (tg_status s = launch_rest(one ? w : tg::MxQuantParams{}, x, sums, a->dtype, hs))
+            return s;
+        if (!one)
+            if (tg_status s = launch_rest(w, {}, {}, a->wtype, hs))
+                return s;
     }
     if (g.dx) {
-        if (tg_status s = launch_quant(N, K, a->wtype, a->W, a->ldw, TG_MX_E2M1, nullptr, nullptr,
-                                       ws + g.wt, ws + g.wts, nullptr, hs))
-            return s;
         const Product q{M,          K,          g.Np,        a->fmt,  a->dtype, ws + g.dy,
                         ws + g.dys, ws + g.wt,  ws + g.wts,  nullptr, a->dX,    a->lddx,
                         false};
@@ -462,9 +500,6 @@ tg_status tg_linear_mx_backward(const tg_linear_mx_grad_args* a, void* workspace
             return s;
     }
     if (g.dw) {
-        if (tg_status s = launch_quant(M, K, a->dtype, a->X, a->ldx, TG_MX_E2M1, nullptr, nullptr,
-                                       ws + g.xt, ws + g.xts, nullptr, hs))
-            return s;
         const Product q{N,           K,          g.Mp,        a->fmt,  a->wtype, ws + g.dyt,
                         ws + g.dyts, ws + g.xt,  ws + g.xts,  nullptr, a->dW,    a->lddw,
                         false};
@@ -474,12 +509,7 @@ tg_status tg_linear_mx_backward(const tg_linear_mx_grad_args* a, void* workspace
         if (tg_status s = launch_fill(N, K, a->wtype, nullptr, a->dW, a->lddw, false, hs))
             return s;
     }
-    if (g.db) {
-        tg::MxSumParams p{(const float*)(ws + g.sums), a->dbias, (int)(g.Mp / 128), (int)N};
-        return tg::launch_kernel((const void*)&tg::mx_sums_kernel, ceil_div(N, 64), 1, 64, &p, hs,
-                                 "mx_sums");
-    }
-    return a->dbias ? launch_fill(1, N, TG_F32, nullptr, a->dbias, N, false, hs) : TG_OK;
+    return a->dbias && !g.db ? launch_fill(1, N, TG_F32, nullptr, a->dbias, N, false, hs) : TG_OK;
 }
 
 }  // extern "C"
