@@ -4,13 +4,14 @@
 // a block.
 //
 // mx_columns_kernel: blocks along the columns, written as rows of the transpose,
-// and on request those along the rows from the same read.  A lane holds 32 rows of
-// four columns in registers, so that no value crosses lanes: its codes of a column
-// are 16 or 32 consecutive bytes of the transpose, and its part of a row an eighth
-// of that row's block, whose largest magnitude is found over 8 lanes.  A wave takes
-// 128 rows (four lanes down) by 64 columns (16 lanes across); the four waves of a
-// workgroup two by two, and neighbouring workgroups stay on one XCD, whose L2 joins
-// their parts of cache lines.
+// in tiles of 256 rows by 128 columns.  A lane holds 32 rows of four columns in
+// registers, so that no value crosses lanes: its codes of a column are 16 or 32
+// consecutive bytes of the transpose.  A wave takes 128 rows (four lanes down) by 64
+// columns (16 lanes across); the four waves of a workgroup two by two.  Neighbouring
+// workgroups stay on one XCD, whose L2 joins their parts of cache lines.  Blocks along
+// both: every other workgroup takes the rows of the tile whose columns the one
+// beside it takes, from the same L2 (one workgroup for both, each value loaded once:
+// 512 x 512 bf16 7.1 us and 4.6, 2048 x 4096 10.5 and 9.3, 8192 x 8192 54.6 and 55.6).
 #pragma once
 
 #include "tg_mx.h"
@@ -168,18 +169,80 @@ __device__ __forceinline__ u32x2 mx_column_codes(const MxLane<DT>* x, int j, con
     return s.ok ? w : u32x2{0u, 0u};
 }
 
-// Workgroup `block` of p's tiles_m x tiles_n.
-template <int DT, int FMT, bool ROWS, bool COLS, bool SUMS>
-__device__ __forceinline__ void mx_columns(const MxQuantParams& p, int block)
+// The rows of one tile of 256 rows by 128 columns, eight elements to a lane.
+template <int DT, int FMT>
+__device__ __forceinline__ void mx_tile_rows(const MxQuantParams& p, int m0, int c0)
+{
+    using Lane = MxLane<DT>;
+    constexpr int ES = Lane::ES, U = 16;  // units of a thread
+    const int c = c0 + ((int)threadIdx.x & 15) * 8;
+    const int m = m0 + ((int)threadIdx.x >> 4);
+    Raw8<DT> r[U];
+    if (m0 + 256 <= p.M && c0 + 128 <= p.K) {
+        const char* at = (const char*)p.X + ((int64_t)m * p.ldx + c) * ES;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            load8<DT>(r[u], at + (int64_t)(16 * u) * p.ldx * ES, 0, 8);
+    } else {
+        // across an edge, in two halves, as mx_columns does
+        Lane h[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int row = m + 16 * u;
+            const char* at = (const char*)p.X + (int64_t)(row < p.M ? row : p.M - 1) * p.ldx * ES;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int k = c + 4 * i, over = k - (p.K - 4);
+                if (p.K >= 4)
+                    h[u][i].load(at + (int64_t)(over > 0 ? p.K - 4 : k) * ES);
+                else
+                    h[u][i].load_few(at, k == 0 ? p.K : 0);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int over = p.K >= 4 ? c + 4 * i - (p.K - 4) : 0;
+                h[u][i].drop(m + 16 * u < p.M ? (over < 0 ? 0 : (over < 4 ? over : 4)) : 4);
+#pragma unroll
+                for (int w = 0; w < Lane::NW; ++w) {
+                    if constexpr (DT == DT_F32)
+                        r[u].v[i][w] = h[u][i].v[w];
+                    else
+                        r[u].v[0][2 * i + w] = h[u][i].v[w];
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        u32 byte;
+        const u32x2 w = mx_codes<DT, FMT>(r[u], byte);
+        const int row = m + 16 * u;
+        if (row >= p.M)
+            continue;
+        const int64_t at = ((int64_t)row * p.Kp + c) / 8;
+        if constexpr (FMT == MX_E2M1)
+            ((u32*)p.Q)[at] = w[0];
+        else
+            ((u32x2*)p.Q)[at] = w;
+        if ((threadIdx.x & 3) == 0)
+            p.S[at / 4] = (uint8_t)byte;
+    }
+}
+
+// The columns of one tile of 256 rows by 128 columns.
+template <int DT, int FMT, bool COLS, bool SUMS>
+__device__ __forceinline__ void mx_tile_columns(const MxQuantParams& p, int tile_m, int tile_c)
 {
     using Lane = MxLane<DT>;
     constexpr int V = 4, CL = 16, TC = CL * V;  // a wave's columns
     constexpr int ES = Lane::ES;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const TileCoord tc = tile_of(block, p.tiles_m, p.tiles_n, 1);
-    const int m0 = tc.m * 256 + (w >> 1) * 128;
-    const int c0 = tc.n * 2 * TC + (w & 1) * TC;
+    const int m0 = tile_m + (w >> 1) * 128;
+    const int c0 = tile_c + (w & 1) * TC;
     if (m0 >= p.Mp || c0 >= p.Kp)
         return;  // whole waves, and no barrier follows
     const int cl = lane & (CL - 1), b = lane / CL;
@@ -261,60 +324,6 @@ __device__ __forceinline__ void mx_columns(const MxQuantParams& p, int block)
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        mx_repack(x);
-    }
-    if constexpr (ROWS) {
-        // Eight lanes hold a row's block.  Of E2M1 a lane's codes of two rows are
-        // half dwords: neighbours exchange them, so that each stores a whole one of
-        // one row.  Of eight rows' scales each of the eight lanes stores one.
-        const int odd = lane & 1, l8 = lane & 7;
-#pragma unroll
-        for (int i0 = 0; i0 < 32; i0 += 8) {
-            u32 byte = 0;
-#pragma unroll
-            for (int i = i0; i < i0 + 8; i += 2) {
-                u32 code[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const Lane& r = x[i + h];
-                    u32 t = 0;
-#pragma unroll
-                    for (int j = 0; j < Lane::NW; ++j)
-                        t = mx_max_word<DT>(t, r.v[j]);
-                    if constexpr (DT != DT_F32)
-                        t = MaxOp::of(mx_bits<DT>(t, false), mx_bits<DT>(t, true));
-                    MxScale s;
-                    s.of_amax<FMT>(mx_block_max<8>(t));
-                    byte = i + h - i0 == l8 ? s.byte : byte;
-                    if constexpr (FMT == MX_E4M3) {
-                        code[h] = mx_codes8(r.get(0), r.get(1), r.get(2), r.get(3), s.p);
-                    } else if constexpr (DT == DT_F32) {
-                        const float v[8] = {r.get(0), r.get(1), r.get(2), r.get(3), 0, 0, 0, 0};
-                        code[h] = mx_codes4(v, s.p) & 0xFFFFu;
-                    } else {
-                        code[h] = mx_codes4_16<DT>(r.v[0], r.v[1], 0u, 0u, s.p) & 0xFFFFu;
-                    }
-                    code[h] = s.ok ? code[h] : 0u;
-                }
-                if constexpr (FMT == MX_E4M3) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (m + i + h < p.M)
-                            *(u32*)(p.Q + (int64_t)(m + i + h) * p.Kp + c) = code[h];
-                } else {
-                    const u32 give = odd ? code[0] : code[1], keep = odd ? code[1] : code[0];
-                    const u32 got = dpp<0xB1>(give);
-                    const u32 word = odd ? got | keep << 16 : keep | got << 16;
-                    const int row = m + i + odd;
-                    if (row < p.M)
-                        *(u32*)(p.Q + ((int64_t)row * p.Kp + (c & ~7)) / 2) = word;
-                }
-            }
-            const int row = m + i0 + l8;
-            if (row < p.M)
-                p.S[((int64_t)row * p.Kp + c) / 32] = (uint8_t)byte;
-            __builtin_amdgcn_sched_barrier(0);
-        }
     }
 }
 
@@ -322,7 +331,14 @@ template <int DT, int FMT, bool ROWS, bool COLS, bool SUMS>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void
 mx_columns_kernel(MxQuantParams p)
 {
-    mx_columns<DT, FMT, ROWS, COLS, SUMS>(p, (int)blockIdx.x);
+    // ROWS: every other workgroup takes a tile's rows, the one beside it, on the same
+    // XCD, its columns
+    const TileCoord tc = tile_of((int)blockIdx.x, p.tiles_m, ROWS ? 2 * p.tiles_n : p.tiles_n, 1);
+    const int m0 = tc.m * 256, c0 = (ROWS ? tc.n >> 1 : tc.n) * 128;
+    if (ROWS && (tc.n & 1))
+        mx_tile_rows<DT, FMT>(p, m0, c0);
+    else
+        mx_tile_columns<DT, FMT, COLS, SUMS>(p, m0, c0);
 }
 
 // Sums of the columns' partial sums, in order, 256 to a workgroup.
@@ -368,11 +384,13 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void
 mx_rest_kernel(MxRestParams p)
 {
     const int b = (int)blockIdx.x;
-    if (b < p.end[1])
-        mx_columns<DT, MX_E2M1, false, true, false>(b < p.end[0] ? p.q[0] : p.q[1],
-                                                    b < p.end[0] ? b : b - p.end[0]);
-    else
+    if (b >= p.end[1]) {
         mx_sums(p.sums, b - p.end[1]);
+        return;
+    }
+    const MxQuantParams& q = b < p.end[0] ? p.q[0] : p.q[1];
+    const TileCoord tc = tile_of(b < p.end[0] ? b : b - p.end[0], q.tiles_m, q.tiles_n, 1);
+    mx_tile_columns<DT, MX_E2M1, true, false>(q, tc.m * 256, tc.n * 128);
 }
 
 struct MxDequantParams {

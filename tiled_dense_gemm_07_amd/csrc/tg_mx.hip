@@ -106,7 +106,8 @@ tg_status launch_quant(tg::MxQuantParams p, int dt, int fmt, hipStream_t stream)
     }
     return tg::launch_kernel(columns_kernel(dt, fmt, p.Q != nullptr, p.Qt != nullptr,
                                             p.sums != nullptr),
-                             (int64_t)p.tiles_m * p.tiles_n, 1, 256, &p, stream, "mx_columns");
+                             (p.Q ? 2 : 1) * (int64_t)p.tiles_m * p.tiles_n, 1, 256, &p, stream,
+                             "mx_columns");
 }
 
 // Columns of up to two matrices of one type to E2M1 (those with Qt), and the sums
