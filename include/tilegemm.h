@@ -511,8 +511,8 @@ tg_status tg_dequant_mx(int64_t M, int64_t K, tg_mx_format fmt, const uint8_t* Q
  *     concurrently.
  *   K == 0: C = epilogue(bias); X, Wq and Ws may be NULL then.
  * Errors: TG_ERR_BAD_DTYPE (also fmt), TG_ERR_BAD_EPILOGUE, TG_ERR_BAD_SHAPE
- *   (also a stride below its row length, K > 8388479), TG_ERR_NULL_POINTER,
- *   TG_ERR_NO_CONFIG (Wq not 16-byte or Ws not 4-byte aligned),
+ *   (also a stride below its row length, K > 8388479, M or N above 2^29 - 1),
+ *   TG_ERR_NULL_POINTER, TG_ERR_NO_CONFIG (Wq not 16-byte or Ws not 4-byte aligned),
  *   TG_ERR_WORKSPACE, TG_ERR_ALIAS (C or the workspace overlaps an operand or
  *   each other), TG_ERR_HIP.
  */

@@ -31,7 +31,8 @@ def case(T, Hq, Hk, D, R, dtype, seed=0, P=None):
     return q, k, wq, wk, cos, sin, pos
 
 
-SHAPES = [(1, 1, 0, 1, 0), (1, 1, 1, 2, 2), (3, 2, 1, 7, 4), (5, 3, 2, 16, 16), (1, 32, 8, 128, 128),
+SHAPES = [(4, 3, 1, 3, 2), (7, 2, 1, 4, 2), (7, 2, 1, 5, 4), (3, 3, 2, 30, 6), (5, 2, 2, 129, 10), (3, 2, 1, 515, 514),
+          (3, 2, 1, 1023, 6), (1, 1, 0, 1, 0), (1, 1, 1, 2, 2), (3, 2, 1, 7, 4), (5, 3, 2, 16, 16), (1, 32, 8, 128, 128),
           (2, 7, 3, 64, 64), (33, 5, 2, 80, 80), (20, 4, 4, 96, 32), (9, 9, 1, 99, 66),
           (17, 6, 2, 128, 64), (4, 3, 3, 127, 126), (6, 2, 2, 192, 64), (3, 2, 1, 256, 256),
           (2, 2, 2, 300, 100), (2, 3, 1, 512, 512), (2, 2, 1, 1000, 500), (2, 1, 1, 1024, 1024),
@@ -163,6 +164,27 @@ def test_far_positions_and_extreme_values():
     assert torch.equal(bad.cpu(), torch.tensor([[False, True], [False, False], [True, False],
                                                 [False, False]]))
     assert not torch.isnan(out.k).any()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,R,P", [(1024, 2, 1), (300, 2, 3), (200, 6, 1), (64, 64, 1), (99, 66, 2),
+                                   (70, 6, 2), (1024, 6, 1), (5, 2, 5)])
+def test_ends_of_small_tables(D, R, P, interleaved):
+    q, k, wq, wk, cos, sin, _ = case(5, 3, 1, D, R, F32, P=P)
+    pos = torch.tensor([P - 1, 0, P - 1, 0, P // 2], device="cuda")
+    # in the middle of a larger buffer of NaN: what is past a table's end has no part
+    raw = torch.full((2, P * (R // 2) + 64), float("nan"), device="cuda")
+    c, s = (raw[i, 32:32 + P * (R // 2)].view(P, R // 2) for i in range(2))
+    c.copy_(cos)
+    s.copy_(sin)
+    out = binding.head_norm_rope(q, k, wq, wk, c, s, pos, EPS, interleaved)
+    want, err = ref.heads_forward(q, wq, cos[pos], sin[pos], R, EPS, interleaved)
+    ref.assert_close(out.q, want, err, F32)
+    d = rand(q.shape, 4, F32)
+    g = binding.head_norm_rope_backward(d, k, q, k, wq, wk, c, s, pos, EPS, interleaved)
+    dx, dw, ex, ew = ref.heads_backward(d, q, wq, cos[pos], sin[pos], R, EPS, interleaved)
+    ref.assert_close(g.dq, dx, ex, F32)
+    ref.assert_close(g.dw_q, dw, ew, F32)
 
 
 def test_heads_far_apart():

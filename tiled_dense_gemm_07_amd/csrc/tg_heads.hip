@@ -23,69 +23,70 @@ struct Pick {
     int per_wave;  // heads of a unit
 };
 
-template <int DT, int V, int G, int NC, bool INTER>
+template <int DT, int V, int G, int NC, bool INTER, bool RAGGED>
 Pick pick_of(bool grad)
 {
-    return {grad ? (const void*)&tg::heads_grad_kernel<DT, V, G, NC, INTER>
-                 : (const void*)&tg::heads_kernel<DT, V, G, NC, INTER>,
+    return {grad ? (const void*)&tg::heads_grad_kernel<DT, V, G, NC, INTER, RAGGED>
+                 : (const void*)&tg::heads_kernel<DT, V, G, NC, INTER, RAGGED>,
             64 / G};
 }
 
-template <int DT, bool INTER>
+// far: one head to a unit.
+template <int DT, bool INTER, bool RAGGED>
 Pick pick_wide(int64_t chunks, bool grad, bool far)
 {
     constexpr int V = 4;
-    if (far && chunks <= 64)
-        return pick_of<DT, V, 64, 1, INTER>(grad);
+    if constexpr (RAGGED && !INTER)
+        if (chunks > 128)  // 1023 values, 6 of them turned
+            return pick_of<DT, V, 64, 3, INTER, RAGGED>(grad);
+    if (chunks > 64)
+        return pick_of<DT, V, 64, 2, INTER, RAGGED>(grad);
+    if (far || chunks > 32)
+        return pick_of<DT, V, 64, 1, INTER, RAGGED>(grad);
     if (chunks <= 4)
-        return pick_of<DT, V, 4, 1, INTER>(grad);
+        return pick_of<DT, V, 4, 1, INTER, RAGGED>(grad);
     if (chunks <= 8)
-        return pick_of<DT, V, 8, 1, INTER>(grad);
+        return pick_of<DT, V, 8, 1, INTER, RAGGED>(grad);
     if (chunks <= 16)
-        return pick_of<DT, V, 16, 1, INTER>(grad);
-    if (chunks <= 32)
-        return pick_of<DT, V, 32, 1, INTER>(grad);
-    if (chunks <= 64)
-        return pick_of<DT, V, 64, 1, INTER>(grad);
-    return pick_of<DT, V, 64, 2, INTER>(grad);
+        return pick_of<DT, V, 16, 1, INTER, RAGGED>(grad);
+    return pick_of<DT, V, 32, 1, INTER, RAGGED>(grad);
 }
 
-// Four values to a load where the rotated pairs and what is left are whole runs of
-// them (eight of 16 bits, 8192 tokens of 40 heads of 128: forward 30.0 us either way,
-// backward 50.2 and 45.1 with four, whose registers hold another wave to a SIMD).
+// Four values to a load (eight of 16 bits, 8192 tokens of 40 heads of 128: forward
+// 30.0 us either way, backward 50.2 and 45.1 with four, whose registers hold another
+// wave to a SIMD).  Sizes that they do not divide cost shifts and
+// selects (backward of 1537 tokens of 15 heads of 99 in fp32 11.2 us; 13.0 with one
+// value at a time);
+// heads of fewer than four values, or tables of fewer in all, take one at a time.
 template <int DT>
-Pick pick_type(int64_t D, int64_t R, bool inter, bool grad, bool far)
+Pick pick_type(int64_t D, int64_t R, int64_t P, bool inter, bool grad, bool far)
 {
     constexpr int V = 4;
-    const int64_t pairs = (D + 1) / 2;
+    if (D < V || (R > 0 && P * (R / 2) < V)) {
+        const int64_t pairs = (D + 1) / 2;
+        return pairs <= 64    ? pick_of<DT, 1, 64, 1, false, false>(grad)
+               : pairs <= 128 ? pick_of<DT, 1, 64, 2, false, false>(grad)
+               : pairs <= 256 ? pick_of<DT, 1, 64, 4, false, false>(grad)
+                              : pick_of<DT, 1, 64, 8, false, false>(grad);
+    }
     if (D % (2 * V) == 0 && R % (2 * V) == 0)
-        return inter ? pick_wide<DT, true>(pairs / V, grad, far)
-                     : pick_wide<DT, false>(pairs / V, grad, far);
-    if (far && pairs <= 64)
-        return pick_of<DT, 1, 64, 1, false>(grad);
-    if (pairs <= 16)
-        return pick_of<DT, 1, 16, 1, false>(grad);
-    if (pairs <= 32)
-        return pick_of<DT, 1, 32, 1, false>(grad);
-    if (pairs <= 64)
-        return pick_of<DT, 1, 64, 1, false>(grad);
-    if (pairs <= 128)
-        return pick_of<DT, 1, 64, 2, false>(grad);
-    if (pairs <= 256)
-        return pick_of<DT, 1, 64, 4, false>(grad);
-    return pick_of<DT, 1, 64, 8, false>(grad);
+        return inter ? pick_wide<DT, true, false>(D / (2 * V), grad, far)
+                     : pick_wide<DT, false, false>(D / (2 * V), grad, far);
+    if (inter)
+        return pick_wide<DT, true, true>(ceil_div(D, 2 * V), grad, far);
+    return pick_wide<DT, false, true>(ceil_div(R / 2, V) + ceil_div((D - R + 1) / 2, V), grad, far);
 }
 
 // apart: the largest stride of heads; a unit's heads are within 32 bits of bytes, or
 // one head is a unit.
-Pick pick(int dt, int64_t D, int64_t R, bool inter, bool grad, int64_t apart)
+Pick pick(int dt, int64_t D, int64_t R, int64_t P, bool inter, bool grad, int64_t apart)
 {
     const auto of = [&](bool far) {
         if (dt == TG_F32)
-            return pick_type<tg::DT_F32>(D, R, inter, grad, far);
+            return pick_type<tg::DT_F32>(D, R, P, inter, grad, far);
         if (dt == TG_F16)
-            return pick_type<tg::DT_F16>(D, R, inter, grad, far);
-        return pick_type<tg::DT_BF16>(D, R, inter, grad, far);
+            return pick_type<tg::DT_F16>(D, R, P, inter, grad, far);
+        return pick_type<tg::DT_BF16>(D, R, P, inter, grad, far);
     };
     const Pick k = of(false);
     const int64_t most = ((int64_t)1 << 32) / tg::dtype_size(dt) - kMaxHeadD;
@@ -211,7 +212,7 @@ struct GradPlan {
 GradPlan grad_plan(const tg_head_norm_rope_grad_args& a)
 {
     GradPlan g{};
-    g.k = pick(a.dtype, a.D, a.R, a.interleaved != 0, true,
+    g.k = pick(a.dtype, a.D, a.R, a.P, a.interleaved != 0, true,
                larger(larger(larger(a.q_h, a.k_h), larger(a.dq_out_h, a.dk_out_h)),
                       larger(a.dq_h, a.dk_h)));
     const int64_t uq = a.T * ceil_div(a.Hq, g.k.per_wave), uk = a.T * ceil_div(a.Hk, g.k.per_wave);
@@ -262,7 +263,7 @@ tg_status tg_head_norm_rope(const tg_head_norm_rope_args* a, tg_stream_t stream)
                 return TG_ERR_ALIAS;
     if (overlap(out[0], out[1]))
         return TG_ERR_ALIAS;
-    const Pick k = pick(a->dtype, a->D, a->R, a->interleaved != 0, false,
+    const Pick k = pick(a->dtype, a->D, a->R, a->P, a->interleaved != 0, false,
                         larger(larger(a->q_h, a->k_h), larger(a->q_out_h, a->k_out_h)));
     tg::HeadsParams p = params(c, a->eps, a->interleaved, k.per_wave);
     p.s[0].out = a->q_out;

@@ -11,7 +11,9 @@
 // those G V further): the V values that are their first members and the V that are
 // their second, so that a turn crosses no lanes (members half of R apart;
 // neighbours are 2 V consecutive values).  Values past R form such pairs, too, half
-// of what is left apart, and are not turned.  Where sizes do not divide so, V is 1.
+// of what is left apart, and are not turned.  RAGGED: sizes that V does not divide; the
+// last chunk of a run has fewer pairs, and a chunk that would end past the head is
+// loaded that much lower and shifted.
 // A unit is one token and 64 / G heads of one kind, to a wave, so that a token's
 // position is uniform and what addresses it scalar.
 // Measured (bf16, 8192 tokens of 32 + 8 heads of 128, slices of one buffer): forward
@@ -96,7 +98,7 @@ struct HeadRaw {
         return (float)__builtin_bit_cast(_Float16, (uint16_t)((i & 1) ? (w >> 16) : w));
     }
     // Rounds once to the type (nearest even).
-    __device__ __forceinline__ void put(const float* f)
+    __device__ __forceinline__ void put(const float (&f)[V])
     {
         if constexpr (DT == DT_F32) {
 #pragma unroll
@@ -137,7 +139,7 @@ __device__ __forceinline__ float group_sum(float f)
 }
 
 // What a lane holds of a head of D values.
-template <int DT, int V, int G, int NC, bool INTER>
+template <int DT, int V, int G, int NC, bool INTER, bool RAGGED>
 struct HeadLane {
     using Raw = HeadRaw<DT, V>;
     static constexpr int ES = DT == DT_F32 ? 4 : 2;
@@ -148,7 +150,8 @@ struct HeadLane {
     struct Turn {
         float c[NC][V], s[NC][V];
     };
-    int oa[NC], ob[NC];  // places of the first and the second members; past D: none
+    int oa[NC], ob[NC];  // places of the first and the second members
+    int na[NC], nb[NC];  // how many there are: V or 0, RAGGED any
     int i0[NC];          // first pair
     int D, R;
     int g;  // which of the unit's heads
@@ -156,21 +159,29 @@ struct HeadLane {
     __device__ __forceinline__ HeadLane(const HeadsParams& p, int lane)
         : D(p.D), R(p.R), g(lane / G)
     {
+        // chunks of pairs that are turned, then of those that are not (halves)
+        const int turned = (R / 2 + V - 1) / V, half = (D - R + 1) / 2;
+        const auto count = [](int n) { return n < 0 ? 0 : (n < V ? n : V); };
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int i = (lane % G + c * G) * V;
-            i0[c] = i;
+            const int j = lane % G + c * G;
+            i0[c] = j * V;
             if (V == 1 ? p.interleaved != 0 : INTER) {
-                oa[c] = 2 * i;
-                ob[c] = 2 * i + V;
-            } else if (i < R / 2) {
-                oa[c] = i;
-                ob[c] = i + R / 2;
+                oa[c] = 2 * V * j;
+                ob[c] = 2 * V * j + V;
+                na[c] = count(D - oa[c]);
+                nb[c] = count(D - ob[c]);
+            } else if (j < turned) {
+                oa[c] = V * j;
+                ob[c] = V * j + R / 2;
+                na[c] = nb[c] = count(R / 2 - V * j);
             } else {
-                const int half = (D - R + 1) / 2;
-                const int t = i - R / 2;
-                oa[c] = t < half ? R + t : D;
+                const int t = V * (j - turned);
+                oa[c] = R + t;
                 ob[c] = R + half + t;
+                na[c] = count(half - t);
+                nb[c] = count(D - R - half - t);
+                i0[c] = R / 2 + t;
             }
         }
     }
@@ -185,50 +196,102 @@ struct HeadLane {
     {
         return (u32)head * (u32)sh * (u32)ES;
     }
-    // No load stands in a branch, so that all of them are in flight together: places
-    // past D read the head's first values, which have no part in anything.
+    // Where the chunk at o of n values is loaded from; n == 0: the head's first values,
+    // which have no part in anything.
+    __device__ __forceinline__ int from(int o, int n) const
+    {
+        if (n == 0)
+            return 0;
+        return RAGGED && o > D - V ? D - V : o;
+    }
+    // No load stands in a branch, so that all of them are in flight together.
     __device__ __forceinline__ void load(Values& v, const char* p, u32 off) const
     {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            v.a[c].load(p + (off + (u32)(oa[c] < D ? oa[c] * ES : 0)));
-            v.b[c].load(p + (off + (u32)(ob[c] < D ? ob[c] * ES : 0)));
+            v.a[c].load(p + (off + (u32)(from(oa[c], na[c]) * ES)));
+            v.b[c].load(p + (off + (u32)(from(ob[c], nb[c]) * ES)));
         }
     }
     __device__ __forceinline__ void store(char* p, u32 off, const float (&f)[NC][2 * V]) const
     {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
+            store_chunk<0>(p + (off + (u32)(oa[c] * ES)), f[c], na[c]);
+            store_chunk<V>(p + (off + (u32)(ob[c] * ES)), f[c], nb[c]);
+        }
+    }
+    // Values AT .. of f: n of them.
+    template <int AT>
+    static __device__ __forceinline__ void store_chunk(char* to, const float (&f)[2 * V], int n)
+    {
+        if (n == V) {
             Raw r;
-            if (oa[c] < D) {
-                r.put(&f[c][0]);
-                r.store(p + (off + (u32)(oa[c] * ES)));
-            }
-            if (ob[c] < D) {
-                r.put(&f[c][V]);
-                r.store(p + (off + (u32)(ob[c] * ES)));
-            }
+            float v[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                v[e] = f[AT + e];
+            r.put(v);
+            r.store(to);
+        } else if constexpr (RAGGED) {
+#pragma unroll
+            for (int e = 0; e < V - 1; ++e)
+                if (e < n) {
+                    HeadRaw<DT, 1> r;
+                    const float v[1] = {f[AT + e]};
+                    r.put(v);
+                    r.store(to + e * ES);
+                }
         }
     }
     // Values in the order of the lane's registers: pair i is (i, V + i), or
-    // (2 i, 2 i + 1) where members are neighbours.
-    static __device__ __forceinline__ void unpack(const Values& v, float (&f)[NC][2 * V])
+    // (2 i, 2 i + 1) where members are neighbours.  RAGGED: shifted down to their
+    // places, zeros where there are none.
+    __device__ __forceinline__ void unpack(const Values& v, float (&f)[NC][2 * V]) const
     {
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < NC; ++c) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 f[c][i] = v.a[c].get(i);
                 f[c][V + i] = v.b[c].get(i);
             }
+            if constexpr (RAGGED) {
+                shift<0>(f[c], na[c] ? oa[c] - from(oa[c], na[c]) : 0, na[c]);
+                shift<V>(f[c], nb[c] ? ob[c] - from(ob[c], nb[c]) : 0, nb[c]);
+            }
+        }
+    }
+    // Values AT .. AT + V - 1 of f moved down by `by`, zeros from n on (V is 4).
+    template <int AT, int N>
+    static __device__ __forceinline__ void shift(float (&f)[N], int by, int n)
+    {
+        static_assert(!RAGGED || V == 4, "two steps of a shift");
+        const bool one = by & 1, two = by & 2;
+        float v[V];  // by value: a choice between elements of f would keep it in memory
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            v[e] = f[AT + e];
+#pragma unroll
+        for (int e = 0; e + 1 < V; ++e) {
+            const float lo = v[e], hi = v[e + 1];
+            v[e] = one ? hi : lo;
+        }
+#pragma unroll
+        for (int e = 0; e + 2 < V; ++e) {
+            const float lo = v[e], hi = v[e + 2];
+            v[e] = two ? hi : lo;
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            f[AT + e] = e < n ? v[e] : 0.0f;
     }
     static constexpr __device__ __forceinline__ int first(int i) { return INTER && V > 1 ? 2 * i : i; }
     static constexpr __device__ __forceinline__ int second(int i)
     {
         return INTER && V > 1 ? 2 * i + 1 : V + i;
     }
-    // Sum over the head of x y.  A chunk of several pairs is in the head as a whole
-    // or not at all.
+    // Sum over the head of x y.
     __device__ __forceinline__ float dot(const float (&x)[NC][2 * V],
                                          const float (&y)[NC][2 * V]) const
     {
@@ -241,10 +304,14 @@ struct HeadLane {
                 ta = __builtin_fmaf(x[c][e], y[c][e], ta);
                 tb = __builtin_fmaf(x[c][V + e], y[c][V + e], tb);
             }
-            if constexpr (V > 1)
-                t += oa[c] < D ? ta + tb : 0.0f;
+            // not RAGGED: V > 1 both are there or neither, and what was read in
+            // their place counts for nothing
+            if constexpr (RAGGED)
+                t += ta + tb;
+            else if constexpr (V > 1)
+                t += na[c] ? ta + tb : 0.0f;
             else
-                t += (oa[c] < D ? ta : 0.0f) + (ob[c] < D ? tb : 0.0f);
+                t += (na[c] ? ta : 0.0f) + (nb[c] ? tb : 0.0f);
         }
         return group_sum<G>(t);
     }
@@ -292,7 +359,8 @@ struct HeadLane {
         };
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const u32 off = (u32)(i0[c] < R / 2 ? i0[c] : 0) * 4u;
+            // RAGGED: on into the next row, but not past the tables
+            const int off = ((i0[c] < R / 2 ? i0[c] : 0) - lower(p, row, c)) * 4;
             const Vec vc = ((const Any*)(pc + off))->v, vs = ((const Any*)(ps + off))->v;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -301,19 +369,34 @@ struct HeadLane {
             }
         }
     }
+    // By how much lower the chunk's cosines are loaded so as to end with the table.
+    __device__ __forceinline__ int lower(const HeadsParams& p, int64_t row, int c) const
+    {
+        if (!RAGGED)
+            return 0;
+        const int64_t end = row + (i0[c] < R / 2 ? i0[c] : 0) + V - (int64_t)p.P * (R / 2);
+        return end > 0 ? (int)end : 0;
+    }
     __device__ __forceinline__ void settle(Turn& t, const HeadsParams& p, int64_t pos) const
     {
         const bool in = pos >= 0 && pos < p.P;
-        if (in && R == D)
+        if (!RAGGED && in && R == D)
             return;
+        const int n = R / 2;
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < NC; ++c) {
+            if constexpr (RAGGED) {
+                const int by = lower(p, (in ? pos : 0) * n, c);
+                shift<0>(t.c[c], by, V);
+                shift<0>(t.s[c], by, V);
+            }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const bool turned = i0[c] < R / 2;
+                const bool turned = (RAGGED ? i0[c] + i : i0[c]) < n;
                 t.c[c][i] = turned ? (in ? t.c[c][i] : __builtin_nanf("")) : 1.0f;
                 t.s[c][i] = turned ? (in ? t.s[c][i] : __builtin_nanf("")) : 0.0f;
             }
+        }
     }
     // Turned to the token's position, or back.
     template <bool BACK>
@@ -331,10 +414,10 @@ struct HeadLane {
     }
 };
 
-template <int DT, int V, int G, int NC, bool INTER>
+template <int DT, int V, int G, int NC, bool INTER, bool RAGGED>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void heads_kernel(HeadsParams p)
 {
-    using Lane = HeadLane<DT, V, G, NC, INTER>;
+    using Lane = HeadLane<DT, V, G, NC, INTER, RAGGED>;
     constexpr int NG = 64 / G;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const Lane L(p, threadIdx.x & 63);
@@ -368,7 +451,7 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void heads_ker
             side = sd;
         }
         float x[NC][2 * V];
-        Lane::unpack(xv, x);
+        L.unpack(xv, x);
         const float r = L.root(x, p);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -390,13 +473,13 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void heads_ker
 // partial sums, which heads_sums_kernel adds in order.
 constexpr int kHeadsGradWaves = 8;
 
-template <int DT, int V, int G, int NC, bool INTER>
+template <int DT, int V, int G, int NC, bool INTER, bool RAGGED>
 __global__ __attribute__((amdgpu_flat_work_group_size(64 * kHeadsGradWaves,
                                                       64 * kHeadsGradWaves))) void
 heads_grad_kernel(HeadsParams p)
 {
     constexpr int NW = kHeadsGradWaves;
-    using Lane = HeadLane<DT, V, G, NC, INTER>;
+    using Lane = HeadLane<DT, V, G, NC, INTER, RAGGED>;
     constexpr int NG = 64 / G;
     __shared__ float red[NW][NC * 2 * V * G];
     const int lane = threadIdx.x & 63;
@@ -470,8 +553,8 @@ heads_grad_kernel(HeadsParams p)
             }
         }
         float x[NC][2 * V], d[NC][2 * V];
-        Lane::unpack(n.x, x);
-        Lane::unpack(n.d, d);
+        L.unpack(n.x, x);
+        L.unpack(n.d, d);
         const float r = L.root(x, p);
         Lane::template turn<true>(d, n.t);
 #pragma unroll
@@ -515,10 +598,8 @@ heads_grad_kernel(HeadsParams p)
         for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int e = 0; e < 2 * V; ++e)
-                if (r == c * 2 * V + e) {
-                    const int base = e < V ? l.oa[c] : l.ob[c];
-                    o = base < p.D ? base + e % V : p.D;
-                }
+                if (r == c * 2 * V + e && e % V < (e < V ? l.na[c] : l.nb[c]))
+                    o = (e < V ? l.oa[c] : l.ob[c]) + e % V;
         if (o < p.D) {
             float t = red[0][i];
 #pragma unroll

@@ -247,7 +247,7 @@ tg_status check_linear(int64_t M, int64_t N, int64_t K, int dtype, int fmt)
 {
     if (!tg::dtype_ok(dtype) || !fmt_ok(fmt))
         return TG_ERR_BAD_DTYPE;
-    if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxLen - 128)
+    if (M < 0 || N < 0 || K < 0 || M > kMaxDim / 4 || N > kMaxDim / 4 || K > kMaxLen - 128)
         return TG_ERR_BAD_SHAPE;
     return TG_OK;
 }
