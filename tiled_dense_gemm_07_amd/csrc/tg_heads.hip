@@ -54,9 +54,8 @@ Pick pick_wide(int64_t chunks, bool grad, bool far)
 
 // Four values to a load (eight of 16 bits, 8192 tokens of 40 heads of 128: forward
 // 30.0 us either way, backward 50.2 and 45.1 with four, whose registers hold another
-// wave to a SIMD).  Sizes that they do not divide cost shifts and
-// selects (backward of 1537 tokens of 15 heads of 99 in fp32 11.2 us; 13.0 with one
-// value at a time);
+// wave to a SIMD).  Sizes that they do not divide cost shifts and selects (backward
+// of 1537 tokens of 15 heads of 99 in fp32 11.2 us; 13.0 with one value at a time);
 // heads of fewer than four values, or tables of fewer in all, take one at a time.
 template <int DT>
 Pick pick_type(int64_t D, int64_t R, int64_t P, bool inter, bool grad, bool far)

@@ -435,13 +435,14 @@ mx_dequant_kernel(MxDequantParams p)
             float, sb[u] == 255 ? 0x7FC00000u : (sb[u] > 0 ? sb[u] << 23 : 0x00400000u));
         float v[8];
         if constexpr (FMT == MX_E2M1) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                // twice the magnitude, 0 to 12, from a word of nibbles
-                const u32 c = q[u][0] >> (4 * i);
-                const float m = (float)((0xC8643210u >> ((c & 7) * 4)) & 15u) * 0.5f;
-                v[i] = ((c & 8) ? -m : m) * s;
-            }
+            const auto two = [&](auto v2, int i) {
+                v[i] = v2[0] * s;
+                v[i + 1] = v2[1] * s;
+            };
+            two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u][0], 1.0f, 0), 0);
+            two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u][0], 1.0f, 1), 2);
+            two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u][0], 1.0f, 2), 4);
+            two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u][0], 1.0f, 3), 6);
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {

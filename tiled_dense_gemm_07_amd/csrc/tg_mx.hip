@@ -49,12 +49,17 @@ auto by_type(int dt, int fmt, const F& f)
 // --------------------------------------------------------------------------
 // Quantisation.
 // --------------------------------------------------------------------------
-constexpr int kUnits = 2;  // of a thread, in flight together
+// Units of eight elements of a thread, in flight together: two of 16 bits from 8 Mi
+// elements on, else one (4096 x 4096 bf16 8.7 us, 9.3 with one; 1000 x 4096 4.2 and
+// 4.0; 8192 x 8192 fp32 56.1 and 53.8; four are slower still but for large bf16).
+int units_of(int dt, int64_t elements) { return dt != TG_F32 && elements >= (8 << 20) ? 2 : 1; }
 
-tg::u32 unit_magic(int64_t Kp)
+tg::u32 unit_magic(int64_t Kp, int units)
 {
     const uint64_t per = (uint64_t)Kp / 8;
-    return per == 0 || per >= 256 * kUnits ? 0 : (tg::u32)((((uint64_t)1 << 32) + per - 1) / per);
+    return per == 0 || per >= 256u * units
+               ? 0
+               : (tg::u32)((((uint64_t)1 << 32) + per - 1) / per);
 }
 
 const void* columns_kernel(int dt, int fmt, bool rows, bool cols, bool sums)
@@ -89,7 +94,6 @@ tg::MxQuantParams quant_params(int64_t M, int64_t K, const void* X, int64_t ldx,
     p.Qt = Qt;
     p.St = St;
     p.sums = sums;
-    p.magic = unit_magic(p.Kp);
     p.tiles_m = (int)ceil_div(p.Mp, 256);
     p.tiles_n = (int)ceil_div(K, 128);
     return p;
@@ -98,11 +102,17 @@ tg::MxQuantParams quant_params(int64_t M, int64_t K, const void* X, int64_t ldx,
 tg_status launch_quant(tg::MxQuantParams p, int dt, int fmt, hipStream_t stream)
 {
     if (!p.Qt && !p.sums) {
-        const void* k = by_type(dt, fmt, [](auto D, auto F) {
-            return (const void*)&tg::mx_rows_kernel<decltype(D)::value, decltype(F)::value, kUnits>;
+        const int64_t all = (int64_t)p.M * (p.Kp / 8);
+        const int u = units_of(dt, 8 * all);
+        const void* k = by_type(dt, fmt, [u](auto D, auto F) {
+            constexpr int DT = decltype(D)::value, FMT = decltype(F)::value;
+            if constexpr (DT != tg::DT_F32)
+                if (u == 2)
+                    return (const void*)&tg::mx_rows_kernel<DT, FMT, 2>;
+            return (const void*)&tg::mx_rows_kernel<DT, FMT, 1>;
         });
-        return tg::launch_kernel(k, ceil_div((int64_t)p.M * (p.Kp / 8), 256 * kUnits), 1, 256, &p,
-                                 stream, "mx_rows");
+        p.magic = unit_magic(p.Kp, u);
+        return tg::launch_kernel(k, ceil_div(all, 256 * u), 1, 256, &p, stream, "mx_rows");
     }
     return tg::launch_kernel(columns_kernel(dt, fmt, p.Q != nullptr, p.Qt != nullptr,
                                             p.sums != nullptr),
@@ -353,12 +363,18 @@ tg_status tg_dequant_mx(int64_t M, int64_t K, tg_mx_format fmt, const uint8_t* Q
     const Span x = span(X, M, K, ldx, tg::dtype_size(dtype));
     if (overlap(x, span1(Q, M * code_bytes(fmt, Kp), 1)) || overlap(x, span1(S, M * (Kp / 32), 1)))
         return TG_ERR_ALIAS;
-    tg::MxDequantParams p{Q, S, X, ldx, (int)M, (int)K, (int)Kp, unit_magic(Kp)};
-    const void* k = by_type(dtype, fmt, [](auto D, auto F) {
-        return (const void*)&tg::mx_dequant_kernel<decltype(D)::value, decltype(F)::value, kUnits>;
+    const int64_t all = M * (Kp / 8);
+    const int u = units_of(dtype, 8 * all);
+    tg::MxDequantParams p{Q, S, X, ldx, (int)M, (int)K, (int)Kp, unit_magic(Kp, u)};
+    const void* k = by_type(dtype, fmt, [u](auto D, auto F) {
+        constexpr int DT = decltype(D)::value, FMT = decltype(F)::value;
+        if constexpr (DT != tg::DT_F32)
+            if (u == 2)
+                return (const void*)&tg::mx_dequant_kernel<DT, FMT, 2>;
+        return (const void*)&tg::mx_dequant_kernel<DT, FMT, 1>;
     });
-    return tg::launch_kernel(k, ceil_div(M * (Kp / 8), 256 * kUnits), 1, 256, &p,
-                             (hipStream_t)stream, "mx_dequant");
+    return tg::launch_kernel(k, ceil_div(all, 256 * u), 1, 256, &p, (hipStream_t)stream,
+                             "mx_dequant");
 }
 
 tg_status tg_linear_mx_workspace_size(int64_t M, int64_t N, int64_t K, tg_dtype dtype,
