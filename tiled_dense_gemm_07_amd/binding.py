@@ -978,23 +978,39 @@ def quant_mx(X, fmt=TG_MX_E2M1, sides="rows", q=None, s=None, qt=None, st=None, 
     _mx_format(fmt)
     ldx = _rows("X", X)
     M, K = X.shape
-    ptr = [None] * 4
+    u8 = torch.uint8
+    pq = ps = pqt = pst = None
     if sides != "columns":
         sq, ss = _mx_shapes(M, K, fmt)
-        q = _empty(sq, torch.uint8, X, stream) if q is None else q
-        s = _empty(ss, torch.uint8, X, stream) if s is None else s
-        ptr[:2] = _mx_dense("q", q, sq), _mx_dense("s", s, ss)
+        if q is None:
+            q = _empty(sq, u8, X, stream)
+            pq = q.data_ptr()
+        else:
+            pq = _mx_dense("q", q, sq)
+        if s is None:
+            s = _empty(ss, u8, X, stream)
+            ps = s.data_ptr()
+        else:
+            ps = _mx_dense("s", s, ss)
     elif q is not None or s is not None:
         raise ValueError("q and s are not written with sides 'columns'")
     if sides != "rows":
         sq, ss = _mx_shapes(K, M, fmt)
-        qt = _empty(sq, torch.uint8, X, stream) if qt is None else qt
-        st = _empty(ss, torch.uint8, X, stream) if st is None else st
-        ptr[2:] = _mx_dense("qt", qt, sq), _mx_dense("st", st, ss)
+        if qt is None:
+            qt = _empty(sq, u8, X, stream)
+            pqt = qt.data_ptr()
+        else:
+            pqt = _mx_dense("qt", qt, sq)
+        if st is None:
+            st = _empty(ss, u8, X, stream)
+            pst = st.data_ptr()
+        else:
+            pst = _mx_dense("st", st, ss)
     elif qt is not None or st is not None:
         raise ValueError("qt and st are not written with sides 'rows'")
     _same_device(X, q, s, qt, st)
-    _call(X, load_library().tg_quant_mx, M, K, _dtype_code(X), X.data_ptr(), ldx, fmt, *ptr, stream)
+    _call(X, load_library().tg_quant_mx, M, K, _dtype_code(X), X.data_ptr(), ldx, fmt, pq, ps, pqt,
+          pst, stream)
     return QuantMx(q, s, qt, st)
 
 
@@ -1012,10 +1028,11 @@ def dequant_mx(q, s, fmt=TG_MX_E2M1, K=None, dtype=None, X=None, stream=None):
     sq, ss = _mx_shapes(M, K, fmt)
     pq, ps = _mx_dense("q", q, sq), _mx_dense("s", s, ss)
     if X is None:
-        X = _empty((M, K), dtype or torch.bfloat16, q, stream)
-    elif dtype is not None and X.dtype != dtype:
-        raise TypeError("X must be %s, got %s" % (dtype, X.dtype))
-    ldx = _rows("X", X, (M, K))
+        X, ldx = _empty((M, K), dtype or torch.bfloat16, q, stream), K
+    else:
+        if dtype is not None and X.dtype != dtype:
+            raise TypeError("X must be %s, got %s" % (dtype, X.dtype))
+        ldx = _rows("X", X, (M, K))
     _same_device(q, s, X)
     _call(q, load_library().tg_dequant_mx, M, K, fmt, pq, ps, _dtype_code(X), X.data_ptr(), ldx,
           stream)
@@ -1047,8 +1064,9 @@ def linear_mx(X, Wq, Ws, bias=None, fmt=TG_MX_E2M1, C=None, epilogue=None, works
     sq, ss = _mx_shapes(N, K, TG_MX_E2M1)
     pq, ps = _mx_dense("Wq", Wq, sq), _mx_dense("Ws", Ws, ss)
     if C is None:
-        C = _empty((M, N), X.dtype, X, stream)
-    ldc = _rows("C", C, (M, N), X.dtype)
+        C, ldc = _empty((M, N), X.dtype, X, stream), N
+    else:
+        ldc = _rows("C", C, (M, N), X.dtype)
     dt = _dtype_code(X)
     need = linear_mx_workspace_size(M, N, K, dt, fmt) if workspace is None else 0
     wp, wn = None, 0
