@@ -187,6 +187,24 @@ def test_ends_of_small_tables(D, R, P, interleaved):
     ref.assert_close(g.dw_q, dw, ew, F32)
 
 
+def test_offsets_past_32_bits():
+    # more than 2^31 values; the last tokens are looked at
+    T, H, D = 1100000, 8, 256
+    say("heads of %d tokens" % T)
+    q = torch.empty((T, H, D), dtype=BF16, device="cuda").normal_()
+    _, k, wq, wk, cos, sin, _ = case(T, 1, 1, D, D, BF16, P=100)
+    pos = torch.arange(T, device="cuda") % 100
+    end = slice(T - 50, T)
+    out = binding.head_norm_rope(q, k, wq, wk, cos, sin, pos, EPS)
+    want, err = ref.heads_forward(q[end], wq, cos[pos[end]], sin[pos[end]], D, EPS, False)
+    ref.assert_close(out.q[end], want, err, BF16)
+    g = binding.head_norm_rope_backward(out.q, out.k, q, k, wq, wk, cos, sin, pos, EPS)
+    dx, _, ex, _ = ref.heads_backward(out.q[end], q[end], wq, cos[pos[end]], sin[pos[end]], D, EPS,
+                                      False)
+    ref.assert_close(g.dq[end], dx, ex, BF16)
+    assert torch.isfinite(g.dw_q).all() and torch.isfinite(g.dw_k).all()
+
+
 def test_heads_far_apart():
     # heads more than 32 bits of bytes from the first of their unit
     T, H, D, far = 3, 8, 64, 640 * 2 ** 20 // 2

@@ -31,7 +31,7 @@ def check_rows(x, q, s, fmt, name):
     assert torch.equal(ref.unpack(q, fmt), codes), name + ": codes"
 
 
-QUANT_SHAPES = [(1, 1), (1, 32), (3, 33), (31, 7), (128, 128), (129, 127), (130, 257), (257, 1003),
+QUANT_SHAPES = [(1, 1), (5, 2), (40, 3), (7, 4), (260, 5), (1, 32), (3, 33), (31, 7), (128, 128), (129, 127), (130, 257), (257, 1003),
                 (2, 8200), (1000, 64), (640, 640)]
 
 
@@ -140,6 +140,27 @@ def test_dequant_every_code_and_scale(fmt, dtype):
     nan = torch.isnan(want)
     assert torch.equal(torch.isnan(got), nan)
     assert torch.equal(got[~nan], want[~nan])
+
+
+def test_offsets_past_32_bits():
+    # more than 2^31 elements in, out and between; the ends are looked at
+    M, K = 300001, 8192
+    say("quant_mx and linear_mx %d x %d" % (M, K))
+    x = torch.empty((M, K), dtype=BF16, device="cuda").normal_()
+    both = binding.quant_mx(x, sides="both")
+    end = x[-300:]
+    check_rows(end, both.q[-300:], both.s[-300:], ref.E2M1, "rows")
+    c, s = ref.quantise(x[-(M % 32) - 320:, -9:].t(), ref.E2M1)
+    n = 320 + M % 32  # whole blocks from there on
+    assert torch.equal(both.st[-9:, (M - n) // 32:(M + 31) // 32].long(), s[:, :(n + 31) // 32])
+    assert torch.equal(ref.unpack(both.qt[-9:, (M - n) // 2:], 0)[:, :n], c[:, :n])
+    v = binding.dequant_mx(both.q, both.s)
+    assert torch.equal(v[-300:], ref.values(*ref.quantise(end, 0), 0).to(BF16))
+    del v, both
+    wq, ws = weights(8192, 128, 3)
+    c = binding.linear_mx(x[:, 5:133], wq, ws)
+    want, err = linear_want(end[:, 5:133], wq, ws, 0, None, False)
+    ref.assert_close(c[-300:], want, err, BF16)
 
 
 def test_quant_of_nothing():
@@ -277,6 +298,32 @@ def test_linear_reuses_a_workspace_and_other_streams():
         c = binding.linear_mx(x, wq, wsc, workspace=ws, stream=side)
         side.synchronize()
         assert torch.equal(c, w)
+
+
+def test_two_graphs_with_a_workspace_each():
+    # replayed in turn and at once, on two streams
+    wq, ws = weights(256, 512, 9)
+    graphs = []
+    for i in range(2):
+        x, c = rand((60, 512), 90 + i, BF16), torch.empty((60, 256), dtype=BF16, device="cuda")
+        need = binding.linear_mx_workspace_size(60, 256, 512, binding.TG_BF16)
+        w = torch.empty((need,), dtype=torch.uint8, device="cuda")
+        binding.linear_mx(x, wq, ws, C=c, workspace=w)
+        torch.cuda.synchronize()
+        g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(g, stream=st):
+            binding.linear_mx(x, wq, ws, C=c, workspace=w)
+        graphs.append((g, st, x, c))
+    for _ in range(3):
+        for g, st, x, c in graphs:
+            c.zero_()
+        torch.cuda.synchronize()
+        for g, st, x, c in graphs:
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for g, st, x, c in graphs:
+            assert torch.equal(c, binding.linear_mx(x, wq, ws))
 
 
 @pytest.mark.parametrize("M", [1, 40])
