@@ -68,7 +68,7 @@ struct DmaMx2 {
     static constexpr int NCOPY = JA + JW;
     static constexpr int NCA = BM / 32;             // chunk copies of A scales (32 rows each)
     static constexpr int NCW = BN / 32;
-    static constexpr int JS = (NCA + NCW) / NW;     // chunk copies per wave
+    static constexpr int JS = (NCA + NCW + NW - 1) / NW;  // chunk copies per wave, at most
     static constexpr int NM = FM * FN;              // MFMAs per step
     static constexpr int NRD_A = FM * (A8 ? 2 : 1);
     static constexpr int NRD = NRD_A + FN;          // fragment reads per step
@@ -80,7 +80,7 @@ struct DmaMx2 {
     static_assert(WTM % 32 == 0 && WTN % 32 == 0, "wave tiles of 32x32 blocks");
     static_assert(JA >= 1 && JW >= 1 && A_STAGE % (1024 * NW) == 0 && W_STAGE % (1024 * NW) == 0,
                   "strips split into whole 1 KiB copies per wave");
-    static_assert((NCA + NCW) % NW == 0 && JS >= 1 && 2 * JS <= STEPS, "chunk copies split evenly");
+    static_assert(JS >= 1 && 2 * JS <= STEPS, "chunk copies in every other slot");
     static_assert(SA_REGION % 1024 == 0 && SW_REGION % 1024 == 0,
                   "scale buffers 1 KiB aligned (the chunk halves are selected by an xor)");
     static_assert(LDS_BYTES <= 160 * 1024, "LDS budget");
@@ -208,6 +208,8 @@ struct DmaMx2 {
     {
         const int g = W * JS + d;
         const u32 buf = (u32)(c & 1);
+        if (g >= NCA + NCW)
+            return;  // the last waves have fewer
         const u32 off = 1024 * c < p.K ? L.s_off[d] + (u32)(c * 32) : kOob;
         if (g < NCA)
             dma16(smem0 + SA_REGION + buf * SA_BUF + g * 1024, off, r.sa);

@@ -9,12 +9,11 @@ static const MxKernel kKernels[] = {
     TG_MX_STREAM(MX_E4M3, 1, 1, 4, 8, 1, 2.14f, 0.0667f, 0.34f, 0.0927f),
     TG_MX_STREAM(MX_E4M3, 2, 1, 4, 4, 2, 2.22f, 0.108f, 0.64f, 0.2433f),
     TG_MX_STREAM(MX_E4M3, 2, 2, 2, 8, 1, 2.45f, 0.1391f, 1.1f, 0.1921f),
-    TG_MX_TILE(MX_S128, MX_E4M3, 64, 64, 2, 2, 4, 128, 3.31f, 0.2198f, 1.72f, 0.2513f),
-    TG_MX_TILE(MX_S256, MX_E4M3, 64, 64, 2, 2, 2, 128, 3.31f, 0.2553f, 1.87f, 0.269f),
-    TG_MX_TILE(MX_S256, MX_E4M3, 128, 128, 2, 4, 2, 128, 4.04f, 0.4036f, 2.67f, 0.4606f),
-    TG_MX_TILE(MX_S128, MX_E4M3, 128, 256, 2, 4, 4, 128, 5.69f, 0.6785f, 3.88f, 0.8259f),
-    TG_MX_TILE(MX_S256, MX_E4M3, 128, 256, 2, 2, 2, 128, 8.25f, 0.5983f, 5.06f, 0.669f),
-    TG_MX_TILE(MX_S128, MX_E4M3, 256, 256, 2, 4, 3, 128, 9.66f, 1.3377f, 6.76f, 1.3234f),
+    TG_MX_TILE(MX_S128, MX_E4M3, 64, 64, 2, 2, 4, 128, 3.31f, 0.2197f, 1.68f, 0.2535f),
+    TG_MX_TILE(MX_S256, MX_E4M3, 64, 64, 2, 2, 2, 128, 3.31f, 0.2551f, 1.83f, 0.2708f),
+    TG_MX_TILE(MX_S256, MX_E4M3, 128, 128, 2, 4, 2, 128, 4.05f, 0.4018f, 2.55f, 0.4553f),
+    TG_MX_TILE(MX_S256, MX_E4M3, 128, 256, 2, 4, 2, 128, 5.56f, 0.6108f, 3.59f, 0.67f),
+    TG_MX_TILE(MX_S128, MX_E4M3, 256, 256, 2, 4, 3, 128, 9.66f, 1.3307f, 6.68f, 1.3315f),
 };
 
 MxKernels mx_kernels_e4m3()
