@@ -482,10 +482,10 @@ tg_status tg_block_norm_backward_workspace_size(const tg_block_norm_grad_args* a
  *   X: [M][K], row stride ldx.
  * M or K == 0: nothing is launched.
  * Errors: TG_ERR_BAD_DTYPE (also fmt), TG_ERR_BAD_SHAPE (negative, above 2^29 - 1,
- *   or a stride below K), TG_ERR_NULL_POINTER (X, neither Q nor Qt, or codes
- *   without scales or the reverse), TG_ERR_NO_CONFIG (codes not 16-byte or
- *   scales not 4-byte aligned), TG_ERR_ALIAS (an output overlaps X or another),
- *   TG_ERR_HIP.
+ *   a stride below K, or M Kp of 2^36 and more, in fp32 2^35), TG_ERR_NULL_POINTER
+ *   (X, neither Q nor Qt, or codes without scales or the reverse),
+ *   TG_ERR_NO_CONFIG (codes not 16-byte or scales not 4-byte aligned),
+ *   TG_ERR_ALIAS (an output overlaps X or another), TG_ERR_HIP.
  */
 tg_status tg_quant_mx(int64_t M, int64_t K, tg_dtype dtype, const void* X, int64_t ldx,
                       tg_mx_format fmt, uint8_t* Q, uint8_t* S, uint8_t* Qt, uint8_t* St,
@@ -511,7 +511,8 @@ tg_status tg_dequant_mx(int64_t M, int64_t K, tg_mx_format fmt, const uint8_t* Q
  *     concurrently.
  *   K == 0: C = epilogue(bias); X, Wq and Ws may be NULL then.
  * Errors: TG_ERR_BAD_DTYPE (also fmt), TG_ERR_BAD_EPILOGUE, TG_ERR_BAD_SHAPE
- *   (also a stride below its row length, K > 8388479, M or N above 2^29 - 1),
+ *   (also a stride below its row length, K > 8388479, M above 2^29 - 1, N above
+ *   2^27 - 16, or an X that tg_quant_mx does not take),
  *   TG_ERR_NULL_POINTER, TG_ERR_NO_CONFIG (Wq not 16-byte or Ws not 4-byte aligned),
  *   TG_ERR_WORKSPACE, TG_ERR_ALIAS (C or the workspace overlaps an operand or
  *   each other), TG_ERR_HIP.

@@ -205,6 +205,19 @@ def test_offsets_past_32_bits():
     assert torch.isfinite(g.dw_q).all() and torch.isfinite(g.dw_k).all()
 
 
+def test_more_tokens_than_waves():
+    # a wave takes units of several tokens
+    T, D = 2 ** 26 + 3, 4
+    say("heads of %d tokens" % T)
+    q = torch.empty((T, 1, D), dtype=BF16, device="cuda").normal_()
+    w = rand((D,), 2, BF16)
+    out = binding.head_norm_rope(q, w_q=w, eps=EPS)
+    for part in (slice(0, 100), slice(2 ** 25 - 7, 2 ** 25 + 93), slice(T - 100, T), slice(5, T, 99991)):
+        none = torch.zeros((q[part].shape[0], 0), device="cuda")
+        want, err = ref.heads_forward(q[part], w, none, none, 0, EPS, False)
+        ref.assert_close(out.q[part], want, err, BF16)
+
+
 def test_heads_far_apart():
     # heads more than 32 bits of bytes from the first of their unit
     T, H, D, far = 3, 8, 64, 640 * 2 ** 20 // 2

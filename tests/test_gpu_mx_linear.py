@@ -451,3 +451,13 @@ def test_backward_captured():
         want = binding.linear_mx_backward(dY, X=X, W=W, dbias=True)
         for n in ("dx", "dw", "dbias"):
             assert torch.equal(getattr(out, n), getattr(want, n)), n
+
+
+def test_no_k_and_more_results_than_one_pass():
+    M, N = 70000, 4096
+    say("linear %d x %d x 0" % (M, N))
+    bias = torch.arange(N, dtype=torch.float32, device="cuda") - 2000
+    none = torch.zeros((N, 0), dtype=torch.uint8, device="cuda")
+    C = binding.linear_mx(torch.empty((M, 0), dtype=BF16, device="cuda"), none, none, bias,
+                          epilogue="relu")
+    assert (C == bias.clamp(min=0).to(BF16)).all()

@@ -45,6 +45,20 @@ def test_quant_argument_errors(lib):
     assert quant(lib, K=0, X=None, Q=None, S=None, Qt=None, St=None) == OK
 
 
+def test_sizes_beyond_one_launch(lib):
+    """2^32 threads of eight elements (of 16 in 16 bits) are refused, not launched."""
+    far = dict(X=1 << 44, Q=1 << 45, S=1 << 46, Qt=None, St=None)
+    assert quant(lib, M=1 << 20, K=1 << 15, dt=F32, **far) == SHAPE
+    assert quant(lib, M=1 << 20, K=1 << 16, dt=BF16, **far) == SHAPE
+    far = dict(Q=1 << 44, S=1 << 45, X=1 << 46)
+    assert dequant(lib, M=1 << 20, K=1 << 15, dt=F32, **far) == SHAPE
+    assert dequant(lib, M=1 << 20, K=1 << 16, dt=F16, **far) == SHAPE
+    size = ctypes.c_size_t(0)
+    bytes_of = lib.tg_linear_mx_workspace_size
+    assert bytes_of(1, (1 << 27) - 16, 128, BF16, 0, ctypes.byref(size)) == OK
+    assert bytes_of(1, (1 << 27) - 15, 128, BF16, 0, ctypes.byref(size)) == SHAPE
+
+
 def dequant(lib, M=4, K=40, fmt=0, Q=P[0], S=P[1], dt=BF16, X=P[2], ldx=None):
     return lib.tg_dequant_mx(M, K, fmt, Q, S, dt, X, K if ldx is None else ldx, None)
 

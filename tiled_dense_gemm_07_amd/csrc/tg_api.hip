@@ -793,7 +793,8 @@ int swizzle_override() { return g_group_override.load(std::memory_order_relaxed)
 tg_status launch_kernel(const void* kernel, int64_t grid_x, int64_t grid_y, int threads,
                         void* params, hipStream_t stream, const char* what, unsigned lds)
 {
-    if (grid_x > kMaxDim || grid_y > 65535)
+    // a launch has fewer than 2^32 threads in x
+    if (grid_x > kMaxDim || grid_x * threads > (int64_t)UINT32_MAX || grid_y > 65535)
         return TG_ERR_BAD_SHAPE;
     const char* fault = getenv("TG_FAULT");
     if (fault && strcmp(fault, "launch") == 0)

@@ -17,6 +17,7 @@ using tg::span1;
 constexpr int64_t kMaxHeadD = 1024;
 constexpr int64_t kMaxT = 1 << 30;
 constexpr int64_t kMaxHeads = 1 << 16;
+constexpr int64_t kMaxWaves = 1 << 25;  // of the forward kernel: 2^31 threads
 
 struct Pick {
     const void* kernel;
@@ -274,6 +275,7 @@ tg_status tg_head_norm_rope(const tg_head_norm_rope_args* a, tg_stream_t stream)
     const int64_t units = p.s[0].units + p.s[1].units, total = units * a->T;
     int64_t per = total / 16384;
     per = per < 1 ? 1 : (per > units ? units : per);
+    per = larger(per, ceil_div(total, kMaxWaves));
     p.per = (int)per;
     return tg::launch_kernel(k.kernel, ceil_div(total, 4 * per), 1, 256, &p, (hipStream_t)stream,
                              "heads");

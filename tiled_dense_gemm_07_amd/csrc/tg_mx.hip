@@ -19,6 +19,7 @@ using tg::Span;
 using tg::span;
 using tg::span1;
 
+constexpr int64_t kMaxN = (1 << 27) - 16;   // workgroups of 16 columns, 512 threads
 constexpr int64_t kMaxLen = kMaxDim / 256;  // of a summed axis: a tile's offsets fit 31 bits
 
 bool fmt_ok(int f) { return f == TG_MX_E2M1 || f == TG_MX_E4M3; }
@@ -227,8 +228,9 @@ tg_status launch_fill(int64_t M, int64_t N, int dt, const float* bias, void* C, 
     if (M == 0 || N == 0)
         return TG_OK;
     tg::MxFillParams p{bias, C, ldc, (int)M, (int)N, dt, relu};
-    return tg::launch_kernel((const void*)&tg::mx_fill_kernel, ceil_div(M * N, 256), 1, 256, &p,
-                             stream, "mx_fill");
+    const int64_t groups = ceil_div(M * N, 256);
+    return tg::launch_kernel((const void*)&tg::mx_fill_kernel, groups < (1 << 20) ? groups : 1 << 20,
+                             1, 256, &p, stream, "mx_fill");
 }
 
 // --------------------------------------------------------------------------
@@ -257,7 +259,7 @@ tg_status check_linear(int64_t M, int64_t N, int64_t K, int dtype, int fmt)
 {
     if (!tg::dtype_ok(dtype) || !fmt_ok(fmt))
         return TG_ERR_BAD_DTYPE;
-    if (M < 0 || N < 0 || K < 0 || M > kMaxDim / 4 || N > kMaxDim / 4 || K > kMaxLen - 128)
+    if (M < 0 || N < 0 || K < 0 || M > kMaxDim / 4 || N > kMaxN || K > kMaxLen - 128)
         return TG_ERR_BAD_SHAPE;
     return TG_OK;
 }
