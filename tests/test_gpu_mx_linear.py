@@ -215,6 +215,14 @@ def test_linear_large(M, N, K, dtype, fmt):
     check_linear(M, N, K, dtype, fmt, bias=True, relu=False)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(17, 8001, 200), (18, 5001, 2000), (32, 4097, 4200), (33, 6999, 384),
+                                   (40, 6001, 1152), (48, 7011, 640), (49, 5001, 896), (64, 4097, 1500)])
+def test_linear_some_tens_of_tokens(M, N, K, fmt):
+    # 32 and 64 rows of weights to a workgroup, runs of 512 k and one to three steps
+    check_linear(M, N, K, BF16, fmt, bias=M % 2 == 0, relu=M % 3 == 0)
+
+
 def test_linear_is_the_product_of_its_parts():
     # bit for bit what quant_mx and gemm_mx give one after the other
     for M, K in ((48, 1024), (300, 2048)):

@@ -22,8 +22,9 @@
 //    take runs of 128 ST k in turn.  An instruction loads 64 bytes of 16 rows; with
 //    ST 4 one more loads the 16 scale bytes that each row has in the run (a dword for
 //    each 128 k touches as many cache lines as the codes: 16 x 8192 x 8192 E4M3 17.2
-//    us, and 13.2).  32 rows share the reads of the activations, which every
-//    workgroup takes whole, where there are workgroups enough.
+//    us, and 13.2).  32 or 64 rows share the reads of the activations, which every
+//    workgroup takes whole, where there are workgroups enough (128 x 4096 x 4096 E4M3
+//    13.3 us with 64 rows and 32 tokens, 18.0 with 32 rows, 27.2 with 16 and 16).
 //  * The loads of a wave's next run are issued before the MFMAs of this one.
 //  * The waves' sums are added in LDS, in the waves' order.
 //  * Rows past M or N read the last row again; their results are not stored.
@@ -32,7 +33,7 @@
 //    one launch instead of two.
 // Bound by the stream of W and, on small ones, by launch and latency.  8192 x 8192 with
 // W from HBM (36 MB): 16 tokens 12.1 us (2.9 TB/s; a large copy reaches 5.2), in E4M3
-// 13.4, 32 tokens 15.4 and 19.0; FUSED one token 12.3, on 1024 x 1024 3.3 us.
+// 13.4, 32 tokens 14.9 and 18.0; FUSED one token 12.3, on 1024 x 1024 3.3 us.
 #pragma once
 
 #include "tg_kernel_mx2.h"

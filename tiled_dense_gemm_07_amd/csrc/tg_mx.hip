@@ -152,8 +152,7 @@ float kernel_cost(const MxKernel& k, int64_t M, int64_t N, int64_t K)
     const int64_t groups = ceil_div(M, k.bm) * ceil_div(N, k.bn);
     const float strips = (float)(K / 128);
     return k.t0 + (groups <= 256 ? strips * k.one
-                                 : (float)ceil_div(groups, 256 * k.per_cu) *
-                                       (k.round + strips * k.full));
+                                 : (float)ceil_div(groups, 256) * (k.round + strips * k.full));
 }
 
 // The cheapest; up to 16 tokens among the streaming kernels (1 x 14336 x 4096 in E4M3

@@ -5,10 +5,11 @@
 namespace tg {
 
 static const MxKernel kKernels[] = {
-    TG_MX_STREAM(MX_E2M1, 1, 1, 4, 4, 1, 2.08f, 0.0565f, 0.08f, 0.0611f),
-    TG_MX_STREAM(MX_E2M1, 1, 1, 4, 8, 1, 2.09f, 0.0521f, 0.23f, 0.0611f),
-    TG_MX_STREAM(MX_E2M1, 2, 1, 4, 4, 2, 2.2f, 0.0929f, 0.44f, 0.1914f),
-    TG_MX_STREAM(MX_E2M1, 2, 2, 2, 8, 1, 2.39f, 0.1114f, 1.05f, 0.149f),
+    TG_MX_STREAM(MX_E2M1, 1, 1, 4, 4, 2.09f, 0.0598f, 0.09f, 0.0621f),
+    TG_MX_STREAM(MX_E2M1, 1, 1, 4, 8, 2.12f, 0.0566f, 0.24f, 0.0605f),
+    TG_MX_STREAM(MX_E2M1, 2, 1, 4, 4, 2.25f, 0.0981f, 0.26f, 0.0955f),
+    TG_MX_STREAM(MX_E2M1, 2, 2, 4, 4, 2.51f, 0.1226f, 0.45f, 0.1302f),
+    TG_MX_STREAM(MX_E2M1, 4, 2, 4, 4, 3.07f, 0.187f, 1.57f, 0.2177f),
     TG_MX_TILE(MX_S128, MX_E2M1, 64, 64, 2, 2, 4, 128, 3.05f, 0.1963f, 0.6f, 0.2093f),
     TG_MX_TILE(MX_S256, MX_E2M1, 64, 64, 2, 2, 2, 128, 3.12f, 0.2207f, 1.66f, 0.2292f),
     TG_MX_TILE(MX_S256, MX_E2M1, 128, 128, 2, 4, 2, 128, 3.76f, 0.319f, 2.47f, 0.3431f),

@@ -7,10 +7,11 @@
 namespace tg {
 
 static const MxKernel kKernels[] = {
-    TG_MX_STREAM(MX_E4M3, 1, 1, 4, 4, 1, 2.04f, 0.0759f, 0.13f, 0.0852f),
-    TG_MX_STREAM(MX_E4M3, 1, 1, 4, 8, 1, 2.14f, 0.0667f, 0.34f, 0.0927f),
-    TG_MX_STREAM(MX_E4M3, 2, 1, 4, 4, 2, 2.22f, 0.108f, 0.64f, 0.2433f),
-    TG_MX_STREAM(MX_E4M3, 2, 2, 2, 8, 1, 2.45f, 0.1391f, 1.1f, 0.1921f),
+    TG_MX_STREAM(MX_E4M3, 1, 1, 4, 4, 2.08f, 0.0816f, 0.13f, 0.0874f),
+    TG_MX_STREAM(MX_E4M3, 1, 1, 4, 8, 2.17f, 0.0746f, 0.35f, 0.0956f),
+    TG_MX_STREAM(MX_E4M3, 2, 1, 4, 4, 2.28f, 0.1171f, 0.36f, 0.1204f),
+    TG_MX_STREAM(MX_E4M3, 2, 2, 4, 4, 2.55f, 0.1625f, 1.07f, 0.1962f),
+    TG_MX_STREAM(MX_E4M3, 4, 2, 4, 4, 3.08f, 0.2382f, 1.52f, 0.2812f),
     TG_MX_TILE(MX_S128, MX_E4M3, 64, 64, 2, 2, 4, 128, 3.31f, 0.2197f, 1.68f, 0.2535f),
     TG_MX_TILE(MX_S256, MX_E4M3, 64, 64, 2, 2, 2, 128, 3.31f, 0.2551f, 1.83f, 0.2708f),
     TG_MX_TILE(MX_S256, MX_E4M3, 128, 128, 2, 4, 2, 128, 4.05f, 0.4018f, 2.55f, 0.4553f),

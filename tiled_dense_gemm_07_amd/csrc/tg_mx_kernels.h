@@ -6,20 +6,19 @@
 
 namespace tg {
 
-// One of the product's kernels, and what it costs on this card in microseconds
-// with its weights from HBM: t0 + strips of 128 k times `one` while its workgroups
-// are at most 256, else for each round of 256 per_cu workgroups `round` + strips
-// times `full`.  Fitted to 270 shapes of each format (M 1 to 8192, N 128 to 14336,
-// K 128 to 8192, odd ones among them), within 8 to 16% on average; the choice by it
-// is 2 to 3% on average above the fastest of all that were measured (30% at most, on
-// calls of a few microseconds).
+// One of the product's kernels, and what it costs on this card in microseconds: t0 +
+// strips of 128 k times `one` while its workgroups are at most 256, else for each
+// round of 256 workgroups `round` + strips times `full`.  Fitted to 270 to 330 shapes
+// of each format (M 1 to 8192, N 128 to 14336, K 128 to 8192, odd ones among them),
+// within 8 to 13% on average; the choice by it is 2 to 3% on average above the fastest
+// of all that were measured (30% at most on calls of a few microseconds; 60% on 64
+// tokens by weights of 25 MB in E4M3: the cost does not know HBM from the cache).
 struct MxKernel {
     const char* name;
     const void* kernel[3];  // by C's type
     int bm, bn, threads;
     int strip;      // K has to be a multiple of it
     unsigned lds;   // bytes, streaming kernels (0: a tile)
-    int per_cu;
     float t0, one, round, full;
 };
 
@@ -39,15 +38,15 @@ MxKernels mx_kernels_e4m3();
                                                 NS>,                                               \
              (const void*)&tg::mx_linear_kernel<tg::KIND, tg::DT_BF16, tg::AFMT, BM, BN, WGM, WGN, \
                                                 NS>},                                              \
-            BM, BN, WGM* WGN * 64, STRIP, 0, 1, T0, ONE, ROUND, FULL                               \
+            BM, BN, WGM* WGN * 64, STRIP, 0, T0, ONE, ROUND, FULL                                  \
     }
-#define TG_MX_STREAM(AFMT, NT, MT, ST, NW, PER_CU, T0, ONE, ROUND, FULL)                          \
+#define TG_MX_STREAM(AFMT, NT, MT, ST, NW, T0, ONE, ROUND, FULL)                                  \
     {                                                                                             \
         "mx_stream_" #AFMT "_n" #NT "_m" #MT "_st" #ST "_w" #NW,                                  \
             {(const void*)&tg::mx_stream_kernel<tg::DT_F32, tg::AFMT, NT, MT, ST, NW, false>,     \
              (const void*)&tg::mx_stream_kernel<tg::DT_F32, tg::AFMT, NT, MT, ST, NW, false>,     \
              (const void*)&tg::mx_stream_kernel<tg::DT_F32, tg::AFMT, NT, MT, ST, NW, false>},    \
-            16 * MT, 16 * NT, NW * 64, 128, NW* NT* MT * 1024, PER_CU, T0, ONE, ROUND, FULL       \
+            16 * MT, 16 * NT, NW * 64, 128, NW* NT* MT * 1024, T0, ONE, ROUND, FULL               \
     }
 
 }  // namespace tg
