@@ -501,9 +501,11 @@ tg_status tg_dequant_mx(int64_t M, int64_t K, tg_mx_format fmt, const uint8_t* Q
  *   Wq, Ws: E2M1 weights [N][Kp] as tg_quant_mx writes them (Kp: K rounded up to
  *     a multiple of 128); what they hold past K has no part in C as long as its
  *     scale bytes are not 255.
- *   The product is that of tg_gemm_mx (whose arithmetic on E4M3 holds here, too),
- *   the bias is added in fp32 and C rounded once; sums are taken in an order that
- *   depends on the sizes only.
+ *   Products are exact and summed in fp32, the bias is added in fp32 and C rounded
+ *   once; sums are taken in an order that depends on the sizes only.  Only a 16-bit
+ *   C of more than 16 tokens with E4M3 activations may take the arithmetic that
+ *   tg_gemm_mx states for them, which cuts the products of each eight k at 2^-13 of
+ *   their largest (measured: 7e-6 of the result; rounding to fp16 alone is 2.1e-4).
  *   workspace: device memory, 16-byte aligned, of at least the size
  *     tg_linear_mx_workspace_size reports for these sizes (it holds X's codes
  *     and scales; 0 bytes, and NULL, where the call needs none).  Its contents
@@ -532,6 +534,7 @@ tg_status tg_linear_mx_workspace_size(int64_t M, int64_t N, int64_t K, tg_dtype 
  *   dbias[N] = sum_m dY[m][n]    from dY as given, fp32, in a fixed order.
  * The roundings of the quantisation are passed over (their gradient is taken to be
  * that of the value itself).  dY is the gradient before the ReLU, if there is one.
+ * Products and sums are those of tg_linear_mx.
  *   dY: [M][N], X, dX: [M][K] of `dtype`; W, dW: [N][K] of `wtype`, which is
  *   `dtype` or TG_F32 (W as the optimiser holds it, not in 4 bits).  Row strides in
  *   elements, any alignment.  dX, dW, dbias: NULL if not wanted; dX needs W, dW

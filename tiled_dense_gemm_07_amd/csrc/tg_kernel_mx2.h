@@ -42,7 +42,8 @@
 
 namespace tg {
 
-template <int AFMT, int BM, int BN, int WGM, int WGN, int GROUP_M>
+// WHOLE: E4M3 codes in two halves, whose products are exact.
+template <int AFMT, int BM, int BN, int WGM, int WGN, int GROUP_M, bool WHOLE = false>
 struct DmaMx2 {
     static constexpr int BK = 256;
     static constexpr bool A8 = AFMT == MX_E4M3;
@@ -84,6 +85,7 @@ struct DmaMx2 {
     static_assert(SA_REGION % 1024 == 0 && SW_REGION % 1024 == 0,
                   "scale buffers 1 KiB aligned (the chunk halves are selected by an xor)");
     static_assert(LDS_BYTES <= 160 * 1024, "LDS budget");
+    static_assert(A8 || !WHOLE, "products of E2M1 codes are exact as they are");
 
     struct Lane {
         u32 a_off[JA];
@@ -257,9 +259,16 @@ struct DmaMx2 {
         const int fm = i / FN, fn = i % FN;
         const u32x4 wv = F.w[fn], lo = F.a[fm][0], hi = F.a[fm][A8 ? 1 : 0];
         const i32x8 wop = {(int)wv[0], (int)wv[1], (int)wv[2], (int)wv[3], 0, 0, 0, 0};
-        const i32x8 aop = A8 ? i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
-                                     (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]}
-                             : i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], 0, 0, 0, 0};
+        i32x8 aop = A8 ? i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
+                               (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]}
+                       : i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], 0, 0, 0, 0};
+        if constexpr (WHOLE) {
+            const MxHalves h = mx_halves(aop);
+            acc[fm][fn] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                wop, h.small, acc[fm][fn], MX_E2M1, AFMT, 0,
+                (int)(S.w[fn][Q >> 1] >> L.sh[Q & 1]), 0, (int)(S.a[fm][Q >> 1] >> L.sh[Q & 1]));
+            aop = h.large;
+        }
         acc[fm][fn] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
             wop, aop, acc[fm][fn], MX_E2M1, AFMT, 0, (int)(S.w[fn][Q >> 1] >> L.sh[Q & 1]), 0,
             (int)(S.a[fm][Q >> 1] >> L.sh[Q & 1]));

@@ -26,6 +26,8 @@
 //    workgroup takes whole, where there are workgroups enough (128 x 4096 x 4096 E4M3
 //    13.3 us with 64 rows and 32 tokens, 18.0 with 32 rows, 27.2 with 16 and 16).
 //  * The loads of a wave's next run are issued before the MFMAs of this one.
+//  * E4M3 activations go in two halves (mx_halves), whose products are exact: 16 x
+//    8192 x 8192 took 16.2 us in both launches with one instruction, now 17.0.
 //  * The waves' sums are added in LDS, in the waves' order.
 //  * Rows past M or N read the last row again; their results are not stored.
 //  * FUSED: the activations are given in 16 or 32 bits and every workgroup
@@ -198,9 +200,9 @@ __device__ __forceinline__ void mx_linear_run(const MxLinearParams& p, int group
 // its groups of four strips come up to three single ones, and the first two steps of
 // a last one.  What the copies of that one bring from past a row's end (the next
 // row, zeros past the last) is not multiplied.
-template <int AFMT, int BM, int BN, int WGM, int WGN>
-struct DmaMx2Any : DmaMx2<AFMT, BM, BN, WGM, WGN, 4> {
-    using Base = DmaMx2<AFMT, BM, BN, WGM, WGN, 4>;
+template <int AFMT, int BM, int BN, int WGM, int WGN, bool WHOLE>
+struct DmaMx2Any : DmaMx2<AFMT, BM, BN, WGM, WGN, 4, WHOLE> {
+    using Base = DmaMx2<AFMT, BM, BN, WGM, WGN, 4, WHOLE>;
     using typename Base::Frag;
     using typename Base::Lane;
     using typename Base::Res;
@@ -282,22 +284,28 @@ struct DmaMx2Any : DmaMx2<AFMT, BM, BN, WGM, WGN, 4> {
 // A tile's kernel.  KIND 0: strips of 128 k; 1: of 256, K a whole number of 1024; 2:
 // of 256, any K.
 enum { MX_S128 = 0, MX_S256_1024 = 1, MX_S256 = 2 };
+// E4M3 products exact (two instructions for one).  fp32 C shows what is cut off of them
+// otherwise; in 16 bits it is far less than C's last step, and the tiles are bound by
+// those instructions: 8192^3 bf16 460 us, and 869 with both; 2048 x 4096 x 4096 39 and 60 (fp32 C 45 and
+// 68).
+constexpr bool mx_whole(int dt, int afmt) { return afmt == MX_E4M3 && dt == DT_F32; }
 template <int KIND, int DT, int AFMT, int BM, int BN, int WGM, int WGN, int NS>
 struct MxTileOf;
 template <int DT, int AFMT, int BM, int BN, int WGM, int WGN, int NS>
 struct MxTileOf<MX_S128, DT, AFMT, BM, BN, WGM, WGN, NS>
-    : DmaMx<AFMT, BM, BN, WGM, WGN, NS, 4, false> {
+    : DmaMx<AFMT, BM, BN, WGM, WGN, NS, 4, false, mx_whole(DT, AFMT)> {
     static constexpr int BMT = BM, BNT = BN;
     static constexpr int OCC = MxOcc<AFMT, BM, BN, WGM * WGN>::value;
 };
 template <int DT, int AFMT, int BM, int BN, int WGM, int WGN, int NS>
 struct MxTileOf<MX_S256_1024, DT, AFMT, BM, BN, WGM, WGN, NS>
-    : DmaMx2<AFMT, BM, BN, WGM, WGN, 4> {
+    : DmaMx2<AFMT, BM, BN, WGM, WGN, 4, mx_whole(DT, AFMT)> {
     static constexpr int BMT = BM, BNT = BN;
     static constexpr int OCC = WGM * WGN > 4 ? 2 : 1;
 };
 template <int DT, int AFMT, int BM, int BN, int WGM, int WGN, int NS>
-struct MxTileOf<MX_S256, DT, AFMT, BM, BN, WGM, WGN, NS> : DmaMx2Any<AFMT, BM, BN, WGM, WGN> {
+struct MxTileOf<MX_S256, DT, AFMT, BM, BN, WGM, WGN, NS>
+    : DmaMx2Any<AFMT, BM, BN, WGM, WGN, mx_whole(DT, AFMT)> {
     static constexpr int BMT = BM, BNT = BN;
     static constexpr int OCC = WGM * WGN > 4 ? 2 : 1;
 };
@@ -401,7 +409,7 @@ struct MxStream {
         }
     }
 
-    static __device__ __forceinline__ void multiply(f32x4 (&acc)[NT][MT], const Run& R,
+    static __device__ __forceinline__ void multiply(f32x4 (&acc)[NT][MT][A8 ? 2 : 1], const Run& R,
                                                     const uint8_t* codes, const uint8_t* scales,
                                                     int k0, bool whole, int g)
     {
@@ -425,14 +433,18 @@ struct MxStream {
                 }
                 const i32x8 aop = {(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
                                    (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+                const MxHalves half = A8 ? mx_halves(aop) : MxHalves{aop, aop};
+                // first one half, then the other: no instruction waits for the one before
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const u32x4 w = R.w[n][s];
-                    const i32x8 wop = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-                    acc[n][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        wop, aop, acc[n][m], MX_E2M1, AFMT, 0, (int)(R.ws[n][s] >> (8 * g)), 0,
-                        (int)(as >> (8 * g)));
-                }
+                for (int h = 0; h < (A8 ? 2 : 1); ++h)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const u32x4 w = R.w[n][s];
+                        const i32x8 wop = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+                        acc[n][m][h] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            wop, h ? half.small : half.large, acc[n][m][h], MX_E2M1, AFMT, 0,
+                            (int)(R.ws[n][s] >> (8 * g)), 0, (int)(as >> (8 * g)));
+                    }
             }
         }
     }
@@ -504,12 +516,14 @@ struct MxStream {
                 at.as[i] = (const uint8_t*)gp.As + m * (K / 32);
             }
         }
-        f32x4 acc[NT][MT];
+        f32x4 acc[NT][MT][A8 ? 2 : 1];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int m = 0; m < MT; ++m)
-                acc[n][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int h = 0; h < (A8 ? 2 : 1); ++h)
+                    acc[n][m][h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         // whole runs w, w + NW, ...; the steps of a partial one go to the waves after
         const int whole = K / RUN, rest = K % RUN / 128;
         Run R;
@@ -543,7 +557,7 @@ struct MxStream {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int m = 0; m < MT; ++m)
-                *(f32x4*)&red[((w * NT + n) * MT + m) * 256 + lane * 4] = acc[n][m];
+                *(f32x4*)&red[((w * NT + n) * MT + m) * 256 + lane * 4] = A8 ? acc[n][m][0] + acc[n][m][A8 ? 1 : 0] : acc[n][m][0];
         __syncthreads();
         // element e of lane l: token l % 16, row 4 (l / 16) + e of its block; threads
         // go along the rows
