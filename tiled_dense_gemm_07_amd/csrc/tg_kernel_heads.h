@@ -346,7 +346,7 @@ struct HeadLane {
         return p.pos ? ((Const*)(uintptr_t)p.pos)[token] : token;
     }
     // Its cosines and sines as loaded, and as they are used: NaN for a position that
-    // the tables lack, no turn for values past R.
+    // the tables lack, RAGGED no turn for what stands past a run's end in its last chunk.
     __device__ __forceinline__ void load(Turn& t, const HeadsParams& p, int64_t pos) const
     {
         if (R == 0)
@@ -380,7 +380,7 @@ struct HeadLane {
     __device__ __forceinline__ void settle(Turn& t, const HeadsParams& p, int64_t pos) const
     {
         const bool in = pos >= 0 && pos < p.P;
-        if (!RAGGED && in && R == D)
+        if (!RAGGED && in)
             return;
         const int n = R / 2;
 #pragma unroll
@@ -398,19 +398,26 @@ struct HeadLane {
             }
         }
     }
-    // Turned to the token's position, or back.
+    // Turned to the token's position, or back.  Values past R stay as they are: times
+    // one and zero an infinity or NaN would spread to the other of its pair.  Chunks are
+    // turned whole or not at all but where neighbours are pairs and R ends in one.
     template <bool BACK>
-    static __device__ __forceinline__ void turn(float (&x)[NC][2 * V], const Turn& t)
+    __device__ __forceinline__ void turn(float (&x)[NC][2 * V], const Turn& t) const
     {
+        constexpr bool PART = RAGGED && INTER;
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < NC; ++c) {
+            if (!PART && i0[c] >= R / 2)
+                continue;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float a = x[c][first(e)], b = x[c][second(e)];
                 const float k = t.c[c][e], n = BACK ? -t.s[c][e] : t.s[c][e];
-                x[c][first(e)] = a * k - b * n;
-                x[c][second(e)] = a * n + b * k;
+                const bool on = !PART || i0[c] + e < R / 2;
+                x[c][first(e)] = on ? a * k - b * n : a;
+                x[c][second(e)] = on ? a * n + b * k : b;
             }
+        }
     }
 };
 
@@ -458,7 +465,7 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256))) void heads_ker
 #pragma unroll
             for (int e = 0; e < 2 * V; ++e)
                 x[c][e] = x[c][e] * r * wf[c][e];
-        Lane::template turn<false>(x, t);
+        L.template turn<false>(x, t);
         if (there)
             L.store(Lane::first_head(s.out, s.ot, s.oh, token, a), Lane::head_offset(s.oh, L.g), x);
         if (++at == units) {
@@ -556,7 +563,7 @@ heads_grad_kernel(HeadsParams p)
         L.unpack(n.x, x);
         L.unpack(n.d, d);
         const float r = L.root(x, p);
-        Lane::template turn<true>(d, n.t);
+        L.template turn<true>(d, n.t);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
