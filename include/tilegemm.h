@@ -541,7 +541,8 @@ tg_status tg_linear_mx_workspace_size(int64_t M, int64_t N, int64_t K, tg_dtype 
  *   needs X.
  *   workspace: as for tg_linear_mx, of the size that
  *     tg_linear_mx_backward_workspace_size reports for the same arguments.
- * With no tokens dW and dbias are zero, with N == 0 dX is.
+ * With no tokens dW and dbias are zero, with N == 0 dX is.  Outputs without elements
+ * may be NULL.
  * Errors: TG_ERR_NULL_POINTER (an input that an output needs, or no output),
  *   TG_ERR_BAD_DTYPE, TG_ERR_BAD_SHAPE (also a size above 8388479),
  *   TG_ERR_WORKSPACE, TG_ERR_ALIAS (an output or the workspace overlaps an input

@@ -462,7 +462,8 @@ tg_status tg_linear_mx_backward(const tg_linear_mx_grad_args* a, void* workspace
         return s;
     const int64_t M = a->M, N = a->N, K = a->K;
     const bool out = (a->dX && M > 0 && K > 0) || (a->dW && N > 0 && K > 0) || (a->dbias && N > 0);
-    if (!a->dX && !a->dW && !a->dbias && N > 0 && (M > 0 || K > 0))
+    // nothing to write: outputs that are empty may be NULL
+    if (!a->dX && !a->dW && !a->dbias && M > 0 && N > 0 && K > 0)
         return TG_ERR_NULL_POINTER;
     if (!out)
         return TG_OK;
