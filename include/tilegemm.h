@@ -587,6 +587,8 @@ tg_status tg_linear_mx_backward_workspace_size(const tg_linear_mx_grad_args* arg
  *     position t.  Values turned by a position outside [0, P) are NaN; tables are
  *     not read out of range.
  *   q_out, k_out: of `dtype`; may be q and k themselves (same address and strides).
+ *   Heads of queries and keys may lie between each other (the same strides, other
+ *   places); of other strides, ranges that overlap count as overlapping.
  * Sums and intermediate values are fp32, one rounding to `dtype`.
  * D <= 1024, T <= 2^30, Hq and Hk <= 65536.
  * Errors: TG_ERR_BAD_DTYPE, TG_ERR_BAD_SHAPE (sizes, R odd or above D, strides

@@ -109,6 +109,41 @@ Span heads_span(const void* p, int64_t T, int64_t H, int64_t D, int64_t st, int6
     return span1(p, H > 0 ? (T - 1) * st + in_token : 0, es);
 }
 
+// Heads of T tokens at given strides, and the range that heads_span has for them.
+struct Heads {
+    Span s;
+    const char* p;
+    int64_t H, st, sh;
+};
+Heads heads_at(const void* p, int64_t T, int64_t H, int64_t D, int64_t st, int64_t sh, int es)
+{
+    return {heads_span(p, T, H, D, st, sh, es), (const char*)p, H, st, sh};
+}
+
+// Whether two sets of heads have a value in common.  Ranges that overlap are looked at
+// by heads where both have the same strides (heads of queries and keys in turn): head i
+// of a and head j of b are o apart, j - i being what counts, and of the tokens the two
+// that bring them nearest.
+bool overlap(const Heads& a, const Heads& b, int64_t T, int64_t D, int es)
+{
+    if (!overlap(a.s, b.s))
+        return false;
+    const int64_t st = T <= 1 ? 0 : a.st, sh = a.H > 1 ? a.sh : b.sh;
+    if ((T > 1 && a.st != b.st) || (a.H > 1 && b.H > 1 && a.sh != b.sh))
+        return true;
+    const int64_t width = D * es, step = st * es;
+    for (int64_t h = 1 - a.H; h < b.H; ++h) {
+        const int64_t o = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p) + h * sh * es;
+        int64_t t = step > 0 ? -o / step : 0;  // rounded towards zero: it or a neighbour
+        for (int64_t n = t - 1; n <= t + 1; ++n) {
+            const int64_t c = n < 1 - T ? 1 - T : (n > T - 1 ? T - 1 : n), off = o + c * step;
+            if (off < width && off > -width)
+                return true;
+        }
+    }
+    return false;
+}
+
 // Strides are not negative, and offsets stay far below 63 bits.
 bool bad_in(const void* p, int64_t T, int64_t H, int64_t st, int64_t sh)
 {
@@ -162,14 +197,15 @@ tg_status check_inputs(const Common& a)
 }
 
 struct Inputs {
-    Span s[7];
+    Heads heads[2];
+    Span s[5];
 };
 Inputs input_spans(const Common& a)
 {
     const int es = tg::dtype_size(a.dtype);
-    return {{heads_span(a.q, a.T, a.Hq, a.D, a.q_t, a.q_h, es),
-             heads_span(a.k, a.T, a.Hk, a.D, a.k_t, a.k_h, es), span1(a.w_q, a.D, es),
-             span1(a.w_k, a.D, es), span1(a.cos, a.P * (a.R / 2), 4),
+    return {{heads_at(a.q, a.T, a.Hq, a.D, a.q_t, a.q_h, es),
+             heads_at(a.k, a.T, a.Hk, a.D, a.k_t, a.k_h, es)},
+            {span1(a.w_q, a.D, es), span1(a.w_k, a.D, es), span1(a.cos, a.P * (a.R / 2), 4),
              span1(a.sin, a.P * (a.R / 2), 4), span1(a.positions, a.T, 8)}};
 }
 
@@ -253,15 +289,19 @@ tg_status tg_head_norm_rope(const tg_head_norm_rope_args* a, tg_stream_t stream)
         return TG_ERR_NULL_POINTER;
     const int es = tg::dtype_size(a->dtype);
     const Inputs in = input_spans(c);
-    const Span out[] = {heads_span(a->q_out, a->T, a->Hq, a->D, a->q_out_t, a->q_out_h, es),
-                        heads_span(a->k_out, a->T, a->Hk, a->D, a->k_out_t, a->k_out_h, es)};
+    const Heads out[] = {heads_at(a->q_out, a->T, a->Hq, a->D, a->q_out_t, a->q_out_h, es),
+                         heads_at(a->k_out, a->T, a->Hk, a->D, a->k_out_t, a->k_out_h, es)};
     const bool same[] = {a->q_out == a->q && a->q_out_t == a->q_t && a->q_out_h == a->q_h,
                          a->k_out == a->k && a->k_out_t == a->k_t && a->k_out_h == a->k_h};
-    for (int o = 0; o < 2; ++o)
-        for (int i = 0; i < 7; ++i)
-            if (!(i == o && same[o]) && overlap(out[o], in.s[i]))
+    for (int o = 0; o < 2; ++o) {
+        for (int i = 0; i < 2; ++i)
+            if (!(i == o && same[o]) && overlap(out[o], in.heads[i], a->T, a->D, es))
                 return TG_ERR_ALIAS;
-    if (overlap(out[0], out[1]))
+        for (const Span& i : in.s)
+            if (overlap(out[o].s, i))
+                return TG_ERR_ALIAS;
+    }
+    if (overlap(out[0], out[1], a->T, a->D, es))
         return TG_ERR_ALIAS;
     const Pick k = pick(a->dtype, a->D, a->R, a->P, a->interleaved != 0, false,
                         larger(larger(a->q_h, a->k_h), larger(a->q_out_h, a->k_out_h)));
@@ -322,21 +362,31 @@ tg_status tg_head_norm_rope_backward(const tg_head_norm_rope_grad_args* a, void*
     }
     const int es = tg::dtype_size(a->dtype);
     const Inputs in = input_spans(c);
-    const Span grads[] = {heads_span(a->dq_out, a->T, a->Hq, a->D, a->dq_out_t, a->dq_out_h, es),
-                          heads_span(a->dk_out, a->T, a->Hk, a->D, a->dk_out_t, a->dk_out_h, es)};
-    const Span out[] = {heads_span(a->dq, a->T, a->Hq, a->D, a->dq_t, a->dq_h, es),
-                        heads_span(a->dk, a->T, a->Hk, a->D, a->dk_t, a->dk_h, es),
-                        span1(a->dw_q, a->D, 4), span1(a->dw_k, a->D, 4),
-                        span1(workspace, (int64_t)g.bytes, 1)};
-    for (int o = 0; o < 5; ++o) {
-        for (const Span& i : in.s)
-            if (overlap(out[o], i))
+    // heads: those out, then those in
+    const Heads heads[] = {heads_at(a->dq, a->T, a->Hq, a->D, a->dq_t, a->dq_h, es),
+                           heads_at(a->dk, a->T, a->Hk, a->D, a->dk_t, a->dk_h, es),
+                           in.heads[0], in.heads[1],
+                           heads_at(a->dq_out, a->T, a->Hq, a->D, a->dq_out_t, a->dq_out_h, es),
+                           heads_at(a->dk_out, a->T, a->Hk, a->D, a->dk_out_t, a->dk_out_h, es)};
+    const Span more[] = {span1(a->dw_q, a->D, 4), span1(a->dw_k, a->D, 4),
+                         span1(workspace, (int64_t)g.bytes, 1)};
+    for (int o = 0; o < 2; ++o) {
+        for (int i = o + 1; i < 6; ++i)
+            if (overlap(heads[o], heads[i], a->T, a->D, es))
                 return TG_ERR_ALIAS;
-        for (const Span& i : grads)
-            if (overlap(out[o], i))
+        for (const Span& i : in.s)
+            if (overlap(heads[o].s, i))
+                return TG_ERR_ALIAS;
+    }
+    for (int o = 0; o < 3; ++o) {
+        for (const Heads& i : heads)
+            if (overlap(more[o], i.s))
+                return TG_ERR_ALIAS;
+        for (const Span& i : in.s)
+            if (overlap(more[o], i))
                 return TG_ERR_ALIAS;
         for (int i = 0; i < o; ++i)
-            if (overlap(out[o], out[i]))
+            if (overlap(more[o], more[i]))
                 return TG_ERR_ALIAS;
     }
     float* at = (float*)workspace;
