@@ -31,8 +31,9 @@
 //    go into the stage strip t used, spread over the last step of t and the
 //    first step of t + 1;
 //  * K % 1024 == 0 (whole scale chunks; the loop runs 4 strips at a time so
-//    that the stage and the place in the chunk are compile-time constants),
-//    16-byte aligned operand and scale rows.  Rows past M or N copy zeros.
+//    that the stage and the place in the chunk are compile-time constants).
+//    Rows past M or N copy zeros.  DmaMx2Any (tg_kernel_mx_linear.h) has a loop
+//    for any K that is a multiple of 128.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -202,7 +203,10 @@ struct DmaMx2 {
     }
 
     // Chunk copy d of wave W: the scale bytes of strips 4 c .. 4 c + 3 into
-    // buffer c & 1 (K % 1024 == 0: a chunk is inside the rows or past K).
+    // buffer c & 1.  K % 1024 == 0: a chunk is inside the rows or past K.  Other K:
+    // a row's last chunk goes on into the next row (zeros past the last one); those
+    // bytes belong to steps that are not multiplied.  Rows of scales are whole dwords,
+    // which is the alignment that the copies need.
     template <int W>
     static __device__ __forceinline__ void issue_chunk(const Lane& L, const Res& r,
                                                        const GemmParams& p, int c, int d,

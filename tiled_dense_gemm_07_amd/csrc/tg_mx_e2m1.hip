@@ -11,7 +11,6 @@ static const MxKernel kKernels[] = {
     TG_MX_STREAM(MX_E2M1, 2, 2, 4, 4, 2.51f, 0.1226f, 0.45f, 0.1302f),
     TG_MX_STREAM(MX_E2M1, 4, 2, 4, 4, 3.07f, 0.187f, 1.57f, 0.2177f),
     TG_MX_TILE(MX_S128, MX_E2M1, 64, 64, 2, 2, 4, 128, 3.05f, 0.1963f, 0.6f, 0.2093f),
-    TG_MX_TILE(MX_S256, MX_E2M1, 64, 64, 2, 2, 2, 128, 3.12f, 0.2207f, 1.66f, 0.2292f),
     TG_MX_TILE(MX_S256, MX_E2M1, 128, 128, 2, 4, 2, 128, 3.76f, 0.319f, 2.47f, 0.3431f),
     TG_MX_TILE(MX_S256, MX_E2M1, 256, 128, 2, 4, 2, 128, 5.11f, 0.4695f, 3.21f, 0.5066f),
     TG_MX_TILE(MX_S256, MX_E2M1, 128, 256, 2, 4, 2, 128, 5.22f, 0.4618f, 3.32f, 0.496f),

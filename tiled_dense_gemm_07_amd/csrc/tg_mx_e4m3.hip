@@ -13,7 +13,6 @@ static const MxKernel kKernels[] = {
     TG_MX_STREAM(MX_E4M3, 2, 2, 4, 4, 2.55f, 0.1625f, 1.07f, 0.1962f),
     TG_MX_STREAM(MX_E4M3, 4, 2, 4, 4, 3.08f, 0.2382f, 1.52f, 0.2812f),
     TG_MX_TILE(MX_S128, MX_E4M3, 64, 64, 2, 2, 4, 128, 3.31f, 0.2197f, 1.68f, 0.2535f),
-    TG_MX_TILE(MX_S256, MX_E4M3, 64, 64, 2, 2, 2, 128, 3.31f, 0.2551f, 1.83f, 0.2708f),
     TG_MX_TILE(MX_S256, MX_E4M3, 128, 128, 2, 4, 2, 128, 4.05f, 0.4018f, 2.55f, 0.4553f),
     TG_MX_TILE(MX_S256, MX_E4M3, 128, 256, 2, 4, 2, 128, 5.56f, 0.6108f, 3.59f, 0.67f),
 };
