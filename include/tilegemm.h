@@ -469,7 +469,7 @@ tg_status tg_block_norm_backward_workspace_size(const tg_block_norm_grad_args* a
  * it is NaN (with TG_EPI_RELU zero).  A block of zeros gets the scale byte 0.
  *
  * tg_quant_mx writes X's blocks along its rows (Q, S), along its columns as rows
- * of the transpose (Qt, St), or both from one read (NULL: not wanted).
+ * of the transpose (Qt, St), or both in one launch (NULL: not wanted).
  *   X: [M][K] of `dtype`, row stride ldx in elements, any alignment.
  *   Q: codes of [M][Kp] elements, Kp = K rounded up to a multiple of 128, zeros
  *     past K: uint8 [M][Kp / 2], two E2M1 codes to a byte (even k in bits 3:0),
@@ -532,6 +532,8 @@ tg_status tg_linear_mx_workspace_size(int64_t M, int64_t N, int64_t K, tg_dtype 
  *   dX[M][K] = Q(dY) Q4(W)       blocks along N,
  *   dW[N][K] = Q(dY)^T Q4(X)     blocks along M,
  *   dbias[N] = sum_m dY[m][n]    from dY as given, fp32, in a fixed order.
+ * X and W are in 4 bits here whatever `fmt` is: a layer whose forward pass took X in
+ * E4M3 gets dW from X in E2M1.
  * The roundings of the quantisation are passed over (their gradient is taken to be
  * that of the value itself).  dY is the gradient before the ReLU, if there is one.
  * Products and sums are those of tg_linear_mx.

@@ -967,8 +967,8 @@ def _mx_dense(name, t, shape):
 def quant_mx(X, fmt=TG_MX_E2M1, sides="rows", q=None, s=None, qt=None, st=None, stream=None):
     """X [M, K] (fp32, fp16 or bf16) to microscaled blocks of 32 elements
     (tg_quant_mx).  sides: "rows" (q, s: blocks along the rows), "columns" (qt,
-    st: blocks along the columns, as rows of the transpose) or "both", from one
-    read.  q: uint8 [M, Kp / 2] (E2M1, two codes to a byte) or [M, Kp] (E4M3), s:
+    st: blocks along the columns, as rows of the transpose) or "both", in one
+    launch.  q: uint8 [M, Kp / 2] (E2M1, two codes to a byte) or [M, Kp] (E4M3), s:
     uint8 [M, Kp / 32], Kp = K rounded up to a multiple of 128; qt and st likewise
     with M and K exchanged.  Returns a QuantMx(q, s, qt, st), None where not
     asked for."""

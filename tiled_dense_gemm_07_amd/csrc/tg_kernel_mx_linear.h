@@ -7,7 +7,7 @@
 // tg_kernel_mx2.h, with bias, any C type and any C rows in the epilogue.  bf16 out:
 // 8192^3 264 to 288 us (E2M1, 3.8 to 4.2 PFLOP/s, 256 x 256 tiles; MFMAs 56% busy at
 // the power-limited clock, the units' LDS behind them) and 445 us (E4M3, 2.5 PFLOP/s,
-// 128 x 256 tiles), 2048 x 4096 x 4096 24 and 31 us (128 x 256), 1000 x 1001 x 1024
+// 128 x 256 tiles), 2048 x 4096 x 4096 25 and 31 us (128 x 256), 1000 x 1001 x 1024
 // 5.6 us (64 x 64; launch, and latency of eight steps of k).
 //
 // mx_stream_kernel: for few tokens the time is that of streaming W once, so W
@@ -27,15 +27,17 @@
 //    13.3 us with 64 rows and 32 tokens, 18.0 with 32 rows, 27.2 with 16 and 16).
 //  * The loads of a wave's next run are issued before the MFMAs of this one.
 //  * E4M3 activations go in two halves (mx_halves), whose products are exact: 16 x
-//    8192 x 8192 took 16.2 us in both launches with one instruction, now 17.0.
+//    8192 x 8192 took 16.2 us in both launches with one instruction, now 17.0 (half of
+//    it the second instruction, half the masks; eight waves 16.9).  The comparisons
+//    above are of one instruction.
 //  * The waves' sums are added in LDS, in the waves' order.
 //  * Rows past M or N read the last row again; their results are not stored.
 //  * FUSED: the activations are given in 16 or 32 bits and every workgroup
 //    quantises them itself, into LDS, while its first loads of W are in flight:
 //    one launch instead of two.
 // Bound by the stream of W and, on small ones, by launch and latency.  8192 x 8192 with
-// W from HBM (36 MB): 16 tokens 12.1 us (2.9 TB/s; a large copy reaches 5.2), in E4M3
-// 13.4, 32 tokens 14.9 and 18.0; FUSED one token 12.3, on 1024 x 1024 3.3 us.
+// W from HBM (36 MB): 16 tokens 12.3 us (2.9 TB/s; a large copy reaches 5.2), in E4M3
+// 14.8, 32 tokens 14.6 and 19.3; FUSED one token 12.4, on 1024 x 1024 3.4 us.
 #pragma once
 
 #include "tg_kernel_mx2.h"

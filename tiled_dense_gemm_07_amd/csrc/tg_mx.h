@@ -83,15 +83,11 @@ __device__ __forceinline__ u32 mx_codes8(float a, float b, float c, float d, flo
     return __builtin_bit_cast(u32, r);
 }
 
-// Largest magnitude over the quad (4 lanes) or half row (8 lanes) of a lane.
-template <int LANES>
+// Largest magnitude over the quad (4 lanes) of a lane.
 __device__ __forceinline__ u32 mx_block_max(u32 m)
 {
     m = MaxOp::of(m, dpp<0xB1>(m));
-    m = MaxOp::of(m, dpp<0x4E>(m));
-    if constexpr (LANES == 8)
-        m = MaxOp::of(m, dpp<0x141>(m));
-    return m;
+    return MaxOp::of(m, dpp<0x4E>(m));
 }
 
 // Magnitudes as stored, two of 16 bits to a word: their order is that of their
@@ -133,7 +129,7 @@ __device__ __forceinline__ u32x2 mx_codes(const Raw8<DT>& r, u32& byte)
     if constexpr (DT != DT_F32)
         m = MaxOp::of(mx_bits<DT>(m, false), mx_bits<DT>(m, true));
     MxScale s;
-    s.of_amax<FMT>(mx_block_max<4>(m));
+    s.of_amax<FMT>(mx_block_max(m));
     byte = s.byte;
     u32x2 w;
     if constexpr (FMT == MX_E2M1 && DT != DT_F32) {

@@ -78,7 +78,7 @@ const void* columns_kernel(int dt, int fmt, bool rows, bool cols, bool sums)
     });
 }
 
-// Blocks along the rows (Q), the columns (Qt), or both from one read; sums: the
+// Blocks along the rows (Q), the columns (Qt), or both in one launch; sums: the
 // columns' sums over each 128 rows.
 tg::MxQuantParams quant_params(int64_t M, int64_t K, const void* X, int64_t ldx, uint8_t* Q,
                                uint8_t* S, uint8_t* Qt, uint8_t* St, float* sums)

@@ -8,11 +8,14 @@ namespace tg {
 
 // One of the product's kernels, and what it costs on this card in microseconds: t0 +
 // strips of 128 k times `one` while its workgroups are at most 256, else for each
-// round of 256 workgroups `round` + strips times `full`.  Fitted to 270 to 330 shapes
-// of each format (M 1 to 8192, N 128 to 14336, K 128 to 8192, odd ones among them),
-// within 8 to 13% on average; the choice by it is 2 to 3% on average above the fastest
-// of all that were measured (30% at most on calls of a few microseconds; 60% on 64
-// tokens by weights of 25 MB in E4M3: the cost does not know HBM from the cache).
+// round of 256 workgroups `round` + strips times `full`.  The tiles' rows were fitted to
+// 270 to 330 shapes of each format (M 1 to 8192, N 128 to 14336, K 128 to 8192, odd ones
+// among them), within 8 to 13% on average; the streams' rows afterwards to shapes of up
+// to 256 tokens alone, E4M3 with one instruction (two take some 4% more) and a 16-bit
+// C.  The choice by both was then 2.8% (E2M1) and 3.1% (E4M3) on average above the
+// fastest of all that were measured: 30% at most on calls of a few microseconds, but 60%
+// on 64 tokens by weights of 25 MB in E4M3, since the cost does not know HBM from the
+// cache.
 struct MxKernel {
     const char* name;
     const void* kernel[3];  // by C's type
