@@ -80,3 +80,20 @@ def test_the_same_call_gives_the_same_bits(M, N, K, fmt):
     for _ in range(8):
         binding.linear_mx(other, w.q, w.s, fmt=fmt)
         assert torch.equal(binding.linear_mx(x, w.q, w.s, fmt=fmt), first)
+
+
+@pytest.mark.parametrize("fmt", [ref.E2M1, ref.E4M3])
+@pytest.mark.parametrize("M,N,K", [(1, 200, 1003), (16, 100, 4100), (40, 300, 601), (300, 129, 130),
+                                   (389, 2423, 1150), (1439, 5439, 200)])
+def test_what_weights_hold_past_k_has_no_part(M, N, K, fmt):
+    say("weights past k %d x %d x %d fmt %d" % (M, N, K, fmt))
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn((M, K), generator=g, device="cuda").to(BF16)
+    w = binding.quant_mx(torch.randn((N, K), generator=g, device="cuda"))
+    want = binding.linear_mx(x, w.q, w.s, fmt=fmt)
+    codes, s = ref.unpack(w.q, ref.E2M1).clone(), w.s.clone()
+    codes[:, K:] = torch.randint(0, 16, codes[:, K:].shape, generator=g, device="cuda")
+    whole = -(-K // 32)  # blocks past the last one that holds values
+    s[:, whole:] = torch.randint(0, 255, s[:, whole:].shape, generator=g, device="cuda",
+                                 dtype=torch.uint8)
+    assert torch.equal(binding.linear_mx(x, ref.pack(codes, ref.E2M1), s, fmt=fmt), want)
