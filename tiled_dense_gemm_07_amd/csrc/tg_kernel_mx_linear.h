@@ -27,9 +27,8 @@
 //    13.3 us with 64 rows and 32 tokens, 18.0 with 32 rows, 27.2 with 16 and 16).
 //  * The loads of a wave's next run are issued before the MFMAs of this one.
 //  * E4M3 activations go in two halves (mx_halves), whose products are exact: 16 x
-//    8192 x 8192 took 16.2 us in both launches with one instruction, now 17.0 (half of
-//    it the second instruction, half the masks; eight waves 16.9).  The comparisons
-//    above are of one instruction.
+//    8192 x 8192 took 16.2 us in both launches with one instruction, now 16.9 (half of
+//    it the second instruction, half the masks).  The comparisons above are of one.
 //  * The waves' sums are added in LDS, in the waves' order.
 //  * Rows past M or N read the last row again; their results are not stored.
 //  * FUSED: the activations are given in 16 or 32 bits and every workgroup
@@ -340,6 +339,10 @@ struct MxStreamParams {
 template <int DTX, int AFMT, int NT, int MT, int ST, int NW, bool FUSED>
 struct MxStream {
     static constexpr bool A8 = AFMT == MX_E4M3;
+    // Sums of the two halves: apart where a wave has one group of rows, whose second
+    // instruction would wait for its first (one token, 8192 x 8192: 10.8 us, together 11.1);
+    // together otherwise (16 tokens 16.9 us, apart 17.1).
+    static constexpr int NH = A8 && FUSED ? 2 : 1;
     static constexpr int RUN = 128 * ST;
     static constexpr int TOKENS = 16 * MT, ROWS = 16 * NT;
 
@@ -411,7 +414,7 @@ struct MxStream {
         }
     }
 
-    static __device__ __forceinline__ void multiply(f32x4 (&acc)[NT][MT][A8 ? 2 : 1], const Run& R,
+    static __device__ __forceinline__ void multiply(f32x4 (&acc)[NT][MT][NH], const Run& R,
                                                     const uint8_t* codes, const uint8_t* scales,
                                                     int k0, bool whole, int g)
     {
@@ -436,15 +439,15 @@ struct MxStream {
                 const i32x8 aop = {(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
                                    (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
                 const MxHalves half = A8 ? mx_halves(aop) : MxHalves{aop, aop};
-                // first one half, then the other: no instruction waits for the one before
+                // first one half of all rows, then the other
 #pragma unroll
                 for (int h = 0; h < (A8 ? 2 : 1); ++h)
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const u32x4 w = R.w[n][s];
                         const i32x8 wop = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-                        acc[n][m][h] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            wop, h ? half.small : half.large, acc[n][m][h], MX_E2M1, AFMT, 0,
+                        acc[n][m][h % NH] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            wop, h ? half.small : half.large, acc[n][m][h % NH], MX_E2M1, AFMT, 0,
                             (int)(R.ws[n][s] >> (8 * g)), 0, (int)(as >> (8 * g)));
                     }
             }
@@ -518,13 +521,13 @@ struct MxStream {
                 at.as[i] = (const uint8_t*)gp.As + m * (K / 32);
             }
         }
-        f32x4 acc[NT][MT][A8 ? 2 : 1];
+        f32x4 acc[NT][MT][NH];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int h = 0; h < (A8 ? 2 : 1); ++h)
+                for (int h = 0; h < NH; ++h)
                     acc[n][m][h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         // whole runs w, w + NW, ...; the steps of a partial one go to the waves after
         const int whole = K / RUN, rest = K % RUN / 128;
@@ -559,7 +562,8 @@ struct MxStream {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int m = 0; m < MT; ++m)
-                *(f32x4*)&red[((w * NT + n) * MT + m) * 256 + lane * 4] = A8 ? acc[n][m][0] + acc[n][m][A8 ? 1 : 0] : acc[n][m][0];
+                *(f32x4*)&red[((w * NT + n) * MT + m) * 256 + lane * 4] =
+                    NH == 2 ? acc[n][m][0] + acc[n][m][NH - 1] : acc[n][m][0];
         __syncthreads();
         // element e of lane l: token l % 16, row 4 (l / 16) + e of its block; threads
         // go along the rows
